@@ -422,6 +422,145 @@ ssm_status ssm_conv1d_update(int64_t S, int64_t D, int64_t K, ssm_dtype dt, floa
                              const void *x, const float *w, const float *bias,
                              int32_t activation, void *y, void *stream);
 
+/* Largest N the gated delta rule kernels are built for. */
+#define SSM_GDR_MAX_N 256
+
+/*
+ * ssm_gdr_fwd -- the gated delta rule over a prefill of L tokens: the SSD
+ * recurrence whose write corrects what the state already answers for the key.
+ *
+ * Per sequence b, head h and channel p, with group g = h / (H / G) and the
+ * state S (P, N), starting from h0 (zeros if NULL):
+ *   a_t    = exp(dt[b,t,h] * A[h])               (dt after ssm_delta_opts)
+ *   e_t[p] = v[b,t,h,p] - a_t * sum_n S_{t-1}[p,n] k[b,t,g,n]
+ *   S_t[p,n] = a_t * S_{t-1}[p,n] + beta[b,t,h] * e_t[p] * k[b,t,g,n]
+ *   y[b,t,h,p] = scale * sum_n S_t[p,n] q[b,t,g,n]
+ *   h_final = S_L
+ * qk_norm == 1: q and k are divided by sqrt(sum_n x[n]^2 + 1e-6) first.
+ * beta enters as given (a model's sigmoid is applied by the caller); dt and A
+ * as in ssm_ssd_fwd, the decay a_t = exp(dt * A) being at most 1 for the
+ * positive dt and negative A that models have (neither sign is required).
+ *
+ * q, k      : (B, L, G, N) dtype `dt`;  v, y : (B, L, H, P) dtype `dt`
+ * dt_in, beta : (B, L, H) dtype `dt`;   A : (H) fp32
+ * h0, h_final : (B, H, P, N) fp32 or NULL
+ * y and h_final must not overlap any input or each other.  Arithmetic and
+ * state are fp32 (on the matrix cores computed operands are split into three
+ * bf16 parts, which hold all 24 bits).
+ * workspace : ssm_gdr_fwd_workspace_size() bytes, 16-byte aligned (NULL where
+ *             that is 0); contents ignored on entry; two calls that overlap
+ *             in time must not share it.
+ * Sizes: 1 <= N <= SSM_GDR_MAX_N, G divides H, B and H <= 65535 (else
+ * SSM_ERR_UNSUPPORTED); any L >= 0 (L == 0 writes h_final = h0) and P >= 0.
+ */
+ssm_status ssm_gdr_fwd(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G, int64_t N,
+                       ssm_dtype dt, const void *q, const void *k, const void *v,
+                       const void *dt_in, const float *A, const void *beta, const float *h0,
+                       float scale, int32_t qk_norm, void *y, float *h_final,
+                       void *workspace, size_t workspace_bytes,
+                       const ssm_delta_opts *dopts, void *stream);
+
+/* Device workspace of ssm_gdr_fwd for these sizes (bytes). */
+size_t ssm_gdr_fwd_workspace_size(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G,
+                                  int64_t N, ssm_dtype dt);
+
+/*
+ * ssm_gdr_decode_steps -- T tokens of the gated delta rule for each of S
+ * sequences whose states are rows of a pool, in place (T = 1: one decode
+ * step).  Bitwise the results of T calls with one token each; a sequence's
+ * results do not depend on which others share the call.
+ *
+ * state_pool : (pool_rows, H, P, N) fp32, in/out
+ * slot_idx   : (S) int32 DEVICE array or NULL (slot s = s; pool_rows >= S);
+ *              slots outside [0, pool_rows) skip the sequence, whose y rows
+ *              are not written; the others must be distinct.
+ * q, k : (S, T, G, N);  v, y : (S, T, H, P);  dt_in, beta : (S, T, H)
+ * y and the pool must not overlap the inputs or each other.  Sizes as
+ * ssm_gdr_fwd.
+ */
+ssm_status ssm_gdr_decode_steps(int64_t S, int64_t T, int64_t H, int64_t P, int64_t G, int64_t N,
+                                ssm_dtype dt, float *state_pool, int64_t pool_rows,
+                                const int32_t *slot_idx, const void *q, const void *k,
+                                const void *v, const void *dt_in, const float *A,
+                                const void *beta, float scale, int32_t qk_norm, void *y,
+                                const ssm_delta_opts *dopts, void *stream);
+
+/*
+ * ssm_gdr_bwd -- gradients of ssm_gdr_fwd for the loss gradients dy
+ * (B, L, H, P) and dh_final (B, H, P, N) fp32 (NULL = zero).  The forward's
+ * states are recomputed.  Outputs, each overwritten:
+ *   dq, dk    : (B, L, G, N) dtype `dt`, summed over the heads of a group
+ *               and through the norm where qk_norm asks for it
+ *   dv        : (B, L, H, P);  ddt, dbeta : (B, L, H), dtype `dt` (ddt is the
+ *               gradient of the dt INPUT, through bias and softplus)
+ *   dA        : (H) fp32;  d_dt_bias : (H) fp32 or NULL
+ *   dh0       : (B, H, P, N) fp32 or NULL
+ * All sums are fp32 and in a fixed order: results are run-to-run
+ * reproducible.  Outputs must not overlap inputs, the workspace or each other.
+ * Sizes as ssm_gdr_fwd, and P, H >= 1.
+ * workspace : ssm_gdr_bwd_workspace_size() bytes, 16-byte aligned.
+ */
+ssm_status ssm_gdr_bwd(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G, int64_t N,
+                       ssm_dtype dt, const void *q, const void *k, const void *v,
+                       const void *dt_in, const float *A, const void *beta, const float *h0,
+                       const void *dy, const float *dh_final, float scale, int32_t qk_norm,
+                       void *dq, void *dk, void *dv, void *ddt, void *dbeta, float *dA,
+                       float *dh0, float *d_dt_bias, void *workspace, size_t workspace_bytes,
+                       const ssm_delta_opts *dopts, void *stream);
+
+size_t ssm_gdr_bwd_workspace_size(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G,
+                                  int64_t N, ssm_dtype dt);
+
+/*
+ * ssm_group_norm_fwd -- group norm over channels-last x (S, T, D) with an
+ * activation and a gate: the norm that follows a mixer's output (T = 1, one
+ * row per token), or that of whole sequences (T tokens).
+ *
+ * For row s and group g of W = D / G consecutive channels, with
+ * u = x * silu(z) (gate_first == 1 and z != NULL) or u = x:
+ *   mean = average of u over the T * W values (0 if center == 0)
+ *   rstd = 1 / sqrt(average of (u - mean)^2 + eps)
+ *   n    = (u - mean) * rstd * weight[d] + bias[d]
+ *   y    = act(n), times silu(z) where z != NULL and gate_first == 0
+ * act is the identity (activation == 0) or SiLU (1); center == 0 is the
+ * root-mean-square norm.  A NaN in a group reaches that group only.
+ *
+ * x, z, y      : (S, T, D) dtype `dt`; z may be NULL
+ * weight, bias : (D) fp32; NULL = ones, zeros
+ * mean, rstd   : (S, G) fp32 or NULL (not returned); mean only with center
+ * Outputs must not overlap inputs or each other.  G divides D, T <= 2^20,
+ * S * D < 2^31 (else SSM_ERR_UNSUPPORTED); eps finite and >= 0.  An empty x
+ * is a no-op.
+ * workspace : ssm_group_norm_fwd_workspace_size() bytes, 16-byte aligned
+ *             (NULL where 0, as for T == 1 up to W = 1280 and more).
+ */
+ssm_status ssm_group_norm_fwd(int64_t S, int64_t T, int64_t D, int64_t G, ssm_dtype dt,
+                              const void *x, const void *z, const float *weight,
+                              const float *bias, float eps, int32_t center,
+                              int32_t activation, int32_t gate_first, void *y, float *mean,
+                              float *rstd, void *workspace, size_t workspace_bytes,
+                              void *stream);
+
+size_t ssm_group_norm_fwd_workspace_size(int64_t S, int64_t T, int64_t D, int64_t G);
+
+/*
+ * ssm_group_norm_bwd -- gradients of ssm_group_norm_fwd for the output
+ * gradient dy (S, T, D), from the same inputs and the mean and rstd (S, G)
+ * that the forward returned (mean only with center).  dx, dz in dtype `dt`
+ * (dz exactly when z is given), dweight, dbias (D) fp32 or NULL; each
+ * overwritten, sums in fp32 and in a fixed order.  An empty x writes zeros to
+ * dweight and dbias.
+ */
+ssm_status ssm_group_norm_bwd(int64_t S, int64_t T, int64_t D, int64_t G, ssm_dtype dt,
+                              const void *x, const void *z, const float *weight,
+                              const float *bias, const void *dy, const float *mean,
+                              const float *rstd, float eps, int32_t center,
+                              int32_t activation, int32_t gate_first, void *dx, void *dz,
+                              float *dweight, float *dbias, void *workspace,
+                              size_t workspace_bytes, void *stream);
+
+size_t ssm_group_norm_bwd_workspace_size(int64_t S, int64_t T, int64_t D, int64_t G);
+
 /* Static description of a status code. */
 const char *ssm_status_string(ssm_status s);
 

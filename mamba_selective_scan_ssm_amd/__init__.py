@@ -92,6 +92,27 @@ def lib():
         L.ssm_conv1d_fwd.restype = ctypes.c_int
         L.ssm_conv1d_update.argtypes = [i64] * 3 + [ctypes.c_int] + [vp] * 4 + [ctypes.c_int32, vp, vp]
         L.ssm_conv1d_update.restype = ctypes.c_int
+        f32, i32 = ctypes.c_float, ctypes.c_int32
+        L.ssm_gdr_fwd.argtypes = [i64] * 6 + [ctypes.c_int] + [vp] * 7 + [f32, i32, vp, vp, vp, sz, vp, vp]
+        L.ssm_gdr_fwd.restype = ctypes.c_int
+        L.ssm_gdr_fwd_workspace_size.argtypes = [i64] * 6 + [ctypes.c_int]
+        L.ssm_gdr_fwd_workspace_size.restype = sz
+        L.ssm_gdr_decode_steps.argtypes = ([i64] * 6 + [ctypes.c_int, vp, i64, vp] + [vp] * 6 +
+                                           [f32, i32, vp, vp, vp])
+        L.ssm_gdr_decode_steps.restype = ctypes.c_int
+        L.ssm_gdr_bwd.argtypes = [i64] * 6 + [ctypes.c_int] + [vp] * 9 + [f32, i32] + [vp] * 8 + [vp, sz, vp, vp]
+        L.ssm_gdr_bwd.restype = ctypes.c_int
+        L.ssm_gdr_bwd_workspace_size.argtypes = [i64] * 6 + [ctypes.c_int]
+        L.ssm_gdr_bwd_workspace_size.restype = sz
+        L.ssm_group_norm_fwd.argtypes = ([i64] * 4 + [ctypes.c_int] + [vp] * 4 + [f32, i32, i32, i32] +
+                                         [vp] * 3 + [vp, sz, vp])
+        L.ssm_group_norm_fwd.restype = ctypes.c_int
+        L.ssm_group_norm_bwd.argtypes = ([i64] * 4 + [ctypes.c_int] + [vp] * 7 + [f32, i32, i32, i32] +
+                                         [vp] * 4 + [vp, sz, vp])
+        L.ssm_group_norm_bwd.restype = ctypes.c_int
+        for f in (L.ssm_group_norm_fwd_workspace_size, L.ssm_group_norm_bwd_workspace_size):
+            f.argtypes = [i64] * 4
+            f.restype = sz
         L.ssm_status_string.argtypes = [ctypes.c_int]
         L.ssm_status_string.restype = ctypes.c_char_p
         L.ssm_version.argtypes = []
@@ -441,4 +462,199 @@ def scan_bwd(x, delta, A, Bm, Cm, D_skip=None, z=None, h0=None, dy=None, dh_fina
           _ptr(out["ddelta"]), _ptr(out["dz"]), _ptr(out["dA"]), _ptr(out["dB"]), _ptr(out["dC"]),
           _ptr(out["dD"]), _ptr(out["dh0"]), _ptr(out["dbias"]), _dopts(delta_bias, delta_softplus),
           _ptr(workspace), wsb, _stream(dev))
+    return out
+
+
+def _gpu_call(dev, fn_name, *args):
+    """A call whose stream is the current one of the tensors' device, made with
+    that device current (it need not be the caller's)."""
+    if dev.type != "cuda":
+        raise ValueError(f"tensors must be on a GPU, not on {dev}")
+    with torch.cuda.device(dev):
+        _call(fn_name, *args, _stream(dev))
+
+
+def _workspace(workspace, need, dev):
+    """The caller's workspace, checked, or a new one: (tensor or None, bytes)."""
+    if workspace is None:
+        return (torch.empty(need, dtype=torch.uint8, device=dev) if need > 0 else None), need
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on {dev}")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def _gdr_inputs(q, k, v, dt, A, beta, dt_bias):
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q must be (B, L, G, N) and v (B, L, H, P)")
+    B, L, G, N = q.shape
+    H, P = v.shape[2], v.shape[3]
+    dev, typ = q.device, q.dtype
+    code = _dtype_code(q)
+    _check("q", q, (B, L, G, N), typ, dev)
+    _check("k", k, (B, L, G, N), typ, dev)
+    _check("v", v, (B, L, H, P), typ, dev)
+    _check("dt", dt, (B, L, H), typ, dev)
+    _check("beta", beta, (B, L, H), typ, dev)
+    _check("A", A, (H,), torch.float32, dev)
+    _check("dt_bias", dt_bias, (H,), torch.float32, dev)
+    return (B, L, H, P, G, N), code, typ, dev
+
+
+def _scale(scale, N):
+    return float(N ** -0.5 if N > 0 else 1.0) if scale is None else float(scale)
+
+
+def gdr_fwd(q, k, v, dt, A, beta, h0=None, *, scale=None, qk_norm=False, y=None, h_final=None,
+            return_final=True, workspace=None, dt_bias=None, dt_softplus=False):
+    """Gated delta rule over a prefill (ssm_gdr_fwd).
+
+    q, k: (B, L, G, N); v: (B, L, H, P); dt, beta: (B, L, H), all float32 or
+    all bfloat16; A: (H,) float32; h0: (B, H, P, N) float32.  The decay is
+    exp(dt * A), with dt_bias (H,) float32 added to dt and softplus applied if
+    dt_softplus.  scale: of the output, N ** -0.5 by default.  qk_norm: q and k
+    are divided by their 2-norms.  Returns (y, h_final)."""
+    sizes, code, typ, dev = _gdr_inputs(q, k, v, dt, A, beta, dt_bias)
+    B, L, H, P, G, N = sizes
+    _check("h0", h0, (B, H, P, N), torch.float32, dev)
+    if y is None:
+        y = torch.empty((B, L, H, P), dtype=typ, device=dev)
+    _check("y", y, (B, L, H, P), typ, dev)
+    if h_final is None and return_final:
+        h_final = torch.empty((B, H, P, N), dtype=torch.float32, device=dev)
+    _check("h_final", h_final, (B, H, P, N), torch.float32, dev)
+    workspace, ws_len = _workspace(workspace, gdr_fwd_workspace_size(*sizes, typ), dev)
+    _gpu_call(dev, "ssm_gdr_fwd", *sizes, code, _ptr(q), _ptr(k), _ptr(v), _ptr(dt), _ptr(A), _ptr(beta), _ptr(h0),
+              _scale(scale, N), int(bool(qk_norm)), _ptr(y), _ptr(h_final), _ptr(workspace), ws_len,
+              _dopts(dt_bias, dt_softplus))
+    return y, h_final
+
+
+def _code_of(dtype):
+    return _dtype_code(torch.empty(0, dtype=dtype))
+
+
+def gdr_fwd_workspace_size(B, L, H, P, G, N, dtype=torch.bfloat16) -> int:
+    return int(lib().ssm_gdr_fwd_workspace_size(B, L, H, P, G, N, _code_of(dtype)))
+
+
+def gdr_bwd_workspace_size(B, L, H, P, G, N, dtype=torch.bfloat16) -> int:
+    return int(lib().ssm_gdr_bwd_workspace_size(B, L, H, P, G, N, _code_of(dtype)))
+
+
+def gdr_decode_steps(state_pool, q, k, v, dt, A, beta, *, slots=None, scale=None, qk_norm=False, y=None,
+                     dt_bias=None, dt_softplus=False):
+    """T tokens of the gated delta rule for S sequences whose states are rows
+    of a pool (ssm_gdr_decode_steps).  state_pool (rows, H, P, N) float32 is
+    updated in place; q, k: (S, T, G, N); v: (S, T, H, P); dt, beta: (S, T, H);
+    slots: (S,) int32 device tensor of pool rows (None: row s for sequence s;
+    outside the pool: skip, y's rows are left as they were).  Returns y."""
+    sizes, code, typ, dev = _gdr_inputs(q, k, v, dt, A, beta, dt_bias)
+    S, T, H, P, G, N = sizes
+    if state_pool.dim() != 4:
+        raise ValueError("state_pool must be (rows, H, P, N)")
+    rows = state_pool.shape[0]
+    _check("state_pool", state_pool, (rows, H, P, N), torch.float32, dev)
+    _check("slots", slots, (S,), torch.int32, dev)
+    if y is None:
+        y = torch.empty((S, T, H, P), dtype=typ, device=dev)
+    _check("y", y, (S, T, H, P), typ, dev)
+    _gpu_call(dev, "ssm_gdr_decode_steps", *sizes, code, _ptr(state_pool), rows, _ptr(slots), _ptr(q), _ptr(k),
+              _ptr(v), _ptr(dt), _ptr(A), _ptr(beta), _scale(scale, N), int(bool(qk_norm)), _ptr(y),
+              _dopts(dt_bias, dt_softplus))
+    return y
+
+
+def gdr_bwd(q, k, v, dt, A, beta, h0=None, dy=None, dh_final=None, *, scale=None, qk_norm=False, dt_bias=None,
+            dt_softplus=False, want_dh0=True, want_dbias=False, workspace=None):
+    """Gradients of gdr_fwd (ssm_gdr_bwd) for the output gradient dy and the
+    final-state gradient dh_final (None = zero).  Returns a dict: dq, dk, dv,
+    ddt, dbeta (input dtype), dA (float32), dh0 (None unless want_dh0), dbias
+    (float32; None unless want_dbias)."""
+    sizes, code, typ, dev = _gdr_inputs(q, k, v, dt, A, beta, dt_bias)
+    B, L, H, P, G, N = sizes
+    if dy is None:
+        raise ValueError("dy is required")
+    _check("dy", dy, (B, L, H, P), typ, dev)
+    _check("h0", h0, (B, H, P, N), torch.float32, dev)
+    _check("dh_final", dh_final, (B, H, P, N), torch.float32, dev)
+    out = {"dq": torch.empty_like(q), "dk": torch.empty_like(k), "dv": torch.empty_like(v),
+           "ddt": torch.empty_like(dt), "dbeta": torch.empty_like(beta),
+           "dA": torch.empty((H,), dtype=torch.float32, device=dev),
+           "dh0": torch.empty((B, H, P, N), dtype=torch.float32, device=dev) if want_dh0 else None,
+           "dbias": torch.empty((H,), dtype=torch.float32, device=dev) if want_dbias else None}
+    workspace, ws_len = _workspace(workspace, gdr_bwd_workspace_size(*sizes, typ), dev)
+    _gpu_call(dev, "ssm_gdr_bwd", *sizes, code, _ptr(q), _ptr(k), _ptr(v), _ptr(dt), _ptr(A), _ptr(beta), _ptr(h0),
+              _ptr(dy), _ptr(dh_final), _scale(scale, N), int(bool(qk_norm)), _ptr(out["dq"]), _ptr(out["dk"]),
+              _ptr(out["dv"]), _ptr(out["ddt"]), _ptr(out["dbeta"]), _ptr(out["dA"]), _ptr(out["dh0"]),
+              _ptr(out["dbias"]), _ptr(workspace), ws_len, _dopts(dt_bias, dt_softplus))
+    return out
+
+
+def _norm_args(x, groups, weight, bias, z, activation, gate, per_token):
+    if x.dim() != 3:
+        raise ValueError("x must be (B, L, D)")
+    B, L, D = x.shape
+    dev, typ = x.device, x.dtype
+    code = _dtype_code(x)
+    _check("x", x, (B, L, D), typ, dev)
+    _check("z", z, (B, L, D), typ, dev)
+    _check("weight", weight, (D,), torch.float32, dev)
+    _check("bias", bias, (D,), torch.float32, dev)
+    if gate not in (None, "before", "after"):
+        raise ValueError(f"gate must be None, 'before' or 'after', got {gate!r}")
+    if (z is None) != (gate is None):
+        raise ValueError("z and gate ('before' or 'after' the norm) are given together")
+    S, T = (B * L, 1) if per_token else (B, L)
+    return (S, T, D, int(groups)), code, (_act_code(activation), int(gate == "before"))
+
+
+def group_norm_fwd(x, groups, weight=None, bias=None, z=None, *, eps=1e-5, center=True, activation=None, gate=None,
+                   per_token=True, y=None, return_stats=True, workspace=None):
+    """Group norm, channels last, with an activation and a gate
+    (ssm_group_norm_fwd).
+
+    x, z: (B, L, D) float32 or bfloat16; weight, bias: (D,) float32.  The
+    statistics are those of one token's D // groups channels (per_token) or of
+    the whole sequence's.  center=False: the root-mean-square norm.
+    activation: None or "silu", of the normalised value.  gate: "before" (x *
+    silu(z) is normalised) or "after" (the result times silu(z)), with z.
+    Returns (y, mean, rstd); mean (None where not centred) and rstd are
+    float32, (B, L, groups) per token or (B, groups), None without
+    return_stats."""
+    sizes, code, (act, first) = _norm_args(x, groups, weight, bias, z, activation, gate, per_token)
+    S, T, D, G = sizes
+    dev = x.device
+    if y is None:
+        y = torch.empty_like(x)
+    _check("y", y, x.shape, x.dtype, dev)
+    stat = (x.shape[0], x.shape[1], G) if per_token else (x.shape[0], G)
+    mean = torch.empty(stat, dtype=torch.float32, device=dev) if return_stats and center else None
+    rstd = torch.empty(stat, dtype=torch.float32, device=dev) if return_stats else None
+    workspace, ws_len = _workspace(workspace, int(lib().ssm_group_norm_fwd_workspace_size(*sizes)), dev)
+    _gpu_call(dev, "ssm_group_norm_fwd", *sizes, code, _ptr(x), _ptr(z), _ptr(weight), _ptr(bias), float(eps),
+              int(bool(center)), act, first, _ptr(y), _ptr(mean), _ptr(rstd), _ptr(workspace), ws_len)
+    return y, mean, rstd
+
+
+def group_norm_bwd(x, groups, dy, mean, rstd, weight=None, bias=None, z=None, *, eps=1e-5, center=True,
+                   activation=None, gate=None, per_token=True, workspace=None):
+    """Gradients of group_norm_fwd (ssm_group_norm_bwd) from its inputs and its
+    mean and rstd.  Returns a dict: dx, dz (None without z), dweight, dbias
+    (None without weight, bias)."""
+    sizes, code, (act, first) = _norm_args(x, groups, weight, bias, z, activation, gate, per_token)
+    S, T, D, G = sizes
+    dev = x.device
+    stat = (x.shape[0], x.shape[1], G) if per_token else (x.shape[0], G)
+    _check("dy", dy, x.shape, x.dtype, dev)
+    _check("mean", mean, stat, torch.float32, dev)
+    _check("rstd", rstd, stat, torch.float32, dev)
+    if dy is None or rstd is None or (center and mean is None):
+        raise ValueError("dy, rstd and (where centred) mean are required")
+    out = {"dx": torch.empty_like(x), "dz": None if z is None else torch.empty_like(z),
+           "dweight": None if weight is None else torch.empty_like(weight),
+           "dbias": None if bias is None else torch.empty_like(bias)}
+    workspace, ws_len = _workspace(workspace, int(lib().ssm_group_norm_bwd_workspace_size(*sizes)), dev)
+    _gpu_call(dev, "ssm_group_norm_bwd", *sizes, code, _ptr(x), _ptr(z), _ptr(weight), _ptr(bias), _ptr(dy),
+              _ptr(mean) if center else None, _ptr(rstd), float(eps), int(bool(center)), act, first, _ptr(out["dx"]),
+              _ptr(out["dz"]), _ptr(out["dweight"]), _ptr(out["dbias"]), _ptr(workspace), ws_len)
     return out

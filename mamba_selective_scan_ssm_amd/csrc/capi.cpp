@@ -8,34 +8,13 @@
 #include <cstdint>
 
 #include "bwd.h"
+#include "capi_common.h"
 #include "launch.h"
 
 namespace {
 
 using ssm::DType;
-
-constexpr int64_t kMaxGridYZ = 65535;
-
-bool valid_dtype(ssm_dtype dt) { return dt == SSM_F32 || dt == SSM_BF16; }
-int64_t esize(ssm_dtype dt) { return dt == SSM_BF16 ? 2 : 4; }
-
-struct Range {
-  const void *p;
-  int64_t bytes;
-};
-
-bool overlap(Range a, Range b) {
-  if (!a.p || !b.p || a.bytes <= 0 || b.bytes <= 0) return false;
-  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
-  return a0 < b0 + static_cast<uintptr_t>(b.bytes) && b0 < a0 + static_cast<uintptr_t>(a.bytes);
-}
-
-template <size_t K>
-bool overlaps_any(Range out, const Range (&ins)[K]) {
-  for (size_t i = 0; i < K; ++i)
-    if (overlap(out, ins[i])) return true;
-  return false;
-}
+using namespace ssm::capi;
 
 bool tuning_ok(const ssm_tuning *t) {
   if (!t) return true;
@@ -50,15 +29,6 @@ bool tuning_ok(const ssm_tuning *t) {
 }
 
 int spl_of(const ssm_tuning *t) { return t ? t->states_per_lane : 0; }
-
-bool dopts_ok(const ssm_delta_opts *o) {
-  if (!o) return true;
-  for (int i = 0; i < 3; ++i)
-    if (o->reserved[i] != 0) return false;
-  return o->softplus == 0 || o->softplus == 1;
-}
-const float *dbias_of(const ssm_delta_opts *o) { return o ? o->bias : nullptr; }
-bool dsoft_of(const ssm_delta_opts *o) { return o && o->softplus == 1; }
 
 // Variant choice: a function of (L, D, N) only, so a sequence's result does
 // not depend on the batch it is in.  Sequential when one sequence already
@@ -86,8 +56,6 @@ Plan plan_scan(int64_t L, int64_t D, const ssm_tuning *t) {
   if (variant == 2 && seg <= 0) seg = 64;
   return Plan{variant, seg};
 }
-
-ssm_status hip_status(hipError_t e) { return e == hipSuccess ? SSM_OK : SSM_ERR_HIP; }
 
 // SIMDs of the current device (4 per CU; cached per device; 0 if the query
 // fails, where the halved schedule is then not chosen automatically).

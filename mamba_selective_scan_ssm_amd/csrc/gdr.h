@@ -1,0 +1,69 @@
+// Launcher interface of the gated delta rule (gdr_seq.hip, gdr_chunk.hip,
+// gdr_bwd.hip).  The arguments are validated by the C ABI before the launch.
+#pragma once
+
+#include "launch.h"
+
+namespace ssm {
+
+// 1 / sqrt(sum of squares + kQkNormEps): the norm of q and k.
+constexpr float kQkNormEps = 1e-6f;
+
+struct GdrArgs {
+  int64_t B, L, H, P, G, N;
+  DType dt_type;              // storage type of q, k, v, dt, beta and y
+  const void *q, *k;          // (B, L, G, N)
+  const void *v;              // (B, L, H, P)
+  const void *dt;             // (B, L, H)
+  const float *A;             // (H)
+  const void *beta;           // (B, L, H)
+  const float *h0;            // (B, H, P, N) or null
+  float scale;                // of the output
+  bool qk_norm;               // divide q and k by their 2-norms
+  void *y;                    // (B, L, H, P)
+  float *h_final;             // (B, H, P, N) or null
+  const float *dt_bias;       // (H) or null: added to dt
+  bool dt_softplus;           // softplus of (dt + bias)
+  // Optional: sequence b reads h0 and writes h_final at row slots[b] of a
+  // pool of pool_rows rows; a slot outside [0, pool_rows) skips it.
+  const int32_t *slots;
+  int64_t pool_rows;
+  // Optional (token path): the state entering every kGdrSeg-token segment,
+  // at (((b * H + h) * nseg + s) * P + p) * N + n.
+  float *h_ckpt;
+};
+
+constexpr int kGdrSeg = 8;  // tokens per saved state of the token path
+
+// Token by token on the vector ALU (gdr_seq.hip): any dtype, P, 1 <= N <= 256,
+// any alignment, no workspace.  y may be null (states only).
+hipError_t launch_gdr_seq(const GdrArgs &a, hipStream_t s);
+// The same recurrence for a few tokens: the state goes from memory to
+// registers and back once, nothing is staged.
+hipError_t launch_gdr_step(const GdrArgs &a, hipStream_t s);
+
+struct GdrBwdArgs {
+  GdrArgs f;                  // the forward's inputs (y, h_final unused)
+  const void *dy;             // (B, L, H, P)
+  const float *dh_final;      // (B, H, P, N) or null
+  void *dq, *dk;              // (B, L, G, N), dtype
+  void *dv, *ddt, *dbeta;     // dtype
+  float *dA;                  // (H)
+  float *dbias;               // (H) or null
+  float *dh0;                 // (B, H, P, N) or null
+  float *ws;
+};
+
+// Gradients token by token on the vector ALU: any dtype, P, 1 <= N <= 256.
+int64_t gdr_bwd_seq_ws_floats(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G, int64_t N);
+hipError_t launch_gdr_bwd_seq(const GdrBwdArgs &a, hipStream_t s);
+
+// Sums of the per-head, per-tile partial gradients (gdr_bwd.hip), shared by
+// the token path and the chunked path.  dq_part, dk_part: (tiles, B, L, H, N)
+// of the normalised q and k; sc_part: (2, tiles, B, L, H), the gradients of
+// beta and of the log decay; red: gdr_reduce_ws_floats floats.
+int64_t gdr_reduce_ws_floats(int64_t B, int64_t L, int64_t H);
+hipError_t launch_gdr_reduce(const GdrBwdArgs &a, int64_t tiles, const float *dq_part, const float *dk_part,
+                             const float *sc_part, float *red, hipStream_t s);
+
+}  // namespace ssm

@@ -1,0 +1,733 @@
+// Group norm with an activation, channels last, and its gradients.
+//
+// x (S, T, D), G groups of W = D / G channels; mean and variance over the T
+// tokens and W channels of a group (T = 1: per token, the norm that follows a
+// mixer; T = L: a whole sequence).  With u = x silu(z) (gate first) or x,
+//   xh = (u - mean) rstd,  n = xh w + b,  y = (SiLU? n) (silu(z) where the gate comes last)
+// and, with dn the gradient of n and g = dn w,
+//   du = rstd (g - mean(g) - xh mean(g xh)),  dw = sum dn xh,  db = sum dn
+// (no mean(g) and no mean where not centred).
+//
+// Two paths, by the sizes alone:
+//  - rows (T = 1, W up to 256 lanes x 8 pieces): a group's channels lie in the
+//    registers of LPG adjacent lanes, so the statistics (the mean first, then
+//    the squares about it) and the result take one pass over memory.  The
+//    backward keeps its channels over a block of rows and sums dw and db in
+//    registers; the blocks' sums are added in order by a second kernel.
+//  - columns (everything else): per-channel sums over slices of the tokens,
+//    coalesced whatever W is; a kernel that joins the slices and the channels
+//    of a group (mean and squares about it by Chan's formula; the backward's
+//    group sums are sums of its per-channel ones weighted by w); and a pass
+//    that applies them.
+// All sums are fp32 and in a fixed order.
+#include "device_common.h"
+#include "group_norm.h"
+
+namespace ssm {
+namespace {
+
+constexpr int kThreads = 256;
+
+__device__ __forceinline__ float sigmoid(float v) {
+  return __builtin_amdgcn_rcpf(1.0f + fast_exp2(-v * kLog2e));
+}
+// silu(v) and its derivative s + v s (1 - s)
+__device__ __forceinline__ float silu_grad(float v, float &slope) {
+  const float s = sigmoid(v);
+  slope = s * fmaf(v, 1.f - s, 1.f);
+  return v * s;
+}
+
+// rounding may leave a variance below 0; a NaN stays one
+__device__ __forceinline__ float not_negative(float v) { return v < 0.f ? 0.f : v; }
+
+// VE consecutive elements (16 bytes where VE > 1)
+template <typename T, int VE>
+struct Piece {
+  T v[VE];
+};
+template <typename T, int VE>
+__device__ __forceinline__ Piece<T, VE> load_piece(const T *p) {
+  Piece<T, VE> r;
+  if constexpr (VE == 1) {
+    r.v[0] = *p;
+  } else {
+    static_assert(sizeof(T) * VE == 16, "16-byte pieces");
+    const uint4 u = *reinterpret_cast<const uint4 *>(p);
+    __builtin_memcpy(r.v, &u, 16);
+  }
+  return r;
+}
+template <typename T, int VE>
+__device__ __forceinline__ void store_piece(T *p, const float *f) {
+  if constexpr (VE == 1) {
+    *p = from_f32<T>(f[0]);
+  } else {
+    T v[VE];
+#pragma unroll
+    for (int e = 0; e < VE; ++e) v[e] = from_f32<T>(f[e]);
+    uint4 u;
+    __builtin_memcpy(&u, v, 16);
+    *reinterpret_cast<uint4 *>(p) = u;
+  }
+}
+template <int VE>
+__device__ __forceinline__ void load_f32(const float *p, float *f) {
+  if constexpr (VE == 1) {
+    f[0] = *p;
+  } else {
+#pragma unroll
+    for (int e = 0; e < VE; e += 4) {
+      const float4 q = *reinterpret_cast<const float4 *>(p + e);
+      f[e] = q.x;
+      f[e + 1] = q.y;
+      f[e + 2] = q.z;
+      f[e + 3] = q.w;
+    }
+  }
+}
+
+// Sum over LPG adjacent lanes, every lane getting it; LPG = 256: the workgroup
+// (s_red: 4 floats; the barriers order repeated uses).
+template <int kCtrl>
+__device__ __forceinline__ float dpp_get(float v) {
+  return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), kCtrl, 0xF, 0xF, true));
+}
+template <int LPG>
+__device__ __forceinline__ float lanes_sum(float v, float *s_red) {
+  if constexpr (LPG >= 2) v += dpp_get<0xB1>(v);
+  if constexpr (LPG >= 4) v += dpp_get<0x4E>(v);
+  if constexpr (LPG >= 8) v += dpp_get<0x141>(v);
+  if constexpr (LPG >= 16) v += dpp_get<0x140>(v);
+  if constexpr (LPG >= 32) v += __shfl_xor(v, 16);
+  if constexpr (LPG >= 64) v += __shfl_xor(v, 32);
+  if constexpr (LPG == 256) {
+    __syncthreads();
+    if (threadIdx.x % 64 == 0) s_red[threadIdx.x / 64] = v;
+    __syncthreads();
+    v = (s_red[0] + s_red[1]) + (s_red[2] + s_red[3]);
+  }
+  return v;
+}
+
+// ------------------------------------------------------------------ rows
+// Unit u = s G + g covers the W elements from u W.  Lane l of the unit holds
+// the pieces l, l + LPG, ...
+template <typename T, int VE, int LPG, int NV>
+__global__ __launch_bounds__(kThreads) void norm_rows_fwd_kernel(NormArgs a) {
+  __shared__ float s_red[4];
+  const int64_t W = a.D / a.G, units = a.S * a.G;
+  const int l = threadIdx.x % LPG;
+  const int64_t u_raw = static_cast<int64_t>(blockIdx.x) * (kThreads / LPG) + threadIdx.x / LPG;
+  const bool live = u_raw < units;
+  const int64_t u = live ? u_raw : units - 1;
+  const int64_t g = u % a.G;
+  const int pieces = static_cast<int>(W / VE);
+  const T *xp = static_cast<const T *>(a.x) + u * W;
+  const T *zp = a.z ? static_cast<const T *>(a.z) + u * W : xp;  // read alike; unused without a gate
+  Piece<T, VE> xr[NV], zr[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int at = l + j * LPG < pieces ? l + j * LPG : 0;
+    xr[j] = load_piece<T, VE>(xp + at * VE);
+    if (a.z) zr[j] = load_piece<T, VE>(zp + at * VE);
+  }
+  float v[NV][VE];
+  float sum = 0.f;
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int e = 0; e < VE; ++e) {
+      float f = to_f32(xr[j].v[e]);
+      if (a.z && a.gate_first) f *= silu(to_f32(zr[j].v[e]));
+      if (l + j * LPG >= pieces) f = 0.f;
+      v[j][e] = f;
+      sum += f;
+    }
+  const float inv = 1.f / static_cast<float>(W);
+  const float mean = a.center ? lanes_sum<LPG>(sum, s_red) * inv : 0.f;
+  // the values about the mean, and what the rounded mean leaves of their sum
+  float sq = 0.f, left = 0.f;
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int e = 0; e < VE; ++e) {
+      v[j][e] = l + j * LPG < pieces ? v[j][e] - mean : 0.f;
+      left += v[j][e];
+      sq = fmaf(v[j][e], v[j][e], sq);
+    }
+  const float delta = a.center ? lanes_sum<LPG>(left, s_red) * inv : 0.f;
+  const float var = not_negative(fmaf(lanes_sum<LPG>(sq, s_red), inv, -delta * delta));
+  const float rstd = 1.f / sqrtf(var + a.eps);
+  if (!live) return;
+  if (l == 0) {
+    if (a.mean) a.mean[u] = mean + delta;
+    if (a.rstd) a.rstd[u] = rstd;
+  }
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int at = l + j * LPG;
+    if (at < pieces) {
+      float wv[VE], bv[VE], out[VE];
+#pragma unroll
+      for (int e = 0; e < VE; ++e) {
+        wv[e] = 1.f;
+        bv[e] = 0.f;
+      }
+      if (a.w) load_f32<VE>(a.w + g * W + at * VE, wv);
+      if (a.b) load_f32<VE>(a.b + g * W + at * VE, bv);
+#pragma unroll
+      for (int e = 0; e < VE; ++e) {
+        float n = fmaf((v[j][e] - delta) * rstd, wv[e], bv[e]);
+        if (a.act) n = silu(n);
+        if (a.z && !a.gate_first) n *= silu(to_f32(zr[j].v[e]));
+        out[e] = n;
+      }
+      store_piece<T, VE>(static_cast<T *>(a.y) + u * W + at * VE, out);
+    }
+  }
+}
+
+// One element of the backward up to its normalised value and the gradient dn
+// of n; what the gate's gradient needs is formed again where it is stored.
+__device__ __forceinline__ void norm_elem(const NormArgs &a, float x, float z, float dy, float w, float b, float mean,
+                                          float rstd, float &xh, float &dn) {
+  const float zs = a.z ? silu(z) : 1.f;
+  xh = ((a.gate_first ? x * zs : x) - mean) * rstd;
+  float slope = 1.f;
+  if (a.act) silu_grad(fmaf(xh, w, b), slope);
+  dn = (a.gate_first ? dy : dy * zs) * slope;
+}
+// dx and dz of one element, from du
+__device__ __forceinline__ void norm_elem_out(const NormArgs &a, float x, float z, float dy, float w, float b, float xh,
+                                              float du, float &dx, float &dz) {
+  dx = du;
+  if (!a.z) return;
+  float zslope;
+  const float zs = silu_grad(z, zslope);
+  if (a.gate_first) {
+    dx = du * zs;
+    dz = du * x * zslope;
+  } else {
+    const float n = fmaf(xh, w, b);
+    dz = dy * (a.act ? silu(n) : n) * zslope;
+  }
+}
+
+// The unit of the forward, its group fixed, walks the rows r0, r0 + step, ...
+// of a block: units of a workgroup are gsub groups by rsub rows.
+template <typename T, int VE, int LPG, int NV>
+__global__ __launch_bounds__(kThreads) void norm_rows_bwd_kernel(NormArgs a, int gsub, int64_t rows, int64_t parts) {
+  __shared__ float s_red[4];
+  const int64_t W = a.D / a.G;
+  const int l = threadIdx.x % LPG, ui = threadIdx.x / LPG;
+  const int rsub = kThreads / LPG / gsub;
+  const int64_t g_raw = static_cast<int64_t>(blockIdx.x) * gsub + ui % gsub;
+  const bool glive = g_raw < a.G;
+  const int64_t g = glive ? g_raw : a.G - 1;
+  const int64_t s0 = static_cast<int64_t>(blockIdx.y) * rows, s1 = s0 + rows < a.S ? s0 + rows : a.S;
+  const int pieces = static_cast<int>(W / VE);
+  const float inv = 1.f / static_cast<float>(W);
+  float wv[NV][VE], bv[NV][VE], dw[NV][VE], db[NV][VE];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int at = l + j * LPG < pieces ? l + j * LPG : 0;
+#pragma unroll
+    for (int e = 0; e < VE; ++e) {
+      wv[j][e] = 1.f;
+      bv[j][e] = dw[j][e] = db[j][e] = 0.f;
+    }
+    if (a.w) load_f32<VE>(a.w + g * W + at * VE, wv[j]);
+    if (a.b) load_f32<VE>(a.b + g * W + at * VE, bv[j]);
+  }
+  const int64_t steps = (s1 - s0 + rsub - 1) / rsub;  // the same for every lane of the workgroup
+  for (int64_t i = 0; i < steps; ++i) {
+    const int64_t s_raw = s0 + i * rsub + ui / gsub;
+    const bool live = glive && s_raw < s1;
+    const int64_t s = s_raw < s1 ? s_raw : s1 - 1;
+    const int64_t base = (s * a.G + g) * W;
+    const T *xp = static_cast<const T *>(a.x) + base, *yp = static_cast<const T *>(a.dy) + base;
+    const T *zp = a.z ? static_cast<const T *>(a.z) + base : xp;
+    Piece<T, VE> xr[NV], yr[NV], zr[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int at = l + j * LPG < pieces ? l + j * LPG : 0;
+      xr[j] = load_piece<T, VE>(xp + at * VE);
+      yr[j] = load_piece<T, VE>(yp + at * VE);
+      if (a.z) zr[j] = load_piece<T, VE>(zp + at * VE);
+    }
+    const float mean = a.center ? a.mean[s * a.G + g] : 0.f, rstd = a.rstd[s * a.G + g];
+    float sg = 0.f, sgx = 0.f;
+    float xh[NV][VE], dn[NV][VE];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const bool in = l + j * LPG < pieces;
+#pragma unroll
+      for (int e = 0; e < VE; ++e) {
+        norm_elem(a, to_f32(xr[j].v[e]), a.z ? to_f32(zr[j].v[e]) : 0.f, to_f32(yr[j].v[e]), wv[j][e], bv[j][e],
+                  mean, rstd, xh[j][e], dn[j][e]);
+        if (in) {
+          const float gr = dn[j][e] * wv[j][e];
+          sg += gr;
+          sgx = fmaf(gr, xh[j][e], sgx);
+        }
+        if (in && live) {
+          dw[j][e] = fmaf(dn[j][e], xh[j][e], dw[j][e]);
+          db[j][e] += dn[j][e];
+        }
+      }
+    }
+    const float mg = a.center ? lanes_sum<LPG>(sg, s_red) * inv : 0.f;
+    const float mgx = lanes_sum<LPG>(sgx, s_red) * inv;
+    if (live) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int at = l + j * LPG;
+        if (at < pieces) {
+          float ox[VE], oz[VE];
+#pragma unroll
+          for (int e = 0; e < VE; ++e) {
+            const float du = rstd * (dn[j][e] * wv[j][e] - mg - xh[j][e] * mgx);
+            norm_elem_out(a, to_f32(xr[j].v[e]), a.z ? to_f32(zr[j].v[e]) : 0.f, to_f32(yr[j].v[e]), wv[j][e],
+                          bv[j][e], xh[j][e], du, ox[e], oz[e]);
+          }
+          store_piece<T, VE>(static_cast<T *>(a.dx) + base + at * VE, ox);
+          if (a.z) store_piece<T, VE>(static_cast<T *>(a.dz) + base + at * VE, oz);
+        }
+      }
+    }
+  }
+  if (!glive) return;
+  const int64_t part = static_cast<int64_t>(blockIdx.y) * rsub + ui / gsub;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int at = l + j * LPG;
+    if (at < pieces)
+#pragma unroll
+      for (int e = 0; e < VE; ++e) {
+        const int64_t d = g * W + at * VE + e;
+        a.ws[part * a.D + d] = dw[j][e];
+        a.ws[(parts + part) * a.D + d] = db[j][e];
+      }
+  }
+}
+
+// dw and db: the partial sums of a channel, added in order.  A workgroup holds
+// 64 channels; its 4 waves take every fourth part and meet in LDS.
+__global__ __launch_bounds__(kThreads) void norm_params_kernel(NormArgs a, int64_t parts, const float *pw,
+                                                               const float *pb) {
+  __shared__ float s_w[4][64], s_b[4][64];
+  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+  const int64_t d = static_cast<int64_t>(blockIdx.x) * 64 + lane;
+  float x = 0.f, y = 0.f;
+  if (d < a.D)
+    for (int64_t i = wave; i < parts; i += 4) {
+      x += pw[i * a.D + d];
+      y += pb[i * a.D + d];
+    }
+  s_w[wave][lane] = x;
+  s_b[wave][lane] = y;
+  __syncthreads();
+  if (wave == 0 && d < a.D) {
+    if (a.dw) a.dw[d] = (s_w[0][lane] + s_w[1][lane]) + (s_w[2][lane] + s_w[3][lane]);
+    if (a.db) a.db[d] = (s_b[0][lane] + s_b[1][lane]) + (s_b[2][lane] + s_b[3][lane]);
+  }
+}
+
+// ------------------------------------------------------------------ columns
+// Slices of `rows` tokens; a wave holds 64 VE channels of one slice, a
+// workgroup 4 slices.  fwd: per channel the mean and the squares about it,
+// from sums shifted by the slice's first value.
+template <typename T, int VE>
+__global__ __launch_bounds__(kThreads) void norm_cols_sums_kernel(NormArgs a, int64_t rows, int64_t slices) {
+  const int lane = threadIdx.x % 64;
+  const int64_t cb = (a.D + 64 * VE - 1) / (64 * VE), s = blockIdx.x / cb;
+  const int64_t slice = static_cast<int64_t>(blockIdx.y) * 4 + threadIdx.x / 64;
+  const int64_t d = (blockIdx.x % cb * 64 + lane) * VE;
+  if (slice >= slices || d >= a.D) return;
+  const int64_t t0 = slice * rows, t1 = t0 + rows < a.T ? t0 + rows : a.T;
+  const bool gate = a.z && a.gate_first;
+  float first[VE], s1[VE], s2[VE];
+#pragma unroll
+  for (int e = 0; e < VE; ++e) s1[e] = s2[e] = first[e] = 0.f;
+#pragma unroll 4
+  for (int64_t t = t0; t < t1; ++t) {
+    const int64_t at = (s * a.T + t) * a.D + d;
+    const Piece<T, VE> xr = load_piece<T, VE>(static_cast<const T *>(a.x) + at);
+    Piece<T, VE> zr;
+    if (gate) zr = load_piece<T, VE>(static_cast<const T *>(a.z) + at);
+#pragma unroll
+    for (int e = 0; e < VE; ++e) {
+      float u = to_f32(xr.v[e]);
+      if (gate) u *= silu(to_f32(zr.v[e]));
+      if (t == t0 && a.center) first[e] = u;
+      const float c = u - first[e];
+      s1[e] += c;
+      s2[e] = fmaf(c, c, s2[e]);
+    }
+  }
+  const float n = static_cast<float>(t1 - t0);
+#pragma unroll
+  for (int e = 0; e < VE; ++e) {
+    const int64_t at = (s * slices + slice) * a.D + d + e;
+    // not centred: the squares about 0, and no mean
+    a.ws[at] = a.center ? first[e] + s1[e] / n : 0.f;
+    a.ws[a.S * slices * a.D + at] = a.center ? not_negative(s2[e] - s1[e] * (s1[e] / n)) : s2[e];
+  }
+}
+
+// one workgroup per (s, g): joins slices and channels
+__global__ __launch_bounds__(kThreads) void norm_cols_join_kernel(NormArgs a, int64_t rows, int64_t slices, float *stat) {
+  __shared__ float s_red[4];
+  const int64_t W = a.D / a.G, g = blockIdx.x % a.G, s = blockIdx.x / a.G;
+  const float *pm = a.ws + s * slices * a.D + g * W, *p2 = pm + a.S * slices * a.D;
+  const int64_t all = slices * W;
+  const float inv = 1.f / (static_cast<float>(a.T) * static_cast<float>(W));
+  auto count = [&](int64_t slice) {
+    return static_cast<float>(slice + 1 < slices ? rows : a.T - slice * rows);
+  };
+  float mean = 0.f;
+  if (a.center) {
+    float m = 0.f;
+    for (int64_t i = threadIdx.x; i < all; i += kThreads) m = fmaf(count(i / W), pm[(i / W) * a.D + i % W], m);
+    mean = lanes_sum<256>(m, s_red) * inv;
+  }
+  float sq = 0.f, left = 0.f;
+  for (int64_t i = threadIdx.x; i < all; i += kThreads) {
+    const float d = pm[(i / W) * a.D + i % W] - mean, nd = count(i / W) * d;
+    left += nd;
+    sq += fmaf(nd, d, p2[(i / W) * a.D + i % W]);
+  }
+  const float delta = a.center ? lanes_sum<256>(left, s_red) * inv : 0.f;
+  const float var = not_negative(fmaf(lanes_sum<256>(sq, s_red), inv, -delta * delta));
+  const float rstd = 1.f / sqrtf(var + a.eps);
+  if (threadIdx.x == 0) {
+    stat[3 * (s * a.G + g)] = mean;
+    stat[3 * (s * a.G + g) + 1] = rstd;
+    stat[3 * (s * a.G + g) + 2] = delta;
+    if (a.mean) a.mean[s * a.G + g] = mean + delta;
+    if (a.rstd) a.rstd[s * a.G + g] = rstd;
+  }
+}
+
+// y; VE divides W or is 1.  A thread holds VE channels of 4 tokens.
+template <typename T, int VE>
+__global__ __launch_bounds__(kThreads) void norm_cols_apply_kernel(NormArgs a, const float *stat) {
+  const int lane = threadIdx.x % 64;
+  const int64_t cb = (a.D + 64 * VE - 1) / (64 * VE), s = blockIdx.x / cb;
+  const int64_t W = a.D / a.G, d = (blockIdx.x % cb * 64 + lane) * VE;
+  if (d >= a.D) return;
+  const int64_t g = d / W;
+  const float mean = stat[3 * (s * a.G + g)], rstd = stat[3 * (s * a.G + g) + 1];
+  const float delta = stat[3 * (s * a.G + g) + 2];  // the mean's part below its fp32 step
+  float wv[VE], bv[VE];
+#pragma unroll
+  for (int e = 0; e < VE; ++e) {
+    wv[e] = a.w ? a.w[d + e] : 1.f;
+    bv[e] = a.b ? a.b[d + e] : 0.f;
+  }
+  const int64_t t0 = (static_cast<int64_t>(blockIdx.y) * 4 + threadIdx.x / 64) * 4;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t t = t0 + i;
+    if (t >= a.T) return;
+    const int64_t at = (s * a.T + t) * a.D + d;
+    const Piece<T, VE> xr = load_piece<T, VE>(static_cast<const T *>(a.x) + at);
+    Piece<T, VE> zr;
+    if (a.z) zr = load_piece<T, VE>(static_cast<const T *>(a.z) + at);
+    float out[VE];
+#pragma unroll
+    for (int e = 0; e < VE; ++e) {
+      const float zs = a.z ? silu(to_f32(zr.v[e])) : 1.f;
+      float u = to_f32(xr.v[e]);
+      if (a.gate_first) u *= zs;
+      float n = fmaf((u - mean - delta) * rstd, wv[e], bv[e]);
+      if (a.act) n = silu(n);
+      if (!a.gate_first) n *= zs;
+      out[e] = n;
+    }
+    store_piece<T, VE>(static_cast<T *>(a.y) + at, out);
+  }
+}
+
+// bwd: per channel the sums of dn and dn xh over a slice
+template <typename T, int VE>
+__global__ __launch_bounds__(kThreads) void norm_cols_bsums_kernel(NormArgs a, int64_t rows, int64_t slices) {
+  const int lane = threadIdx.x % 64;
+  const int64_t cb = (a.D + 64 * VE - 1) / (64 * VE), s = blockIdx.x / cb;
+  const int64_t slice = static_cast<int64_t>(blockIdx.y) * 4 + threadIdx.x / 64;
+  const int64_t d = (blockIdx.x % cb * 64 + lane) * VE;
+  if (slice >= slices || d >= a.D) return;
+  const int64_t g = d / (a.D / a.G);
+  const float mean = a.center ? a.mean[s * a.G + g] : 0.f, rstd = a.rstd[s * a.G + g];
+  const int64_t t0 = slice * rows, t1 = t0 + rows < a.T ? t0 + rows : a.T;
+  float wv[VE], bv[VE], s1[VE], s2[VE];
+#pragma unroll
+  for (int e = 0; e < VE; ++e) {
+    wv[e] = a.w ? a.w[d + e] : 1.f;
+    bv[e] = a.b ? a.b[d + e] : 0.f;
+    s1[e] = s2[e] = 0.f;
+  }
+#pragma unroll 2
+  for (int64_t t = t0; t < t1; ++t) {
+    const int64_t at = (s * a.T + t) * a.D + d;
+    const Piece<T, VE> xr = load_piece<T, VE>(static_cast<const T *>(a.x) + at);
+    const Piece<T, VE> yr = load_piece<T, VE>(static_cast<const T *>(a.dy) + at);
+    Piece<T, VE> zr;
+    if (a.z) zr = load_piece<T, VE>(static_cast<const T *>(a.z) + at);
+#pragma unroll
+    for (int e = 0; e < VE; ++e) {
+      float xh, dn;
+      norm_elem(a, to_f32(xr.v[e]), a.z ? to_f32(zr.v[e]) : 0.f, to_f32(yr.v[e]), wv[e], bv[e], mean, rstd, xh, dn);
+      s1[e] += dn;
+      s2[e] = fmaf(dn, xh, s2[e]);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < VE; ++e) {
+    const int64_t at = (s * slices + slice) * a.D + d + e;
+    a.ws[at] = s2[e];
+    a.ws[a.S * slices * a.D + at] = s1[e];
+  }
+}
+
+// one workgroup per (s, g): mean(g) and mean(g xh)
+__global__ __launch_bounds__(kThreads) void norm_cols_bjoin_kernel(NormArgs a, int64_t slices, float *stat) {
+  __shared__ float s_red[4];
+  const int64_t W = a.D / a.G, g = blockIdx.x % a.G, s = blockIdx.x / a.G;
+  const float *p2 = a.ws + s * slices * a.D + g * W, *p1 = p2 + a.S * slices * a.D;
+  const int64_t all = slices * W;
+  const float inv = 1.f / (static_cast<float>(a.T) * static_cast<float>(W));
+  float x = 0.f, y = 0.f;
+  for (int64_t i = threadIdx.x; i < all; i += kThreads) {
+    const int64_t at = (i / W) * a.D + i % W;
+    const float w = a.w ? a.w[g * W + i % W] : 1.f;
+    x = fmaf(w, p1[at], x);
+    y = fmaf(w, p2[at], y);
+  }
+  x = lanes_sum<256>(x, s_red);
+  y = lanes_sum<256>(y, s_red);
+  if (threadIdx.x == 0) {
+    stat[2 * (s * a.G + g)] = a.center ? x * inv : 0.f;
+    stat[2 * (s * a.G + g) + 1] = y * inv;
+  }
+}
+
+template <typename T, int VE>
+__global__ __launch_bounds__(kThreads) void norm_cols_bapply_kernel(NormArgs a, const float *stat) {
+  const int lane = threadIdx.x % 64;
+  const int64_t cb = (a.D + 64 * VE - 1) / (64 * VE), s = blockIdx.x / cb;
+  const int64_t W = a.D / a.G, d = (blockIdx.x % cb * 64 + lane) * VE;
+  if (d >= a.D) return;
+  const int64_t g = d / W;
+  const float mean = a.center ? a.mean[s * a.G + g] : 0.f, rstd = a.rstd[s * a.G + g];
+  const float mg = stat[2 * (s * a.G + g)], mgx = stat[2 * (s * a.G + g) + 1];
+  float wv[VE], bv[VE];
+#pragma unroll
+  for (int e = 0; e < VE; ++e) {
+    wv[e] = a.w ? a.w[d + e] : 1.f;
+    bv[e] = a.b ? a.b[d + e] : 0.f;
+  }
+  const int64_t t0 = (static_cast<int64_t>(blockIdx.y) * 4 + threadIdx.x / 64) * 4;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t t = t0 + i;
+    if (t >= a.T) return;
+    const int64_t at = (s * a.T + t) * a.D + d;
+    const Piece<T, VE> xr = load_piece<T, VE>(static_cast<const T *>(a.x) + at);
+    const Piece<T, VE> yr = load_piece<T, VE>(static_cast<const T *>(a.dy) + at);
+    Piece<T, VE> zr;
+    if (a.z) zr = load_piece<T, VE>(static_cast<const T *>(a.z) + at);
+    float ox[VE], oz[VE];
+#pragma unroll
+    for (int e = 0; e < VE; ++e) {
+      const float x = to_f32(xr.v[e]), z = a.z ? to_f32(zr.v[e]) : 0.f, dy = to_f32(yr.v[e]);
+      float xh, dn;
+      norm_elem(a, x, z, dy, wv[e], bv[e], mean, rstd, xh, dn);
+      const float du = rstd * (dn * wv[e] - mg - xh * mgx);
+      norm_elem_out(a, x, z, dy, wv[e], bv[e], xh, du, ox[e], oz[e]);
+    }
+    store_piece<T, VE>(static_cast<T *>(a.dx) + at, ox);
+    if (a.z) store_piece<T, VE>(static_cast<T *>(a.dz) + at, oz);
+  }
+}
+
+// ------------------------------------------------------------------ choice
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+bool aligned16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+int vector_width(const NormArgs &a) {
+  const int ve = a.dt == DType::BF16 ? 8 : 4;
+  const bool ok = (a.D / a.G) % ve == 0 && aligned16(a.x) && aligned16(a.z) && aligned16(a.y) && aligned16(a.dy) &&
+                  aligned16(a.dx) && aligned16(a.dz) && aligned16(a.w) && aligned16(a.b);
+  return ok ? ve : 1;
+}
+
+// Lanes and pieces per lane of a group of `pieces` pieces of ve elements: 8
+// lanes (128 bytes in a row) and more, with at most 5 pieces per lane; then the
+// workgroup.  The backward, which holds six values an element, takes at most 2
+// (3 where the workgroup shares the group).
+struct RowPlan {
+  int lpg, nv;  // nv 0: the columns path
+};
+RowPlan plan_rows(int64_t pieces, int ve, bool bwd) {
+  if (pieces <= 1) return {1, 1};
+  if (pieces <= 2) return {2, 1};
+  if (pieces <= 4) return {4, 1};
+  if (pieces <= 8) return {8, 1};
+  if (pieces <= 16) return {8, 2};
+  if (bwd) {
+    if (pieces <= 32) return {16, 2};
+    if (pieces <= 64) return {32, 2};
+    if (pieces <= 128) return {64, 2};
+  } else {
+    if (pieces <= 40) return {8, 5};
+    if (pieces <= 48) return {16, 3};
+    if (pieces <= 80) return {16, 5};
+    if (pieces <= 96) return {32, 3};
+    if (pieces <= 160) return {32, 5};
+    if (pieces <= 320) return {64, 5};
+  }
+  if (pieces <= 512) return {256, 2};
+  if (pieces <= 768) return {256, 3};
+  if (pieces <= 1280 && !(bwd && ve == 8)) return {256, 5};
+  if (pieces <= 2048 && ve == 1) return {256, 8};
+  return {0, 0};
+}
+
+constexpr int64_t kRowBlocks = 256;  // blocks of rows of the backward, at most
+struct RowBwd {
+  int gsub, rsub;
+  int64_t rows, blocks, parts;
+};
+RowBwd plan_rows_bwd(int64_t S, int64_t G, int lpg) {
+  RowBwd r;
+  const int units = kThreads / lpg;
+  r.gsub = 1;
+  while (r.gsub < units && r.gsub < G) r.gsub *= 2;
+  r.rsub = units / r.gsub;
+  const int64_t passes = ceil_div(S, r.rsub);  // rows in steps of rsub
+  r.rows = ceil_div(passes, kRowBlocks) * r.rsub;
+  r.blocks = ceil_div(S, r.rows > 0 ? r.rows : 1);
+  r.parts = r.blocks * r.rsub;
+  return r;
+}
+// Tokens per slice: at least 32 where there are that many, at most 128 slices.
+int64_t slice_rows(int64_t T) {
+  int64_t r = ceil_div(T, 128);
+  if (r < 32) r = 32;
+  return r;
+}
+int64_t cols_ws_floats(int64_t S, int64_t T, int64_t D, int64_t G) {
+  const int64_t slices = ceil_div(T, slice_rows(T));
+  return 2 * S * slices * D + 3 * S * G;
+}
+
+template <typename T, int VE, int LPG, int NV>
+void rows_fwd(const NormArgs &a, hipStream_t s) {
+  const int64_t blocks = ceil_div(a.S * a.G, kThreads / LPG);
+  norm_rows_fwd_kernel<T, VE, LPG, NV><<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(a);
+}
+template <typename T, int VE, int LPG, int NV>
+void rows_bwd(const NormArgs &a, hipStream_t s) {
+  const RowBwd r = plan_rows_bwd(a.S, a.G, LPG);
+  const dim3 grid(static_cast<unsigned>(ceil_div(a.G, r.gsub)), static_cast<unsigned>(r.blocks));
+  norm_rows_bwd_kernel<T, VE, LPG, NV><<<grid, kThreads, 0, s>>>(a, r.gsub, r.rows, r.parts);
+  norm_params_kernel<<<static_cast<unsigned>(ceil_div(a.D, 64)), kThreads, 0, s>>>(a, r.parts, a.ws,
+                                                                                   a.ws + r.parts * a.D);
+}
+template <typename T, int VE, bool BWD>
+bool rows(const NormArgs &a, hipStream_t s) {
+  const RowPlan p = plan_rows(a.D / a.G / VE, VE, BWD);
+#define SSM_NORM_CASE(LPG, NV)                         \
+  if (p.lpg == LPG && p.nv == NV) {                    \
+    if constexpr (BWD) rows_bwd<T, VE, LPG, NV>(a, s); \
+    else rows_fwd<T, VE, LPG, NV>(a, s);               \
+    return true;                                       \
+  }
+  SSM_NORM_CASE(1, 1) SSM_NORM_CASE(2, 1) SSM_NORM_CASE(4, 1) SSM_NORM_CASE(8, 1) SSM_NORM_CASE(8, 2)
+  if constexpr (BWD) {
+    SSM_NORM_CASE(16, 2) SSM_NORM_CASE(32, 2) SSM_NORM_CASE(64, 2)
+  } else {
+    SSM_NORM_CASE(8, 5) SSM_NORM_CASE(16, 3) SSM_NORM_CASE(16, 5) SSM_NORM_CASE(32, 3) SSM_NORM_CASE(32, 5)
+    SSM_NORM_CASE(64, 5)
+  }
+  SSM_NORM_CASE(256, 2) SSM_NORM_CASE(256, 3)
+  if constexpr (!(BWD && VE == 8)) { SSM_NORM_CASE(256, 5) }
+  if constexpr (VE == 1) { SSM_NORM_CASE(256, 8) }
+#undef SSM_NORM_CASE
+  return false;
+}
+
+template <typename T, int VE, bool BWD>
+void cols(const NormArgs &a, hipStream_t s) {
+  const int64_t rows = slice_rows(a.T), slices = ceil_div(a.T, rows);
+  const unsigned cb = static_cast<unsigned>(ceil_div(a.D, 64 * VE) * a.S), gj = static_cast<unsigned>(a.G * a.S);
+  const dim3 gs(cb, static_cast<unsigned>(ceil_div(slices, 4))), ga(cb, static_cast<unsigned>(ceil_div(a.T, 16)));
+  float *stat = a.ws + 2 * a.S * slices * a.D;
+  if constexpr (BWD) {
+    norm_cols_bsums_kernel<T, VE><<<gs, kThreads, 0, s>>>(a, rows, slices);
+    norm_cols_bjoin_kernel<<<gj, kThreads, 0, s>>>(a, slices, stat);
+    norm_cols_bapply_kernel<T, VE><<<ga, kThreads, 0, s>>>(a, stat);
+    norm_params_kernel<<<static_cast<unsigned>(ceil_div(a.D, 64)), kThreads, 0, s>>>(a, a.S * slices, a.ws,
+                                                                                     a.ws + a.S * slices * a.D);
+  } else {
+    norm_cols_sums_kernel<T, VE><<<gs, kThreads, 0, s>>>(a, rows, slices);
+    norm_cols_join_kernel<<<gj, kThreads, 0, s>>>(a, rows, slices, stat);
+    norm_cols_apply_kernel<T, VE><<<ga, kThreads, 0, s>>>(a, stat);
+  }
+}
+
+template <typename T, int VE, bool BWD>
+void launch_ve(const NormArgs &a, hipStream_t s) {
+  if (a.T == 1 && rows<T, VE, BWD>(a, s)) return;
+  cols<T, VE, BWD>(a, s);
+}
+template <bool BWD>
+hipError_t launch(const NormArgs &a, hipStream_t s) {
+  const bool vec = vector_width(a) > 1;
+  if (a.dt == DType::BF16) {
+    if (vec) launch_ve<bf16_t, 8, BWD>(a, s);
+    else launch_ve<bf16_t, 1, BWD>(a, s);
+  } else {
+    if (vec) launch_ve<float, 4, BWD>(a, s);
+    else launch_ve<float, 1, BWD>(a, s);
+  }
+  return hipGetLastError();
+}
+
+// The workspace covers either type and any alignment of these sizes.
+template <typename F>
+void each_width(int64_t W, F f) {
+  for (int ve : {1, 4, 8})
+    if (W % ve == 0) f(ve);
+}
+
+}  // namespace
+
+int64_t group_norm_fwd_ws_floats(int64_t S, int64_t T, int64_t D, int64_t G) {
+  bool cols = T != 1;
+  each_width(D / G, [&](int ve) { cols = cols || plan_rows(D / G / ve, ve, false).nv == 0; });
+  return cols ? cols_ws_floats(S, T, D, G) : 0;
+}
+int64_t group_norm_bwd_ws_floats(int64_t S, int64_t T, int64_t D, int64_t G) {
+  int64_t n = T != 1 ? cols_ws_floats(S, T, D, G) : 0;
+  if (T != 1) return n;
+  each_width(D / G, [&](int ve) {
+    const RowPlan p = plan_rows(D / G / ve, ve, true);
+    const int64_t m = p.nv == 0 ? cols_ws_floats(S, T, D, G) : 2 * plan_rows_bwd(S, G, p.lpg).parts * D;
+    if (m > n) n = m;
+  });
+  return n;
+}
+
+hipError_t launch_group_norm_fwd(const NormArgs &a, hipStream_t s) { return launch<false>(a, s); }
+hipError_t launch_group_norm_bwd(const NormArgs &a, hipStream_t s) {
+  if (a.S == 0 || a.T == 0) {
+    norm_params_kernel<<<static_cast<unsigned>(ceil_div(a.D, 64)), kThreads, 0, s>>>(a, 0, nullptr, nullptr);
+    return hipGetLastError();
+  }
+  return launch<true>(a, s);
+}
+
+}  // namespace ssm

@@ -356,3 +356,147 @@ def test_scan_noalloc_limit_and_validation(lib):
     assert na(y=Q[0]) == INVALID                     # y on x
     assert na(N=65) == UNSUPPORTED
     assert na(tun=ssm.Tuning(5, 0)) == INVALID
+
+
+# ---- gated delta rule and group norm: refusals, all on the host
+
+R = [ctypes.c_void_p(0x10000000 * (i + 1)) for i in range(32)]
+
+
+def gdr(lib, B=2, L=8, H=4, Pd=64, G=2, N=128, dt=BF16, norm=1, ws=None, ws_len=0, opts=None, **over):
+    names = ["q", "k", "v", "step", "A", "beta", "h0", "y", "h_final"]
+    p = {n: R[i] for i, n in enumerate(names)}
+    p.update(over)
+    return lib.ssm_gdr_fwd(B, L, H, Pd, G, N, dt, *(p[n] for n in names[:7]), 1.0, norm, p["y"], p["h_final"], ws,
+                           ws_len, None if opts is None else ctypes.byref(opts), None)
+
+
+def test_gdr_fwd_validation(lib):
+    assert gdr(lib, B=-1) == INVALID
+    assert gdr(lib, L=-1) == INVALID
+    assert gdr(lib, dt=7) == INVALID
+    assert gdr(lib, norm=2) == INVALID
+    assert gdr(lib, N=0) == UNSUPPORTED
+    assert gdr(lib, N=257) == UNSUPPORTED
+    assert gdr(lib, G=3) == UNSUPPORTED
+    assert gdr(lib, G=0) == UNSUPPORTED
+    assert gdr(lib, B=70000) == UNSUPPORTED
+    assert gdr(lib, L=1 << 60) == UNSUPPORTED                  # sizes whose product passes 64 bits
+    for name in ("q", "k", "v", "step", "A", "beta", "y"):
+        assert gdr(lib, **{name: None}) == INVALID
+    assert gdr(lib, y=R[2]) == INVALID                         # on v
+    assert gdr(lib, h_final=R[6]) == INVALID                   # on h0
+    assert gdr(lib, h_final=R[7]) == INVALID                   # on y
+    bad = ssm.DeltaOpts(None, 2)
+    assert gdr(lib, opts=bad) == INVALID
+    assert gdr(lib, B=0) == OK and gdr(lib, Pd=0) == OK
+
+
+def test_gdr_decode_validation(lib):
+    names = ["pool", "slots", "q", "k", "v", "step", "A", "beta", "y"]
+
+    def dec(S=2, T=1, H=4, Pd=64, G=2, N=128, dt=BF16, rows=5, norm=0, **over):
+        p = {n: R[i] for i, n in enumerate(names)}
+        p.update(over)
+        return lib.ssm_gdr_decode_steps(S, T, H, Pd, G, N, dt, p["pool"], rows, p["slots"],
+                                        *(p[n] for n in names[2:8]), 1.0, norm, p["y"], None, None)
+    assert dec(S=-1) == INVALID
+    assert dec(rows=-1) == INVALID
+    assert dec(slots=None, rows=1) == INVALID                  # fewer rows than sequences
+    assert dec(N=300) == UNSUPPORTED
+    for name in ("pool", "q", "k", "v", "step", "A", "beta", "y"):
+        assert dec(**{name: None}) == INVALID
+    assert dec(y=R[0]) == INVALID                              # on the pool
+    assert dec(pool=R[2]) == INVALID                           # the pool on q
+    assert dec(rows=0) == OK                                   # every slot outside: nothing to do
+    assert dec(T=0) == OK
+
+
+def test_gdr_bwd_validation(lib):
+    names = ["q", "k", "v", "step", "A", "beta", "h0", "dy", "dh", "dq", "dk", "dv", "ddt", "dbeta", "dA", "dh0", "db"]
+    ws = ctypes.c_void_p(0x10000000 * 40)
+
+    def b(B=1, L=8, H=4, Pd=64, G=2, N=128, dt=BF16, norm=0, ws=ws, ws_len=1 << 30, **over):
+        p = {n: R[i] for i, n in enumerate(names)}
+        p.update(over)
+        return lib.ssm_gdr_bwd(B, L, H, Pd, G, N, dt, *(p[n] for n in names[:9]), 1.0, norm,
+                               *(p[n] for n in names[9:]), ws, ws_len, None, None)
+    assert b(B=-1) == INVALID
+    assert b(Pd=0) == UNSUPPORTED
+    assert b(N=257) == UNSUPPORTED
+    for name in ("q", "v", "dy", "dq", "dk", "dv", "ddt", "dbeta", "dA"):
+        assert b(**{name: None}) == INVALID
+    assert b(ws=None) == WORKSPACE
+    assert b(ws_len=64) == WORKSPACE
+    assert b(ws=ctypes.c_void_p(ws.value + 4)) == WORKSPACE
+    assert b(dq=R[0]) == INVALID                               # output on an input
+    assert b(dk=R[9]) == INVALID                               # two outputs on one buffer
+    assert b(dv=ws) == INVALID                                 # output on the workspace
+    assert lib.ssm_gdr_bwd_workspace_size(1, 8, 4, 64, 3, 128, BF16) == 0
+    assert lib.ssm_gdr_bwd_workspace_size(1, 8, 4, 64, 2, 128, BF16) > 0
+
+
+def test_group_norm_validation(lib):
+    def f(S=4, T=1, D=64, G=4, dt=F32, eps=1e-5, center=1, act=0, first=0, ws=None, ws_len=0, **over):
+        names = ["x", "z", "w", "b", "y", "mean", "rstd"]
+        p = {n: R[i] for i, n in enumerate(names)}
+        p.update(over)
+        return lib.ssm_group_norm_fwd(S, T, D, G, dt, p["x"], p["z"], p["w"], p["b"], eps, center, act, first, p["y"],
+                                      p["mean"], p["rstd"], ws, ws_len, None)
+
+    def g(S=4, T=1, D=64, G=4, dt=F32, center=1, ws=R[20], ws_len=1 << 20, **over):
+        names = ["x", "z", "w", "b", "dy", "mean", "rstd", "dx", "dz", "dw", "db"]
+        p = {n: R[i] for i, n in enumerate(names)}
+        p.update(over)
+        return lib.ssm_group_norm_bwd(S, T, D, G, dt, *(p[n] for n in names[:7]), 1e-5, center, 0, 0,
+                                      *(p[n] for n in names[7:]), ws, ws_len, None)
+    assert f(S=-1) == INVALID
+    assert f(eps=-1.0) == INVALID
+    assert f(eps=float("nan")) == INVALID
+    assert f(center=2) == INVALID
+    assert f(act=3) == INVALID
+    assert f(G=3) == UNSUPPORTED
+    assert f(G=0) == UNSUPPORTED
+    assert f(T=1 << 21) == UNSUPPORTED
+    assert f(x=None) == INVALID
+    assert f(y=None) == INVALID
+    assert f(y=R[0]) == INVALID                                # on x
+    assert f(center=0) == INVALID                              # a mean asked of a norm without one
+    assert f(T=8) == WORKSPACE                                 # over a sequence, without workspace
+    assert f(S=0) == OK and f(D=0) == OK
+    assert g(dy=None) == INVALID
+    assert g(rstd=None) == INVALID
+    assert g(mean=None) == INVALID
+    assert g(dz=None) == INVALID                               # gate given, its gradient not
+    assert g(z=None) == INVALID                                # and the other way round
+    assert g(dx=R[4]) == INVALID                               # on dy
+    assert g(ws=None) == WORKSPACE
+    assert g(dw=R[20]) == INVALID                              # on the workspace
+
+
+def test_mixer_binding_refusals():
+    import torch
+    q = torch.zeros(1, 4, 2, 8)
+    v = torch.zeros(1, 4, 4, 8)
+    dt, A = torch.zeros(1, 4, 4), torch.zeros(4)
+    with pytest.raises(ValueError, match="GPU"):
+        ssm.gdr_fwd(q, q, v, dt, A, dt)
+    with pytest.raises(ValueError, match="contiguous"):
+        ssm.gdr_fwd(q, torch.zeros(1, 2, 4, 8).transpose(1, 2), v, dt, A, dt)
+    with pytest.raises(ValueError, match="shape"):
+        ssm.gdr_fwd(q, q, v, dt[:, :3], A, dt)
+    with pytest.raises(TypeError):
+        ssm.gdr_fwd(q, q.bfloat16(), v, dt, A, dt)
+    with pytest.raises(TypeError):
+        ssm.gdr_fwd(q.half(), q.half(), v.half(), dt.half(), A, dt.half())
+    with pytest.raises(ValueError, match="dy"):
+        ssm.gdr_bwd(q, q, v, dt, A, dt)
+    x = torch.zeros(2, 3, 8)
+    with pytest.raises(ValueError, match="gate"):
+        ssm.group_norm_fwd(x, 2, gate="sideways", z=x)
+    with pytest.raises(ValueError, match="together"):
+        ssm.group_norm_fwd(x, 2, z=x)
+    with pytest.raises(ValueError, match="activation"):
+        ssm.group_norm_fwd(x, 2, activation="gelu")
+    with pytest.raises(ValueError, match="required"):
+        ssm.group_norm_bwd(x, 2, x, None, None)
