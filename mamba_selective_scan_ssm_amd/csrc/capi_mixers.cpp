@@ -89,7 +89,8 @@ ssm_status ssm_gdr_fwd(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G, in
   ssm::GdrArgs a = gdr_args(B, L, H, P, G, N, dt, q, k, v, dt_in, A, beta, h0, scale, qk_norm, dopts);
   a.y = y;
   a.h_final = h_final;
-  return hip_status(ssm::launch_gdr_seq(a, static_cast<hipStream_t>(stream)));
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return hip_status(ssm::gdr_chunk_applies(a) ? ssm::launch_gdr_chunk(a, s) : ssm::launch_gdr_seq(a, s));
 }
 
 ssm_status ssm_gdr_decode_steps(int64_t S, int64_t T, int64_t H, int64_t P, int64_t G, int64_t N, ssm_dtype dt,

@@ -42,6 +42,13 @@ hipError_t launch_gdr_seq(const GdrArgs &a, hipStream_t s);
 // registers and back once, nothing is staged.
 hipError_t launch_gdr_step(const GdrArgs &a, hipStream_t s);
 
+// By chunks of 64 tokens on the matrix cores (gdr_chunk.hip): bf16, N a
+// multiple of 8 up to 128, L >= kGdrChunkMinL, q, k and the states 16-byte
+// aligned; no workspace.
+constexpr int64_t kGdrChunkMinL = 32;
+bool gdr_chunk_applies(const GdrArgs &a);
+hipError_t launch_gdr_chunk(const GdrArgs &a, hipStream_t s);
+
 struct GdrBwdArgs {
   GdrArgs f;                  // the forward's inputs (y, h_final unused)
   const void *dy;             // (B, L, H, P)

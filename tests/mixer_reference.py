@@ -17,11 +17,9 @@ from tests.helpers import FP32_RTOL
 QK_EPS = 1e-6
 
 
-def close(got, want, what="", terms=None, steps=0):
+def close(got, want, what="", slack=None, steps=0):
     """Entry by entry: 1e-5 max(|r|, rms), and half a step of a bf16 output.
-    terms: the size of the terms whose difference the entry is, where they may
-    cancel: each is formed in fp32 by fewer than 16 roundings of 2^-24, so the
-    entry may be off by 2^-20 of them however small it is itself.
+    slack: more, entry by entry, with its reason where it is made.
     steps: tokens whose decay is the same number: it is rounded the same way
     each time, by up to 2^-24 (a step of the exponential unit below 1), so what
     has passed through them is off by steps 2^-24 of itself."""
@@ -34,8 +32,8 @@ def close(got, want, what="", terms=None, steps=0):
     rms = r.pow(2).mean().sqrt()
     allowed = FP32_RTOL * torch.maximum(r.abs(), rms) + half * (1 + FP32_RTOL) * torch.maximum(r.abs(), FP32_RTOL * rms)
     allowed = allowed + steps * 2.0 ** -24 * torch.maximum(r.abs(), rms)
-    if terms is not None:
-        allowed = allowed + 2.0 ** -20 * terms
+    if slack is not None:
+        allowed = allowed + slack
     off = (g - r).abs()
     bad = off > allowed.clamp_min(1e-30)
     if bad.any():
@@ -109,16 +107,56 @@ def gdr_grads_of(w, qk_norm, scale=None):
     return {n: torch.zeros_like(x[n]) if g is None else g for n, g in zip(names, grads)}
 
 
-def gdr_grad_terms(w, qk_norm, scale=None):
-    """The sizes of the two terms of the norm's gradient dx = r (g - u (g . u)),
-    u = r x, for q and k: they cancel where g lies along x (always, for one
-    value).  Empty without the norm."""
+def gdr_output_slack(w, qk_norm, scale=None, chunk=64):
+    """For y where chunks of 64 tokens go through the matrix cores: y = b (Q S0)
+    + M E over the chunk's tokens, with S0, M and E in two bf16 parts, each off
+    by at most 2^-16 of itself and the smallest of the four products of M and E
+    left out (2^-16 again): 3 2^-16 of the sum of the terms' sizes."""
+    x = {n: None if w[n] is None else w[n].double() for n in NAMES}
+    B, L, G, N = w["q"].shape
+    H = w["v"].shape[2]
+    q, k = x["q"], x["k"]
+    if qk_norm:
+        q, k = (t / (t.pow(2).sum(-1, keepdim=True) + QK_EPS).sqrt() for t in (q, k))
+    head = torch.arange(H) // (H // G)
+    q, k = q[:, :, head], k[:, :, head]
+    d = x["dt"] if x["bias"] is None else torch.nn.functional.softplus(x["dt"] + x["bias"])
+    lg = (d * x["A"]).clamp_min(-1e4)
+    S = torch.zeros(B, H, w["v"].shape[3], N, dtype=torch.float64) if w["h0"] is None else x["h0"]
+    out = torch.empty_like(x["v"])
+    for t0 in range(0, L, chunk):
+        S0, c, u, ks = S, torch.zeros(B, H, dtype=torch.float64), [], []
+        cs = []
+        for t in range(t0, min(L, t0 + chunk)):
+            c = c + lg[:, t]
+            cs.append(c)
+            S = S * lg[:, t].exp()[..., None, None]
+            e = x["beta"][:, t, :, None] * (x["v"][:, t] - (S * k[:, t, :, None]).sum(-1))
+            S = S + e[..., None] * k[:, t, :, None]
+            u.append(e.abs())
+            ks.append(k[:, t])
+            D = torch.exp(c[..., None] - torch.stack(cs, -1))                        # (B, H, j)
+            m = (D * (torch.stack(ks, 2) * q[:, t, :, None]).sum(-1)).abs()         # (B, H, j)
+            out[:, t] = (c.exp()[..., None] * (S0.abs() * q[:, t, :, None].abs()).sum(-1) +
+                         (torch.stack(u, -1) * m[:, :, None]).sum(-1))
+    return 3 * 2.0 ** -16 * (N ** -0.5 if scale is None else scale) * out
+
+
+# Terms whose difference an entry is may cancel: each is formed in fp32 by fewer
+# than 16 roundings of 2^-24, so the entry is off by up to 2^-20 of their size
+# however small it is itself.
+CANCEL = 2.0 ** -20
+
+
+def gdr_grad_slack(w, qk_norm, scale=None):
+    """For q and k under the norm, whose gradient dx = r (g - u (g . u)), u = r x,
+    cancels where g lies along x (always, for one value).  Empty without it."""
     if not qk_norm:
         return {}
     r = {n: (w[n].double().pow(2).sum(-1, keepdim=True) + QK_EPS).rsqrt() for n in "qk"}
     u = {n: w[n].double() * r[n] for n in "qk"}
     g = gdr_grads_of({**w, **u}, False, scale)
-    return {n: r[n] * (g[n].abs() + u[n].abs() * (g[n] * u[n]).abs().sum(-1, keepdim=True)) for n in "qk"}
+    return {n: CANCEL * r[n] * (g[n].abs() + u[n].abs() * (g[n] * u[n]).abs().sum(-1, keepdim=True)) for n in "qk"}
 
 
 def norm(x, groups, w=None, b=None, z=None, eps=1e-5, center=True, act=False, gate=None, per_token=True):
@@ -136,10 +174,10 @@ def norm(x, groups, w=None, b=None, z=None, eps=1e-5, center=True, act=False, ga
     return n * silu(z) if gate == "after" else n
 
 
-def norm_grad_terms(w, groups, eps, center, act, gate, per_token):
-    """The sizes of the terms of dx = rstd (g - mean(g) - xh mean(g xh)) and, for
-    a gate before the norm, of the dz formed from it (g = w dn): what rounding
-    is relative to where the three nearly cancel, as in a group of one value."""
+def norm_grad_slack(w, groups, eps, center, act, gate, per_token):
+    """For dx = rstd (g - mean(g) - xh mean(g xh)), g = w dn, and, with a gate
+    before the norm, the dz formed from it: the three terms nearly cancel in
+    a group of one value and the like."""
     x = w["x"].double()
     z = None if w["z"] is None else w["z"].double()
     silu = torch.nn.functional.silu
@@ -156,7 +194,7 @@ def norm_grad_terms(w, groups, eps, center, act, gate, per_token):
     dn = w["dy"].double() * (silu(z) if gate == "after" else 1) * ((s + n * s * (1 - s)) if act else 1)
     g = (dn if w["w"] is None else dn * w["w"].double()).reshape(shape).abs()
     t = rstd * (g + (g.mean((1, 3), keepdim=True) if center else 0) + xh.abs() * (g * xh.abs()).mean((1, 3), keepdim=True))
-    t = t.reshape(B, L, D)
+    t = CANCEL * t.reshape(B, L, D)
     if gate != "before":
         return t, None
     sz = torch.sigmoid(z)

@@ -36,19 +36,26 @@ def bwd(w, qk_norm, **kw):
     return g
 
 
+def y_slack(w, qk_norm, scale=None):
+    """For shapes that may take the matrix cores."""
+    if w["q"].dtype != BF16 or w["q"].shape[3] % 8 or w["q"].shape[3] > 128:
+        return None
+    return ref.gdr_output_slack(w, qk_norm, scale)
+
+
 def check_fwd(w, qk_norm, what, scale=None, steps=0):
     y, h = fwd(w, qk_norm, scale=scale)
     ry, rh = ref.gdr_of(w, qk_norm, scale)
-    ref.close(y, ry, what + " y", steps=steps)
+    ref.close(y, ry, what + " y", y_slack(w, qk_norm, scale), steps)
     ref.close(h, rh, what + " h", steps=steps)
 
 
 def check_bwd(w, qk_norm, what, scale=None, steps=0):
     g = bwd(w, qk_norm, scale=scale)
     r = ref.gdr_grads_of(w, qk_norm, scale)
-    terms = ref.gdr_grad_terms(w, qk_norm, scale)
+    slack = ref.gdr_grad_slack(w, qk_norm, scale)
     for n in r:
-        ref.close(g["d" + n], r[n], f"{what} d{n}", terms.get(n), steps)
+        ref.close(g["d" + n], r[n], f"{what} d{n}", slack.get(n), steps)
 
 
 # every split of a row over the lanes, odd sizes, one head to a key and several
@@ -67,6 +74,16 @@ SHAPES = [
     (1, 31, 2, 24, 1, 192),
     (1, 30, 2, 20, 2, 256),
     (1, 15, 1, 200, 1, 255),
+    # whole chunks of 64 tokens, one more and one less, several, ragged tiles
+    # of columns, N between the sizes of a tile, more groups than 8
+    (1, 64, 1, 64, 1, 64),
+    (2, 63, 6, 33, 2, 120),
+    (1, 32, 2, 80, 2, 8),
+    (1, 128, 3, 16, 3, 40),
+    (2, 200, 4, 64, 2, 128),
+    (1, 321, 4, 128, 1, 128),
+    (1, 97, 2, 72, 2, 96),
+    (9, 70, 2, 64, 2, 64),
 ]
 
 
@@ -158,7 +175,8 @@ def test_batch_and_split_invariance(dtype):
     ya, ha = fwd(a, True)
     b["h0"] = ha.cpu()
     yb, hb = fwd(b, True)
-    ref.close(torch.cat((ya, yb), 1), ry, "split y")
+    slack = y_slack(a, True), y_slack(b, True)
+    ref.close(torch.cat((ya, yb), 1), ry, "split y", None if slack[0] is None else torch.cat(slack, 1))
     ref.close(hb, rh, "split h")
 
 
@@ -189,7 +207,7 @@ def test_unaligned_tensors(dtype, off):
                        dt_softplus=True, y=shift(w["v"]), h_final=shift(w["h0"]))
     torch.cuda.synchronize()
     ry, rh = ref.gdr_of(w, True)
-    ref.close(y, ry, "y")
+    ref.close(y, ry, "y", y_slack(w, True))
     ref.close(h, rh, "h")
     g = ssm.gdr_bwd(s["q"], s["k"], s["v"], s["dt"], s["A"], s["beta"], s["h0"], s["dy"], s["dh"], qk_norm=True,
                     dt_bias=s["bias"], dt_softplus=True, want_dbias=True)
@@ -294,7 +312,7 @@ def test_prefill_then_decode():
         ys.append(ssm.gdr_decode_steps(pool, *tok, A, beta[:, t:t + 1].contiguous(), slots=slots, **kw))
     torch.cuda.synchronize()
     ry, rh = ref.gdr_of(w, True)
-    ref.close(torch.cat(ys, 1), ry, "y")
+    ref.close(torch.cat(ys, 1), ry, "y", y_slack(w, True))
     ref.close(pool[slots.long()], rh, "state")
 
 
@@ -396,7 +414,7 @@ def test_other_stream():
     torch.cuda.synchronize()
     for w, ((y, h), g) in zip(ws, got):
         ry, rh = ref.gdr_of(w, True)
-        ref.close(y, ry, "y")
+        ref.close(y, ry, "y", y_slack(w, True))
         ref.close(h, rh, "h")
         r = ref.gdr_grads_of(w, True)
         for n in r:

@@ -44,9 +44,9 @@ def check(w, groups, center, act, gate, per_token, eps=1e-5):
     ref.close(y, r, "y")
     grads = torch.autograd.grad(r, list(leaves.values()), w["dy"].double())
     names = {"x": "dx", "w": "dweight", "b": "dbias", "z": "dz"}
-    terms = dict(zip("xz", ref.norm_grad_terms(w, groups, eps, center, act, gate, per_token)))
+    slack = dict(zip("xz", ref.norm_grad_slack(w, groups, eps, center, act, gate, per_token)))
     for n, want in zip(leaves, grads):
-        ref.close(g[names[n]], want, names[n], terms.get(n))
+        ref.close(g[names[n]], want, names[n], slack.get(n))
     for n in ("w", "b", "z"):
         assert (g[names[n]] is None) == (w[n] is None)
     assert (mean is None) == (not center)
