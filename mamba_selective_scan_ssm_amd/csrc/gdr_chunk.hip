@@ -20,11 +20,9 @@
 // and Q into LDS, K K^T and Q K^T, the decays (c in 64 bits: its differences
 // count, not its size), X by substitution in 16 x 16 blocks (the chunk's keys
 // may be all alike, where a series for the inverse loses everything) and block
-// rows joined by fp32 MFMA.  Nothing but the inputs, y and the two states
-// touches memory.  Four barriers per chunk pair the chain's products with the
-// preparation's steps:
-//   chain:   split S, K S0 | R, X R        | w E, K^T (w E) | Q S0, M E, y
-//   prepare: X, M, K, Q in | K K^T, Q K^T  | block inverses | block rows, loads
+// rows joined by fp32 MFMA.  What they make is double-buffered, so one barrier
+// a chunk joins the two; the preparing waves meet among themselves at a count
+// in LDS.  Nothing but the inputs, y and the two states touches memory.
 //
 // Precision: k, q and v are exact in bf16.  What is computed -- S, R, E, X --
 // enters a product that makes S in three bf16 parts (all 24 bits; products of
@@ -42,33 +40,81 @@ namespace {
 constexpr int kC = 64;          // tokens per chunk
 constexpr int kCols = 64;       // columns per workgroup
 constexpr int kThreads = 512;
-constexpr int kTokPitch = 72;   // uint16 per row of 64 contraction tokens (144 bytes)
-constexpr int kAtPitch = 68;    // floats
-constexpr int kXtPitch = 20;    // floats
+constexpr int kAtPitch = 20;    // floats per row of a 16 x 16 block
 
-// The conflict-free place of tokens 8 ch .. + 7 in row n of K^T: rows 16 bytes
-// apart modulo the banks for reads, chunks spread over the banks for the
-// transposing writes.
-__device__ __forceinline__ int kt_at(int n, int ch) { return n * kTokPitch + 8 * (ch ^ ((n >> 4) & 7)); }
+// X and M, [i][j] by kpos(j): rows 0..31 meet 32 tokens, rows 32..63 all 64;
+// 16 bytes of padding put 16 rows on different banks.
+constexpr int kTriSize = 32 * 40 + 32 * 72;
+__device__ __forceinline__ constexpr int tri_at(int i) { return i < 32 ? i * 40 : 32 * 40 + (i - 32) * 72; }
+// Block (j, k) of the transposed A', k >= j.
+__device__ __forceinline__ constexpr int at_block(int j, int k) {
+  return (j * 4 - j * (j - 1) / 2 + k - j) * 16 * kAtPitch;
+}
 
 template <int NT>
 struct ChunkLds {
-  static constexpr int kNPitch = 16 * NT + 8;  // uint16 per row of N
-  __attribute__((aligned(16))) uint16_t k[2][kC * kNPitch];
-  __attribute__((aligned(16))) uint16_t q[2][kC * kNPitch];
-  __attribute__((aligned(16))) uint16_t kt[16 * NT * kTokPitch];
-  __attribute__((aligned(16))) uint16_t x[3][kC * kTokPitch];
-  __attribute__((aligned(16))) uint16_t m[2][kC * kTokPitch];
-  __attribute__((aligned(16))) float at[kC * kAtPitch];         // A'[i][j] at [j][i]
-  __attribute__((aligned(16))) float xt[4][16 * kXtPitch];      // diagonal blocks of X, transposed
+  __attribute__((aligned(16))) uint16_t k[2][kC * 16 * NT];
+  __attribute__((aligned(16))) uint16_t q[2][kC * 16 * NT];
+  __attribute__((aligned(16))) uint16_t x[2][3][kTriSize];
+  __attribute__((aligned(16))) uint16_t m[2][2][kTriSize];
+  // A'[i][j] at [j][i]; a diagonal block gives way to its inverse, transposed
+  __attribute__((aligned(16))) float at[10 * 16 * kAtPitch];
   __attribute__((aligned(16))) float va[2][kC], vb[2][kC], vw[2][kC];
   __attribute__((aligned(16))) double c[kC];                    // in units of log 2
   __attribute__((aligned(16))) float rk[kC], rq[kC], beta[kC];
   float whole[2];
+  uint32_t met;
+  // byte offsets between the parts
+  static constexpr uint32_t kTile = 2 * kC * 16 * NT, kTri = 2 * kTriSize;
 };
 
-__device__ __forceinline__ u32x4 lds128(const uint16_t *p) { return *reinterpret_cast<const u32x4 *>(p); }
-__device__ __forceinline__ f32x4 lds_f4(const float *p) { return *reinterpret_cast<const f32x4 *>(p); }
+// 16-byte piece `ch` (kpos / 8) of token `tok` in a K or Q tile: the pieces of
+// a row are exchanged by the token, so that a piece of 16 rows (an operand), a
+// row of pieces (staging) and 4 x 4 (row, piece) (the transposing read) spread
+// over the banks.
+template <int NT>
+__device__ __forceinline__ int tile_at(int tok, int ch) {
+  const int f = NT == 8 ? (tok % 4) * 4 + tok / 4 % 4 : tok / 2 % 8;
+  return tok * 16 * NT + 8 * (ch ^ f);
+}
+
+// LDS by address.  A lane keeps the few addresses it reads around (`hold` hides
+// how they were formed, or the compiler keeps one per read) and the rest is in
+// the instructions' offsets, 16 bits each.
+typedef __attribute__((address_space(3))) char lds_char;
+__device__ __forceinline__ uint32_t lds_address(const void *p) {
+  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((const lds_char *)(p)));
+}
+__device__ __forceinline__ uint32_t hold(uint32_t v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+template <typename T>
+__device__ __forceinline__ T lds_get(uint32_t at) {
+  return *reinterpret_cast<const __attribute__((address_space(3))) T *>(at);
+}
+template <typename T>
+__device__ __forceinline__ void lds_put(uint32_t at, T v) {
+  *reinterpret_cast<__attribute__((address_space(3))) T *>(at) = v;
+}
+// Four values of 4 rows by 16 columns, transposed on their way out of LDS: lane
+// 16 g + i names the 8 bytes (row i / 4, columns 4 (i % 4) .. + 3) of its group
+// and lane 16 g + r receives column r of the 4 rows.
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ u32x2 lds_transposed(uint32_t at) {
+  return __builtin_bit_cast(
+      u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<__attribute__((address_space(3))) s16x4 *>(at)));
+}
+
+// Rows t0 .. of a (.., rows, row elements) tensor of 16-bit values from one
+// element on: reads behind the last row give 0 and writes there are dropped.
+// `left` rows from t0 (0 and less: none), of which `tail` elements count in the
+// last.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(const void *base, int left, uint32_t row, uint32_t tail) {
+  const uint32_t bytes = left > 0 ? 2 * (static_cast<uint32_t>(left - 1) * row + tail) : 0;
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, static_cast<int>(bytes), 0x00020000);
+}
+constexpr uint32_t kNowhere = 0xfffffff0u;  // an offset outside every buffer
 
 // exp2 of a difference of two cumulative decays
 __device__ __forceinline__ float decay_of(double d) { return fast_exp2(static_cast<float>(d)); }
@@ -103,76 +149,107 @@ __device__ __forceinline__ double wave_scan(double v) {
 template <int NT>
 struct Chain {
   static constexpr int KB = NT / 2;   // blocks of 32 states
-  static constexpr int kNP = ChunkLds<NT>::kNPitch;
   const GdrArgs &a;
   ChunkLds<NT> &s;
   const MinusOne minus;
-  const int r, g;      // lane = 16 g + r
-  const bool col;      // this lane's column is inside P
-  const uint16_t *v;   // of this column, token 0
+  const int r, g;        // lane = 16 g + r
+  const uint16_t *v;     // of this head, token 0
   bf16_t *y;
-  int64_t row;         // elements from token to token
+  const uint32_t row;    // elements from token to token
+  const uint32_t width;  // columns of a row from this head on that are its own
+  const uint32_t rows16; // bytes of 16 rows
+  uint32_t at[4];        // bytes to this lane's column in rows 4 g .. 4 g + 3
+  // LDS addresses: rows r of K (Q behind it) by block of 32 states, the same
+  // for the transposing reads, rows r of X and M, element 4 g of the vectors
+  uint32_t lk[KB], lt[KB], lx[2], lm[2], lv;
   f32x4 S[NT];
-  u32x4 planes[KB][2];  // the two leading parts of S0, kept for y
-  f32x4 R[4], E[4];
   uint16_t vr[16];
-  int bad;             // first token whose value is not finite (kC: none)
 
-  __device__ __forceinline__ void load_v(int64_t t0) {
+  __device__ __forceinline__ void place() {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {  // clamped: every load is in bounds, and none waits behind a branch
-      const int64_t t = t0 + 16 * (i / 4) + 4 * g + i % 4;
-      vr[i] = v[(t < a.L ? t : a.L - 1) * row];
+    for (int kb = 0; kb < KB; ++kb) {
+      lk[kb] = hold(lds_address(&s.k[0][tile_at<NT>(r, 4 * kb + g)]));
+      lt[kb] = hold(lds_address(&s.k[0][tile_at<NT>(4 * g + r / 4, 4 * kb + r % 4)]));
     }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {  // rows r and 32 + r
+      lx[i] = hold(lds_address(&s.x[0][0][tri_at(32 * i + r) + 8 * g]));
+      lm[i] = hold(lds_address(&s.m[0][0][tri_at(32 * i + r) + 8 * g]));
+    }
+    lv = hold(lds_address(&s.va[0][4 * g]));
   }
-  // K S0 into R, S0's leading parts kept
-  __device__ __forceinline__ void ks(int buf) {
-    const uint16_t *kp = &s.k[buf][r * kNP + 8 * g];
-    u32x4 ka[2][4], sp[2][3];
+  // rows 16 rt + r, block kb of part `part` of X (M) in buffer buf
+  template <int buf>
+  __device__ __forceinline__ u32x4 row_x(int part, int rt, int kb) const {
+    return lds_get<u32x4>(lx[rt / 2] + (3 * buf + part) * ChunkLds<NT>::kTri +
+                          2 * (tri_at(16 * rt) - tri_at(32 * (rt / 2)) + 32 * kb));
+  }
+  template <int buf>
+  __device__ __forceinline__ u32x4 row_m(int part, int rt, int kb) const {
+    return lds_get<u32x4>(lm[rt / 2] + (2 * buf + part) * ChunkLds<NT>::kTri +
+                          2 * (tri_at(16 * rt) - tri_at(32 * (rt / 2)) + 32 * kb));
+  }
+  // element 16 rt + 4 g .. + 3 of vector w (va, vb, vw) of the chunk
+  template <int buf>
+  __device__ __forceinline__ f32x4 vec(int w, int rt) const {
+    return lds_get<f32x4>(lv + 4 * ((2 * w + buf) * kC + 16 * rt));
+  }
+
+  // v of the chunk of `left` tokens at t0
+  __device__ __forceinline__ void load_v(int64_t t0, int left) {
+    const __amdgpu_buffer_rsrc_t rv = rows_of(v + t0 * row, left, row, width);
 #pragma unroll
-    for (int rt = 0; rt < 4; ++rt) {
-      ka[0][rt] = lds128(kp + 16 * rt * kNP);
-      R[rt] = f32x4{0.f, 0.f, 0.f, 0.f};
-    }
+    for (int i = 0; i < 16; ++i)
+      vr[i] = __builtin_amdgcn_raw_buffer_load_b16(rv, static_cast<int>(at[i % 4]), static_cast<int>(i / 4 * rows16), 0);
+  }
+
+  // One chunk: y and the state behind it.
+  template <int buf>
+  __device__ __forceinline__ void step(int64_t t0) {
+    const int more = static_cast<int>(a.L - t0 < 2 * kC ? a.L - t0 : 2 * kC), left = more < kC ? more : kC;
+    // K S0 and Q S0, the next block of the state split while one multiplies
+    f32x4 R[4], Y[4];
+#pragma unroll
+    for (int rt = 0; rt < 4; ++rt) R[rt] = Y[rt] = f32x4{0.f, 0.f, 0.f, 0.f};
+    u32x4 sp[2][3];
     split_operand<3>(S[0], S[1], sp[0], minus);
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb) {
-      planes[kb][0] = sp[kb % 2][0];
-      planes[kb][1] = sp[kb % 2][1];
-      if (kb + 1 < KB) {
+      u32x4 ka[4], qa[4];
 #pragma unroll
-        for (int rt = 0; rt < 4; ++rt) ka[(kb + 1) % 2][rt] = lds128(kp + 16 * rt * kNP + 32 * (kb + 1));
-        split_operand<3>(S[2 * kb + 2], S[2 * kb + 3], sp[(kb + 1) % 2], minus);
+      for (int rt = 0; rt < 4; ++rt) {
+        const uint32_t tile = buf * ChunkLds<NT>::kTile + 2 * 16 * rt * 16 * NT;
+        ka[rt] = lds_get<u32x4>(lk[kb] + tile);
+        qa[rt] = lds_get<u32x4>(lk[kb] + tile + 2 * ChunkLds<NT>::kTile);
       }
+      if (kb + 1 < KB) split_operand<3>(S[2 * kb + 2], S[2 * kb + 3], sp[(kb + 1) % 2], minus);
 #pragma unroll
       for (int pl = 2; pl >= 0; --pl)
 #pragma unroll
-        for (int rt = 0; rt < 4; ++rt) R[rt] = mma(ka[kb % 2][rt], sp[kb % 2][pl], R[rt]);
+        for (int rt = 0; rt < 4; ++rt) R[rt] = mma(ka[rt], sp[kb % 2][pl], R[rt]);
+#pragma unroll
+      for (int pl = 1; pl >= 0; --pl)
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) Y[rt] = mma(qa[rt], sp[kb % 2][pl], Y[rt]);
     }
-  }
-  // R = v - a (K S0); E = X R.  A row that is not finite is left out of the
-  // products, where 0 times it would reach the tokens before it.
-  __device__ __forceinline__ void xr(int buf) {
-    u32x4 xa[4][2][3];
-#pragma unroll
-    for (int rt = 0; rt < 4; ++rt)
-#pragma unroll
-      for (int kb = 0; kb <= rt / 2; ++kb)
-#pragma unroll
-        for (int pl = 0; pl < 3; ++pl)
-          xa[rt][kb][pl] = lds128(&s.x[pl][(16 * rt + r) * kTokPitch + 32 * kb + 8 * g]);
+
+    __builtin_amdgcn_sched_barrier(0);
+    // R = v - a (K S0).  A row that is not finite is left out of the products,
+    // where 0 times it would reach the tokens before it.
     float test = 0.f;
 #pragma unroll
     for (int rt = 0; rt < 4; ++rt) {
-      const f32x4 av = lds_f4(&s.va[buf][16 * rt + 4 * g]);
+      const f32x4 av = vec<buf>(0, rt);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         R[rt][e] = fmaf(-av[e], R[rt][e], __uint_as_float(static_cast<uint32_t>(vr[4 * rt + e]) << 16));
         test = fmaf(R[rt][e], 0.f, test);
       }
     }
-    bad = kC;
-    if (__builtin_expect(__any(test != 0.f), 0)) {
+    load_v(t0 + kC, more - kC);
+    int bad = kC;  // the first such token of this lane's column
+    const bool any_bad = __any(test != 0.f);
+    if (__builtin_expect(any_bad, 0)) {
 #pragma unroll
       for (int i = 15; i >= 0; --i)
         if (!(fabsf(R[i / 4][i % 4]) < __builtin_inff())) {
@@ -182,104 +259,103 @@ struct Chain {
       bad = min(bad, __shfl_xor(bad, 16));
       bad = min(bad, __shfl_xor(bad, 32));
     }
-    u32x4 rp[2][3];
+
+    __builtin_amdgcn_sched_barrier(0);
+    // E = X R: small terms first, the four row tiles side by side
+    f32x4 E[4];
+    {
+      u32x4 rp[2][3];
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb) split_operand<3>(R[2 * kb], R[2 * kb + 1], rp[kb], minus);
+      for (int kb = 0; kb < 2; ++kb) split_operand<3>(R[2 * kb], R[2 * kb + 1], rp[kb], minus);
 #pragma unroll
-    for (int rt = 0; rt < 4; ++rt) E[rt] = f32x4{0.f, 0.f, 0.f, 0.f};
-    // small terms first; the four row tiles side by side
-    constexpr int kX[6] = {2, 0, 1, 1, 0, 0}, kR[6] = {0, 2, 1, 0, 1, 0};
+      for (int rt = 0; rt < 4; ++rt) E[rt] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < 6; ++i)
+      for (int xp = 2; xp >= 0; --xp) {
+        u32x4 xa[4][2];
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt)
+#pragma unroll
+          for (int kb = 0; kb <= rt / 2; ++kb) xa[rt][kb] = row_x<buf>(xp, rt, kb);
+#pragma unroll
+        for (int pl = 2 - xp; pl >= 0; --pl)
+#pragma unroll
+          for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+            for (int rt = 2 * kb; rt < 4; ++rt) E[rt] = mma(xa[rt][kb], rp[kb][pl], E[rt]);
+      }
+    }
+
+    __builtin_amdgcn_sched_barrier(0);
+    // S1 = whole S0 + K^T (w E)
+    {
+      u32x4 up[2][3];
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb)
+        split_operand<3>(E[2 * kb] * vec<buf>(2, 2 * kb), E[2 * kb + 1] * vec<buf>(2, 2 * kb + 1), up[kb], minus);
+      const float whole = s.whole[buf];
+      constexpr int kSide = 4;  // state tiles side by side
+#pragma unroll
+      for (int n0 = 0; n0 < NT; n0 += kSide) {
+        u32x4 kt[kSide][2];
+#pragma unroll
+        for (int i = 0; i < kSide; ++i) {
+          const int nt = n0 + i;
+#pragma unroll
+          for (int kb = 0; kb < 2; ++kb) {
+            u32x2 half[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+              half[u] = lds_transposed(lt[nt / 2] + buf * ChunkLds<NT>::kTile +
+                                       2 * ((32 * kb + 16 * u) * 16 * NT + 4 * (nt % 2)));
+            kt[i][kb] = u32x4{half[0][0], half[0][1], half[1][0], half[1][1]};
+          }
+          S[nt] = S[nt] * whole;
+        }
+#pragma unroll
+        for (int pl = 2; pl >= 0; --pl)
+#pragma unroll
+          for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+            for (int i = 0; i < kSide; ++i) S[n0 + i] = mma(kt[i][kb], up[kb][pl], S[n0 + i]);
+      }
+    }
+
+    __builtin_amdgcn_sched_barrier(0);
+    // y = b (Q S0) + M E
+    u32x4 ep[2][2];
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) split_operand<2>(E[2 * kb], E[2 * kb + 1], ep[kb], minus);
+#pragma unroll
+    for (int rt = 0; rt < 4; ++rt) Y[rt] = Y[rt] * vec<buf>(1, rt);
+#pragma unroll
+    for (int mp = 1; mp >= 0; --mp) {
+      u32x4 ma[4][2];
 #pragma unroll
       for (int rt = 0; rt < 4; ++rt)
 #pragma unroll
-        for (int kb = 0; kb <= rt / 2; ++kb) E[rt] = mma(xa[rt][kb][kX[i]], rp[kb][kR[i]], E[rt]);
-  }
-  // S1 = whole S0 + K^T (w E)
-  __device__ __forceinline__ void update(int buf) {
-    u32x4 up[2][3];
+        for (int kb = 0; kb <= rt / 2; ++kb) ma[rt][kb] = row_m<buf>(mp, rt, kb);
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
-      split_operand<3>(E[2 * kb] * lds_f4(&s.vw[buf][32 * kb + 4 * g]),
-                       E[2 * kb + 1] * lds_f4(&s.vw[buf][32 * kb + 16 + 4 * g]), up[kb], minus);
-    const float whole = s.whole[buf];
-#pragma unroll
-    for (int n0 = 0; n0 < NT; n0 += 4) {
-      u32x4 ka[4][2];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb) ka[i][kb] = lds128(&s.kt[kt_at(16 * (n0 + i) + r, 4 * kb + g)]);
-        S[n0 + i] = S[n0 + i] * whole;
-      }
-#pragma unroll
-      for (int pl = 2; pl >= 0; --pl)
+      for (int pl = 1 - mp; pl >= 0; --pl)
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) S[n0 + i] = mma(ka[i][kb], up[kb][pl], S[n0 + i]);
+          for (int rt = 2 * kb; rt < 4; ++rt) Y[rt] = mma(ma[rt][kb], ep[kb][pl], Y[rt]);
     }
-    if (__builtin_expect(__any(bad < kC), 0))
+    if (__builtin_expect(any_bad, 0)) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (16 * (i / 4) + 4 * g + i % 4 >= bad) Y[i / 4][i % 4] = __builtin_nanf("");
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           if (bad < kC) S[nt][e] = __builtin_nanf("");
-  }
-  __device__ __forceinline__ void output(int buf, int64_t t0) {
-    const uint16_t *qp = &s.q[buf][r * kNP + 8 * g];
-    u32x4 ep[2][2], qa[2][4];
-    f32x4 acc[4];
-#pragma unroll
-    for (int rt = 0; rt < 4; ++rt) {
-      qa[0][rt] = lds128(qp + 16 * rt * kNP);
-      acc[rt] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
+    const __amdgpu_buffer_rsrc_t ry = rows_of(y + t0 * row, left, row, width);
 #pragma unroll
-    for (int kb = 0; kb < KB; ++kb) {
-      if (kb + 1 < KB)
-#pragma unroll
-        for (int rt = 0; rt < 4; ++rt) qa[(kb + 1) % 2][rt] = lds128(qp + 16 * rt * kNP + 32 * (kb + 1));
-#pragma unroll
-      for (int pl = 1; pl >= 0; --pl)
-#pragma unroll
-        for (int rt = 0; rt < 4; ++rt) acc[rt] = mma(qa[kb % 2][rt], planes[kb][pl], acc[rt]);
-    }
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb) split_operand<2>(E[2 * kb], E[2 * kb + 1], ep[kb], minus);
-    u32x4 ma[4][2][2];
-#pragma unroll
-    for (int rt = 0; rt < 4; ++rt)
-#pragma unroll
-      for (int kb = 0; kb <= rt / 2; ++kb)
-#pragma unroll
-        for (int pl = 0; pl < 2; ++pl)
-          ma[rt][kb][pl] = lds128(&s.m[pl][(16 * rt + r) * kTokPitch + 32 * kb + 8 * g]);
-#pragma unroll
-    for (int rt = 0; rt < 4; ++rt) acc[rt] = acc[rt] * lds_f4(&s.vb[buf][16 * rt + 4 * g]);
-    constexpr int kM[3] = {1, 0, 0}, kE[3] = {0, 1, 0};
-#pragma unroll
-    for (int i = 0; i < 3; ++i)
-#pragma unroll
-      for (int rt = 0; rt < 4; ++rt)
-#pragma unroll
-        for (int kb = 0; kb <= rt / 2; ++kb) acc[rt] = mma(ma[rt][kb][kM[i]], ep[kb][kE[i]], acc[rt]);
-    if (__builtin_expect(__any(bad < kC), 0))
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (16 * (i / 4) + 4 * g + i % 4 >= bad) acc[i / 4][i % 4] = __builtin_nanf("");
-    if (!col) return;
-    bf16_t *out = y + (t0 + 4 * g) * row;
-    if (t0 + kC <= a.L) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) out[(16 * (i / 4) + i % 4) * row] = from_f32<bf16_t>(acc[i / 4][i % 4]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (t0 + 16 * (i / 4) + 4 * g + i % 4 < a.L)
-          out[(16 * (i / 4) + i % 4) * row] = from_f32<bf16_t>(acc[i / 4][i % 4]);
-    }
+    for (int i = 0; i < 16; ++i)
+      __builtin_amdgcn_raw_buffer_store_b16(from_f32<bf16_t>(Y[i / 4][i % 4]).bits, ry, static_cast<int>(at[i % 4]),
+                                            static_cast<int>(i / 4 * rows16), 0);
   }
 };
 
@@ -289,35 +365,75 @@ struct Chain {
 template <int NT>
 struct Prepare {
   static constexpr int KB = NT / 2;
-  static constexpr int kNP = ChunkLds<NT>::kNPitch;
   const GdrArgs &a;
   ChunkLds<NT> &s;
   const MinusOne minus;
-  const int tid, lane, wave, r, g;
+  const int tid, lane, r, g;
   const int64_t b, h, grp;
   const float A2, bias;
   static constexpr int kPieces = 2 * NT;                    // 16-byte pieces of a row
   static constexpr int kLoaders = kPieces * kC / 4;         // threads that hold a piece
   static_assert(kLoaders <= 256, "four tokens by one piece per thread");
-  u32x4 kr[4], qr[4], kstaged[4];
+  uint32_t meetings;
+  // LDS addresses: this thread's pieces of K (two halves by four tokens), rows r
+  // of K by block of 32 states, c and rk at r and at 4 g (rq and beta behind rk),
+  // row r, element 4 g of the blocks of A'
+  uint32_t lp[4][2], lk[KB], lc1, lc4, lf1, lf4, la;
+  uint32_t piece;  // bytes to this thread's piece of K and Q, first token
+  u32x4 kr[4], qr[4];
   bf16_t dtr, ber;
   f32x4 X[4], M[4];
 
-  __device__ __forceinline__ void load(int64_t t0) {
+  __device__ __forceinline__ void place() {
+    const int pos = kpos(8 * (tid % kPieces)), tq = 4 * (tid / kPieces) % kC;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)  // the second four of a piece lie one piece further
+#pragma unroll
+      for (int u = 0; u < 2; ++u) lp[i][u] = hold(lds_address(&s.k[0][tile_at<NT>(tq + i, pos / 8 + u) + pos % 8]));
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) lk[kb] = hold(lds_address(&s.k[0][tile_at<NT>(r, 4 * kb + g)]));
+    lc1 = hold(lds_address(&s.c[r]));
+    lc4 = hold(lds_address(&s.c[4 * g]));
+    lf1 = hold(lds_address(&s.rk[r]));
+    lf4 = hold(lds_address(&s.rk[4 * g]));
+    la = hold(lds_address(&s.at[r * kAtPitch + 4 * g]));
     const int m = tid % kPieces;
-    // behind the last token the last one's address, and zeros in its place
-    // when it is staged; no load waits behind a branch
-    const int64_t n = 8 * m < a.N ? 8 * m : 0;
+    piece = tid < kLoaders && 8 * m < a.N ? 2 * (tq * static_cast<uint32_t>(a.G * a.N) + 8 * m) : kNowhere;
+  }
+  __device__ __forceinline__ double c1(int t) const { return lds_get<double>(lc1 + 8 * t); }
+  __device__ __forceinline__ double c4(int t) const { return lds_get<double>(lc4 + 8 * t); }
+  enum { kRk, kRq, kBeta };  // behind each other
+  __device__ __forceinline__ float f1(int which, int t) const { return lds_get<float>(lf1 + 4 * (which * kC + t)); }
+  __device__ __forceinline__ f32x4 f4(int which, int t) const { return lds_get<f32x4>(lf4 + 4 * (which * kC + t)); }
+  static constexpr uint32_t block(int j, int k) { return 4 * at_block(j, k); }
+
+  // The four preparing waves meet: all arrive without waiting for anybody else.
+  __device__ __forceinline__ void meet() {
+    meetings += 4;
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
+    if (lane == 0) __hip_atomic_fetch_add(&s.met, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+    while (__hip_atomic_load(&s.met, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP) < meetings)
+      __builtin_amdgcn_s_sleep(1);
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
+  }
+
+  __device__ __forceinline__ void load(int64_t t0) {
+    const int left = static_cast<int>(a.L - t0 < kC ? a.L - t0 : kC);
+    const uint32_t row = static_cast<uint32_t>(a.G * a.N), H = static_cast<uint32_t>(a.H);
+    const int64_t base = ((b * a.L + t0) * a.G + grp) * a.N, gate = (b * a.L + t0) * a.H + h;
+    const __amdgpu_buffer_rsrc_t rk = rows_of(static_cast<const uint16_t *>(a.k) + base, left, row, a.N);
+    const __amdgpu_buffer_rsrc_t rq = rows_of(static_cast<const uint16_t *>(a.q) + base, left, row, a.N);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int64_t t = t0 + 4 * (tid / kPieces) + i;
-      const int64_t at = ((b * a.L + (t < a.L ? t : a.L - 1)) * a.G + grp) * a.N + n;
-      kr[i] = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(a.k) + at);
-      qr[i] = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(a.q) + at);
+      kr[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rk, static_cast<int>(piece),
+                                                                              static_cast<int>(2 * i * row), 0));
+      qr[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rq, static_cast<int>(piece),
+                                                                              static_cast<int>(2 * i * row), 0));
     }
-    const int64_t at = (b * a.L + (t0 + lane < a.L ? t0 + lane : a.L - 1)) * a.H + h;
-    dtr = static_cast<const bf16_t *>(a.dt)[at];
-    ber = static_cast<const bf16_t *>(a.beta)[at];
+    dtr.bits = __builtin_amdgcn_raw_buffer_load_b16(rows_of(static_cast<const uint16_t *>(a.dt) + gate, left, H, 1),
+                                                    static_cast<int>(2 * lane * H), 0, 0);
+    ber.bits = __builtin_amdgcn_raw_buffer_load_b16(rows_of(static_cast<const uint16_t *>(a.beta) + gate, left, H, 1),
+                                                    static_cast<int>(2 * lane * H), 0, 0);
   }
   static __device__ __forceinline__ float sum_squares(u32x4 u) {
     float ss = 0.f;
@@ -329,63 +445,42 @@ struct Prepare {
     return row_sum<(kPieces < 16 ? kPieces : 16)>(ss);
   }
   // K, Q, the norms, beta and the cumulative decay of the loaded chunk
-  __device__ __forceinline__ void stage(int buf, int64_t t0) {
-    const int m = tid % kPieces;
-    if (tid < kLoaders) {
-      float ss[4], qq[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int tok = 4 * (tid / kPieces) + i;
-        const bool in = t0 + tok < a.L && 8 * m < a.N;
-        kstaged[i] = in ? kr[i] : u32x4{0, 0, 0, 0};
-        qr[i] = in ? qr[i] : u32x4{0, 0, 0, 0};
-        const int at = tok * kNP + kpos(8 * m);
-        *reinterpret_cast<u32x2 *>(&s.k[buf][at]) = u32x2{kstaged[i][0], kstaged[i][1]};
-        *reinterpret_cast<u32x2 *>(&s.k[buf][at + 8]) = u32x2{kstaged[i][2], kstaged[i][3]};
-        *reinterpret_cast<u32x2 *>(&s.q[buf][at]) = u32x2{qr[i][0], qr[i][1]};
-        *reinterpret_cast<u32x2 *>(&s.q[buf][at + 8]) = u32x2{qr[i][2], qr[i][3]};
-      }
-      if (a.qk_norm) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          ss[i] = __builtin_amdgcn_rsqf(sum_squares(kstaged[i]) + kQkNormEps);
-          qq[i] = a.scale * __builtin_amdgcn_rsqf(sum_squares(qr[i]) + kQkNormEps);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          ss[i] = 1.f;
-          qq[i] = a.scale;
-        }
-      }
-      if (m == 0) {
-        *reinterpret_cast<f32x4 *>(&s.rk[4 * (tid / kPieces)]) = f32x4{ss[0], ss[1], ss[2], ss[3]};
-        *reinterpret_cast<f32x4 *>(&s.rq[4 * (tid / kPieces)]) = f32x4{qq[0], qq[1], qq[2], qq[3]};
-      }
-    }
-    if (wave == 0) {
+  template <int W, int buf>
+  __device__ __forceinline__ void stage(int64_t t0) {
+    if (W == 0) {
       const bool in = t0 + lane < a.L;  // behind the last token nothing decays and nothing is written
-      s.beta[lane] = in ? to_f32(ber) : 0.f;
+      s.beta[lane] = to_f32(ber);
       // a step below -2000 leaves nothing of the state, however it is summed;
       // held there, the differences of later tokens keep their bits
       float lg = in ? step_size(to_f32(dtr), bias, a.dt_softplus) * A2 : 0.f;
       if (lg < -2000.f) lg = -2000.f;
       s.c[lane] = wave_scan(lg);
     }
-  }
-  __device__ __forceinline__ void transpose() {  // K^T of the staged chunk
     if (tid >= kLoaders) return;
-    const int m = tid % kPieces, pos = kpos(4 * (tid / kPieces)), ch = pos >> 3, half = pos & 7;
+    const int m = tid % kPieces, tq = 4 * (tid / kPieces);
+    f32x4 nk = {1.f, 1.f, 1.f, 1.f}, nq = {1.f, 1.f, 1.f, 1.f};
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const uint32_t sel = e & 1 ? 0x07060302u : 0x05040100u;
-      *reinterpret_cast<u32x2 *>(&s.kt[kt_at(8 * m + e, ch) + half]) =
-          u32x2{__builtin_amdgcn_perm(kstaged[1][e / 2], kstaged[0][e / 2], sel),
-                __builtin_amdgcn_perm(kstaged[3][e / 2], kstaged[2][e / 2], sel)};
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const uint32_t at = lp[i][u] + buf * ChunkLds<NT>::kTile;
+        lds_put(at, u32x2{kr[i][2 * u], kr[i][2 * u + 1]});
+        lds_put(at + 2 * ChunkLds<NT>::kTile, u32x2{qr[i][2 * u], qr[i][2 * u + 1]});
+      }
+    if (a.qk_norm)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        nk[i] = __builtin_amdgcn_rsqf(sum_squares(kr[i]) + kQkNormEps);
+        nq[i] = __builtin_amdgcn_rsqf(sum_squares(qr[i]) + kQkNormEps);
+      }
+    if (m == 0) {
+      *reinterpret_cast<f32x4 *>(&s.rk[tq]) = nk;
+      *reinterpret_cast<f32x4 *>(&s.rq[tq]) = nq * a.scale;
     }
   }
   // the chain's vectors
-  __device__ __forceinline__ void vectors(int buf) {
+  template <int buf>
+  __device__ __forceinline__ void vectors() {
     const double c = s.c[lane], end = s.c[kC - 1];
     const float into = decay_of(c), rk = s.rk[lane];
     s.va[buf][lane] = into * rk;
@@ -394,10 +489,9 @@ struct Prepare {
     if (lane == kC - 1) s.whole[buf] = into;
   }
   // A' (transposed into LDS) for block row W, M^T for block row 3 - W (kept)
-  template <int W>
-  __device__ __forceinline__ void products(int buf) {
+  template <int W, int buf>
+  __device__ __forceinline__ void products() {
     constexpr int V = 3 - W;
-    const uint16_t *kp = &s.k[buf][r * kNP + 8 * g], *qp = &s.q[buf][r * kNP + 8 * g];
     constexpr int kMost = (W > V ? W : V) + 1;  // block rows of K that either needs
     f32x4 ap[W + 1];
 #pragma unroll
@@ -408,8 +502,9 @@ struct Prepare {
     for (int kb = 0; kb < KB; ++kb) {
       u32x4 kf[kMost];
 #pragma unroll
-      for (int i = 0; i < kMost; ++i) kf[i] = lds128(kp + 16 * i * kNP + 32 * kb);
-      const u32x4 qf = lds128(qp + 16 * V * kNP + 32 * kb);
+      for (int i = 0; i < kMost; ++i)
+        kf[i] = lds_get<u32x4>(lk[kb] + buf * ChunkLds<NT>::kTile + 2 * 16 * i * 16 * NT);
+      const u32x4 qf = lds_get<u32x4>(lk[kb] + (2 + buf) * ChunkLds<NT>::kTile + 2 * 16 * V * 16 * NT);
 #pragma unroll
       for (int jt = 0; jt <= W; ++jt) ap[jt] = mma(kf[W], kf[jt], ap[jt]);
 #pragma unroll
@@ -417,28 +512,27 @@ struct Prepare {
     }
     double ci[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) ci[e] = s.c[16 * W + 4 * g + e];
-    const f32x4 si = lds_f4(&s.rk[16 * W + 4 * g]);
+    for (int e = 0; e < 4; ++e) ci[e] = c4(16 * W + e);
+    const f32x4 si = f4(kRk, 16 * W);
 #pragma unroll
     for (int jt = 0; jt <= W; ++jt) {
-      const int j = 16 * jt + r;
-      const double cj = s.c[j];
-      const float sj = s.rk[j] * s.beta[j];
+      const double cj = c1(16 * jt);
+      const float sj = f1(kRk, 16 * jt) * f1(kBeta, 16 * jt);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float f = ap[jt][e] * (si[e] * sj) * decay_of(ci[e] - cj);
         ap[jt][e] = jt < W || 4 * g + e > r ? f : 0.f;
       }
-      *reinterpret_cast<f32x4 *>(&s.at[j * kAtPitch + 16 * W + 4 * g]) = ap[jt];
+      lds_put(la + block(jt, W), ap[jt]);
     }
-    const double cv = s.c[16 * V + r];
-    const float sv = s.rq[16 * V + r];
+    const double cv = c1(16 * V);
+    const float sv = f1(kRq, 16 * V);
 #pragma unroll
     for (int jt = 0; jt <= V; ++jt) {
-      const f32x4 rkj = lds_f4(&s.rk[16 * jt + 4 * g]), bej = lds_f4(&s.beta[16 * jt + 4 * g]);
+      const f32x4 sj = f4(kRk, 16 * jt) * f4(kBeta, 16 * jt);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float f = M[jt][e] * (sv * (rkj[e] * bej[e])) * decay_of(cv - s.c[16 * jt + 4 * g + e]);
+        const float f = M[jt][e] * (sv * sj[e]) * decay_of(cv - c4(16 * jt + e));
         M[jt][e] = jt < V || 4 * g + e <= r ? f : 0.f;
       }
     }
@@ -448,31 +542,28 @@ struct Prepare {
   // block on their way.
   __device__ __forceinline__ void diagonal() {
     const int blk = g, col = r;
-    const float *at = &s.at[16 * blk * kAtPitch + 16 * blk];
-    f32x4 l[2][4][4];
-    auto fetch = [&](int k4) {  // A'[16 blk + i][16 blk + k], k = 4 k4 .. + 3, i >= 4 k4
-#pragma unroll
-      for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-        for (int q4 = 0; q4 < 4; ++q4)
-          if (q4 >= k4) l[k4 % 2][kk][q4] = lds_f4(at + (4 * k4 + kk) * kAtPitch + 4 * q4);
-    };
+    const uint32_t at = hold(lds_address(&s.at[(blk * 4 - blk * (blk - 1) / 2) * 16 * kAtPitch]));
     float x[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) x[i] = i == col ? 1.f : 0.f;
-    fetch(0);
 #pragma unroll
-    for (int k4 = 0; k4 < 4; ++k4) {
-      if (k4 < 3) fetch(k4 + 1);
+    for (int k4 = 0; k4 < 16; k4 += 4) {
+      f32x4 l[4][4];
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk)
+      for (int k = 0; k < 4; ++k)  // A'[16 blk + i][16 blk + k4 + k], i >= k4
 #pragma unroll
-        for (int i = 4 * k4 + kk + 1; i < 16; ++i) x[i] = fmaf(-l[k4 % 2][kk][i / 4][i % 4], x[4 * k4 + kk], x[i]);
+        for (int q4 = 0; q4 < 4; ++q4)
+          if (q4 >= k4 / 4) l[k][q4] = lds_get<f32x4>(at + 4 * ((k4 + k) * kAtPitch + 4 * q4));
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (i > k4 + k) x[i] = fmaf(-l[k][i / 4][i % 4], x[k4 + k], x[i]);
+      __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
     for (int q4 = 0; q4 < 4; ++q4)
-      *reinterpret_cast<f32x4 *>(&s.xt[blk][col * kXtPitch + 4 * q4]) =
-          f32x4{x[4 * q4], x[4 * q4 + 1], x[4 * q4 + 2], x[4 * q4 + 3]};
+      lds_put(at + 4 * col * kAtPitch + 16 * q4, f32x4{x[4 * q4], x[4 * q4 + 1], x[4 * q4 + 2], x[4 * q4 + 3]});
   }
   // Block row W of X, transposed tiles: X_Wj^T = -X_jj^T sum_{j<k<=W} A'_kj^T X_Wk^T
   template <int W>
@@ -480,12 +571,12 @@ struct Prepare {
     f32x4 at[4][4], xj[4];
 #pragma unroll
     for (int j = 0; j < W; ++j) {
-      xj[j] = lds_f4(&s.xt[j][r * kXtPitch + 4 * g]);
+      xj[j] = lds_get<f32x4>(la + block(j, j));
 #pragma unroll
-      for (int k = j + 1; k <= W; ++k) at[j][k] = lds_f4(&s.at[(16 * j + r) * kAtPitch + 16 * k + 4 * g]);
+      for (int k = j + 1; k <= W; ++k) at[j][k] = lds_get<f32x4>(la + block(j, k));
     }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) X[W][e] = s.xt[W][(4 * g + e) * kXtPitch + r];
+    for (int e = 0; e < 4; ++e) X[W][e] = s.at[at_block(W, W) + (4 * g + e) * kAtPitch + r];
 #pragma unroll
     for (int j = W - 1; j >= 0; --j) {
       f32x4 t = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -495,80 +586,89 @@ struct Prepare {
     }
   }
   // X and M of the prepared chunk where the chain reads them
-  template <int W>
+  template <int W, int buf>
   __device__ __forceinline__ void publish() {
     constexpr int V = 3 - W;
-#pragma unroll
-    for (int j = 0; j <= W; ++j) {
-      u32x2 p[3];
-      split4<3>(X[j], p, minus);
-#pragma unroll
-      for (int pl = 0; pl < 3; ++pl)
-        *reinterpret_cast<u32x2 *>(&s.x[pl][(16 * W + r) * kTokPitch + kpos(16 * j) + 8 * g]) = p[pl];
-    }
+    const uint32_t xw = hold(lds_address(&s.x[buf][0][tri_at(16 * W + r) + 8 * g]));
+    const uint32_t mv = hold(lds_address(&s.m[buf][0][tri_at(16 * V + r) + 8 * g]));
 #pragma unroll
     for (int j = 0; j <= V; ++j) {
       u32x2 p[2];
       split4<2>(M[j], p, minus);
 #pragma unroll
-      for (int pl = 0; pl < 2; ++pl)
-        *reinterpret_cast<u32x2 *>(&s.m[pl][(16 * V + r) * kTokPitch + kpos(16 * j) + 8 * g]) = p[pl];
+      for (int pl = 0; pl < 2; ++pl) lds_put(mv + pl * ChunkLds<NT>::kTri + 2 * kpos(16 * j), p[pl]);
     }
+#pragma unroll
+    for (int j = 0; j <= W; ++j) {
+      u32x2 p[3];
+      split4<3>(X[j], p, minus);
+#pragma unroll
+      for (int pl = 0; pl < 3; ++pl) lds_put(xw + pl * ChunkLds<NT>::kTri + 2 * kpos(16 * j), p[pl]);
+    }
+  }
+  template <int W, int buf>
+  __device__ __forceinline__ void prepare(int64_t c) {
+    stage<W, buf>(c * kC);
+    load((c + 1) * kC);
+    meet();
+    products<W, buf>();
+    meet();
+    if (W == 3) diagonal();
+    if (W == 1) vectors<buf>();
+    meet();
+    block_row<W>();
+    publish<W, buf>();
   }
   // Chunk c + 1 beside the chain's chunk c (chunk 0 has nobody to overlap with).
   template <int W>
   __device__ __forceinline__ void run(int64_t nc) {
     load(0);
-    for (int64_t c = -1; c < nc; ++c) {
-      const bool more = c + 1 < nc;
-      const int buf = static_cast<int>((c + 1) & 1);
-      if (c >= 0) publish<W>();
-      if (more) {
-        stage(buf, (c + 1) * kC);
-        load((c + 2) * kC);
+    for (int64_t c = 0; c < nc; c += 2) {
+      prepare<W, 0>(c);
+      __syncthreads();
+      if (c + 1 < nc) {
+        prepare<W, 1>(c + 1);
+        __syncthreads();
       }
-      __syncthreads();
-      if (more) products<W>(buf);
-      __syncthreads();
-      if (more) {
-        if (W == 0) diagonal();
-        if (W == 1) vectors(buf);
-      }
-      __syncthreads();
-      if (more) {
-        transpose();
-        block_row<W>();
-      }
-      __syncthreads();
     }
+    __syncthreads();  // the chain's last chunk
   }
 };
 
 template <int NT>
 __global__ __launch_bounds__(kThreads) void gdr_chunk_kernel(GdrArgs a, int64_t ptiles) {
   __shared__ ChunkLds<NT> s;
-  const int64_t per = a.H / a.G * ptiles;  // workgroups of a (sequence, group), which share K and Q
+  const uint32_t heads = static_cast<uint32_t>(a.H / a.G);  // of a group
+  const uint32_t per = heads * static_cast<uint32_t>(ptiles);  // workgroups of a (sequence, group), which share K and Q
   // workgroups of one (sequence, group) on one XCD (consecutive ids go to the
   // 8 XCDs in turn), so that its K and Q come from that L2
-  const int64_t idx = blockIdx.x / 8, bg = blockIdx.x % 8 + 8 * (idx / per), mem = idx % per;
+  const uint32_t idx = blockIdx.x / 8, bg = blockIdx.x % 8 + 8 * (idx / per), mem = idx % per;
   if (bg >= a.B * a.G) return;
-  const int64_t b = bg / a.G, grp = bg % a.G, h = grp * (a.H / a.G) + mem / ptiles, p0 = mem % ptiles * kCols;
+  // the same for the workgroup, and said so: they address buffers
+  auto same = [](uint32_t v) { return static_cast<int64_t>(__builtin_amdgcn_readfirstlane(v)); };
+  const uint32_t G = static_cast<uint32_t>(a.G);
+  const int64_t b = same(bg / G), grp = same(bg % G), h = same(bg % G * heads + mem / static_cast<uint32_t>(ptiles));
+  const int64_t p0 = same(mem % static_cast<uint32_t>(ptiles) * kCols);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
   const int r = lane % 16, g = lane / 16;
   const int64_t nc = (a.L + kC - 1) / kC;
 
   // block pairs above the diagonal are read with their 32 tokens and stay 0
-  for (int i = threadIdx.x; i < kC * kTokPitch / 2; i += kThreads) {
+  for (int i = threadIdx.x; i < kTriSize / 2; i += kThreads)
 #pragma unroll
-    for (int pl = 0; pl < 3; ++pl) reinterpret_cast<uint32_t *>(s.x[pl])[i] = 0;
+    for (int bf = 0; bf < 2; ++bf) {
 #pragma unroll
-    for (int pl = 0; pl < 2; ++pl) reinterpret_cast<uint32_t *>(s.m[pl])[i] = 0;
-  }
+      for (int pl = 0; pl < 3; ++pl) reinterpret_cast<uint32_t *>(s.x[bf][pl])[i] = 0;
+#pragma unroll
+      for (int pl = 0; pl < 2; ++pl) reinterpret_cast<uint32_t *>(s.m[bf][pl])[i] = 0;
+    }
+  if (threadIdx.x == 0) s.met = 0;
   __syncthreads();
 
   if (wave >= 4) {
-    Prepare<NT> w{a, s, MinusOne(), static_cast<int>(threadIdx.x) - 256, lane, wave - 4, r, g, b, h, grp,
-                  a.A[h] * kLog2e, a.dt_bias ? a.dt_bias[h] : 0.f, {}, {}, {}, {}, {}, {}, {}};
+    Prepare<NT> w{a, s, MinusOne(), static_cast<int>(threadIdx.x) - 256, lane, r, g, b, h, grp,
+                  a.A[h] * kLog2e, a.dt_bias ? a.dt_bias[h] : 0.f, 0u, {}, {}, 0, 0, 0, 0, 0, 0, {}, {}, {}, {}, {}, {}};
+    w.place();
     if (wave == 4) w.template run<0>(nc);
     else if (wave == 5) w.template run<1>(nc);
     else if (wave == 6) w.template run<2>(nc);
@@ -576,33 +676,30 @@ __global__ __launch_bounds__(kThreads) void gdr_chunk_kernel(GdrArgs a, int64_t 
     return;
   }
 
-  const int64_t p = p0 + 16 * wave + r, row = a.H * a.P;
+  const int64_t p = p0 + 16 * wave + r;
+  const uint32_t row = static_cast<uint32_t>(a.H * a.P);
   const bool live = p0 + 16 * wave < a.P, col = p < a.P;  // some column, this lane's column
-  const int64_t at0 = (b * a.L * a.H + h) * a.P + (col ? p : a.P - 1);
-  Chain<NT> w{a, s, MinusOne(), r, g, col, static_cast<const uint16_t *>(a.v) + at0, static_cast<bf16_t *>(a.y) + at0,
-              row, {}, {}, {}, {}, {}, kC};
+  const int64_t head = (b * a.L * a.H + h) * a.P;
+  Chain<NT> w{a, s, MinusOne(), r, g, static_cast<const uint16_t *>(a.v) + head, static_cast<bf16_t *>(a.y) + head,
+              row, static_cast<uint32_t>(a.P), 32 * row, {}, {}, {}, {}, {}, 0, {}, {}};
+  w.place();
+#pragma unroll
+  for (int e = 0; e < 4; ++e) w.at[e] = col ? 2 * ((4 * g + e) * row + static_cast<uint32_t>(p)) : kNowhere;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     w.S[nt] = f32x4{0.f, 0.f, 0.f, 0.f};
     if (a.h0 != nullptr && col && 16 * nt + 4 * g < a.N)
       w.S[nt] = *reinterpret_cast<const f32x4 *>(a.h0 + ((b * a.H + h) * a.P + p) * a.N + 16 * nt + 4 * g);
   }
-  if (live) w.load_v(0);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) __syncthreads();  // the preparation of chunk 0
-  for (int64_t c = 0; c < nc; ++c) {
-    const int buf = static_cast<int>(c & 1);
-    if (live) w.ks(buf);
+  if (live) w.load_v(0, static_cast<int>(a.L < kC ? a.L : kC));
+  __syncthreads();  // the preparation of chunk 0
+  for (int64_t c = 0; c < nc; c += 2) {
+    if (live) w.template step<0>(c * kC);
     __syncthreads();
-    if (live) {
-      w.xr(buf);
-      w.load_v((c + 1) * kC);
+    if (c + 1 < nc) {
+      if (live) w.template step<1>((c + 1) * kC);
+      __syncthreads();
     }
-    __syncthreads();
-    if (live) w.update(buf);
-    __syncthreads();
-    if (live) w.output(buf, c * kC);
-    __syncthreads();
   }
   if (a.h_final != nullptr && col)
 #pragma unroll
@@ -617,7 +714,9 @@ bool aligned16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0;
 
 bool gdr_chunk_applies(const GdrArgs &a) {
   return a.dt_type == DType::BF16 && a.N <= 128 && a.N % 8 == 0 && a.L >= kGdrChunkMinL && aligned16(a.q) &&
-         aligned16(a.k) && aligned16(a.h0) && aligned16(a.h_final);
+         aligned16(a.k) && aligned16(a.h0) && aligned16(a.h_final) &&
+         // 64 rows of a tensor within 32-bit offsets
+         a.H * a.P <= (int64_t(1) << 24) && a.G * a.N <= (int64_t(1) << 24);
 }
 
 hipError_t launch_gdr_chunk(const GdrArgs &a, hipStream_t s) {
