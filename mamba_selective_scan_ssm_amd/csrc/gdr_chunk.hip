@@ -445,8 +445,8 @@ struct Prepare {
     return row_sum<(kPieces < 16 ? kPieces : 16)>(ss);
   }
   // K, Q, the norms, beta and the cumulative decay of the loaded chunk
-  template <int W, int buf>
-  __device__ __forceinline__ void stage(int64_t t0) {
+  template <int W>
+  __device__ __forceinline__ void stage(int buf, int64_t t0) {
     if (W == 0) {
       const bool in = t0 + lane < a.L;  // behind the last token nothing decays and nothing is written
       s.beta[lane] = to_f32(ber);
@@ -479,8 +479,7 @@ struct Prepare {
     }
   }
   // the chain's vectors
-  template <int buf>
-  __device__ __forceinline__ void vectors() {
+  __device__ __forceinline__ void vectors(int buf) {
     const double c = s.c[lane], end = s.c[kC - 1];
     const float into = decay_of(c), rk = s.rk[lane];
     s.va[buf][lane] = into * rk;
@@ -489,8 +488,8 @@ struct Prepare {
     if (lane == kC - 1) s.whole[buf] = into;
   }
   // A' (transposed into LDS) for block row W, M^T for block row 3 - W (kept)
-  template <int W, int buf>
-  __device__ __forceinline__ void products() {
+  template <int W>
+  __device__ __forceinline__ void products(int buf) {
     constexpr int V = 3 - W;
     constexpr int kMost = (W > V ? W : V) + 1;  // block rows of K that either needs
     f32x4 ap[W + 1];
@@ -586,8 +585,8 @@ struct Prepare {
     }
   }
   // X and M of the prepared chunk where the chain reads them
-  template <int W, int buf>
-  __device__ __forceinline__ void publish() {
+  template <int W>
+  __device__ __forceinline__ void publish(int buf) {
     constexpr int V = 3 - W;
     const uint32_t xw = hold(lds_address(&s.x[buf][0][tri_at(16 * W + r) + 8 * g]));
     const uint32_t mv = hold(lds_address(&s.m[buf][0][tri_at(16 * V + r) + 8 * g]));
@@ -606,30 +605,25 @@ struct Prepare {
       for (int pl = 0; pl < 3; ++pl) lds_put(xw + pl * ChunkLds<NT>::kTri + 2 * kpos(16 * j), p[pl]);
     }
   }
-  template <int W, int buf>
-  __device__ __forceinline__ void prepare(int64_t c) {
-    stage<W, buf>(c * kC);
-    load((c + 1) * kC);
-    meet();
-    products<W, buf>();
-    meet();
-    if (W == 3) diagonal();
-    if (W == 1) vectors<buf>();
-    meet();
-    block_row<W>();
-    publish<W, buf>();
-  }
   // Chunk c + 1 beside the chain's chunk c (chunk 0 has nobody to overlap with).
+  // One body for both buffers: the eight waves run five programs, and the
+  // instruction cache holds 64 KB.
   template <int W>
   __device__ __forceinline__ void run(int64_t nc) {
     load(0);
-    for (int64_t c = 0; c < nc; c += 2) {
-      prepare<W, 0>(c);
+    for (int64_t c = 0; c < nc; ++c) {
+      const int buf = static_cast<int>(c & 1);
+      stage<W>(buf, c * kC);
+      load((c + 1) * kC);
+      meet();
+      products<W>(buf);
+      meet();
+      if (W == 3) diagonal();
+      if (W == 1) vectors(buf);
+      meet();
+      block_row<W>();
+      publish<W>(buf);
       __syncthreads();
-      if (c + 1 < nc) {
-        prepare<W, 1>(c + 1);
-        __syncthreads();
-      }
     }
     __syncthreads();  // the chain's last chunk
   }
