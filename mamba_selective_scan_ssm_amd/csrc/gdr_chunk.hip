@@ -111,8 +111,15 @@ __device__ __forceinline__ u32x2 lds_transposed(uint32_t at) {
 // `left` rows from t0 (0 and less: none), of which `tail` elements count in the
 // last.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(const void *base, int left, uint32_t row, uint32_t tail) {
-  const uint32_t bytes = left > 0 ? 2 * (static_cast<uint32_t>(left - 1) * row + tail) : 0;
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, static_cast<int>(bytes), 0x00020000);
+  // the same in all lanes, and said so: a descriptor in vector registers is
+  // loaded from in a loop over its values
+  const uint32_t bytes =
+      __builtin_amdgcn_readfirstlane(left > 0 ? 2 * (static_cast<uint32_t>(left - 1) * row + tail) : 0);
+  const uint64_t at = reinterpret_cast<uint64_t>(base);
+  const uint64_t lo = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(at)));
+  const uint64_t hi = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(at >> 32)));
+  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void *>(hi << 32 | lo), 0, static_cast<int>(bytes),
+                                           0x00020000);
 }
 constexpr uint32_t kNowhere = 0xfffffff0u;  // an offset outside every buffer
 
@@ -435,14 +442,29 @@ struct Prepare {
     ber.bits = __builtin_amdgcn_raw_buffer_load_b16(rows_of(static_cast<const uint16_t *>(a.beta) + gate, left, H, 1),
                                                     static_cast<int>(2 * lane * H), 0, 0);
   }
-  static __device__ __forceinline__ float sum_squares(u32x4 u) {
-    float ss = 0.f;
+  // 1 / norm of the rows of which u holds pieces, rows side by side
+  static __device__ __forceinline__ void norms(const u32x4 (&u)[8], f32x4 *out) {
+    float ss[8];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint32_t w = u[e];
-      ss = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, w), __builtin_bit_cast(bf16x2, w), ss, false);
-    }
-    return row_sum<(kPieces < 16 ? kPieces : 16)>(ss);
+    for (int i = 0; i < 8; ++i) ss[i] = kQkNormEps / kPieces;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t w = u[i][e];
+        ss[i] = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, w), __builtin_bit_cast(bf16x2, w), ss[i], false);
+      }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss[i] += dpp_get<0xB1>(ss[i]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss[i] += dpp_get<0x4E>(ss[i]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss[i] += dpp_get<0x141>(ss[i]);
+    if (kPieces > 8)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss[i] += dpp_get<0x140>(ss[i]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) out[i / 4][i % 4] = __builtin_amdgcn_rsqf(ss[i]);
   }
   // K, Q, the norms, beta and the cumulative decay of the loaded chunk
   template <int W>
@@ -458,7 +480,6 @@ struct Prepare {
     }
     if (tid >= kLoaders) return;
     const int m = tid % kPieces, tq = 4 * (tid / kPieces);
-    f32x4 nk = {1.f, 1.f, 1.f, 1.f}, nq = {1.f, 1.f, 1.f, 1.f};
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -467,15 +488,14 @@ struct Prepare {
         lds_put(at, u32x2{kr[i][2 * u], kr[i][2 * u + 1]});
         lds_put(at + 2 * ChunkLds<NT>::kTile, u32x2{qr[i][2 * u], qr[i][2 * u + 1]});
       }
-    if (a.qk_norm)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        nk[i] = __builtin_amdgcn_rsqf(sum_squares(kr[i]) + kQkNormEps);
-        nq[i] = __builtin_amdgcn_rsqf(sum_squares(qr[i]) + kQkNormEps);
-      }
+    f32x4 n[2] = {f32x4{1.f, 1.f, 1.f, 1.f}, f32x4{1.f, 1.f, 1.f, 1.f}};
+    if (a.qk_norm) {
+      const u32x4 rows[8] = {kr[0], kr[1], kr[2], kr[3], qr[0], qr[1], qr[2], qr[3]};
+      norms(rows, n);
+    }
     if (m == 0) {
-      *reinterpret_cast<f32x4 *>(&s.rk[tq]) = nk;
-      *reinterpret_cast<f32x4 *>(&s.rq[tq]) = nq * a.scale;
+      *reinterpret_cast<f32x4 *>(&s.rk[tq]) = n[0];
+      *reinterpret_cast<f32x4 *>(&s.rq[tq]) = n[1] * a.scale;
     }
   }
   // the chain's vectors
