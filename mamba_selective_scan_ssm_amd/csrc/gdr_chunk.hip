@@ -60,21 +60,22 @@ struct ChunkLds {
   // A'[i][j] at [j][i]; a diagonal block gives way to its inverse, transposed
   __attribute__((aligned(16))) float at[10 * 16 * kAtPitch];
   __attribute__((aligned(16))) float va[2][kC], vb[2][kC], vw[2][kC];
-  __attribute__((aligned(16))) double c[kC];                    // in units of log 2
-  __attribute__((aligned(16))) float rk[kC], rq[kC], beta[kC];
+  __attribute__((aligned(16))) double c[2][kC];                 // in units of log 2
+  __attribute__((aligned(16))) float beta[2][kC], rk[kC], rq[kC];
   float whole[2];
   uint32_t met;
   // byte offsets between the parts
   static constexpr uint32_t kTile = 2 * kC * 16 * NT, kTri = 2 * kTriSize;
 };
 
-// 16-byte piece `ch` (kpos / 8) of token `tok` in a K or Q tile: the pieces of
-// a row are exchanged by the token, so that a piece of 16 rows (an operand), a
-// row of pieces (staging) and 4 x 4 (row, piece) (the transposing read) spread
-// over the banks.
+// 16-byte piece `ch` (kpos / 8) of token `tok` in a K or Q tile.  Eight lanes
+// of an operand read (eight rows, one piece) and sixteen of a transposing one
+// (four rows by four pieces, half of each) share a cycle: the pieces of a row
+// are exchanged by the row so that the former meet 32 banks and the latter as
+// many as their halves allow.
 template <int NT>
 __device__ __forceinline__ int tile_at(int tok, int ch) {
-  const int f = NT == 8 ? (tok % 4) * 4 + tok / 4 % 4 : tok / 2 % 8;
+  const int f = 4 * (tok % 2) + tok / 2 % 4 + (NT == 8 ? 8 * (tok / 8 % 2) : 0);
   return tok * 16 * NT + 8 * (ch ^ f);
 }
 
@@ -383,8 +384,8 @@ struct Prepare {
   static_assert(kLoaders <= 256, "four tokens by one piece per thread");
   uint32_t meetings;
   // LDS addresses: this thread's pieces of K (two halves by four tokens), rows r
-  // of K by block of 32 states, c and rk at r and at 4 g (rq and beta behind rk),
-  // row r, element 4 g of the blocks of A'
+  // of K by block of 32 states, c and beta at r and at 4 g (rk and rq behind
+  // beta), row r, element 4 g of the blocks of A'
   uint32_t lp[4][2], lk[KB], lc1, lc4, lf1, lf4, la;
   uint32_t piece;  // bytes to this thread's piece of K and Q, first token
   u32x4 kr[4], qr[4];
@@ -399,17 +400,17 @@ struct Prepare {
       for (int u = 0; u < 2; ++u) lp[i][u] = hold(lds_address(&s.k[0][tile_at<NT>(tq + i, pos / 8 + u) + pos % 8]));
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb) lk[kb] = hold(lds_address(&s.k[0][tile_at<NT>(r, 4 * kb + g)]));
-    lc1 = hold(lds_address(&s.c[r]));
-    lc4 = hold(lds_address(&s.c[4 * g]));
-    lf1 = hold(lds_address(&s.rk[r]));
-    lf4 = hold(lds_address(&s.rk[4 * g]));
+    lc1 = hold(lds_address(&s.c[0][r]));
+    lc4 = hold(lds_address(&s.c[0][4 * g]));
+    lf1 = hold(lds_address(&s.beta[0][r]));
+    lf4 = hold(lds_address(&s.beta[0][4 * g]));
     la = hold(lds_address(&s.at[r * kAtPitch + 4 * g]));
     const int m = tid % kPieces;
     piece = tid < kLoaders && 8 * m < a.N ? 2 * (tq * static_cast<uint32_t>(a.G * a.N) + 8 * m) : kNowhere;
   }
   __device__ __forceinline__ double c1(int t) const { return lds_get<double>(lc1 + 8 * t); }
   __device__ __forceinline__ double c4(int t) const { return lds_get<double>(lc4 + 8 * t); }
-  enum { kRk, kRq, kBeta };  // behind each other
+  enum { kBeta0, kBeta1, kRk, kRq };  // behind each other
   __device__ __forceinline__ float f1(int which, int t) const { return lds_get<float>(lf1 + 4 * (which * kC + t)); }
   __device__ __forceinline__ f32x4 f4(int which, int t) const { return lds_get<f32x4>(lf4 + 4 * (which * kC + t)); }
   static constexpr uint32_t block(int j, int k) { return 4 * at_block(j, k); }
@@ -426,8 +427,8 @@ struct Prepare {
 
   __device__ __forceinline__ void load(int64_t t0) {
     const int left = static_cast<int>(a.L - t0 < kC ? a.L - t0 : kC);
-    const uint32_t row = static_cast<uint32_t>(a.G * a.N), H = static_cast<uint32_t>(a.H);
-    const int64_t base = ((b * a.L + t0) * a.G + grp) * a.N, gate = (b * a.L + t0) * a.H + h;
+    const uint32_t row = static_cast<uint32_t>(a.G * a.N);
+    const int64_t base = ((b * a.L + t0) * a.G + grp) * a.N;
     const __amdgpu_buffer_rsrc_t rk = rows_of(static_cast<const uint16_t *>(a.k) + base, left, row, a.N);
     const __amdgpu_buffer_rsrc_t rq = rows_of(static_cast<const uint16_t *>(a.q) + base, left, row, a.N);
 #pragma unroll
@@ -437,10 +438,26 @@ struct Prepare {
       qr[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rq, static_cast<int>(piece),
                                                                               static_cast<int>(2 * i * row), 0));
     }
+  }
+  __device__ __forceinline__ void load_gates(int64_t t0) {
+    const int left = static_cast<int>(a.L - t0 < kC ? a.L - t0 : kC);
+    const uint32_t H = static_cast<uint32_t>(a.H);
+    const int64_t gate = (b * a.L + t0) * a.H + h;
     dtr.bits = __builtin_amdgcn_raw_buffer_load_b16(rows_of(static_cast<const uint16_t *>(a.dt) + gate, left, H, 1),
                                                     static_cast<int>(2 * lane * H), 0, 0);
     ber.bits = __builtin_amdgcn_raw_buffer_load_b16(rows_of(static_cast<const uint16_t *>(a.beta) + gate, left, H, 1),
                                                     static_cast<int>(2 * lane * H), 0, 0);
+  }
+  // beta and the cumulative decay of the chunk at t0, by one wave; the next one's on their way
+  __device__ __forceinline__ void gates(int buf, int64_t t0) {
+    const bool in = t0 + lane < a.L;  // behind the last token nothing decays and nothing is written
+    s.beta[buf][lane] = to_f32(ber);
+    // a step below -2000 leaves nothing of the state, however it is summed; held
+    // there, the differences of later tokens keep their bits
+    float lg = in ? step_size(to_f32(dtr), bias, a.dt_softplus) * A2 : 0.f;
+    if (lg < -2000.f) lg = -2000.f;
+    s.c[buf][lane] = wave_scan(lg);
+    load_gates(t0 + kC);
   }
   // 1 / norm of the rows of which u holds pieces, rows side by side
   static __device__ __forceinline__ void norms(const u32x4 (&u)[8], f32x4 *out) {
@@ -466,18 +483,8 @@ struct Prepare {
 #pragma unroll
     for (int i = 0; i < 8; ++i) out[i / 4][i % 4] = __builtin_amdgcn_rsqf(ss[i]);
   }
-  // K, Q, the norms, beta and the cumulative decay of the loaded chunk
-  template <int W>
-  __device__ __forceinline__ void stage(int buf, int64_t t0) {
-    if (W == 0) {
-      const bool in = t0 + lane < a.L;  // behind the last token nothing decays and nothing is written
-      s.beta[lane] = to_f32(ber);
-      // a step below -2000 leaves nothing of the state, however it is summed;
-      // held there, the differences of later tokens keep their bits
-      float lg = in ? step_size(to_f32(dtr), bias, a.dt_softplus) * A2 : 0.f;
-      if (lg < -2000.f) lg = -2000.f;
-      s.c[lane] = wave_scan(lg);
-    }
+  // K, Q and their norms of the loaded chunk
+  __device__ __forceinline__ void stage(int buf) {
     if (tid >= kLoaders) return;
     const int m = tid % kPieces, tq = 4 * (tid / kPieces);
 #pragma unroll
@@ -500,11 +507,11 @@ struct Prepare {
   }
   // the chain's vectors
   __device__ __forceinline__ void vectors(int buf) {
-    const double c = s.c[lane], end = s.c[kC - 1];
+    const double c = s.c[buf][lane], end = s.c[buf][kC - 1];
     const float into = decay_of(c), rk = s.rk[lane];
     s.va[buf][lane] = into * rk;
     s.vb[buf][lane] = into * s.rq[lane];
-    s.vw[buf][lane] = decay_of(end - c) * rk * s.beta[lane];
+    s.vw[buf][lane] = decay_of(end - c) * rk * s.beta[buf][lane];
     if (lane == kC - 1) s.whole[buf] = into;
   }
   // A' (transposed into LDS) for block row W, M^T for block row 3 - W (kept)
@@ -531,12 +538,12 @@ struct Prepare {
     }
     double ci[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) ci[e] = c4(16 * W + e);
+    for (int e = 0; e < 4; ++e) ci[e] = c4(buf * kC + 16 * W + e);
     const f32x4 si = f4(kRk, 16 * W);
 #pragma unroll
     for (int jt = 0; jt <= W; ++jt) {
-      const double cj = c1(16 * jt);
-      const float sj = f1(kRk, 16 * jt) * f1(kBeta, 16 * jt);
+      const double cj = c1(buf * kC + 16 * jt);
+      const float sj = f1(kRk, 16 * jt) * f1(kBeta0 + buf, 16 * jt);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float f = ap[jt][e] * (si[e] * sj) * decay_of(ci[e] - cj);
@@ -544,14 +551,14 @@ struct Prepare {
       }
       lds_put(la + block(jt, W), ap[jt]);
     }
-    const double cv = c1(16 * V);
+    const double cv = c1(buf * kC + 16 * V);
     const float sv = f1(kRq, 16 * V);
 #pragma unroll
     for (int jt = 0; jt <= V; ++jt) {
-      const f32x4 sj = f4(kRk, 16 * jt) * f4(kBeta, 16 * jt);
+      const f32x4 sj = f4(kRk, 16 * jt) * f4(kBeta0 + buf, 16 * jt);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float f = M[jt][e] * (sv * sj[e]) * decay_of(cv - c4(16 * jt + e));
+        const float f = M[jt][e] * (sv * sj[e]) * decay_of(cv - c4(buf * kC + 16 * jt + e));
         M[jt][e] = jt < V || 4 * g + e <= r ? f : 0.f;
       }
     }
@@ -631,18 +638,24 @@ struct Prepare {
   template <int W>
   __device__ __forceinline__ void run(int64_t nc) {
     load(0);
+    if (W == 0) {
+      load_gates(0);
+      gates(0, 0);
+    }
     for (int64_t c = 0; c < nc; ++c) {
       const int buf = static_cast<int>(c & 1);
-      stage<W>(buf, c * kC);
-      load((c + 1) * kC);
+      stage(buf);
       meet();
       products<W>(buf);
       meet();
-      if (W == 3) diagonal();
-      if (W == 1) vectors(buf);
+      if (W == 1) diagonal();
+      if (W == 2) vectors(buf);
+      if (W == 0) gates(buf ^ 1, (c + 1) * kC);
+      if (W != 1) load((c + 1) * kC);
       meet();
       block_row<W>();
       publish<W>(buf);
+      if (W == 1) load((c + 1) * kC);
       __syncthreads();
     }
     __syncthreads();  // the chain's last chunk
@@ -680,6 +693,8 @@ __global__ __launch_bounds__(kThreads) void gdr_chunk_kernel(GdrArgs a, int64_t 
   __syncthreads();
 
   if (wave >= 4) {
+    __builtin_amdgcn_s_setprio(3);  // the chain waits for them rather than they for it
+
     Prepare<NT> w{a, s, MinusOne(), static_cast<int>(threadIdx.x) - 256, lane, r, g, b, h, grp,
                   a.A[h] * kLog2e, a.dt_bias ? a.dt_bias[h] : 0.f, 0u, {}, {}, 0, 0, 0, 0, 0, 0, {}, {}, {}, {}, {}, {}};
     w.place();
