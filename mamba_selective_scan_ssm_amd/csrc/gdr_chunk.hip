@@ -171,7 +171,8 @@ struct Chain {
   // for the transposing reads, rows r of X and M, element 4 g of the vectors
   uint32_t lk[KB], lt[KB], lx[2], lm[2], lv;
   f32x4 S[NT];
-  uint16_t vr[16];
+  uint16_t vr[16];  // v of the next chunk, on its way
+  float vf[16];     // and of this one
 
   __device__ __forceinline__ void place() {
 #pragma unroll
@@ -209,6 +210,16 @@ struct Chain {
 #pragma unroll
     for (int i = 0; i < 16; ++i)
       vr[i] = __builtin_amdgcn_raw_buffer_load_b16(rv, static_cast<int>(at[i % 4]), static_cast<int>(i / 4 * rows16), 0);
+  }
+
+  // Waits for the loads, before anything that is stored after them has to be
+  // waited for too.
+  __device__ __forceinline__ void take_v() {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      vf[i] = __uint_as_float(static_cast<uint32_t>(vr[i]) << 16);
+      asm volatile("" : "+v"(vf[i]));
+    }
   }
 
   // One chunk: y and the state behind it.
@@ -250,7 +261,7 @@ struct Chain {
       const f32x4 av = vec<buf>(0, rt);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        R[rt][e] = fmaf(-av[e], R[rt][e], __uint_as_float(static_cast<uint32_t>(vr[4 * rt + e]) << 16));
+        R[rt][e] = fmaf(-av[e], R[rt][e], vf[4 * rt + e]);
         test = fmaf(R[rt][e], 0.f, test);
       }
     }
@@ -359,6 +370,8 @@ struct Chain {
         for (int e = 0; e < 4; ++e)
           if (bad < kC) S[nt][e] = __builtin_nanf("");
     }
+    take_v();
+    __builtin_amdgcn_sched_barrier(0);
     const __amdgpu_buffer_rsrc_t ry = rows_of(y + t0 * row, left, row, width);
 #pragma unroll
     for (int i = 0; i < 16; ++i)
@@ -710,7 +723,7 @@ __global__ __launch_bounds__(kThreads) void gdr_chunk_kernel(GdrArgs a, int64_t 
   const bool live = p0 + 16 * wave < a.P, col = p < a.P;  // some column, this lane's column
   const int64_t head = (b * a.L * a.H + h) * a.P;
   Chain<NT> w{a, s, MinusOne(), r, g, static_cast<const uint16_t *>(a.v) + head, static_cast<bf16_t *>(a.y) + head,
-              row, static_cast<uint32_t>(a.P), 32 * row, {}, {}, {}, {}, {}, 0, {}, {}};
+              row, static_cast<uint32_t>(a.P), 32 * row, {}, {}, {}, {}, {}, 0, {}, {}, {}};
   w.place();
 #pragma unroll
   for (int e = 0; e < 4; ++e) w.at[e] = col ? 2 * ((4 * g + e) * row + static_cast<uint32_t>(p)) : kNowhere;
@@ -720,7 +733,10 @@ __global__ __launch_bounds__(kThreads) void gdr_chunk_kernel(GdrArgs a, int64_t 
     if (a.h0 != nullptr && col && 16 * nt + 4 * g < a.N)
       w.S[nt] = *reinterpret_cast<const f32x4 *>(a.h0 + ((b * a.H + h) * a.P + p) * a.N + 16 * nt + 4 * g);
   }
-  if (live) w.load_v(0, static_cast<int>(a.L < kC ? a.L : kC));
+  if (live) {
+    w.load_v(0, static_cast<int>(a.L < kC ? a.L : kC));
+    w.take_v();
+  }
   __syncthreads();  // the preparation of chunk 0
   for (int64_t c = 0; c < nc; c += 2) {
     if (live) w.template step<0>(c * kC);
