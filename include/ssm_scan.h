@@ -508,8 +508,11 @@ ssm_status ssm_gdr_bwd(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G, in
                        float *dh0, float *d_dt_bias, void *workspace, size_t workspace_bytes,
                        const ssm_delta_opts *dopts, void *stream);
 
+/* Device workspace of ssm_gdr_bwd (bytes).  aligned == 1: q, k, h0, dy, dh_final
+ * and dh0 (those given) are 16-byte aligned, as the matrix-core path needs; 0:
+ * some are not, and the token path runs, whose workspace is larger. */
 size_t ssm_gdr_bwd_workspace_size(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G,
-                                  int64_t N, ssm_dtype dt);
+                                  int64_t N, ssm_dtype dt, int32_t aligned);
 
 /*
  * ssm_group_norm_fwd -- group norm over channels-last x (S, T, D) with an

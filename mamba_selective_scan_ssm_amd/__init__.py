@@ -102,7 +102,7 @@ def lib():
         L.ssm_gdr_decode_steps.restype = ctypes.c_int
         L.ssm_gdr_bwd.argtypes = [i64] * 6 + [ctypes.c_int] + [vp] * 9 + [f32, i32] + [vp] * 8 + [vp, sz, vp, vp]
         L.ssm_gdr_bwd.restype = ctypes.c_int
-        L.ssm_gdr_bwd_workspace_size.argtypes = [i64] * 6 + [ctypes.c_int]
+        L.ssm_gdr_bwd_workspace_size.argtypes = [i64] * 6 + [ctypes.c_int, i32]
         L.ssm_gdr_bwd_workspace_size.restype = sz
         L.ssm_group_norm_fwd.argtypes = ([i64] * 4 + [ctypes.c_int] + [vp] * 4 + [f32, i32, i32, i32] +
                                          [vp] * 3 + [vp, sz, vp])
@@ -537,8 +537,9 @@ def gdr_fwd_workspace_size(B, L, H, P, G, N, dtype=torch.bfloat16) -> int:
     return int(lib().ssm_gdr_fwd_workspace_size(B, L, H, P, G, N, _code_of(dtype)))
 
 
-def gdr_bwd_workspace_size(B, L, H, P, G, N, dtype=torch.bfloat16) -> int:
-    return int(lib().ssm_gdr_bwd_workspace_size(B, L, H, P, G, N, _code_of(dtype)))
+def gdr_bwd_workspace_size(B, L, H, P, G, N, dtype=torch.bfloat16, aligned=True) -> int:
+    """aligned: q, k, h0, dy, dh_final and dh0 are (those given) 16-byte aligned."""
+    return int(lib().ssm_gdr_bwd_workspace_size(B, L, H, P, G, N, _code_of(dtype), 1 if aligned else 0))
 
 
 def gdr_decode_steps(state_pool, q, k, v, dt, A, beta, *, slots=None, scale=None, qk_norm=False, y=None,
@@ -582,7 +583,8 @@ def gdr_bwd(q, k, v, dt, A, beta, h0=None, dy=None, dh_final=None, *, scale=None
            "dA": torch.empty((H,), dtype=torch.float32, device=dev),
            "dh0": torch.empty((B, H, P, N), dtype=torch.float32, device=dev) if want_dh0 else None,
            "dbias": torch.empty((H,), dtype=torch.float32, device=dev) if want_dbias else None}
-    workspace, ws_len = _workspace(workspace, gdr_bwd_workspace_size(*sizes, typ), dev)
+    aligned = all(t is None or t.data_ptr() % 16 == 0 for t in (q, k, h0, dy, dh_final, out["dh0"]))
+    workspace, ws_len = _workspace(workspace, gdr_bwd_workspace_size(*sizes, typ, aligned), dev)
     _gpu_call(dev, "ssm_gdr_bwd", *sizes, code, _ptr(q), _ptr(k), _ptr(v), _ptr(dt), _ptr(A), _ptr(beta), _ptr(h0),
               _ptr(dy), _ptr(dh_final), _scale(scale, N), int(bool(qk_norm)), _ptr(out["dq"]), _ptr(out["dk"]),
               _ptr(out["dv"]), _ptr(out["ddt"]), _ptr(out["dbeta"]), _ptr(out["dA"]), _ptr(out["dh0"]),

@@ -12,7 +12,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libssmscan.so")
 ARCH = "gfx950"
 SOURCES = ["capi.cpp", "scan_fwd.hip", "state_update.hip", "ssd.hip", "ssd_seq.hip", "conv1d.hip", "scan_bwd.hip", "scratch.hip",
-           "capi_mixers.cpp", "gdr_seq.hip", "gdr_chunk.hip", "gdr_bwd.hip", "group_norm.hip"]
+           "capi_mixers.cpp", "gdr_seq.hip", "gdr_chunk.hip", "gdr_bwd.hip", "gdr_bwd_chunk.hip", "group_norm.hip"]
 # Packed-FP32 VALU forms are disabled for all device code.
 FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-Wall", "-Wno-unused-function",
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]

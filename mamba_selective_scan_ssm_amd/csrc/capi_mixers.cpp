@@ -121,10 +121,22 @@ ssm_status ssm_gdr_decode_steps(int64_t S, int64_t T, int64_t H, int64_t P, int6
   return hip_status(ssm::launch_gdr_step(a, static_cast<hipStream_t>(stream)));
 }
 
-size_t ssm_gdr_bwd_workspace_size(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G, int64_t N, ssm_dtype dt) {
+// Whether sizes and type go by chunks, where the tensors are aligned too.
+static bool gdr_chunk_sizes(int64_t L, int64_t H, int64_t P, int64_t G, int64_t N, ssm_dtype dt) {
+  ssm::GdrArgs a{};
+  a.L = L; a.H = H; a.P = P; a.G = G; a.N = N;
+  a.dt_type = dt == SSM_BF16 ? DType::BF16 : DType::F32;
+  return ssm::gdr_chunk_applies(a);
+}
+
+size_t ssm_gdr_bwd_workspace_size(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G, int64_t N, ssm_dtype dt,
+                                  int32_t aligned) {
   GdrSizes z;
   if (gdr_sizes(B, L, H, P, G, N, dt, 0, nullptr, &z) != SSM_OK || P < 1 || H < 1) return 0;
-  return static_cast<size_t>(ssm::gdr_bwd_seq_ws_floats(B, L, H, P, G, N)) * 4;
+  if (aligned != 0 && aligned != 1) return 0;
+  const bool chunks = aligned == 1 && gdr_chunk_sizes(L, H, P, G, N, dt);
+  return static_cast<size_t>(chunks ? ssm::gdr_bwd_chunk_ws_floats(B, L, H, P, G, N)
+                                    : ssm::gdr_bwd_seq_ws_floats(B, L, H, P, G, N)) * 4;
 }
 
 ssm_status ssm_gdr_bwd(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G, int64_t N, ssm_dtype dt, const void *q,
@@ -144,7 +156,14 @@ ssm_status ssm_gdr_bwd(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G, in
   const Range ins[] = {{q, z.nQ * es},     {k, z.nQ * es},         {v, z.nV * es}, {dt_in, z.nT * es},
                        {A, H * 4},         {beta, z.nT * es},      {h0, z.nS * 4}, {dy, z.nV * es},
                        {dh_final, z.nS * 4}, {dbias_of(dopts), H * 4}};
-  const int64_t need = static_cast<int64_t>(ssm_gdr_bwd_workspace_size(B, L, H, P, G, N, dt));
+  ssm::GdrBwdArgs a{};
+  a.f = gdr_args(B, L, H, P, G, N, dt, q, k, v, dt_in, A, beta, h0, scale, qk_norm, dopts);
+  a.dy = dy; a.dh_final = dh_final;
+  a.dq = dq; a.dk = dk; a.dv = dv; a.ddt = ddt; a.dbeta = dbeta;
+  a.dA = dA; a.dbias = d_dt_bias; a.dh0 = dh0;
+  a.ws = static_cast<float *>(workspace);
+  const bool chunks = ssm::gdr_bwd_chunk_applies(a);
+  const int64_t need = static_cast<int64_t>(ssm_gdr_bwd_workspace_size(B, L, H, P, G, N, dt, chunks ? 1 : 0));
   if (need > 0 && (!workspace || !aligned16(workspace) || static_cast<int64_t>(workspace_bytes) < need))
     return SSM_ERR_WORKSPACE;
   const Range outs[] = {{dq, z.nQ * es},    {dk, z.nQ * es}, {dv, z.nV * es},  {ddt, z.nT * es},
@@ -153,15 +172,9 @@ ssm_status ssm_gdr_bwd(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G, in
   for (const Range &r : outs)
     if (overlaps_any(r, ins)) return SSM_ERR_INVALID_ARG;
   if (any_pair(outs, sizeof(outs) / sizeof(outs[0]))) return SSM_ERR_INVALID_ARG;
-  ssm::GdrBwdArgs a{};
-  a.f = gdr_args(B, L, H, P, G, N, dt, q, k, v, dt_in, A, beta, h0, scale, qk_norm, dopts);
-  a.dy = dy; a.dh_final = dh_final;
-  a.dq = dq; a.dk = dk; a.dv = dv; a.ddt = ddt; a.dbeta = dbeta;
-  a.dA = dA; a.dbias = d_dt_bias; a.dh0 = dh0;
-  a.ws = static_cast<float *>(workspace);
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (B == 0) return hip_status(ssm::launch_gdr_reduce(a, 0, nullptr, nullptr, nullptr, nullptr, s));
-  return hip_status(ssm::launch_gdr_bwd_seq(a, s));
+  return hip_status(chunks ? ssm::launch_gdr_bwd_chunk(a, s) : ssm::launch_gdr_bwd_seq(a, s));
 }
 
 // ---------------------------------------------------------------- group norm

@@ -49,6 +49,27 @@ constexpr int64_t kGdrChunkMinL = 32;
 bool gdr_chunk_applies(const GdrArgs &a);
 hipError_t launch_gdr_chunk(const GdrArgs &a, hipStream_t s);
 
+// What the chunked backward keeps of each (sequence, head, chunk), item
+// (b H + h) ceil(L / 64) + chunk:
+struct GdrSaved {
+  float *S;    // (items, P, N): the state entering the chunk
+  float *dS;   // (items, P, N): the gradient of the state leaving it
+  float *E;    // (items, 64, P): the corrected values
+  float *W;    // (items, 64, P): the gradient of v, before its rounding
+  float *XM;   // (items, 20, 256): tiles of X, then of M, as the lanes hold them
+  float *vec;  // (items, kGdrVec): a, b, w, 1 / |k|, 1 / |q|, and c in 64 bits
+};
+constexpr int64_t kGdrVec = 5 * 64 + 2 * 64;
+// The prefill's chunks, kept (S, E, XM and vec) in place of y and h_final.
+hipError_t launch_gdr_chunk_save(const GdrArgs &a, const GdrSaved &keep, hipStream_t s);
+
+// Gradients by chunks (gdr_bwd_chunk.hip): where gdr_chunk_applies, and dy,
+// dh_final, dh0 and the workspace 16-byte aligned.
+struct GdrBwdArgs;
+bool gdr_bwd_chunk_applies(const GdrBwdArgs &a);
+int64_t gdr_bwd_chunk_ws_floats(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G, int64_t N);
+hipError_t launch_gdr_bwd_chunk(const GdrBwdArgs &a, hipStream_t s);
+
 struct GdrBwdArgs {
   GdrArgs f;                  // the forward's inputs (y, h_final unused)
   const void *dy;             // (B, L, H, P)
@@ -70,6 +91,8 @@ hipError_t launch_gdr_bwd_seq(const GdrBwdArgs &a, hipStream_t s);
 // of the normalised q and k; sc_part: (2, tiles, B, L, H), the gradients of
 // beta and of the log decay; red: gdr_reduce_ws_floats floats.
 int64_t gdr_reduce_ws_floats(int64_t B, int64_t L, int64_t H);
+// the last of them alone: dA and dbias from nblk partial sums (2, H) each
+hipError_t launch_gdr_reduce_params(const GdrBwdArgs &a, int64_t nblk, const float *red, hipStream_t s);
 hipError_t launch_gdr_reduce(const GdrBwdArgs &a, int64_t tiles, const float *dq_part, const float *dk_part,
                              const float *sc_part, float *red, hipStream_t s);
 

@@ -370,7 +370,10 @@ hipError_t launch_gdr_reduce(const GdrBwdArgs &a, int64_t tiles, const float *dq
       gdr_reduce_gates_kernel<float><<<gg, kThreads, 0, s>>>(a, tiles, sc_part, red);
     }
   }
-  gdr_reduce_params_kernel<<<static_cast<unsigned>(f.H), 64, 0, s>>>(a, nblk, red);
+  return launch_gdr_reduce_params(a, nblk, red, s);
+}
+hipError_t launch_gdr_reduce_params(const GdrBwdArgs &a, int64_t nblk, const float *red, hipStream_t s) {
+  gdr_reduce_params_kernel<<<static_cast<unsigned>(a.f.H), 64, 0, s>>>(a, nblk, red);
   return hipGetLastError();
 }
 

@@ -37,15 +37,9 @@
 namespace ssm {
 namespace {
 
-constexpr int kC = 64;          // tokens per chunk
-constexpr int kCols = 64;       // columns per workgroup
 constexpr int kThreads = 512;
 constexpr int kAtPitch = 20;    // floats per row of a 16 x 16 block
 
-// X and M, [i][j] by kpos(j): rows 0..31 meet 32 tokens, rows 32..63 all 64;
-// 16 bytes of padding put 16 rows on different banks.
-constexpr int kTriSize = 32 * 40 + 32 * 72;
-__device__ __forceinline__ constexpr int tri_at(int i) { return i < 32 ? i * 40 : 32 * 40 + (i - 32) * 72; }
 // Block (j, k) of the transposed A', k >= j.
 __device__ __forceinline__ constexpr int at_block(int j, int k) {
   return (j * 4 - j * (j - 1) / 2 + k - j) * 16 * kAtPitch;
@@ -68,96 +62,14 @@ struct ChunkLds {
   static constexpr uint32_t kTile = 2 * kC * 16 * NT, kTri = 2 * kTriSize;
 };
 
-// 16-byte piece `ch` (kpos / 8) of token `tok` in a K or Q tile.  Eight lanes
-// of an operand read (eight rows, one piece) and sixteen of a transposing one
-// (four rows by four pieces, half of each) share a cycle: the pieces of a row
-// are exchanged by the row so that the former meet 32 banks and the latter as
-// many as their halves allow.
-template <int NT>
-__device__ __forceinline__ int tile_at(int tok, int ch) {
-  const int f = 4 * (tok % 2) + tok / 2 % 4 + (NT == 8 ? 8 * (tok / 8 % 2) : 0);
-  return tok * 16 * NT + 8 * (ch ^ f);
-}
-
-// LDS by address.  A lane keeps the few addresses it reads around (`hold` hides
-// how they were formed, or the compiler keeps one per read) and the rest is in
-// the instructions' offsets, 16 bits each.
-typedef __attribute__((address_space(3))) char lds_char;
-__device__ __forceinline__ uint32_t lds_address(const void *p) {
-  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((const lds_char *)(p)));
-}
-__device__ __forceinline__ uint32_t hold(uint32_t v) {
-  asm volatile("" : "+v"(v));
-  return v;
-}
-template <typename T>
-__device__ __forceinline__ T lds_get(uint32_t at) {
-  return *reinterpret_cast<const __attribute__((address_space(3))) T *>(at);
-}
-template <typename T>
-__device__ __forceinline__ void lds_put(uint32_t at, T v) {
-  *reinterpret_cast<__attribute__((address_space(3))) T *>(at) = v;
-}
-// Four values of 4 rows by 16 columns, transposed on their way out of LDS: lane
-// 16 g + i names the 8 bytes (row i / 4, columns 4 (i % 4) .. + 3) of its group
-// and lane 16 g + r receives column r of the 4 rows.
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-__device__ __forceinline__ u32x2 lds_transposed(uint32_t at) {
-  return __builtin_bit_cast(
-      u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<__attribute__((address_space(3))) s16x4 *>(at)));
-}
-
-// Rows t0 .. of a (.., rows, row elements) tensor of 16-bit values from one
-// element on: reads behind the last row give 0 and writes there are dropped.
-// `left` rows from t0 (0 and less: none), of which `tail` elements count in the
-// last.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(const void *base, int left, uint32_t row, uint32_t tail) {
-  // the same in all lanes, and said so: a descriptor in vector registers is
-  // loaded from in a loop over its values
-  const uint32_t bytes =
-      __builtin_amdgcn_readfirstlane(left > 0 ? 2 * (static_cast<uint32_t>(left - 1) * row + tail) : 0);
-  const uint64_t at = reinterpret_cast<uint64_t>(base);
-  const uint64_t lo = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(at)));
-  const uint64_t hi = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(at >> 32)));
-  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void *>(hi << 32 | lo), 0, static_cast<int>(bytes),
-                                           0x00020000);
-}
-constexpr uint32_t kNowhere = 0xfffffff0u;  // an offset outside every buffer
-
-// exp2 of a difference of two cumulative decays
-__device__ __forceinline__ float decay_of(double d) { return fast_exp2(static_cast<float>(d)); }
-
-// Inclusive sum over the 64 lanes in 64 bits: shifts by 1, 2, 4, 8 within rows
-// of 16 lanes (0 where there is no source), then the rows' ends.
-template <int kCtrl>
-__device__ __forceinline__ double dpp_shift(double v) {
-  const uint64_t u = __builtin_bit_cast(uint64_t, v);
-  const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<uint32_t>(u), kCtrl, 0xf, 0xf, true);
-  const uint32_t hi = __builtin_amdgcn_update_dpp(0, static_cast<uint32_t>(u >> 32), kCtrl, 0xf, 0xf, true);
-  return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
-}
-__device__ __forceinline__ double lane_value(double v, int lane) {
-  const uint64_t u = __builtin_bit_cast(uint64_t, v);
-  const uint32_t lo = __builtin_amdgcn_readlane(static_cast<uint32_t>(u), lane);
-  const uint32_t hi = __builtin_amdgcn_readlane(static_cast<uint32_t>(u >> 32), lane);
-  return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
-}
-__device__ __forceinline__ double wave_scan(double v) {
-  v += dpp_shift<0x111>(v);
-  v += dpp_shift<0x112>(v);
-  v += dpp_shift<0x114>(v);
-  v += dpp_shift<0x118>(v);
-  const double e0 = lane_value(v, 15), e1 = lane_value(v, 31), e2 = lane_value(v, 47);
-  const int row = threadIdx.x % 64 / 16;
-  if (row >= 1) v += row == 1 ? e0 : row == 2 ? e0 + e1 : e0 + e1 + e2;
-  return v;
-}
-
 // ---------------------------------------------------------------- the chain
-template <int NT>
+template <int NT, bool SAVE>
 struct Chain {
   static constexpr int KB = NT / 2;   // blocks of 32 states
   const GdrArgs &a;
+  const GdrSaved &keep;
+  const int64_t item0, p;  // of this head and chunk 0; this lane's column
+  const bool col;          // which is inside P
   ChunkLds<NT> &s;
   const MinusOne minus;
   const int r, g;        // lane = 16 g + r
@@ -222,10 +134,28 @@ struct Chain {
     }
   }
 
+  // A column whose token `bad` is not finite: its rows from there on, and the state.
+  __device__ __forceinline__ void spoil(int bad, f32x4 *rows) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (16 * (i / 4) + 4 * g + i % 4 >= bad) rows[i / 4][i % 4] = __builtin_nanf("");
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (bad < kC) S[nt][e] = __builtin_nanf("");
+  }
+
   // One chunk: y and the state behind it.
   template <int buf>
   __device__ __forceinline__ void step(int64_t t0) {
     const int more = static_cast<int>(a.L - t0 < 2 * kC ? a.L - t0 : 2 * kC), left = more < kC ? more : kC;
+    const int64_t item = item0 + t0 / kC;
+    if (SAVE && col)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+        if (16 * nt + 4 * g < a.N)
+          *reinterpret_cast<f32x4 *>(keep.S + (item * a.P + p) * a.N + 16 * nt + 4 * g) = S[nt];
     // K S0 and Q S0, the next block of the state split while one multiplies
     f32x4 R[4], Y[4];
 #pragma unroll
@@ -239,17 +169,18 @@ struct Chain {
       for (int rt = 0; rt < 4; ++rt) {
         const uint32_t tile = buf * ChunkLds<NT>::kTile + 2 * 16 * rt * 16 * NT;
         ka[rt] = lds_get<u32x4>(lk[kb] + tile);
-        qa[rt] = lds_get<u32x4>(lk[kb] + tile + 2 * ChunkLds<NT>::kTile);
+        if (!SAVE) qa[rt] = lds_get<u32x4>(lk[kb] + tile + 2 * ChunkLds<NT>::kTile);
       }
       if (kb + 1 < KB) split_operand<3>(S[2 * kb + 2], S[2 * kb + 3], sp[(kb + 1) % 2], minus);
 #pragma unroll
       for (int pl = 2; pl >= 0; --pl)
 #pragma unroll
         for (int rt = 0; rt < 4; ++rt) R[rt] = mma(ka[rt], sp[kb % 2][pl], R[rt]);
+      if (!SAVE)
 #pragma unroll
-      for (int pl = 1; pl >= 0; --pl)
+        for (int pl = 1; pl >= 0; --pl)
 #pragma unroll
-        for (int rt = 0; rt < 4; ++rt) Y[rt] = mma(qa[rt], sp[kb % 2][pl], Y[rt]);
+          for (int rt = 0; rt < 4; ++rt) Y[rt] = mma(qa[rt], sp[kb % 2][pl], Y[rt]);
     }
 
     __builtin_amdgcn_sched_barrier(0);
@@ -340,6 +271,17 @@ struct Chain {
     }
 
     __builtin_amdgcn_sched_barrier(0);
+    if (SAVE) {
+      if (__builtin_expect(any_bad, 0)) spoil(bad, E);
+      take_v();
+      __builtin_amdgcn_sched_barrier(0);
+      if (col) {
+        float *ep = keep.E + (item * kC + 4 * g) * a.P + p;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) ep[(16 * (i / 4) + i % 4) * a.P] = E[i / 4][i % 4];
+      }
+      return;
+    }
     // y = b (Q S0) + M E
     u32x4 ep[2][2];
 #pragma unroll
@@ -360,16 +302,7 @@ struct Chain {
 #pragma unroll
           for (int rt = 2 * kb; rt < 4; ++rt) Y[rt] = mma(ma[rt][kb], ep[kb][pl], Y[rt]);
     }
-    if (__builtin_expect(any_bad, 0)) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (16 * (i / 4) + 4 * g + i % 4 >= bad) Y[i / 4][i % 4] = __builtin_nanf("");
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (bad < kC) S[nt][e] = __builtin_nanf("");
-    }
+    if (__builtin_expect(any_bad, 0)) spoil(bad, Y);
     take_v();
     __builtin_amdgcn_sched_barrier(0);
     const __amdgpu_buffer_rsrc_t ry = rows_of(y + t0 * row, left, row, width);
@@ -383,10 +316,13 @@ struct Chain {
 // ------------------------------------------------------------ the preparation
 // Threads 0..255 of four waves; thread (tq, m) holds tokens 4 tq .. + 3 and the
 // 8 values n = 8 m .. + 7 of K and Q (m < 2 NT).
-template <int NT>
+template <int NT, bool SAVE>
 struct Prepare {
   static constexpr int KB = NT / 2;
   const GdrArgs &a;
+  const GdrSaved &keep;
+  const int64_t item0;   // of this head and chunk 0
+  const bool first;      // the first columns of the head: they keep what all have in common
   ChunkLds<NT> &s;
   const MinusOne minus;
   const int tid, lane, r, g;
@@ -515,17 +451,26 @@ struct Prepare {
     }
     if (m == 0) {
       *reinterpret_cast<f32x4 *>(&s.rk[tq]) = n[0];
-      *reinterpret_cast<f32x4 *>(&s.rq[tq]) = n[1] * a.scale;
+      *reinterpret_cast<f32x4 *>(&s.rq[tq]) = n[1];
     }
   }
   // the chain's vectors
-  __device__ __forceinline__ void vectors(int buf) {
+  __device__ __forceinline__ void vectors(int buf, int64_t c0) {
     const double c = s.c[buf][lane], end = s.c[buf][kC - 1];
     const float into = decay_of(c), rk = s.rk[lane];
     s.va[buf][lane] = into * rk;
-    s.vb[buf][lane] = into * s.rq[lane];
+    s.vb[buf][lane] = into * s.rq[lane] * a.scale;
     s.vw[buf][lane] = decay_of(end - c) * rk * s.beta[buf][lane];
     if (lane == kC - 1) s.whole[buf] = into;
+    if (SAVE && first) {
+      float *vp = keep.vec + (item0 + c0) * kGdrVec;
+      vp[lane] = into * rk;
+      vp[kC + lane] = into * s.rq[lane] * a.scale;
+      vp[2 * kC + lane] = decay_of(end - c) * rk * s.beta[buf][lane];
+      vp[3 * kC + lane] = rk;
+      vp[4 * kC + lane] = s.rq[lane];
+      reinterpret_cast<double *>(vp + 5 * kC)[lane] = c;
+    }
   }
   // A' (transposed into LDS) for block row W, M^T for block row 3 - W (kept)
   template <int W>
@@ -565,7 +510,7 @@ struct Prepare {
       lds_put(la + block(jt, W), ap[jt]);
     }
     const double cv = c1(buf * kC + 16 * V);
-    const float sv = f1(kRq, 16 * V);
+    const float sv = f1(kRq, 16 * V) * a.scale;
 #pragma unroll
     for (int jt = 0; jt <= V; ++jt) {
       const f32x4 sj = f4(kRk, 16 * jt) * f4(kBeta0 + buf, 16 * jt);
@@ -662,12 +607,20 @@ struct Prepare {
       products<W>(buf);
       meet();
       if (W == 1) diagonal();
-      if (W == 2) vectors(buf);
+      if (W == 2) vectors(buf, c);
       if (W == 0) gates(buf ^ 1, (c + 1) * kC);
       if (W != 1) load((c + 1) * kC);
       meet();
       block_row<W>();
       publish<W>(buf);
+      if (SAVE && first) {
+        constexpr int V = 3 - W;
+        float *xm = keep.XM + (item0 + c) * 20 * 256 + 4 * lane;
+#pragma unroll
+        for (int j = 0; j <= W; ++j) *reinterpret_cast<f32x4 *>(xm + (W * (W + 1) / 2 + j) * 256) = X[j];
+#pragma unroll
+        for (int j = 0; j <= V; ++j) *reinterpret_cast<f32x4 *>(xm + (10 + V * (V + 1) / 2 + j) * 256) = M[j];
+      }
       if (W == 1) load((c + 1) * kC);
       __syncthreads();
     }
@@ -675,8 +628,8 @@ struct Prepare {
   }
 };
 
-template <int NT>
-__global__ __launch_bounds__(kThreads) void gdr_chunk_kernel(GdrArgs a, int64_t ptiles) {
+template <int NT, bool SAVE>
+__global__ __launch_bounds__(kThreads) void gdr_chunk_kernel(GdrArgs a, GdrSaved keep, int64_t ptiles) {
   __shared__ ChunkLds<NT> s;
   const uint32_t heads = static_cast<uint32_t>(a.H / a.G);  // of a group
   const uint32_t per = heads * static_cast<uint32_t>(ptiles);  // workgroups of a (sequence, group), which share K and Q
@@ -708,7 +661,7 @@ __global__ __launch_bounds__(kThreads) void gdr_chunk_kernel(GdrArgs a, int64_t 
   if (wave >= 4) {
     __builtin_amdgcn_s_setprio(3);  // the chain waits for them rather than they for it
 
-    Prepare<NT> w{a, s, MinusOne(), static_cast<int>(threadIdx.x) - 256, lane, r, g, b, h, grp,
+    Prepare<NT, SAVE> w{a, keep, (b * a.H + h) * nc, p0 == 0, s, MinusOne(), static_cast<int>(threadIdx.x) - 256, lane, r, g, b, h, grp,
                   a.A[h] * kLog2e, a.dt_bias ? a.dt_bias[h] : 0.f, 0u, {}, {}, 0, 0, 0, 0, 0, 0, {}, {}, {}, {}, {}, {}};
     w.place();
     if (wave == 4) w.template run<0>(nc);
@@ -722,7 +675,7 @@ __global__ __launch_bounds__(kThreads) void gdr_chunk_kernel(GdrArgs a, int64_t 
   const uint32_t row = static_cast<uint32_t>(a.H * a.P);
   const bool live = p0 + 16 * wave < a.P, col = p < a.P;  // some column, this lane's column
   const int64_t head = (b * a.L * a.H + h) * a.P;
-  Chain<NT> w{a, s, MinusOne(), r, g, static_cast<const uint16_t *>(a.v) + head, static_cast<bf16_t *>(a.y) + head,
+  Chain<NT, SAVE> w{a, keep, (b * a.H + h) * nc, p, col, s, MinusOne(), r, g, static_cast<const uint16_t *>(a.v) + head, static_cast<bf16_t *>(a.y) + head,
               row, static_cast<uint32_t>(a.P), 32 * row, {}, {}, {}, {}, {}, 0, {}, {}, {}};
   w.place();
 #pragma unroll
@@ -764,12 +717,19 @@ bool gdr_chunk_applies(const GdrArgs &a) {
          a.H * a.P <= (int64_t(1) << 24) && a.G * a.N <= (int64_t(1) << 24);
 }
 
-hipError_t launch_gdr_chunk(const GdrArgs &a, hipStream_t s) {
+namespace {
+template <bool SAVE>
+hipError_t launch(const GdrArgs &a, const GdrSaved &keep, hipStream_t s) {
   const int64_t ptiles = (a.P + kCols - 1) / kCols, per = a.H / a.G * ptiles;
   const unsigned grid = static_cast<unsigned>((a.B * a.G + 7) / 8 * 8 * per);
-  if (a.N <= 64) gdr_chunk_kernel<4><<<grid, kThreads, 0, s>>>(a, ptiles);
-  else gdr_chunk_kernel<8><<<grid, kThreads, 0, s>>>(a, ptiles);
+  if (a.N <= 64) gdr_chunk_kernel<4, SAVE><<<grid, kThreads, 0, s>>>(a, keep, ptiles);
+  else gdr_chunk_kernel<8, SAVE><<<grid, kThreads, 0, s>>>(a, keep, ptiles);
   return hipGetLastError();
+}
+}  // namespace
+hipError_t launch_gdr_chunk(const GdrArgs &a, hipStream_t s) { return launch<false>(a, GdrSaved{}, s); }
+hipError_t launch_gdr_chunk_save(const GdrArgs &a, const GdrSaved &keep, hipStream_t s) {
+  return launch<true>(a, keep, s);
 }
 
 }  // namespace ssm

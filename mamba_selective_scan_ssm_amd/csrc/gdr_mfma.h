@@ -72,4 +72,98 @@ __device__ __forceinline__ void split_operand(f32x4 top, f32x4 bottom, u32x4 *ou
   for (int p = 0; p < NP; ++p) out[p] = u32x4{a[p][0], a[p][1], b[p][0], b[p][1]};
 }
 
+
+// ------------------------------------------------------------ chunks
+constexpr int kC = 64;          // tokens per chunk
+constexpr int kCols = 64;       // columns per workgroup
+
+// X and M, [i][j] by kpos(j): rows 0..31 meet 32 tokens, rows 32..63 all 64;
+// 16 bytes of padding put 16 rows on different banks.
+constexpr int kTriSize = 32 * 40 + 32 * 72;
+__device__ __forceinline__ constexpr int tri_at(int i) { return i < 32 ? i * 40 : 32 * 40 + (i - 32) * 72; }
+// 16-byte piece `ch` (kpos / 8) of token `tok` in a K or Q tile.  Eight lanes
+// of an operand read (eight rows, one piece) and sixteen of a transposing one
+// (four rows by four pieces, half of each) share a cycle: the pieces of a row
+// are exchanged by the row so that the former meet 32 banks and the latter as
+// many as their halves allow.
+template <int NT>
+__device__ __forceinline__ int tile_at(int tok, int ch) {
+  const int f = 4 * (tok % 2) + tok / 2 % 4 + (NT == 8 ? 8 * (tok / 8 % 2) : 0);
+  return tok * 16 * NT + 8 * (ch ^ f);
+}
+
+// LDS by address.  A lane keeps the few addresses it reads around (`hold` hides
+// how they were formed, or the compiler keeps one per read) and the rest is in
+// the instructions' offsets, 16 bits each.
+typedef __attribute__((address_space(3))) char lds_char;
+__device__ __forceinline__ uint32_t lds_address(const void *p) {
+  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((const lds_char *)(p)));
+}
+__device__ __forceinline__ uint32_t hold(uint32_t v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+template <typename T>
+__device__ __forceinline__ T lds_get(uint32_t at) {
+  return *reinterpret_cast<const __attribute__((address_space(3))) T *>(at);
+}
+template <typename T>
+__device__ __forceinline__ void lds_put(uint32_t at, T v) {
+  *reinterpret_cast<__attribute__((address_space(3))) T *>(at) = v;
+}
+// Four values of 4 rows by 16 columns, transposed on their way out of LDS: lane
+// 16 g + i names the 8 bytes (row i / 4, columns 4 (i % 4) .. + 3) of its group
+// and lane 16 g + r receives column r of the 4 rows.
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ u32x2 lds_transposed(uint32_t at) {
+  return __builtin_bit_cast(
+      u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<__attribute__((address_space(3))) s16x4 *>(at)));
+}
+
+// Rows t0 .. of a (.., rows, row elements) tensor of 16-bit values from one
+// element on: reads behind the last row give 0 and writes there are dropped.
+// `left` rows from t0 (0 and less: none), of which `tail` elements count in the
+// last.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(const void *base, int left, uint32_t row, uint32_t tail) {
+  // the same in all lanes, and said so: a descriptor in vector registers is
+  // loaded from in a loop over its values
+  const uint32_t bytes =
+      __builtin_amdgcn_readfirstlane(left > 0 ? 2 * (static_cast<uint32_t>(left - 1) * row + tail) : 0);
+  const uint64_t at = reinterpret_cast<uint64_t>(base);
+  const uint64_t lo = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(at)));
+  const uint64_t hi = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(at >> 32)));
+  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void *>(hi << 32 | lo), 0, static_cast<int>(bytes),
+                                           0x00020000);
+}
+constexpr uint32_t kNowhere = 0xfffffff0u;  // an offset outside every buffer
+
+// exp2 of a difference of two cumulative decays
+__device__ __forceinline__ float decay_of(double d) { return fast_exp2(static_cast<float>(d)); }
+
+// Inclusive sum over the 64 lanes in 64 bits: shifts by 1, 2, 4, 8 within rows
+// of 16 lanes (0 where there is no source), then the rows' ends.
+template <int kCtrl>
+__device__ __forceinline__ double dpp_shift(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<uint32_t>(u), kCtrl, 0xf, 0xf, true);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, static_cast<uint32_t>(u >> 32), kCtrl, 0xf, 0xf, true);
+  return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+}
+__device__ __forceinline__ double lane_value(double v, int lane) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_readlane(static_cast<uint32_t>(u), lane);
+  const uint32_t hi = __builtin_amdgcn_readlane(static_cast<uint32_t>(u >> 32), lane);
+  return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+}
+__device__ __forceinline__ double wave_scan(double v) {
+  v += dpp_shift<0x111>(v);
+  v += dpp_shift<0x112>(v);
+  v += dpp_shift<0x114>(v);
+  v += dpp_shift<0x118>(v);
+  const double e0 = lane_value(v, 15), e1 = lane_value(v, 31), e2 = lane_value(v, 47);
+  const int row = threadIdx.x % 64 / 16;
+  if (row >= 1) v += row == 1 ? e0 : row == 2 ? e0 + e1 : e0 + e1 + e2;
+  return v;
+}
+
 }  // namespace ssm

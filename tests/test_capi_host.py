@@ -432,8 +432,8 @@ def test_gdr_bwd_validation(lib):
     assert b(dq=R[0]) == INVALID                               # output on an input
     assert b(dk=R[9]) == INVALID                               # two outputs on one buffer
     assert b(dv=ws) == INVALID                                 # output on the workspace
-    assert lib.ssm_gdr_bwd_workspace_size(1, 8, 4, 64, 3, 128, BF16) == 0
-    assert lib.ssm_gdr_bwd_workspace_size(1, 8, 4, 64, 2, 128, BF16) > 0
+    assert lib.ssm_gdr_bwd_workspace_size(1, 8, 4, 64, 3, 128, BF16, 1) == 0
+    assert lib.ssm_gdr_bwd_workspace_size(1, 8, 4, 64, 2, 128, BF16, 1) > 0
 
 
 def test_group_norm_validation(lib):

@@ -36,11 +36,18 @@ def bwd(w, qk_norm, **kw):
     return g
 
 
+def by_chunks(w):
+    """Shapes that may take the matrix cores."""
+    return w["q"].dtype == BF16 and w["q"].shape[3] % 8 == 0 and w["q"].shape[3] <= 128
+
+
 def y_slack(w, qk_norm, scale=None):
-    """For shapes that may take the matrix cores."""
-    if w["q"].dtype != BF16 or w["q"].shape[3] % 8 or w["q"].shape[3] > 128:
-        return None
-    return ref.gdr_output_slack(w, qk_norm, scale)
+    return ref.gdr_output_slack(w, qk_norm, scale) if by_chunks(w) else None
+
+
+def grad_slack(w, qk_norm, scale=None):
+    gates = ref.gdr_gate_slack(w, qk_norm, scale) if by_chunks(w) else {}
+    return {**ref.gdr_grad_slack(w, qk_norm, scale), **gates}
 
 
 def check_fwd(w, qk_norm, what, scale=None, steps=0):
@@ -53,7 +60,7 @@ def check_fwd(w, qk_norm, what, scale=None, steps=0):
 def check_bwd(w, qk_norm, what, scale=None, steps=0):
     g = bwd(w, qk_norm, scale=scale)
     r = ref.gdr_grads_of(w, qk_norm, scale)
-    slack = ref.gdr_grad_slack(w, qk_norm, scale)
+    slack = grad_slack(w, qk_norm, scale)
     for n in r:
         ref.close(g["d" + n], r[n], f"{what} d{n}", slack.get(n), steps)
 
@@ -212,9 +219,9 @@ def test_unaligned_tensors(dtype, off):
     g = ssm.gdr_bwd(s["q"], s["k"], s["v"], s["dt"], s["A"], s["beta"], s["h0"], s["dy"], s["dh"], qk_norm=True,
                     dt_bias=s["bias"], dt_softplus=True, want_dbias=True)
     torch.cuda.synchronize()
-    r = ref.gdr_grads_of(w, True)
+    r, slack = ref.gdr_grads_of(w, True), grad_slack(w, True)
     for n in r:
-        ref.close(g["d" + n], r[n], "d" + n)
+        ref.close(g["d" + n], r[n], "d" + n, slack.get(n))
     pool = shift(w["h0"])
     y = ssm.gdr_decode_steps(pool, s["q"], s["k"], s["v"], s["dt"], s["A"], s["beta"], qk_norm=True, dt_bias=s["bias"],
                              dt_softplus=True)
@@ -416,9 +423,9 @@ def test_other_stream():
         ry, rh = ref.gdr_of(w, True)
         ref.close(y, ry, "y", y_slack(w, True))
         ref.close(h, rh, "h")
-        r = ref.gdr_grads_of(w, True)
+        r, slack = ref.gdr_grads_of(w, True), grad_slack(w, True)
         for n in r:
-            ref.close(g["d" + n], r[n], "d" + n)
+            ref.close(g["d" + n], r[n], "d" + n, slack.get(n))
 
 
 def test_nan_stays_in_its_row():
