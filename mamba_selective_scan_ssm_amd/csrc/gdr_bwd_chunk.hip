@@ -418,15 +418,16 @@ constexpr int kPitch = 72;  // uint16 per row of 64
 
 template <int NT>
 struct GradLds {
+  // the small ones first, within the offsets that instructions hold
+  __attribute__((aligned(16))) double c[kC];
+  __attribute__((aligned(16))) float rk[kC], rq[kC], beta[kC], into[kC], out[kC];
+  float rows[2][4][kC];  // per half of N: q^.dq^, k^.r, k^.T, k^.(first term of T)
+  float dot[8];
   __attribute__((aligned(16))) uint16_t k[kC * 16 * NT], q[kC * 16 * NT];
   __attribute__((aligned(16))) uint16_t dy[kC * kPitch];         // [token][p by kpos]
   __attribute__((aligned(16))) uint16_t e[3][kC * kPitch];
   __attribute__((aligned(16))) uint16_t w[3][kC * kPitch];
   __attribute__((aligned(16))) uint16_t st[3][16 * NT * kPitch]; // [n][p by kpos], S0 then dS1
-  __attribute__((aligned(16))) double c[kC];
-  __attribute__((aligned(16))) float rk[kC], rq[kC], beta[kC], into[kC], out[kC];
-  float rows[2][4][kC];  // per half of N: q^.dq^, k^.r, k^.T, k^.(first term of T)
-  float dot[8];
 };
 
 // One workgroup per (sequence, chunk, group): its heads one after the other, the
@@ -479,12 +480,104 @@ __global__ __launch_bounds__(kThreads) void gdr_bwd_grads_kernel(GdrBwdArgs ba, 
 #pragma unroll
   for (int i = 0; i < NH; ++i) GQ[i] = GK[i] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  const uint32_t lt = hold(lds_address(&s.k[0]));
+  // columns 16 nt .. of K (o = 0) or Q (1) over 32 tokens, as an operand
+  uint32_t lt[NH];
+#pragma unroll
+  for (int i = 0; i < NH; ++i)
+    lt[i] = hold(lds_address(&s.k[tile_at<NT>(4 * g + r / 4, 4 * ((NH * half + i) / 2) + r % 4) + 4 * ((NH * half + i) % 2)]));
+  auto columns = [&](int o, int i, int kb) {
+    u32x2 u[2];
+#pragma unroll
+    for (int w = 0; w < 2; ++w)
+      u[w] = lds_transposed(lt[i] + 2 * (o * kC * 16 * NT + (32 * kb + 16 * w) * 16 * NT));
+    return u32x4{u[0][0], u[0][1], u[1][0], u[1][1]};
+  };
   const uint32_t l_row = hold(2 * (r * kPitch + 8 * g));  // row r, slot g of a tile of rows
-  const uint32_t l_dy = hold(lds_address(s.dy) + l_row), l_e = hold(lds_address(s.e[0]) + l_row);
-  const uint32_t l_w = hold(lds_address(s.w[0]) + l_row), l_st = hold(lds_address(s.st[0]) + l_row);
+  const uint32_t l_dy = hold(lds_address(s.dy) + l_row), l_st = hold(lds_address(s.st[0]) + l_row);
   constexpr uint32_t kPart = 2 * kC * kPitch, kStPart = 2 * 16 * NT * kPitch, kTileRows = 2 * 16 * kPitch;
 
+  const uint32_t l_rows = hold(lds_address(&s.dy[tid / 16 * kPitch + kpos(4 * (tid % 16))]));  // E and W behind dY
+  const int ptiles = static_cast<int>((P + kCols - 1) / kCols);
+  const bool four = P % 4 == 0;
+  // What a thread loads of a head's columns p0 .. + 63: two times 4 columns of a
+  // token of E, W and dY, and 4 p by 4 n of a state.  Always a step ahead of
+  // where it is staged.
+  f32x4 ev[2], wv[2], sv[4];
+  u32x2 yv[2];
+  auto load_rows = [&](int64_t h, int p0) {
+    const int64_t item = (b * a.H + h) * nc + c;
+    const uint32_t bytes = static_cast<uint32_t>(4 * kC * P);
+    const __amdgpu_buffer_rsrc_t re = buffer_of(keep.E + item * kC * P, bytes), rw = buffer_of(keep.W + item * kC * P, bytes);
+    const uint32_t row = static_cast<uint32_t>(a.H * P);
+    const __amdgpu_buffer_rsrc_t ry =
+        rows_of(static_cast<const uint16_t *>(ba.dy) + ((b * a.L + t0) * a.H + h) * P, left, row, static_cast<uint32_t>(P));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int tok = (tid + i * kThreads) / 16, p = p0 + 4 * (tid % 16);
+      const uint32_t at = p < P ? 4 * (static_cast<uint32_t>(tok * P) + p) : kNowhere;
+      ev[i] = __builtin_bit_cast(f32x4, buffer_b128(re, at));
+      wv[i] = __builtin_bit_cast(f32x4, buffer_b128(rw, at));
+      const uint32_t yat = p < P ? 2 * (tok * row + p) : kNowhere;
+      if (four) {
+        yv[i] = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(ry, static_cast<int>(yat), 0, 0));
+      } else {
+        uint32_t y[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          y[e] = static_cast<uint16_t>(__builtin_amdgcn_raw_buffer_load_b16(
+              ry, static_cast<int>(p + e < P ? yat + 2 * e : kNowhere), 0, 0));
+        yv[i] = u32x2{y[0] | y[1] << 16, y[2] | y[3] << 16};
+      }
+    }
+  };
+  auto stage_rows = [&](int p0) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int q4 = tid % 16;
+      if (!four)  // the columns behind P belong to the next row
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (p0 + 4 * q4 + e >= P) ev[i][e] = wv[i][e] = 0.f;
+      u32x2 ep[3], wp[3];
+      split4<3>(ev[i], ep, minus);
+      split4<3>(wv[i], wp, minus);
+      const uint32_t to = l_rows + i * 2 * kTileRows;  // 32 tokens on
+      lds_put(to, yv[i]);
+#pragma unroll
+      for (int pl = 0; pl < 3; ++pl) {
+        lds_put(to + (1 + pl) * kPart, ep[pl]);
+        lds_put(to + (4 + pl) * kPart, wp[pl]);
+      }
+    }
+  };
+  const int st_p = 4 * (tid % 16), st_n = 4 * (tid / 16);
+  const uint32_t l_stage = hold(lds_address(&s.st[0][(st_n < 16 * NT ? st_n : 0) * kPitch + kpos(st_p)]));
+  auto load_state = [&](const float *from, int64_t h, int p0) {
+    const int64_t item = (b * a.H + h) * nc + c;
+    const __amdgpu_buffer_rsrc_t rs = buffer_of(from + item * P * N, static_cast<uint32_t>(4 * P * N));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int p = p0 + st_p + e;
+      sv[e] = __builtin_bit_cast(
+          f32x4, buffer_b128(rs, p < P && st_n < N ? 4 * (static_cast<uint32_t>(p * N) + st_n) : kNowhere));
+    }
+  };
+  auto stage_state = [&]() {  // turned to rows of n
+    if (st_n >= 16 * NT) return;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      u32x2 sp[3];
+      split4<3>(f32x4{sv[0][j], sv[1][j], sv[2][j], sv[3][j]}, sp, minus);
+#pragma unroll
+      for (int pl = 0; pl < 3; ++pl)
+        lds_put(l_stage + pl * kStPart + j * 2 * kPitch, sp[pl]);
+    }
+  };
+  // products of two three-part operands, small terms first
+  constexpr int kA[6] = {2, 0, 1, 1, 0, 0}, kB[6] = {0, 2, 1, 0, 1, 0};
+
+  load_rows(grp * heads, 0);
+  load_state(keep.S, grp * heads, 0);
   for (int64_t hh = 0; hh < heads; ++hh) {
     const int64_t h = grp * heads + hh, item = (b * a.H + h) * nc + c;
     __syncthreads();  // the head before
@@ -498,224 +591,215 @@ __global__ __launch_bounds__(kThreads) void gdr_bwd_grads_kernel(GdrBwdArgs ba, 
       s.rq[tid] = vp[4 * kC + tid];
       s.beta[tid] = tid < left ? to_f32(static_cast<const bf16_t *>(a.beta)[(b * a.L + t0 + tid) * a.H + h]) : 0.f;
     }
-    f32x4 DQ[NH], KR[NH], T[NH], PT[4], VT[4], PN[4], VN[4];
+    // what goes through the states
+    f32x4 DQ[NH], KR[NH], T[NH];
 #pragma unroll
     for (int i = 0; i < NH; ++i) DQ[i] = KR[i] = T[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) PT[i] = VT[i] = PN[i] = VN[i] = f32x4{0.f, 0.f, 0.f, 0.f};
     float dot = 0.f;
-
-    for (int64_t p0 = 0; p0 < P; p0 += kCols) {
-      if (p0 > 0) __syncthreads();
-      // dY, E and W, rows of tokens
-      const bool four = P % 4 == 0;
-      for (int i = tid; i < kC * 16; i += kThreads) {
-        const int tok = i / 16, q4 = i % 16, at = tok * kPitch + kpos(4 * q4);
-        const int64_t p = p0 + 4 * q4;
-        f32x4 ev = {0.f, 0.f, 0.f, 0.f}, wv = {0.f, 0.f, 0.f, 0.f};
-        u32x2 dv = {0, 0};
-        const int64_t row = (item * kC + tok) * P + p, yrow = ((b * a.L + t0 + tok) * a.H + h) * P + p;
-        const uint16_t *dyp = static_cast<const uint16_t *>(ba.dy);
-        if (four && p < P) {
-          ev = *reinterpret_cast<const f32x4 *>(keep.E + row);
-          wv = *reinterpret_cast<const f32x4 *>(keep.W + row);
-          if (tok < left) dv = *reinterpret_cast<const u32x2 *>(dyp + yrow);
-        } else if (!four) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (p + e < P) {
-              ev[e] = keep.E[row + e];
-              wv[e] = keep.W[row + e];
-              if (tok < left) dv[e / 2] |= static_cast<uint32_t>(dyp[yrow + e]) << (16 * (e % 2));
-            }
-        }
-        u32x2 ep[3], wp[3];
-        split4<3>(ev, ep, minus);
-        split4<3>(wv, wp, minus);
-        *reinterpret_cast<u32x2 *>(&s.dy[at]) = dv;
-#pragma unroll
-        for (int pl = 0; pl < 3; ++pl) {
-          *reinterpret_cast<u32x2 *>(&s.e[pl][at]) = ep[pl];
-          *reinterpret_cast<u32x2 *>(&s.w[pl][at]) = wp[pl];
-        }
+    for (int pt = 0; pt < ptiles; ++pt) {
+      const int p0 = pt * kCols;
+      if (pt > 0) {
+        __syncthreads();
+        load_rows(h, p0);
+        load_state(keep.S, h, p0);
       }
-      // a state, 4 p by 4 n per step, turned to rows of n
-      auto stage_state = [&](const float *from, bool second) {
-        for (int i = tid; i < 16 * 4 * NT; i += kThreads) {
-          const int pg = i % 16, n = 4 * (i / 16);
-          f32x4 v[4], o[4];
+      stage_rows(p0);
+      stage_state();
+      f32x4 before[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int64_t p = p0 + 4 * pg + e, at = (item * P + p) * N + n;
-            v[e] = o[e] = f32x4{0.f, 0.f, 0.f, 0.f};
-            if (p < P && n < N) {
-              v[e] = *reinterpret_cast<const f32x4 *>(from + at);
-              if (second) o[e] = *reinterpret_cast<const f32x4 *>(keep.S + at);
-            }
-          }
-          if (second)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) dot = fmaf(v[e][j], o[e][j], dot);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            u32x2 sp[3];
-            split4<3>(f32x4{v[0][j], v[1][j], v[2][j], v[3][j]}, sp, minus);
-#pragma unroll
-            for (int pl = 0; pl < 3; ++pl)
-              *reinterpret_cast<u32x2 *>(&s.st[pl][(n + j) * kPitch + kpos(4 * pg)]) = sp[pl];
-          }
-        }
-      };
-      stage_state(keep.S, false);
+      for (int e = 0; e < 4; ++e) before[e] = sv[e];
+      load_state(keep.dS, h, p0);
       __syncthreads();
-      // products of a three-part and a three-part operand, small terms first
-      constexpr int kA[6] = {2, 0, 1, 1, 0, 0}, kB[6] = {0, 2, 1, 0, 1, 0};
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb) {
         const uint32_t mine = own * kTileRows + 64 * kb;
         const u32x4 dyo = lds_get<u32x4>(l_dy + mine);
-        u32x4 eo[3], wo[3];
+        u32x4 wo[3];
 #pragma unroll
-        for (int pl = 0; pl < 3; ++pl) {
-          eo[pl] = lds_get<u32x4>(l_e + pl * kPart + mine);
-          wo[pl] = lds_get<u32x4>(l_w + pl * kPart + mine);
-        }
+        for (int pl = 0; pl < 3; ++pl) wo[pl] = lds_get<u32x4>(l_dy + (4 + pl) * kPart + mine);
 #pragma unroll
         for (int i = 0; i < NH; ++i) {
           u32x4 sb[3];
 #pragma unroll
-          for (int pl = 0; pl < 3; ++pl) sb[pl] = lds_get<u32x4>(l_st + pl * kStPart + (NH * half + i) * kTileRows + 64 * kb);
+          for (int pl = 0; pl < 3; ++pl)
+            sb[pl] = lds_get<u32x4>(l_st + pl * kStPart + (NH * half + i) * kTileRows + 64 * kb);
 #pragma unroll
-          for (int pl = 2; pl >= 0; --pl) DQ[i] = mma(dyo, sb[pl], DQ[i]);
-#pragma unroll
-          for (int k = 0; k < 6; ++k) KR[i] = mma(wo[kA[k]], sb[kB[k]], KR[i]);
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t other = j * kTileRows + 64 * kb;
-          if (j <= own) {  // rows j, columns i of the own tile
-            u32x4 ej[3];
-#pragma unroll
-            for (int pl = 0; pl < 3; ++pl) ej[pl] = lds_get<u32x4>(l_e + pl * kPart + other);
-#pragma unroll
-            for (int pl = 2; pl >= 0; --pl) PT[j] = mma(ej[pl], dyo, PT[j]);
-#pragma unroll
-            for (int k = 0; k < 6; ++k) VT[j] = mma(ej[kA[k]], wo[kB[k]], VT[j]);
-          }
-          if (j >= own) {  // rows i, columns j of the own tile
-            const u32x4 di = lds_get<u32x4>(l_dy + other);
-            u32x4 wi[3];
-#pragma unroll
-            for (int pl = 0; pl < 3; ++pl) wi[pl] = lds_get<u32x4>(l_w + pl * kPart + other);
-#pragma unroll
-            for (int pl = 2; pl >= 0; --pl) PN[j] = mma(di, eo[pl], PN[j]);
-#pragma unroll
-            for (int k = 0; k < 6; ++k) VN[j] = mma(wi[kA[k]], eo[kB[k]], VN[j]);
+          for (int k = 0; k < 6; ++k) {
+            KR[i] = mma(wo[kA[k]], sb[kB[k]], KR[i]);
+            if (k % 2 == 1) DQ[i] = mma(dyo, sb[2 - k / 2], DQ[i]);
           }
         }
       }
       __syncthreads();
-      stage_state(keep.dS, true);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) dot = fmaf(sv[e][j], before[e][j], dot);
+      stage_state();
       __syncthreads();
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb) {
         u32x4 eo[3];
 #pragma unroll
-        for (int pl = 0; pl < 3; ++pl) eo[pl] = lds_get<u32x4>(l_e + pl * kPart + own * kTileRows + 64 * kb);
+        for (int pl = 0; pl < 3; ++pl) eo[pl] = lds_get<u32x4>(l_dy + (1 + pl) * kPart + own * kTileRows + 64 * kb);
 #pragma unroll
         for (int i = 0; i < NH; ++i) {
           u32x4 sb[3];
 #pragma unroll
-          for (int pl = 0; pl < 3; ++pl) sb[pl] = lds_get<u32x4>(l_st + pl * kStPart + (NH * half + i) * kTileRows + 64 * kb);
+          for (int pl = 0; pl < 3; ++pl)
+            sb[pl] = lds_get<u32x4>(l_st + pl * kStPart + (NH * half + i) * kTileRows + 64 * kb);
 #pragma unroll
           for (int k = 0; k < 6; ++k) T[i] = mma(eo[kA[k]], sb[kB[k]], T[i]);
         }
       }
     }
-
-    // factors of the own rows
-    const f32x4 into = *reinterpret_cast<const f32x4 *>(&s.into[16 * own + 4 * g]);
-    const f32x4 out = *reinterpret_cast<const f32x4 *>(&s.out[16 * own + 4 * g]);
+    if (hh + 1 < heads) {
+      if (ptiles == 1) load_rows(h + 1, 0);
+      load_state(keep.S, h + 1, 0);
+    }
+    f32x4 first = {0.f, 0.f, 0.f, 0.f};  // k^ . (first term of T)
+    {
+      const f32x4 into = *reinterpret_cast<const f32x4 *>(&s.into[16 * own + 4 * g]);
+      const f32x4 out = *reinterpret_cast<const f32x4 *>(&s.out[16 * own + 4 * g]);
+#pragma unroll
+      for (int i = 0; i < NH; ++i) {
+        DQ[i] = DQ[i] * (into * a.scale);
+        KR[i] = -(KR[i] * into);
+        T[i] = T[i] * out;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) first[e] = fmaf(k_at(i, e), T[i][e], first[e]);
+      }
+    }
+    // the scores.  Rows j and the own tile's i as columns: such a result is an
+    // operand with the tokens i as rows.
+    const double c_own = s.c[16 * own + r];
+    {
+      f32x4 PT[4], VT[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) PT[i] = VT[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int pt = 0; pt < ptiles; ++pt) {
+        if (ptiles > 1) {
+          __syncthreads();
+          load_rows(h, pt * kCols);
+          stage_rows(pt * kCols);
+          __syncthreads();
+        }
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+          const uint32_t mine = own * kTileRows + 64 * kb;
+          const u32x4 dyo = lds_get<u32x4>(l_dy + mine);
+          u32x4 wo[3];
+#pragma unroll
+          for (int pl = 0; pl < 3; ++pl) wo[pl] = lds_get<u32x4>(l_dy + (4 + pl) * kPart + mine);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (j <= own) {
+              u32x4 ej[3];
+#pragma unroll
+              for (int pl = 0; pl < 3; ++pl) ej[pl] = lds_get<u32x4>(l_dy + (1 + pl) * kPart + j * kTileRows + 64 * kb);
+#pragma unroll
+              for (int k = 0; k < 6; ++k) {
+                VT[j] = mma(ej[kA[k]], wo[kB[k]], VT[j]);
+                if (k % 2 == 1) PT[j] = mma(ej[2 - k / 2], dyo, PT[j]);
+              }
+            }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j <= own) {
+          const f32x4 rkj = *reinterpret_cast<const f32x4 *>(&s.rk[16 * j + 4 * g]);
+          const f32x4 bej = *reinterpret_cast<const f32x4 *>(&s.beta[16 * j + 4 * g]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float f = rkj[e] * bej[e] * decay_of(c_own - s.c[16 * j + 4 * g + e]);
+            PT[j][e] = j < own || 4 * g + e <= r ? PT[j][e] * (f * a.scale) : 0.f;
+            VT[j][e] = j < own || 4 * g + e < r ? -(VT[j][e] * f) : 0.f;
+          }
+        }
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb)
+        if (2 * kb <= own) {
+          u32x4 pt[3], vt[3];
+          split_operand<3>(PT[2 * kb], PT[2 * kb + 1], pt, minus);
+          split_operand<3>(VT[2 * kb], VT[2 * kb + 1], vt, minus);
+#pragma unroll
+          for (int i = 0; i < NH; ++i) {
+            const u32x4 kt = columns(0, i, kb);
+#pragma unroll
+            for (int pl = 2; pl >= 0; --pl) {
+              DQ[i] = mma(pt[pl], kt, DQ[i]);
+              KR[i] = mma(vt[pl], kt, KR[i]);
+            }
+          }
+        }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    // Rows i and the own tile's j as columns.
+    {
+      f32x4 PN[4], VN[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) PN[i] = VN[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int pt = 0; pt < ptiles; ++pt) {
+        if (ptiles > 1) {
+          __syncthreads();
+          load_rows(h, pt * kCols);
+          stage_rows(pt * kCols);
+          __syncthreads();
+        }
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+          u32x4 eo[3];
+#pragma unroll
+          for (int pl = 0; pl < 3; ++pl) eo[pl] = lds_get<u32x4>(l_dy + (1 + pl) * kPart + own * kTileRows + 64 * kb);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (j >= own) {
+              const u32x4 di = lds_get<u32x4>(l_dy + j * kTileRows + 64 * kb);
+              u32x4 wi[3];
+#pragma unroll
+              for (int pl = 0; pl < 3; ++pl) wi[pl] = lds_get<u32x4>(l_dy + (4 + pl) * kPart + j * kTileRows + 64 * kb);
+#pragma unroll
+              for (int k = 0; k < 6; ++k) {
+                VN[j] = mma(wi[kA[k]], eo[kB[k]], VN[j]);
+                if (k % 2 == 1) PN[j] = mma(di, eo[2 - k / 2], PN[j]);
+              }
+            }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j >= own) {
+          const f32x4 rqi = *reinterpret_cast<const f32x4 *>(&s.rq[16 * j + 4 * g]);
+          const f32x4 rki = *reinterpret_cast<const f32x4 *>(&s.rk[16 * j + 4 * g]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float f = decay_of(s.c[16 * j + 4 * g + e] - c_own);
+            PN[j][e] = j > own || 4 * g + e >= r ? PN[j][e] * (f * (a.scale * rqi[e])) : 0.f;
+            VN[j][e] = j > own || 4 * g + e > r ? -(VN[j][e] * (f * rki[e])) : 0.f;
+          }
+        }
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb)
+        if (2 * kb + 1 >= own) {
+          u32x4 pn[3], vn[3];
+          split_operand<3>(PN[2 * kb], PN[2 * kb + 1], pn, minus);
+          split_operand<3>(VN[2 * kb], VN[2 * kb + 1], vn, minus);
+#pragma unroll
+          for (int i = 0; i < NH; ++i) {
+            const u32x4 kt = columns(0, i, kb), qt = columns(1, i, kb);
+#pragma unroll
+            for (int pl = 2; pl >= 0; --pl) {
+              T[i] = mma(vn[pl], kt, T[i]);
+              T[i] = mma(pn[pl], qt, T[i]);
+            }
+          }
+        }
+    }
+    if (ptiles > 1 && hh + 1 < heads) load_rows(h + 1, 0);
     const f32x4 rko = *reinterpret_cast<const f32x4 *>(&s.rk[16 * own + 4 * g]);
     const f32x4 rqo = *reinterpret_cast<const f32x4 *>(&s.rq[16 * own + 4 * g]);
     const f32x4 beo = *reinterpret_cast<const f32x4 *>(&s.beta[16 * own + 4 * g]);
-    f32x4 first = {0.f, 0.f, 0.f, 0.f};  // k^ . (first term of T)
-#pragma unroll
-    for (int i = 0; i < NH; ++i) {
-      DQ[i] = DQ[i] * (into * a.scale);
-      KR[i] = -(KR[i] * into);
-      T[i] = T[i] * out;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) first[e] = fmaf(k_at(i, e), T[i][e], first[e]);
-    }
-    // the scores, scaled; PT and VT have rows j and the own tile's i as columns
-    const double c_own = s.c[16 * own + r];
-    const float rk_own = s.rk[16 * own + r];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (j <= own) {
-        const f32x4 rkj = *reinterpret_cast<const f32x4 *>(&s.rk[16 * j + 4 * g]);
-        const f32x4 bej = *reinterpret_cast<const f32x4 *>(&s.beta[16 * j + 4 * g]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float f = rkj[e] * bej[e] * decay_of(c_own - s.c[16 * j + 4 * g + e]);
-          PT[j][e] = j < own || 4 * g + e <= r ? PT[j][e] * (f * a.scale) : 0.f;
-          VT[j][e] = j < own || 4 * g + e < r ? -(VT[j][e] * f) : 0.f;
-        }
-      }
-      if (j >= own) {
-        const f32x4 rqi = *reinterpret_cast<const f32x4 *>(&s.rq[16 * j + 4 * g]);
-        const f32x4 rki = *reinterpret_cast<const f32x4 *>(&s.rk[16 * j + 4 * g]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float f = decay_of(s.c[16 * j + 4 * g + e] - c_own);
-          PN[j][e] = j > own || 4 * g + e >= r ? PN[j][e] * (f * (a.scale * rqi[e])) : 0.f;
-          VN[j][e] = j > own || 4 * g + e > r ? -(VN[j][e] * (f * rki[e])) : 0.f;
-        }
-      }
-    }
-    (void)rk_own;
-    // result tiles with the own tokens as columns are operands with them as rows
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
-      const bool before = 2 * kb <= own, behind = 2 * kb + 1 >= own;
-      u32x4 pt[3], vt[3], pn[3], vn[3];
-      if (before) {
-        split_operand<3>(PT[2 * kb], PT[2 * kb + 1], pt, minus);
-        split_operand<3>(VT[2 * kb], VT[2 * kb + 1], vt, minus);
-      }
-      if (behind) {
-        split_operand<3>(PN[2 * kb], PN[2 * kb + 1], pn, minus);
-        split_operand<3>(VN[2 * kb], VN[2 * kb + 1], vn, minus);
-      }
-#pragma unroll
-      for (int i = 0; i < NH; ++i) {
-        const int nt = NH * half + i;
-        u32x2 kh[2], qh[2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const uint32_t at = lt + 2 * (tile_at<NT>(4 * g + r / 4, 4 * (nt / 2) + r % 4) +
-                                        (32 * kb + 16 * u) * 16 * NT + 4 * (nt % 2));
-          kh[u] = lds_transposed(at);
-          qh[u] = lds_transposed(at + 2 * kC * 16 * NT);
-        }
-        const u32x4 kt = {kh[0][0], kh[0][1], kh[1][0], kh[1][1]}, qt = {qh[0][0], qh[0][1], qh[1][0], qh[1][1]};
-        if (before)
-#pragma unroll
-          for (int pl = 2; pl >= 0; --pl) {
-            DQ[i] = mma(pt[pl], kt, DQ[i]);
-            KR[i] = mma(vt[pl], kt, KR[i]);
-          }
-        if (behind)
-#pragma unroll
-          for (int pl = 2; pl >= 0; --pl) {
-            T[i] = mma(pn[pl], qt, T[i]);
-            T[i] = mma(vn[pl], kt, T[i]);
-          }
-      }
-    }
     // sums over n of the own rows
     f32x4 qdq = {0.f, 0.f, 0.f, 0.f}, kkr = qdq, kt_ = qdq;
 #pragma unroll
