@@ -15,10 +15,16 @@
 //      T_j   = exp(c_C - c_j) dS1^T E_j + sum_{i>=j} scale D_ij P_ij q^_i
 //              - sum_{i>j} D_ij V_ij k^_i                                 (k written)
 //      dk^_j = r_j + beta_j T_j,  dbeta_j = k^_j . T_j
-//    and, each c_i being where token i reads and its negative where it writes,
-//      dc_i = q^_i . dq^_i + k^_i . r_i - beta_i dbeta_i,
-//      dc_C += exp(c_C) <S0, dS1> + sum_j beta_j k^_j . exp(c_C - c_j) dS1^T E_j,
-//    whose sums from the chunk's end are the gradients of the log decays.
+//    The gradient of the log decay of token t counts what passes it: reads of
+//    S0 by tokens i >= t, writes to S1 by tokens j < t, pairs j < t <= i, and S0
+//    as a whole,
+//      dlog_t = exp(c_C) <S0, dS1> + sum_{i>=t} (q^_i . first term of dq^_i + k^_i . first of r_i)
+//               + sum_{j<t} beta_j k^_j . first term of T_j + sum_{j<t<=i} z_ij,
+//      z_ij = beta_j D_ij (scale P_ij q^_i . k^_j - V_ij k^_i . k^_j),
+//    all of them sums of what does pass: a step that wipes the state leaves
+//    zeros, however large its dt that dA multiplies them by.  (From the finished
+//    dq, dk and dbeta the same follows by differences, in which their larger
+//    part cancels, i = j above all.)
 //
 // Operands that are computed (or stored in fp32) are split into three bf16 parts
 // throughout: dA and the bias' gradient are sums in fp32 of what goes through
@@ -421,7 +427,10 @@ struct GradLds {
   // the small ones first, within the offsets that instructions hold
   __attribute__((aligned(16))) double c[kC];
   __attribute__((aligned(16))) float rk[kC], rq[kC], beta[kC], into[kC], out[kC];
-  float rows[2][4][kC];  // per half of N: q^.dq^, k^.r, k^.T, k^.(first term of T)
+  float rows[2][3][kC];  // per half of N: the reads of S0, k^.T, k^.(first term of T)
+  // z: sums of a column in a row tile below its own, of a row left of its
+  // diagonal tile, and of the pairs of the diagonal tile that pass a token
+  float cols[4][kC], zrow[kC], zdiag[kC];
   float dot[8];
   __attribute__((aligned(16))) uint16_t k[kC * 16 * NT], q[kC * 16 * NT];
   __attribute__((aligned(16))) uint16_t dy[kC * kPitch];         // [token][p by kpos]
@@ -497,6 +506,9 @@ __global__ __launch_bounds__(kThreads) void gdr_bwd_grads_kernel(GdrBwdArgs ba, 
   constexpr uint32_t kPart = 2 * kC * kPitch, kStPart = 2 * 16 * NT * kPitch, kTileRows = 2 * 16 * kPitch;
 
   const uint32_t l_rows = hold(lds_address(&s.dy[tid / 16 * kPitch + kpos(4 * (tid % 16))]));  // E and W behind dY
+  const uint32_t l_k = hold(lds_address(&s.k[r * 16 * NT]));  // row r of a tile of K, its pieces exchanged
+  const uint32_t swap = tile_at<NT>(r, 0) / 8 % (2 * NT);
+  constexpr uint32_t kKTile = 2 * 16 * 16 * NT;
   const int ptiles = static_cast<int>((P + kCols - 1) / kCols);
   const bool four = P % 4 == 0;
   // What a thread loads of a head's columns p0 .. + 63: two times 4 columns of a
@@ -657,7 +669,9 @@ __global__ __launch_bounds__(kThreads) void gdr_bwd_grads_kernel(GdrBwdArgs ba, 
       if (ptiles == 1) load_rows(h + 1, 0);
       load_state(keep.S, h + 1, 0);
     }
-    f32x4 first = {0.f, 0.f, 0.f, 0.f};  // k^ . (first term of T)
+    f32x4 first = {0.f, 0.f, 0.f, 0.f}, read = first;  // k^ . (first term of T), and of S0's reads
+    const f32x4 rko = *reinterpret_cast<const f32x4 *>(&s.rk[16 * own + 4 * g]);
+    const f32x4 rqo = *reinterpret_cast<const f32x4 *>(&s.rq[16 * own + 4 * g]);
     {
       const f32x4 into = *reinterpret_cast<const f32x4 *>(&s.into[16 * own + 4 * g]);
       const f32x4 out = *reinterpret_cast<const f32x4 *>(&s.out[16 * own + 4 * g]);
@@ -667,7 +681,10 @@ __global__ __launch_bounds__(kThreads) void gdr_bwd_grads_kernel(GdrBwdArgs ba, 
         KR[i] = -(KR[i] * into);
         T[i] = T[i] * out;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) first[e] = fmaf(k_at(i, e), T[i][e], first[e]);
+        for (int e = 0; e < 4; ++e) {
+          first[e] = fmaf(k_at(i, e), T[i][e], first[e]);
+          read[e] = fmaf(q_at(i, e) * rqo[e], DQ[i][e], fmaf(k_at(i, e) * rko[e], KR[i][e], read[e]));
+        }
       }
     }
     // the scores.  Rows j and the own tile's i as columns: such a result is an
@@ -717,6 +734,62 @@ __global__ __launch_bounds__(kThreads) void gdr_bwd_grads_kernel(GdrBwdArgs ba, 
             VT[j][e] = j < own || 4 * g + e < r ? -(VT[j][e] * f) : 0.f;
           }
         }
+      if (half == 0) {  // z: the scores by q . k and k . k
+        float zrow = 0.f;
+        const float rq_own = s.rq[16 * own + r], rk_own = s.rk[16 * own + r];
+        u32x4 qf[NH], kf[NH];
+#pragma unroll
+        for (int kb = 0; kb < NH; ++kb) {
+          const uint32_t at = l_k + 2 * 8 * ((4 * kb + g) ^ swap) + own * kKTile;
+          kf[kb] = lds_get<u32x4>(at);
+          qf[kb] = lds_get<u32x4>(at + 2 * kC * 16 * NT);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          f32x4 z = {0.f, 0.f, 0.f, 0.f};
+          if (j <= own) {
+            f32x4 gq = z, gk = z;
+#pragma unroll
+            for (int kb = 0; kb < NH; ++kb) {
+              const u32x4 kj = lds_get<u32x4>(l_k + 2 * 8 * ((4 * kb + g) ^ swap) + j * kKTile);
+              gq = mma(kj, qf[kb], gq);
+              gk = mma(kj, kf[kb], gk);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) z[e] = fmaf(PT[j][e], gq[e] * rq_own, VT[j][e] * (gk[e] * rk_own));
+          }
+          if (j != own) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              zrow += z[e];
+              z[e] = row_sum<16>(z[e]);
+            }
+            if (r == 0) *reinterpret_cast<f32x4 *>(&s.cols[own][16 * j + 4 * g]) = z;
+          } else {
+            // sum over j < t <= i, t = 4 g + e: down each column, then along the rows
+            float sum[5];
+            sum[0] = 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum[e + 1] = sum[e] + (4 * g + e < r ? z[e] : 0.f);
+            float above = 0.f;
+#pragma unroll
+            for (int gg = 0; gg < 3; ++gg) {
+              const float o = __shfl(sum[4], 16 * gg + r);
+              if (gg < g) above += o;
+            }
+            f32x4 d;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) d[e] = row_sum<16>(4 * g + e <= r ? above + sum[e] : 0.f);
+            if (r == 0) {
+              *reinterpret_cast<f32x4 *>(&s.zdiag[16 * j + 4 * g]) = d;
+              *reinterpret_cast<f32x4 *>(&s.cols[own][16 * j + 4 * g]) = f32x4{0.f, 0.f, 0.f, 0.f};
+            }
+          }
+        }
+        zrow += __shfl_xor(zrow, 16);
+        zrow += __shfl_xor(zrow, 32);
+        if (g == 0) s.zrow[16 * own + r] = zrow;
+      }
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb)
         if (2 * kb <= own) {
@@ -797,34 +870,26 @@ __global__ __launch_bounds__(kThreads) void gdr_bwd_grads_kernel(GdrBwdArgs ba, 
         }
     }
     if (ptiles > 1 && hh + 1 < heads) load_rows(h + 1, 0);
-    const f32x4 rko = *reinterpret_cast<const f32x4 *>(&s.rk[16 * own + 4 * g]);
-    const f32x4 rqo = *reinterpret_cast<const f32x4 *>(&s.rq[16 * own + 4 * g]);
     const f32x4 beo = *reinterpret_cast<const f32x4 *>(&s.beta[16 * own + 4 * g]);
     // sums over n of the own rows
-    f32x4 qdq = {0.f, 0.f, 0.f, 0.f}, kkr = qdq, kt_ = qdq;
+    f32x4 kt_ = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < NH; ++i) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        qdq[e] = fmaf(q_at(i, e), DQ[i][e], qdq[e]);
-        kkr[e] = fmaf(k_at(i, e), KR[i][e], kkr[e]);
-        kt_[e] = fmaf(k_at(i, e), T[i][e], kt_[e]);
-      }
+      for (int e = 0; e < 4; ++e) kt_[e] = fmaf(k_at(i, e), T[i][e], kt_[e]);
       GQ[i] = GQ[i] + DQ[i];
       GK[i] = GK[i] + (KR[i] + T[i] * beo);
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      qdq[e] = row_sum<16>(qdq[e]) * rqo[e];
-      kkr[e] = row_sum<16>(kkr[e]) * rko[e];
+      read[e] = row_sum<16>(read[e]);
       kt_[e] = row_sum<16>(kt_[e]) * rko[e];
       first[e] = row_sum<16>(first[e]) * rko[e];
     }
     if (r == 0) {
-      *reinterpret_cast<f32x4 *>(&s.rows[half][0][16 * own + 4 * g]) = qdq;
-      *reinterpret_cast<f32x4 *>(&s.rows[half][1][16 * own + 4 * g]) = kkr;
-      *reinterpret_cast<f32x4 *>(&s.rows[half][2][16 * own + 4 * g]) = kt_;
-      *reinterpret_cast<f32x4 *>(&s.rows[half][3][16 * own + 4 * g]) = first;
+      *reinterpret_cast<f32x4 *>(&s.rows[half][0][16 * own + 4 * g]) = read;
+      *reinterpret_cast<f32x4 *>(&s.rows[half][1][16 * own + 4 * g]) = kt_;
+      *reinterpret_cast<f32x4 *>(&s.rows[half][2][16 * own + 4 * g]) = first;
     }
 #pragma unroll
     for (int m = 1; m < 64; m <<= 1) dot += __shfl_xor(dot, m);
@@ -833,16 +898,22 @@ __global__ __launch_bounds__(kThreads) void gdr_bwd_grads_kernel(GdrBwdArgs ba, 
     if (wave == 0) {
       const int t = lane;
       auto both = [&](int w) { return s.rows[0][w][t] + s.rows[1][w][t]; };
-      const float beta = s.beta[t], dbeta = both(2);
-      double end = static_cast<double>(beta) * both(3);
-      double dc = static_cast<double>(both(0)) + both(1) - static_cast<double>(beta) * dbeta;
+      const float dbeta = both(1);
       float d8 = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) d8 += s.dot[i];
-      end = lane_value(wave_scan(end), 63) + static_cast<double>(s.into[kC - 1]) * d8;
-      // from the chunk's end: the whole, less what lies before
-      const double upto = wave_scan(dc);
-      const float dlog = static_cast<float>(end + lane_value(upto, 63) - upto + dc);
+      double below = 0.0, tiles[4];  // column t in all tiles below its own; a tile's columns in tile w
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        below += s.cols[w][t];
+        tiles[w] = row_prefix(s.cols[w][t]);
+      }
+      // tiles below t's and left of it (the lanes are read by all, outside the choice)
+      const double c20 = lane_value(tiles[2], 15), c30 = lane_value(tiles[3], 15), c31 = lane_value(tiles[3], 31);
+      const double corner = t / 16 == 1 ? c20 + c30 : t / 16 == 2 ? c30 + c31 : 0.0;
+      const double pairs = corner + dpp_shift<0x111>(row_prefix(below)) + row_suffix(s.zrow[t]) + s.zdiag[t];
+      const float dlog = static_cast<float>(static_cast<double>(s.into[kC - 1]) * d8 + wave_from(both(0)) +
+                                            wave_before(static_cast<double>(s.beta[t]) * both(2)) + pairs);
       const float A = a.A[h], bias = a.dt_bias ? a.dt_bias[h] : 0.f;
       float sa = 0.f, sb = 0.f;
       if (t < left) {

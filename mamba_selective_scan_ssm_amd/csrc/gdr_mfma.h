@@ -160,15 +160,40 @@ __device__ __forceinline__ double lane_value(double v, int lane) {
   const uint32_t hi = __builtin_amdgcn_readlane(static_cast<uint32_t>(u >> 32), lane);
   return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
 }
-__device__ __forceinline__ double wave_scan(double v) {
+// Inclusive sums within rows of 16 lanes, from the first lane on and from the
+// last one back.
+__device__ __forceinline__ double row_prefix(double v) {
   v += dpp_shift<0x111>(v);
   v += dpp_shift<0x112>(v);
   v += dpp_shift<0x114>(v);
   v += dpp_shift<0x118>(v);
+  return v;
+}
+__device__ __forceinline__ double row_suffix(double v) {
+  v += dpp_shift<0x101>(v);
+  v += dpp_shift<0x102>(v);
+  v += dpp_shift<0x104>(v);
+  v += dpp_shift<0x108>(v);
+  return v;
+}
+__device__ __forceinline__ double wave_scan(double v) {
+  v = row_prefix(v);
   const double e0 = lane_value(v, 15), e1 = lane_value(v, 31), e2 = lane_value(v, 47);
   const int row = threadIdx.x % 64 / 16;
   if (row >= 1) v += row == 1 ? e0 : row == 2 ? e0 + e1 : e0 + e1 + e2;
   return v;
+}
+// Sums over the lanes before this one, and over this one and those behind it:
+// sums alone, so that nothing is left where there is nothing to add.
+__device__ __forceinline__ double wave_before(double v) {
+  const double in = row_prefix(v), e0 = lane_value(in, 15), e1 = lane_value(in, 31), e2 = lane_value(in, 47);
+  const int row = threadIdx.x % 64 / 16;
+  return dpp_shift<0x111>(in) + (row == 0 ? 0.0 : row == 1 ? e0 : row == 2 ? e0 + e1 : e0 + e1 + e2);
+}
+__device__ __forceinline__ double wave_from(double v) {
+  const double in = row_suffix(v), e1 = lane_value(in, 16), e2 = lane_value(in, 32), e3 = lane_value(in, 48);
+  const int row = threadIdx.x % 64 / 16;
+  return in + (row == 3 ? 0.0 : row == 2 ? e3 : row == 1 ? e2 + e3 : e1 + e2 + e3);
 }
 
 }  // namespace ssm

@@ -43,7 +43,7 @@ def close(got, want, what="", slack=None, steps=0):
                              f"relative norm of the error {(off.norm() / r.norm()).item():.2e}")
 
 
-def gdr(q, k, v, dt, A, beta, h0=None, scale=None, qk_norm=False, bias=None, softplus=False, marks=None):
+def gdr(q, k, v, dt, A, beta, h0=None, scale=None, qk_norm=False, bias=None, softplus=False):
     """y (B, L, H, P) and the last state (B, H, P, N), token by token."""
     B, L, G, N = q.shape
     H, P = v.shape[2:]
@@ -59,8 +59,6 @@ def gdr(q, k, v, dt, A, beta, h0=None, scale=None, qk_norm=False, bias=None, sof
     S = torch.zeros(B, H, P, N, dtype=v.dtype) if h0 is None else h0
     ys = []
     for t in range(L):
-        if marks is not None and t % 64 == 0 and t > 0:
-            marks.append(S)
         S = S * a[:, t, :, None, None]
         e = v[:, t] - torch.einsum("bhpn,bhn->bhp", S, k[:, t])
         S = S + torch.einsum("bhp,bhn->bhpn", beta[:, t, :, None] * e, k[:, t])
@@ -159,45 +157,6 @@ def gdr_grad_slack(w, qk_norm, scale=None):
     u = {n: w[n].double() * r[n] for n in "qk"}
     g = gdr_grads_of({**w, **u}, False, scale)
     return {n: CANCEL * r[n] * (g[n].abs() + u[n].abs() * (g[n] * u[n]).abs().sum(-1, keepdim=True)) for n in "qk"}
-
-
-def gdr_gate_slack(w, qk_norm, scale=None):
-    """For ddt, dA and dbias where the gradients go by chunks of 64 tokens: the
-    gradient of a token's log decay is <S1, dS1> at the chunk's end plus the sum
-    from the token on of q.dq + k.(dk as read) - k.(dk as written), sums whose
-    terms cancel: each is off by up to CANCEL of the sizes of its products."""
-    x = {n: None if w[n] is None else w[n].detach().clone().double() for n in NAMES}
-    B, L, G, N = x["q"].shape
-    H = x["v"].shape[2]
-    head = torch.arange(H) // (H // G)
-    for n in "qk":
-        if qk_norm:
-            x[n] = x[n] / (x[n].pow(2).sum(-1, keepdim=True) + QK_EPS).sqrt()
-        x[n] = x[n][:, :, head].contiguous()
-    for n in ("q", "k", "beta"):
-        x[n].requires_grad_()
-    if x["h0"] is None:
-        x["h0"] = torch.zeros(B, H, x["v"].shape[3], N, dtype=torch.float64)
-    x["h0"].requires_grad_()
-    marks = []
-    y, h = gdr(x["q"], x["k"], x["v"], x["dt"], x["A"], x["beta"], x["h0"], scale, False, x["bias"],
-               x["bias"] is not None, marks)
-    loss = (y * w["dy"].double()).sum() + (0 if w["dh"] is None else (h * w["dh"].double()).sum())
-    grads = torch.autograd.grad(loss, [x["q"], x["k"], x["beta"], *marks], allow_unused=True)
-    dq, dk, dbeta = grads[:3]
-    ends = [(S.detach() * g).abs().sum((-1, -2)) for S, g in zip(marks, grads[3:])]
-    ends.append(torch.zeros(B, H, dtype=torch.float64) if w["dh"] is None else
-                (h.detach() * w["dh"].double()).abs().sum((-1, -2)))
-    wrote = (x["beta"].detach() * dbeta).abs()
-    size = (x["q"].detach() * dq).abs().sum(-1) + (x["k"].detach() * dk).abs().sum(-1) + 2 * wrote
-    dlog = torch.empty_like(size)
-    for c, t0 in enumerate(range(0, L, 64)):
-        part = size[:, t0:t0 + 64]
-        dlog[:, t0:t0 + 64] = part.flip(1).cumsum(1).flip(1) + ends[c][:, None]
-    v = x["dt"] if x["bias"] is None else x["dt"] + x["bias"]
-    d, slope = (v, 1.0) if x["bias"] is None else (torch.nn.functional.softplus(v), torch.sigmoid(v))
-    ddt = CANCEL * dlog * x["A"].abs() * slope
-    return {"dt": ddt, "A": (CANCEL * dlog * d.abs()).sum((0, 1)), "bias": ddt.sum((0, 1))}
 
 
 def norm(x, groups, w=None, b=None, z=None, eps=1e-5, center=True, act=False, gate=None, per_token=True):

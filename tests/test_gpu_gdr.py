@@ -45,11 +45,6 @@ def y_slack(w, qk_norm, scale=None):
     return ref.gdr_output_slack(w, qk_norm, scale) if by_chunks(w) else None
 
 
-def grad_slack(w, qk_norm, scale=None):
-    gates = ref.gdr_gate_slack(w, qk_norm, scale) if by_chunks(w) else {}
-    return {**ref.gdr_grad_slack(w, qk_norm, scale), **gates}
-
-
 def check_fwd(w, qk_norm, what, scale=None, steps=0):
     y, h = fwd(w, qk_norm, scale=scale)
     ry, rh = ref.gdr_of(w, qk_norm, scale)
@@ -60,7 +55,7 @@ def check_fwd(w, qk_norm, what, scale=None, steps=0):
 def check_bwd(w, qk_norm, what, scale=None, steps=0):
     g = bwd(w, qk_norm, scale=scale)
     r = ref.gdr_grads_of(w, qk_norm, scale)
-    slack = grad_slack(w, qk_norm, scale)
+    slack = ref.gdr_grad_slack(w, qk_norm, scale)
     for n in r:
         ref.close(g["d" + n], r[n], f"{what} d{n}", slack.get(n), steps)
 
@@ -219,7 +214,7 @@ def test_unaligned_tensors(dtype, off):
     g = ssm.gdr_bwd(s["q"], s["k"], s["v"], s["dt"], s["A"], s["beta"], s["h0"], s["dy"], s["dh"], qk_norm=True,
                     dt_bias=s["bias"], dt_softplus=True, want_dbias=True)
     torch.cuda.synchronize()
-    r, slack = ref.gdr_grads_of(w, True), grad_slack(w, True)
+    r, slack = ref.gdr_grads_of(w, True), ref.gdr_grad_slack(w, True)
     for n in r:
         ref.close(g["d" + n], r[n], "d" + n, slack.get(n))
     pool = shift(w["h0"])
@@ -423,7 +418,7 @@ def test_other_stream():
         ry, rh = ref.gdr_of(w, True)
         ref.close(y, ry, "y", y_slack(w, True))
         ref.close(h, rh, "h")
-        r, slack = ref.gdr_grads_of(w, True), grad_slack(w, True)
+        r, slack = ref.gdr_grads_of(w, True), ref.gdr_grad_slack(w, True)
         for n in r:
             ref.close(g["d" + n], r[n], "d" + n, slack.get(n))
 
