@@ -525,7 +525,7 @@ __global__ __launch_bounds__(kThreads) void gdr_bwd_grads_kernel(GdrBwdArgs ba, 
         rows_of(static_cast<const uint16_t *>(ba.dy) + ((b * a.L + t0) * a.H + h) * P, left, row, static_cast<uint32_t>(P));
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int tok = (tid + i * kThreads) / 16, p = p0 + 4 * (tid % 16);
+      const int me = hold(tid), tok = (me + i * kThreads) / 16, p = p0 + 4 * (me % 16);
       const uint32_t at = p < P ? 4 * (static_cast<uint32_t>(tok * P) + p) : kNowhere;
       ev[i] = __builtin_bit_cast(f32x4, buffer_b128(re, at));
       wv[i] = __builtin_bit_cast(f32x4, buffer_b128(rw, at));
@@ -567,6 +567,7 @@ __global__ __launch_bounds__(kThreads) void gdr_bwd_grads_kernel(GdrBwdArgs ba, 
   auto load_state = [&](const float *from, int64_t h, int p0) {
     const int64_t item = (b * a.H + h) * nc + c;
     const __amdgpu_buffer_rsrc_t rs = buffer_of(from + item * P * N, static_cast<uint32_t>(4 * P * N));
+    const int me = hold(tid), st_p = 4 * (me % 16), st_n = 4 * (me / 16);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int p = p0 + st_p + e;
@@ -591,6 +592,12 @@ __global__ __launch_bounds__(kThreads) void gdr_bwd_grads_kernel(GdrBwdArgs ba, 
   load_rows(grp * heads, 0);
   load_state(keep.S, grp * heads, 0);
   for (int64_t hh = 0; hh < heads; ++hh) {
+    // What comes from the lane is made anew for each head and part, not kept in registers.
+    int r = hold(lane % 16), g = hold(lane / 16);
+#pragma unroll
+    for (int i = 0; i < NH; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) kq[i][e] = hold(kq[i][e]);
     const int64_t h = grp * heads + hh, item = (b * a.H + h) * nc + c;
     __syncthreads();  // the head before
     if (tid < kC) {
@@ -665,10 +672,6 @@ __global__ __launch_bounds__(kThreads) void gdr_bwd_grads_kernel(GdrBwdArgs ba, 
         }
       }
     }
-    if (hh + 1 < heads) {
-      if (ptiles == 1) load_rows(h + 1, 0);
-      load_state(keep.S, h + 1, 0);
-    }
     f32x4 first = {0.f, 0.f, 0.f, 0.f}, read = first;  // k^ . (first term of T), and of S0's reads
     const f32x4 rko = *reinterpret_cast<const f32x4 *>(&s.rk[16 * own + 4 * g]);
     const f32x4 rqo = *reinterpret_cast<const f32x4 *>(&s.rq[16 * own + 4 * g]);
@@ -687,6 +690,7 @@ __global__ __launch_bounds__(kThreads) void gdr_bwd_grads_kernel(GdrBwdArgs ba, 
         }
       }
     }
+    r = hold(r), g = hold(g);
     // the scores.  Rows j and the own tile's i as columns: such a result is an
     // operand with the tokens i as rows.
     const double c_own = s.c[16 * own + r];
@@ -737,13 +741,6 @@ __global__ __launch_bounds__(kThreads) void gdr_bwd_grads_kernel(GdrBwdArgs ba, 
       if (half == 0) {  // z: the scores by q . k and k . k
         float zrow = 0.f;
         const float rq_own = s.rq[16 * own + r], rk_own = s.rk[16 * own + r];
-        u32x4 qf[NH], kf[NH];
-#pragma unroll
-        for (int kb = 0; kb < NH; ++kb) {
-          const uint32_t at = l_k + 2 * 8 * ((4 * kb + g) ^ swap) + own * kKTile;
-          kf[kb] = lds_get<u32x4>(at);
-          qf[kb] = lds_get<u32x4>(at + 2 * kC * 16 * NT);
-        }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           f32x4 z = {0.f, 0.f, 0.f, 0.f};
@@ -751,9 +748,10 @@ __global__ __launch_bounds__(kThreads) void gdr_bwd_grads_kernel(GdrBwdArgs ba, 
             f32x4 gq = z, gk = z;
 #pragma unroll
             for (int kb = 0; kb < NH; ++kb) {
-              const u32x4 kj = lds_get<u32x4>(l_k + 2 * 8 * ((4 * kb + g) ^ swap) + j * kKTile);
-              gq = mma(kj, qf[kb], gq);
-              gk = mma(kj, kf[kb], gk);
+              const uint32_t at = l_k + 2 * 8 * ((4 * kb + g) ^ swap);
+              const u32x4 kj = lds_get<u32x4>(at + j * kKTile);
+              gq = mma(kj, lds_get<u32x4>(at + own * kKTile + 2 * kC * 16 * NT), gq);
+              gk = mma(kj, lds_get<u32x4>(at + own * kKTile), gk);
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e) z[e] = fmaf(PT[j][e], gq[e] * rq_own, VT[j][e] * (gk[e] * rk_own));
@@ -808,6 +806,11 @@ __global__ __launch_bounds__(kThreads) void gdr_bwd_grads_kernel(GdrBwdArgs ba, 
         }
     }
     __builtin_amdgcn_sched_barrier(0);
+    if (hh + 1 < heads) {
+      if (ptiles == 1) load_rows(h + 1, 0);
+      load_state(keep.S, h + 1, 0);
+    }
+    r = hold(r), g = hold(g);
     // Rows i and the own tile's j as columns.
     {
       f32x4 PN[4], VN[4];
