@@ -134,6 +134,8 @@ def _check(name, t, shape, dtype, device):
         return None
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device == device and t.shape == shape and t.dtype == dtype and t.is_contiguous():
+        return t
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     if tuple(t.shape) != tuple(shape):
@@ -146,11 +148,15 @@ def _check(name, t, shape, dtype, device):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(device):
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    # the handle alone: a Stream object made for it costs 1.9 us more, of a 13 us call
+    if device.type != "cuda":
+        raise ValueError(f"tensors must be on a GPU, not on {device}")
+    index = torch.cuda.current_device() if device.index is None else device.index
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def _call(fn_name, *args):
@@ -468,8 +474,11 @@ def scan_bwd(x, delta, A, Bm, Cm, D_skip=None, z=None, h0=None, dy=None, dh_fina
 def _gpu_call(dev, fn_name, *args):
     """A call whose stream is the current one of the tensors' device, made with
     that device current (it need not be the caller's)."""
-    if dev.type != "cuda":
+    if dev.type != "cuda":  # before a device is made current
         raise ValueError(f"tensors must be on a GPU, not on {dev}")
+    if dev.index == torch.cuda.current_device():
+        _call(fn_name, *args, _stream(dev))
+        return
     with torch.cuda.device(dev):
         _call(fn_name, *args, _stream(dev))
 

@@ -52,6 +52,27 @@ __device__ __forceinline__ void load_row(const T *p, int lq, int64_t N, float *v
     }
   }
 }
+// The same in the tensor's own type.
+template <bool VEC, int LPC, int NV, typename T>
+__device__ __forceinline__ void load_raw(const T *p, int lq, int64_t N, T *v) {
+  struct alignas(4 * sizeof(T)) Four {
+    T v[4];
+  };
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int n = 4 * (lq + LPC * j);
+    Four f = {};
+    if constexpr (VEC) {
+      if (n < N) f = *reinterpret_cast<const Four *>(p + n);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (n + e < N) f.v[e] = p[n + e];
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[4 * j + e] = f.v[e];
+  }
+}
 template <bool VEC, int LPC, int NV>
 __device__ __forceinline__ void store_row(float *p, int lq, int64_t N, const float *v) {
 #pragma unroll
