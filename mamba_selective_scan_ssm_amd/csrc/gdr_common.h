@@ -2,23 +2,85 @@
 // over LPC adjacent lanes, NV groups of four consecutive states per lane.
 #pragma once
 
+#include <type_traits>
+
 #include "device_common.h"
 
 namespace ssm {
 
-// Sum over the LPC (1, 2, 4, 8 or 16) adjacent lanes of a row, every lane
-// getting it: DPP quad permutations, then mirrors within half rows and rows.
+// Lanes' values from others by DPP, without the LDS: kCtrl 0xB1 and 0x4E permute
+// quads, 0x141 and 0x140 mirror halves of rows and rows of 16, 0x120 + n rotates rows.
 template <int kCtrl>
 __device__ __forceinline__ float dpp_get(float v) {
   return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), kCtrl, 0xF, 0xF, true));
 }
+// x's sum over the lanes' two halves in the lower 32 lanes, y's in the upper
+__device__ __forceinline__ float join_halves(float x, float y) {
+  const auto u = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(y), false, false);
+  return __uint_as_float(u[0]) + __uint_as_float(u[1]);
+}
+// x's sums over pairs of rows of 16 lanes in the even rows, y's in the odd
+__device__ __forceinline__ float join_rows(float x, float y) {
+  const auto u = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(y), false, false);
+  return __uint_as_float(u[0]) + __uint_as_float(u[1]);
+}
+// Sum over the LPC (1, 2, 4, 8, 16, 32 or 64) adjacent lanes of a row, every lane
+// getting it.
 template <int LPC>
 __device__ __forceinline__ float row_sum(float v) {
   if constexpr (LPC >= 2) v += dpp_get<0xB1>(v);
   if constexpr (LPC >= 4) v += dpp_get<0x4E>(v);
   if constexpr (LPC >= 8) v += dpp_get<0x141>(v);
   if constexpr (LPC >= 16) v += dpp_get<0x140>(v);
+  if constexpr (LPC >= 32) v = join_rows(v, v);
+  if constexpr (LPC >= 64) v = join_halves(v, v);
   return v;
+}
+
+// A buffer of that many bytes: loads behind them give 0, stores nothing.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *base, uint32_t bytes) {
+  // the same in all lanes, and said so: a descriptor in vector registers is
+  // loaded from in a loop over its values
+  bytes = __builtin_amdgcn_readfirstlane(bytes);
+  const uint64_t at = reinterpret_cast<uint64_t>(base);
+  const uint64_t lo = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(at)));
+  const uint64_t hi = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(at >> 32)));
+  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void *>(hi << 32 | lo), 0, static_cast<int>(bytes),
+                                           0x00020000);
+}
+constexpr uint32_t kNowhere = 0xfffffff0u;  // an offset outside every buffer
+template <typename T>
+__device__ __forceinline__ T load_one(__amdgpu_buffer_rsrc_t r, uint32_t at) {
+  if constexpr (sizeof(T) == 4)
+    return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b32(r, static_cast<int>(at), 0, 0));
+  else
+    return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b16(r, static_cast<int>(at), 0, 0));
+}
+__device__ __forceinline__ void store_one(float v, __amdgpu_buffer_rsrc_t r, uint32_t at) {
+  __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), r, static_cast<int>(at), 0, 0);
+}
+__device__ __forceinline__ void store_one(bf16_t v, __amdgpu_buffer_rsrc_t r, uint32_t at) {
+  __builtin_amdgcn_raw_buffer_store_b16(v.bits, r, static_cast<int>(at), 0, 0);
+}
+// f(0) .. f(n - 1), the numbers known to the compiler
+template <int n, int i = 0, typename F>
+__device__ __forceinline__ void each(F &&f) {
+  if constexpr (i < n) {
+    f(std::integral_constant<int, i>());
+    each<n, i + 1>(f);
+  }
+}
+// 1 / sqrt(x): the instruction's, with one step of Newton's
+__device__ __forceinline__ float inverse_root(float x) {
+  const float r = __builtin_amdgcn_rsqf(x);
+  const float s = x * r;  // sqrt(x)
+  const float out = fmaf(0.5f * r, fmaf(-s, r, 1.f), r);
+  return x < __builtin_huge_valf() ? out : r;  // x = inf: 0, and NaN as it is
+}
+// A row's value in its lane j of 16, for all of them.
+template <int j>
+__device__ __forceinline__ float row_lane(float v) {
+  return dpp_get<0x150 + j>(v);
 }
 
 __device__ __forceinline__ void load4(const float *p, float *v) {

@@ -9,7 +9,7 @@
 // that a slot's 8 values are 16 consecutive bytes.
 #pragma once
 
-#include "device_common.h"
+#include "gdr_common.h"
 
 namespace ssm {
 
@@ -124,23 +124,12 @@ __device__ __forceinline__ u32x2 lds_transposed(uint32_t at) {
 // element on: reads behind the last row give 0 and writes there are dropped.
 // `left` rows from t0 (0 and less: none), of which `tail` elements count in the
 // last.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *base, uint32_t bytes) {
-  // the same in all lanes, and said so: a descriptor in vector registers is
-  // loaded from in a loop over its values
-  bytes = __builtin_amdgcn_readfirstlane(bytes);
-  const uint64_t at = reinterpret_cast<uint64_t>(base);
-  const uint64_t lo = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(at)));
-  const uint64_t hi = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(at >> 32)));
-  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void *>(hi << 32 | lo), 0, static_cast<int>(bytes),
-                                           0x00020000);
-}
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(const void *base, int left, uint32_t row, uint32_t tail) {
   return buffer_of(base, left > 0 ? 2 * (static_cast<uint32_t>(left - 1) * row + tail) : 0);
 }
 __device__ __forceinline__ u32x4 buffer_b128(__amdgpu_buffer_rsrc_t r, uint32_t at, uint32_t more = 0) {
   return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, static_cast<int>(at), static_cast<int>(more), 0));
 }
-constexpr uint32_t kNowhere = 0xfffffff0u;  // an offset outside every buffer
 
 // exp2 of a difference of two cumulative decays
 __device__ __forceinline__ float decay_of(double d) { return fast_exp2(static_cast<float>(d)); }
