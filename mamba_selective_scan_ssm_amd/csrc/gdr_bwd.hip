@@ -12,10 +12,16 @@
 // saves the state entering every kGdrSeg tokens, and the reverse pass walks a
 // segment forward from it, keeping the segment's states in registers.
 //
-// A workgroup holds 256 / LPC rows of one head (the forward's layout).  dq and
-// dk sum over the head's rows: over the lanes of a wave by shuffles, over the
-// waves in LDS, over the tiles of rows and the heads of a group by the sums
-// below, always in the same order.
+// A workgroup holds 16 rows of one head, 16 lanes each.  dq and dk sum over the
+// head's rows: over a wave's four by exchanges of lanes, two values at a time
+// that end side by side (3 swaps for 4 values), over the waves in LDS, over the
+// tiles of rows and the heads of a group by the sums below, always in the same
+// order.
+//
+// Bound by the chain of a token, forwards and back (six sums between lanes): 2 x
+// 515 tokens of fp32, 6 heads of 40 x 48: 0.216 ms, 0.42 us a token, with the next
+// segment's loads under it; before it the states, 0.059 ms, behind it the sums,
+// 0.017 ms.
 #include "device_common.h"
 #include "gdr.h"
 #include "gdr_common.h"
@@ -27,32 +33,28 @@ constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kSeg = kGdrSeg;
 
-__host__ __device__ constexpr int lanes_per_row(int64_t N) { return N <= 16 ? 4 : N <= 32 ? 8 : 16; }
-int64_t row_tiles(int64_t P, int64_t N) {
-  const int64_t rows = kThreads / lanes_per_row(N);
-  return (P + rows - 1) / rows;
-}
+constexpr int kLanes = 16, kRows = kThreads / kLanes;
+int64_t row_tiles(int64_t P) { return (P + kRows - 1) / kRows; }
 
-template <typename T, int LPC, int NV, bool VEC>
+template <typename T, int NV, bool VEC>
 __global__ __launch_bounds__(kThreads) void gdr_bwd_seq_kernel(GdrBwdArgs ba, const float *ckpt, float *dq_part,
                                                                float *dk_part, float *sc_part) {
   const GdrArgs &a = ba.f;
-  constexpr int NP = 4 * LPC * NV;
-  constexpr int kRows = kThreads / LPC;
-  __shared__ __attribute__((aligned(16))) float s_k[kSeg][NP], s_q[kSeg][NP];
-  __shared__ float s_r[kSeg][2];
-  __shared__ float s_ab[kSeg][2];  // decay, beta
-  __shared__ float s_dq[kWaves][kSeg][NP], s_dk[kWaves][kSeg][NP];
-  __shared__ float s_sc[kWaves][kSeg][2];
+  constexpr int LPC = kLanes, NP = 4 * LPC * NV;
+  constexpr uint32_t kSize = sizeof(T);
+  static_assert(kSeg == 8 && kThreads == 16 * 2 * kSeg, "16 lanes for each of a segment's rows of k and q");
+  __shared__ __attribute__((aligned(16))) float s_x[2][kSeg][NP];          // k, q, normalised
+  __shared__ __attribute__((aligned(16))) float s_d[2][kWaves][kSeg][NP];  // dq, dk
+  __shared__ float s_sc[kWaves][2 * kSeg];                                 // dbeta, then dlog
   const int64_t L = a.L, H = a.H, P = a.P, G = a.G, N = a.N, B = a.B;
-  const int tid = threadIdx.x, lq = tid % LPC, lr = tid / LPC, lane = tid % 64, wave = tid / 64;
+  const int tid = threadIdx.x, lq = tid % LPC, mine = tid % 8, lane = tid % 64;
+  const int wave = __builtin_amdgcn_readfirstlane(tid / 64);
   const int64_t tile = blockIdx.x, h = blockIdx.y, b = blockIdx.z, g = h / (H / G);
-  const int64_t p_raw = tile * kRows + lr;
+  const int64_t p_raw = tile * kRows + tid / LPC;
   const bool active = p_raw < P;
   const int64_t p = active ? p_raw : P - 1;
   const float A2 = a.A[h] * kLog2e, bias = a.dt_bias ? a.dt_bias[h] : 0.f;
   const int64_t nseg = (L + kSeg - 1) / kSeg;
-  const T *kp = static_cast<const T *>(a.k), *qp = static_cast<const T *>(a.q);
 
   float dS[4 * NV];
   if (ba.dh_final != nullptr && active)
@@ -61,148 +63,150 @@ __global__ __launch_bounds__(kThreads) void gdr_bwd_seq_kernel(GdrBwdArgs ba, co
 #pragma unroll
     for (int i = 0; i < 4 * NV; ++i) dS[i] = 0.f;
 
+  // a segment's rows of `width` elements, `pitch` apart
+  auto rows = [&](const void *base, int64_t s, int64_t first, int64_t pitch, int64_t width) {
+    const int64_t left = s < 0 ? 0 : L - s * kSeg < kSeg ? L - s * kSeg : kSeg;
+    return buffer_of(static_cast<const T *>(base) + (s < 0 ? 0 : (b * L + s * kSeg) * pitch + first),
+                     left > 0 ? static_cast<uint32_t>((left - 1) * pitch + width) * kSize : 0);
+  };
+  constexpr int kFours = NP / 64;
+  const int tok = 4 * (wave % 2) + lane / 16;  // staged by this lane: of k by waves 0, 1, of q by 2, 3
+  const uint32_t row_at = static_cast<uint32_t>(tok * G * N) * kSize;
+  const uint32_t gate_at = static_cast<uint32_t>(mine * H) * kSize, v_at = static_cast<uint32_t>(mine * H * P + p) * kSize;
+  Four<VEC, T> x[kFours];
+  T dn, bn, vn, yn;
+  float S0[4 * NV];
+  auto load = [&](int64_t s) {
+    const __amdgpu_buffer_rsrc_t r = rows(wave < 2 ? a.k : a.q, s, g * N, G * N, N);
+#pragma unroll
+    for (int j = 0; j < kFours; ++j) {
+      const int n = 4 * (tid % 16 + 16 * j);
+      x[j].load(r, n < N ? row_at + n * kSize : kNowhere, n, N);
+    }
+    dn = load_one<T>(rows(a.dt, s, h, H, 1), gate_at);
+    bn = load_one<T>(rows(a.beta, s, h, H, 1), gate_at);
+    vn = load_one<T>(rows(a.v, s, h * P, H * P, P), v_at);
+    yn = load_one<T>(rows(ba.dy, s, h * P, H * P, P), v_at);
+    load_row<VEC, LPC, NV>(ckpt + (((b * H + h) * nseg + (s < 0 ? 0 : s)) * P + p) * N, lq, N, S0);
+  };
+  auto stage = [&]() {
+    float f[4 * kFours], ss = kQkNormEps / 16;
+#pragma unroll
+    for (int i = 0; i < 4 * kFours; ++i) {
+      f[i] = to_f32(x[i / 4].v[i % 4]);
+      ss = fmaf(f[i], f[i], ss);
+    }
+    if (a.qk_norm) {
+      const float r = inverse_root(row_sum<16>(ss));
+#pragma unroll
+      for (int i = 0; i < 4 * kFours; ++i) f[i] *= r;
+    }
+#pragma unroll
+    for (int j = 0; j < kFours; ++j)
+      *reinterpret_cast<float4 *>(&s_x[wave / 2][tok][4 * (tid % 16 + 16 * j)]) =
+          make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
+  };
+
+  if (nseg > 0) {
+    load(nseg - 1);
+    stage();
+    meet_in_lds();
+  }
   for (int64_t s = nseg - 1; s >= 0; --s) {
     const int64_t t0 = s * kSeg;
     const int nt = static_cast<int>(L - t0 < kSeg ? L - t0 : kSeg);
-    for (int e = tid; e < kSeg * NP; e += kThreads) {
-      const int j = e / NP, n = e % NP;
-      const bool ok = j < nt && n < N;
-      const int64_t at = ok ? ((b * L + t0 + j) * G + g) * N + n : 0;
-      s_k[j][n] = ok ? to_f32(kp[at]) : 0.f;
-      s_q[j][n] = ok ? to_f32(qp[at]) : 0.f;
-    }
-    if (tid < nt) {
-      const int64_t at = (b * L + t0 + tid) * H + h;
-      const float d = step_size(to_f32(static_cast<const T *>(a.dt)[at]), bias, a.dt_softplus);
-      s_ab[tid][0] = fast_exp2(d * A2);
-      s_ab[tid][1] = to_f32(static_cast<const T *>(a.beta)[at]);
-    }
-    __syncthreads();
-    if (a.qk_norm) {  // 16 lanes per (token, q or k) row
-      const int j = tid / 32, w = (tid / 16) % 2, i0 = tid % 16;
-      static_assert(kSeg * 32 == kThreads, "32 lanes per token");
-      float *x = w ? s_q[j] : s_k[j];
-      float ss = 0.f;
-      for (int n = i0; n < NP; n += 16) ss = fmaf(x[n], x[n], ss);
-      ss = row_sum<16>(ss);
-      if (i0 == 0) s_r[j][w] = 1.f / sqrtf(ss + kQkNormEps);
-      __syncthreads();
-      for (int e = tid; e < kSeg * NP; e += kThreads) {
-        const int jj = e / NP, n = e % NP;
-        s_k[jj][n] *= s_r[jj][0];
-        s_q[jj][n] *= s_r[jj][1];
-      }
-      __syncthreads();
-    }
-
+    // Tokens behind the last are read as zeros and leave all as it is; so do rows
+    // behind P, whose dy and e are 0, but their saved state is a copy of row P - 1.
+    const float decay = mine < nt ? fast_exp2(step_size(to_f32(dn), bias, a.dt_softplus) * A2) : 1.f;
+    const float beta = to_f32(bn), v = to_f32(vn), dy = active ? a.scale * to_f32(yn) : 0.f;
+    float Sv[kSeg][4 * NV], E[kSeg];
+#pragma unroll
+    for (int i = 0; i < 4 * NV; ++i) Sv[0][i] = S0[i];
+    load(s - 1);
     // forward through the segment: the state before each token, and e
-    float Sv[kSeg][4 * NV], E[kSeg], v[kSeg], dy[kSeg];
+    each<kSeg>([&](auto number) {
+      constexpr int j = decltype(number)::value;
+      float kv[4 * NV];
+      lds_row<LPC, NV>(s_x[0][j], lq, kv);
+      const float al = row_lane<j>(decay);
+      const float e = fmaf(-al, row_dot<LPC, NV>(Sv[j], kv), row_lane<j>(v));
+      E[j] = active ? e : 0.f;
+      if constexpr (j + 1 < kSeg) {
+        const float u = row_lane<j>(beta) * E[j];
 #pragma unroll
-    for (int j = 0; j < kSeg; ++j) {
-      const int64_t t = t0 + (j < nt ? j : nt - 1);
-      const int64_t at = ((b * L + t) * H + h) * P + p;
-      v[j] = to_f32(static_cast<const T *>(a.v)[at]);
-      dy[j] = active ? a.scale * to_f32(static_cast<const T *>(ba.dy)[at]) : 0.f;
-    }
-    load_row<VEC, LPC, NV>(ckpt + (((b * H + h) * nseg + s) * P + p) * N, lq, N, Sv[0]);
-#pragma unroll
-    for (int j = 0; j < kSeg; ++j) {
-      E[j] = 0.f;
-      if (j < nt) {
-        float kv[4 * NV];
-        lds_row<LPC, NV>(s_k[j], lq, kv);
-        const float al = s_ab[j][0];
-        E[j] = active ? fmaf(-al, row_dot<LPC, NV>(Sv[j], kv), v[j]) : 0.f;
-        if (j + 1 < kSeg) {
-          const float u = s_ab[j][1] * E[j];
-#pragma unroll
-          for (int i = 0; i < 4 * NV; ++i) Sv[j + 1][i] = fmaf(al, Sv[j][i], u * kv[i]);
-        }
+        for (int i = 0; i < 4 * NV; ++i) Sv[j + 1][i] = fmaf(al, Sv[j][i], u * kv[i]);
       }
-    }
+    });
     // back through it
+    float dv = 0.f, db[kSeg], dl[kSeg];
+    each<kSeg>([&](auto number) {
+      constexpr int j = kSeg - 1 - decltype(number)::value;
+      float kv[4 * NV], qv[4 * NV], gq[4 * NV], gk[4 * NV];
+      lds_row<LPC, NV>(s_x[0][j], lq, kv);
+      lds_row<LPC, NV>(s_x[1][j], lq, qv);
+      const float al = row_lane<j>(decay), be = row_lane<j>(beta), dyj = row_lane<j>(dy), u = be * E[j];
 #pragma unroll
-    for (int j = kSeg - 1; j >= 0; --j) {
-      if (j < nt) {
-        float kv[4 * NV], qv[4 * NV];
-        lds_row<LPC, NV>(s_k[j], lq, kv);
-        lds_row<LPC, NV>(s_q[j], lq, qv);
-        const float al = s_ab[j][0], be = s_ab[j][1], u = be * E[j];
-        float gq[4 * NV], gk[4 * NV];
-#pragma unroll
-        for (int i = 0; i < 4 * NV; ++i) {
-          const float before = al * Sv[j][i];
-          gq[i] = dy[j] * fmaf(u, kv[i], before);
-          dS[i] = fmaf(dy[j], qv[i], dS[i]);
-        }
-        const float du = row_dot<LPC, NV>(dS, kv);
-        const float de = be * du;
-        float dl = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4 * NV; ++i) {
-          const float before = al * Sv[j][i];
-          gk[i] = fmaf(dS[i], u, -(before * de));
-          dS[i] = fmaf(-de, kv[i], dS[i]);
-          dl = fmaf(dS[i], before, dl);
-          dS[i] *= al;
-        }
-        if (active && lq == 0)
-          static_cast<T *>(ba.dv)[((b * L + t0 + j) * H + h) * P + p] = from_f32<T>(de);
-        // rows past P add nothing: their dy, e and dS are 0, but their saved
-        // state is a copy of row P - 1
-        float db = active && lq == 0 ? du * E[j] : 0.f;
-        if (!active) dl = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4 * NV; ++i) {
-          if (!active) gq[i] = gk[i] = 0.f;
-#pragma unroll
-          for (int m = LPC; m < 64; m <<= 1) {
-            gq[i] += __shfl_xor(gq[i], m);
-            gk[i] += __shfl_xor(gk[i], m);
-          }
-        }
-#pragma unroll
-        for (int m = 1; m < 64; m <<= 1) {
-          db += __shfl_xor(db, m);
-          dl += __shfl_xor(dl, m);
-        }
-        if (lane < LPC) {
-#pragma unroll
-          for (int i = 0; i < 4 * NV; ++i) {
-            const int n = 4 * (lq + LPC * (i / 4)) + i % 4;
-            s_dq[wave][j][n] = gq[i];
-            s_dk[wave][j][n] = gk[i];
-          }
-        }
-        if (lane == 0) {
-          s_sc[wave][j][0] = db;
-          s_sc[wave][j][1] = dl;
-        }
+      for (int i = 0; i < 4 * NV; ++i) {
+        Sv[j][i] *= al;
+        gq[i] = dyj * fmaf(u, kv[i], Sv[j][i]);
+        dS[i] = fmaf(dyj, qv[i], dS[i]);
       }
+      const float du = row_dot<LPC, NV>(dS, kv);
+      const float de = be * du;
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4 * NV; ++i) {
+        gk[i] = fmaf(dS[i], u, -(Sv[j][i] * de));
+        dS[i] = fmaf(-de, kv[i], dS[i]);
+        sum = fmaf(dS[i], Sv[j][i], sum);
+        dS[i] *= al;
+      }
+      if (mine == j) dv = de;
+      db[j] = active && lq == 0 ? du * E[j] : 0.f;
+      dl[j] = active ? sum : 0.f;
+#pragma unroll
+      for (int i = 0; i < 4 * NV; i += 4) {
+        float f[4];  // of q in the lower 32 lanes, of k in the upper
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[e] = join_halves(active ? gq[i + e] : 0.f, active ? gk[i + e] : 0.f);
+        // elements 0, 1 in the even rows of lanes, 2, 3 in the odd
+        *reinterpret_cast<float2 *>(&s_d[lane / 32][wave][j][4 * (lq + LPC * (i / 4)) + lane / 16 % 2 * 2]) =
+            make_float2(join_rows(f[0], f[2]), join_rows(f[1], f[3]));
+      }
+    });
+    store_one(from_f32<T>(dv), rows(ba.dv, s, h * P, H * P, P), active && lq < 8 ? v_at : kNowhere);
+    // dbeta of the segment's tokens in the lower lanes, dlog in the upper; tokens 0 .. 3
+    // in the even rows, 4 .. 7 in the odd
+#pragma unroll
+    for (int j = 0; j < kSeg; ++j) db[j] = join_halves(db[j], dl[j]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float x4 = row_sum<16>(join_rows(db[j], db[j + 4]));
+      if (lq == 0) s_sc[wave][8 * (lane / 32) + 4 * (lane / 16 % 2) + j] = x4;
     }
-    __syncthreads();
+    meet_in_lds();
     for (int e = tid; e < nt * NP; e += kThreads) {
       const int j = e / NP, n = e % NP;
       if (n < N) {
-        float x = 0.f, y = 0.f;
+        float sq = 0.f, sk = 0.f;
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) {
-          x += s_dq[w][j][n];
-          y += s_dk[w][j][n];
+          sq += s_d[0][w][j][n];
+          sk += s_d[1][w][j][n];
         }
         const int64_t at = (((tile * B + b) * L + t0 + j) * H + h) * N + n;
-        dq_part[at] = x;
-        dk_part[at] = y;
+        dq_part[at] = sq;
+        dk_part[at] = sk;
       }
     }
-    if (tid < 2 * nt) {
-      const int j = tid / 2, w2 = tid % 2;
-      float x = 0.f;
+    if (tid < 2 * kSeg && tid % kSeg < nt) {
+      float sum = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) x += s_sc[w][j][w2];
-      sc_part[(((w2 * static_cast<int64_t>(gridDim.x) + tile) * B + b) * L + t0 + j) * H + h] = x;
+      for (int w = 0; w < kWaves; ++w) sum += s_sc[w][tid];
+      sc_part[((tid / kSeg * static_cast<int64_t>(gridDim.x) + tile) * B + b) * L * H + (t0 + tid % kSeg) * H + h] = sum;
     }
-    __syncthreads();  // the next segment stages into the same LDS
+    stage();
+    meet_in_lds();  // the next segment's rows are there, and this one's sums taken
   }
   if (ba.dh0 != nullptr && active)
     store_row<VEC, LPC, NV>(ba.dh0 + ((b * H + h) * P + p) * N, lq, N, dS);
@@ -210,14 +214,15 @@ __global__ __launch_bounds__(kThreads) void gdr_bwd_seq_kernel(GdrBwdArgs ba, co
 
 bool aligned16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
-template <typename T, int LPC, int NV>
+template <typename T, int NV>
 hipError_t launch_shape(const GdrBwdArgs &a, const float *ckpt, float *dqp, float *dkp, float *scp, int64_t tiles,
                         hipStream_t s) {
   const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(a.f.H), static_cast<unsigned>(a.f.B));
-  if (a.f.N % 4 == 0 && aligned16(a.dh_final) && aligned16(a.dh0) && aligned16(ckpt))
-    gdr_bwd_seq_kernel<T, LPC, NV, true><<<grid, kThreads, 0, s>>>(a, ckpt, dqp, dkp, scp);
+  auto fours = [](const void *p) { return reinterpret_cast<uintptr_t>(p) % (4 * sizeof(T)) == 0; };
+  if (a.f.N % 4 == 0 && aligned16(a.dh_final) && aligned16(a.dh0) && aligned16(ckpt) && fours(a.f.q) && fours(a.f.k))
+    gdr_bwd_seq_kernel<T, NV, true><<<grid, kThreads, 0, s>>>(a, ckpt, dqp, dkp, scp);
   else
-    gdr_bwd_seq_kernel<T, LPC, NV, false><<<grid, kThreads, 0, s>>>(a, ckpt, dqp, dkp, scp);
+    gdr_bwd_seq_kernel<T, NV, false><<<grid, kThreads, 0, s>>>(a, ckpt, dqp, dkp, scp);
   return hipGetLastError();
 }
 
@@ -225,12 +230,10 @@ template <typename T>
 hipError_t launch_t(const GdrBwdArgs &a, const float *ckpt, float *dqp, float *dkp, float *scp, int64_t tiles,
                     hipStream_t s) {
   const int64_t N = a.f.N;
-  if (N <= 16) return launch_shape<T, 4, 1>(a, ckpt, dqp, dkp, scp, tiles, s);
-  if (N <= 32) return launch_shape<T, 8, 1>(a, ckpt, dqp, dkp, scp, tiles, s);
-  if (N <= 64) return launch_shape<T, 16, 1>(a, ckpt, dqp, dkp, scp, tiles, s);
-  if (N <= 128) return launch_shape<T, 16, 2>(a, ckpt, dqp, dkp, scp, tiles, s);
-  if (N <= 192) return launch_shape<T, 16, 3>(a, ckpt, dqp, dkp, scp, tiles, s);
-  return launch_shape<T, 16, 4>(a, ckpt, dqp, dkp, scp, tiles, s);
+  if (N <= 64) return launch_shape<T, 1>(a, ckpt, dqp, dkp, scp, tiles, s);
+  if (N <= 128) return launch_shape<T, 2>(a, ckpt, dqp, dkp, scp, tiles, s);
+  if (N <= 192) return launch_shape<T, 3>(a, ckpt, dqp, dkp, scp, tiles, s);
+  return launch_shape<T, 4>(a, ckpt, dqp, dkp, scp, tiles, s);
 }
 
 __device__ __forceinline__ float wave_sum(float v) {
@@ -287,7 +290,7 @@ __global__ __launch_bounds__(kThreads) void gdr_reduce_qk_kernel(GdrBwdArgs ba, 
 
 // dbeta and ddt, one thread per (token, head), and the sums of a block of
 // tokens for dA and the bias (64 heads by 4 tokens per round).
-constexpr int kTokBlock = 128;
+constexpr int kTokBlock = 16;
 template <typename T>
 __global__ __launch_bounds__(kThreads) void gdr_reduce_gates_kernel(GdrBwdArgs ba, int64_t tiles,
                                                                     const float *sc_part, float *red) {
@@ -378,14 +381,14 @@ hipError_t launch_gdr_reduce_params(const GdrBwdArgs &a, int64_t nblk, const flo
 }
 
 int64_t gdr_bwd_seq_ws_floats(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G, int64_t N) {
-  const int64_t nseg = (L + kSeg - 1) / kSeg, tiles = row_tiles(P, N);
+  const int64_t nseg = (L + kSeg - 1) / kSeg, tiles = row_tiles(P);
   return pad4(B * H * nseg * P * N) + 2 * pad4(tiles * B * L * H * N) + pad4(2 * tiles * B * L * H) +
          gdr_reduce_ws_floats(B, L, H);
 }
 
 hipError_t launch_gdr_bwd_seq(const GdrBwdArgs &a, hipStream_t s) {
   const GdrArgs &f = a.f;
-  const int64_t nseg = (f.L + kSeg - 1) / kSeg, tiles = row_tiles(f.P, f.N);
+  const int64_t nseg = (f.L + kSeg - 1) / kSeg, tiles = row_tiles(f.P);
   float *ckpt = a.ws, *dqp = ckpt + pad4(f.B * f.H * nseg * f.P * f.N);
   float *dkp = dqp + pad4(tiles * f.B * f.L * f.H * f.N), *scp = dkp + pad4(tiles * f.B * f.L * f.H * f.N);
   float *red = scp + pad4(2 * tiles * f.B * f.L * f.H);

@@ -62,6 +62,28 @@ __device__ __forceinline__ void store_one(float v, __amdgpu_buffer_rsrc_t r, uin
 __device__ __forceinline__ void store_one(bf16_t v, __amdgpu_buffer_rsrc_t r, uint32_t at) {
   __builtin_amdgcn_raw_buffer_store_b16(v.bits, r, static_cast<int>(at), 0, 0);
 }
+// Four consecutive elements of a row at byte `at` of the buffer, as they are
+// stored: VEC at once, else one by one, up to element n + e < N.
+template <bool VEC, typename T>
+struct alignas(4 * sizeof(T)) Four {
+  T v[4];
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t at, int n, int64_t N) {
+    if constexpr (VEC && sizeof(T) == 4) {
+      *this = __builtin_bit_cast(Four, __builtin_amdgcn_raw_buffer_load_b128(r, static_cast<int>(at), 0, 0));
+    } else if constexpr (VEC) {
+      *this = __builtin_bit_cast(Four, __builtin_amdgcn_raw_buffer_load_b64(r, static_cast<int>(at), 0, 0));
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = load_one<T>(r, n + e < N ? at + e * static_cast<uint32_t>(sizeof(T)) : kNowhere);
+    }
+  }
+};
+// All waves of the workgroup: the LDS alone is waited for, not the loads on their way.
+__device__ __forceinline__ void meet_in_lds() {
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
 // f(0) .. f(n - 1), the numbers known to the compiler
 template <int n, int i = 0, typename F>
 __device__ __forceinline__ void each(F &&f) {

@@ -44,23 +44,6 @@ __device__ __forceinline__ bool state_row(const GdrArgs &a, int64_t b, int64_t &
   return true;
 }
 
-// Four consecutive elements of a row at byte `at` of the buffer, as they are
-// stored: VEC at once, else one by one, up to element n + e < N.
-template <bool VEC, typename T>
-struct alignas(4 * sizeof(T)) Four {
-  T v[4];
-  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t at, int n, int64_t N) {
-    if constexpr (VEC && sizeof(T) == 4) {
-      *this = __builtin_bit_cast(Four, __builtin_amdgcn_raw_buffer_load_b128(r, static_cast<int>(at), 0, 0));
-    } else if constexpr (VEC) {
-      *this = __builtin_bit_cast(Four, __builtin_amdgcn_raw_buffer_load_b64(r, static_cast<int>(at), 0, 0));
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = load_one<T>(r, n + e < N ? at + e * static_cast<uint32_t>(sizeof(T)) : kNowhere);
-    }
-  }
-};
-
 // Rows of a (L, ..) tensor of one sequence, `pitch` bytes apart, from a token on
 // that steps by 8; `width` bytes of the last row count.
 struct Rows {
@@ -149,19 +132,13 @@ __global__ __launch_bounds__(kThreads) void gdr_seq_kernel(GdrArgs a) {
     if (a.qk_norm) r = inverse_root(row_sum<16>(ss));
     if (tid % 16 == 0) s_norm[w][wave / 2][tok] = wave < 2 ? r : a.scale * r;
   };
-  // the LDS alone is waited for, not the loads on their way
-  auto meet = [&]() {
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-  };
   load_x(0);
   load_x(1);
   load_gates(0);
   load_gates(1);
   stage(0);
   load_x(0);
-  meet();
+  meet_in_lds();
   auto group = [&](int64_t t0, auto parity) {
     constexpr int w = decltype(parity)::value;
     if (a.h_ckpt != nullptr && active)
@@ -196,7 +173,7 @@ __global__ __launch_bounds__(kThreads) void gdr_seq_kernel(GdrArgs a) {
     }
     if constexpr (Y)
       store_one(from_f32<T>(rq * y), rows_y.next(), active && lq < 8 ? v_at : kNowhere);
-    meet();
+    meet_in_lds();
   };
   for (int64_t t0 = 0; t0 < L; t0 += 16) {
     group(t0, std::integral_constant<int, 0>());
