@@ -814,6 +814,11 @@ __global__ __launch_bounds__(kThreads) void gdr_bwd_grads_kernel(GdrBwdArgs ba, 
           }
         }
     }
+#pragma unroll
+    for (int i = 0; i < NH; ++i) {
+      GQ[i] = GQ[i] + DQ[i] * sign;
+      GK[i] = GK[i] + KR[i] * sign;
+    }
     __builtin_amdgcn_sched_barrier(0);
     if (hh + 1 < heads) {
       if (ptiles == 1) load_rows(h + 1, 0);
@@ -882,15 +887,14 @@ __global__ __launch_bounds__(kThreads) void gdr_bwd_grads_kernel(GdrBwdArgs ba, 
         }
     }
     if (ptiles > 1 && hh + 1 < heads) load_rows(h + 1, 0);
-    const f32x4 beo = *reinterpret_cast<const f32x4 *>(&s.beta[16 * own + 4 * g]);
+    const f32x4 beo = *reinterpret_cast<const f32x4 *>(&s.beta[16 * own + 4 * g]) * sign;
     // sums over n of the own rows
     f32x4 kt_ = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < NH; ++i) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) kt_[e] = fmaf(k_at(i, e), T[i][e], kt_[e]);
-      GQ[i] = GQ[i] + DQ[i] * sign;
-      GK[i] = GK[i] + (KR[i] + T[i] * beo) * sign;
+      GK[i] = GK[i] + T[i] * beo;
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
