@@ -448,7 +448,9 @@ struct GradLds {
 
 // One workgroup per (sequence, chunk, group): its heads one after the other, the
 // sums over them in registers.  Wave 4 u + t: row tile t, half u of N.
-template <int NT>
+// FOUR: P is a multiple of 4 (as a choice made here, at each load, it would make
+// each wait for its value).
+template <int NT, bool FOUR>
 __global__ __launch_bounds__(kThreads) void gdr_bwd_grads_kernel(GdrBwdArgs ba, GdrSaved keep, float *red) {
   constexpr int NH = NT / 2;  // tiles of N per wave
   __shared__ GradLds<NT> s;
@@ -517,7 +519,6 @@ __global__ __launch_bounds__(kThreads) void gdr_bwd_grads_kernel(GdrBwdArgs ba, 
   const uint32_t swap = tile_at<NT>(r, 0) / 8 % (2 * NT);
   constexpr uint32_t kKTile = 2 * 16 * 16 * NT;
   const int ptiles = static_cast<int>((P + kCols - 1) / kCols);
-  const bool four = P % 4 == 0;
   // What a thread loads of a head's columns p0 .. + 63: two times 4 columns of a
   // token of E, W and dY, and 4 p by 4 n of a state.  Always a step ahead of
   // where it is staged.
@@ -537,7 +538,7 @@ __global__ __launch_bounds__(kThreads) void gdr_bwd_grads_kernel(GdrBwdArgs ba, 
       ev[i] = __builtin_bit_cast(f32x4, buffer_b128(re, at));
       wv[i] = __builtin_bit_cast(f32x4, buffer_b128(rw, at));
       const uint32_t yat = p < P ? 2 * (tok * row + p) : kNowhere;
-      if (four) {
+      if constexpr (FOUR) {
         yv[i] = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(ry, static_cast<int>(yat), 0, 0));
       } else {
         uint32_t y[4];
@@ -555,7 +556,7 @@ __global__ __launch_bounds__(kThreads) void gdr_bwd_grads_kernel(GdrBwdArgs ba, 
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int q4 = tid % 16;
-      if (!four)  // the columns behind P belong to the next row
+      if constexpr (!FOUR)  // the columns behind P belong to the next row
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           if (p0 + 4 * q4 + e >= P) ev[i][e] = wv[i][e] = 0.f;
@@ -820,10 +821,7 @@ __global__ __launch_bounds__(kThreads) void gdr_bwd_grads_kernel(GdrBwdArgs ba, 
       GK[i] = GK[i] + KR[i] * sign;
     }
     __builtin_amdgcn_sched_barrier(0);
-    if (hh + 1 < heads) {
-      if (ptiles == 1) load_rows(h + 1, 0);
-      load_state(keep.S, h + 1, 0);
-    }
+    if (hh + 1 < heads && ptiles == 1) load_rows(h + 1, 0);
     r = hold(r), g = hold(g);
     // Rows i and the own tile's j as columns.
     {
@@ -886,7 +884,10 @@ __global__ __launch_bounds__(kThreads) void gdr_bwd_grads_kernel(GdrBwdArgs ba, 
           }
         }
     }
-    if (ptiles > 1 && hh + 1 < heads) load_rows(h + 1, 0);
+    if (hh + 1 < heads) {
+      if (ptiles > 1) load_rows(h + 1, 0);
+      load_state(keep.S, h + 1, 0);
+    }
     const f32x4 beo = *reinterpret_cast<const f32x4 *>(&s.beta[16 * own + 4 * g]) * sign;
     // sums over n of the own rows
     f32x4 kt_ = {0.f, 0.f, 0.f, 0.f};
@@ -1035,10 +1036,12 @@ hipError_t launch_gdr_bwd_chunk(const GdrBwdArgs &a, hipStream_t s) {
   const dim3 gg(static_cast<unsigned>(nc), static_cast<unsigned>(f.G), static_cast<unsigned>(f.B));
   if (f.N <= 64) {
     gdr_bwd_chain_kernel<4><<<grid, kThreads, 0, s>>>(a, k, ptiles);
-    gdr_bwd_grads_kernel<4><<<gg, kThreads, 0, s>>>(a, k, red);
+    if (f.P % 4 == 0) gdr_bwd_grads_kernel<4, true><<<gg, kThreads, 0, s>>>(a, k, red);
+    else gdr_bwd_grads_kernel<4, false><<<gg, kThreads, 0, s>>>(a, k, red);
   } else {
     gdr_bwd_chain_kernel<8><<<grid, kThreads, 0, s>>>(a, k, ptiles);
-    gdr_bwd_grads_kernel<8><<<gg, kThreads, 0, s>>>(a, k, red);
+    if (f.P % 4 == 0) gdr_bwd_grads_kernel<8, true><<<gg, kThreads, 0, s>>>(a, k, red);
+    else gdr_bwd_grads_kernel<8, false><<<gg, kThreads, 0, s>>>(a, k, red);
   }
   e = hipGetLastError();
   if (e != hipSuccess) return e;
