@@ -433,7 +433,8 @@ template <int NT>
 struct GradLds {
   // the small ones first, within the offsets that instructions hold
   __attribute__((aligned(16))) double c[kC];
-  __attribute__((aligned(16))) float rk[kC], rq[kC], beta[kC], into[kC], out[kC];
+  __attribute__((aligned(16))) float rk[kC], rq[kC], beta[kC], dt[kC];
+  float head[4];  // A, bias
   float rows[2][3][kC];  // per half of N: the reads of S0, k^.T, k^.(first term of T)
   // z: sums of a column in a row tile below its own, of a row left of its
   // diagonal tile, and of the pairs of the diagonal tile that pass a token
@@ -599,6 +600,31 @@ __global__ __launch_bounds__(kThreads) void gdr_bwd_grads_kernel(GdrBwdArgs ba, 
   // products of two three-part operands, small terms first
   constexpr int kA[6] = {2, 0, 1, 1, 0, 0}, kB[6] = {0, 2, 1, 0, 1, 0};
 
+  // What is one number a token, a head ahead: an array (half of c) a wave, and A and
+  // the bias, in one register.
+  uint32_t gw = 0;
+  auto load_gates = [&](int64_t h) {
+    const uint32_t *vp = reinterpret_cast<const uint32_t *>(keep.vec + ((b * a.H + h) * nc + c) * kGdrVec);
+    const __amdgpu_buffer_rsrc_t words = buffer_of(
+        wave < 2 ? vp + 5 * kC + wave : wave < 4 ? vp + (1 + wave) * kC : wave == 6 ? reinterpret_cast<const uint32_t *>(a.A + h)
+                                                                      : reinterpret_cast<const uint32_t *>(a.dt_bias + h),
+        wave < 2 ? 8 * kC - 4 : wave < 4 ? 4 * kC : wave == 6 || a.dt_bias ? 4 : 0);
+    const __amdgpu_buffer_rsrc_t halves =
+        rows_of(static_cast<const uint16_t *>(wave == 4 ? a.beta : a.dt) + (b * a.L + t0) * a.H + h, left,
+                static_cast<uint32_t>(a.H), 1);
+    if (wave == 4 || wave == 5)
+      gw = static_cast<uint16_t>(__builtin_amdgcn_raw_buffer_load_b16(halves, 2 * lane * static_cast<int>(a.H), 0, 0));
+    else
+      gw = __builtin_amdgcn_raw_buffer_load_b32(words, (wave < 2 ? 8 : 4) * lane, 0, 0);
+  };
+  auto stage_gates = [&]() {
+    if (wave < 2) reinterpret_cast<uint32_t *>(s.c)[2 * lane + wave] = gw;
+    else if (wave == 2 || wave == 3) (wave == 2 ? s.rk : s.rq)[lane] = __uint_as_float(gw);
+    else if (wave == 4 || wave == 5) (wave == 4 ? s.beta : s.dt)[lane] = __uint_as_float(gw << 16);
+    else if (lane == 0) s.head[wave - 6] = __uint_as_float(gw);
+  };
+
+  load_gates(grp * heads);
   load_rows(grp * heads, 0);
   load_state(keep.S, grp * heads, 0);
   for (int64_t hh = 0; hh < heads; ++hh) {
@@ -608,18 +634,9 @@ __global__ __launch_bounds__(kThreads) void gdr_bwd_grads_kernel(GdrBwdArgs ba, 
     for (int i = 0; i < NH; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) kq[i][e] = hold(kq[i][e]);
-    const int64_t h = grp * heads + hh, item = (b * a.H + h) * nc + c;
+    const int64_t h = grp * heads + hh;
     __syncthreads();  // the head before
-    if (tid < kC) {
-      const float *vp = keep.vec + item * kGdrVec;
-      const double *cp = reinterpret_cast<const double *>(vp + 5 * kC);
-      s.c[tid] = cp[tid];
-      s.into[tid] = decay_of(cp[tid]);
-      s.out[tid] = decay_of(cp[kC - 1] - cp[tid]);
-      s.rk[tid] = vp[3 * kC + tid];
-      s.rq[tid] = vp[4 * kC + tid];
-      s.beta[tid] = tid < left ? to_f32(static_cast<const bf16_t *>(a.beta)[(b * a.L + t0 + tid) * a.H + h]) : 0.f;
-    }
+    stage_gates();
     // what goes through the states
     f32x4 DQ[NH], KR[NH], T[NH];
 #pragma unroll
@@ -686,8 +703,14 @@ __global__ __launch_bounds__(kThreads) void gdr_bwd_grads_kernel(GdrBwdArgs ba, 
     const f32x4 rko = *reinterpret_cast<const f32x4 *>(&s.rk[16 * own + 4 * g]);
     const f32x4 rqo = *reinterpret_cast<const f32x4 *>(&s.rq[16 * own + 4 * g]);
     {
-      const f32x4 into = *reinterpret_cast<const f32x4 *>(&s.into[16 * own + 4 * g]);
-      const f32x4 out = *reinterpret_cast<const f32x4 *>(&s.out[16 * own + 4 * g]);
+      f32x4 into, out;
+      const double end = s.c[kC - 1];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const double ct = s.c[16 * own + 4 * g + e];
+        into[e] = decay_of(ct);
+        out[e] = decay_of(end - ct);
+      }
 #pragma unroll
       for (int i = 0; i < NH; ++i) {
         DQ[i] = DQ[i] * (into * a.scale);
@@ -884,10 +907,6 @@ __global__ __launch_bounds__(kThreads) void gdr_bwd_grads_kernel(GdrBwdArgs ba, 
           }
         }
     }
-    if (hh + 1 < heads) {
-      if (ptiles > 1) load_rows(h + 1, 0);
-      load_state(keep.S, h + 1, 0);
-    }
     const f32x4 beo = *reinterpret_cast<const f32x4 *>(&s.beta[16 * own + 4 * g]) * sign;
     // sums over n of the own rows
     f32x4 kt_ = {0.f, 0.f, 0.f, 0.f};
@@ -908,9 +927,14 @@ __global__ __launch_bounds__(kThreads) void gdr_bwd_grads_kernel(GdrBwdArgs ba, 
       *reinterpret_cast<f32x4 *>(&s.rows[half][1][16 * own + 4 * g]) = kt_;
       *reinterpret_cast<f32x4 *>(&s.rows[half][2][16 * own + 4 * g]) = first;
     }
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) dot += __shfl_xor(dot, m);
+    dot = row_sum<64>(dot);
     if (lane == 0) s.dot[wave] = dot;
+    __builtin_amdgcn_sched_barrier(0);
+    if (hh + 1 < heads) {
+      load_gates(h + 1);
+      if (ptiles > 1) load_rows(h + 1, 0);
+      load_state(keep.S, h + 1, 0);
+    }
     __syncthreads();
     if (wave == 0) {
       const int t = lane;
@@ -929,13 +953,13 @@ __global__ __launch_bounds__(kThreads) void gdr_bwd_grads_kernel(GdrBwdArgs ba, 
       const double c20 = lane_value(tiles[2], 15), c30 = lane_value(tiles[3], 15), c31 = lane_value(tiles[3], 31);
       const double corner = t / 16 == 1 ? c20 + c30 : t / 16 == 2 ? c30 + c31 : 0.0;
       const double pairs = corner + dpp_shift<0x111>(row_prefix(below)) + row_suffix(s.zrow[t]) + s.zdiag[t];
-      const float dlog = static_cast<float>(sign * (static_cast<double>(s.into[kC - 1]) * d8 + wave_from(both(0)) +
+      const float dlog = static_cast<float>(sign * (static_cast<double>(decay_of(s.c[kC - 1])) * d8 + wave_from(both(0)) +
                                             wave_before(static_cast<double>(s.beta[t]) * both(2)) + pairs));
-      const float A = a.A[h], bias = a.dt_bias ? a.dt_bias[h] : 0.f;
+      const float A = s.head[0], bias = s.head[1];
       float sa = 0.f, sb = 0.f;
       if (t < left) {
         const int64_t at = (b * a.L + t0 + t) * a.H + h;
-        const float raw = to_f32(static_cast<const bf16_t *>(a.dt)[at]);
+        const float raw = s.dt[t];
         const float d = step_size(raw, bias, a.dt_softplus);
         const float slope = a.dt_softplus ? 1.f / (1.f + fast_exp2(-(raw + bias) * kLog2e)) : 1.f;
         sa = dlog * d;
