@@ -313,24 +313,33 @@ __global__ __launch_bounds__(kThreads) void norm_rows_bwd_kernel(NormArgs a, int
 }
 
 // dw and db: the partial sums of a channel, added in order.  A workgroup holds
-// 64 channels; its 4 waves take every fourth part and meet in LDS.
+// 16 channels; 16 threads a channel take every 16th part and meet in LDS.
+constexpr int kParamChannels = 16;
 __global__ __launch_bounds__(kThreads) void norm_params_kernel(NormArgs a, int64_t parts, const float *pw,
                                                                const float *pb) {
-  __shared__ float s_w[4][64], s_b[4][64];
-  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-  const int64_t d = static_cast<int64_t>(blockIdx.x) * 64 + lane;
+  constexpr int kSplit = kThreads / kParamChannels;
+  __shared__ float s_w[kSplit][kParamChannels], s_b[kSplit][kParamChannels];
+  const int c = threadIdx.x % kParamChannels, k = threadIdx.x / kParamChannels;
+  const int64_t d = static_cast<int64_t>(blockIdx.x) * kParamChannels + c;
   float x = 0.f, y = 0.f;
   if (d < a.D)
-    for (int64_t i = wave; i < parts; i += 4) {
+#pragma unroll 8
+    for (int64_t i = k; i < parts; i += kSplit) {
       x += pw[i * a.D + d];
       y += pb[i * a.D + d];
     }
-  s_w[wave][lane] = x;
-  s_b[wave][lane] = y;
+  s_w[k][c] = x;
+  s_b[k][c] = y;
   __syncthreads();
-  if (wave == 0 && d < a.D) {
-    if (a.dw) a.dw[d] = (s_w[0][lane] + s_w[1][lane]) + (s_w[2][lane] + s_w[3][lane]);
-    if (a.db) a.db[d] = (s_b[0][lane] + s_b[1][lane]) + (s_b[2][lane] + s_b[3][lane]);
+  if (k == 0 && d < a.D) {
+    x = y = 0.f;
+#pragma unroll
+    for (int i = 0; i < kSplit; ++i) {
+      x += s_w[i][c];
+      y += s_b[i][c];
+    }
+    if (a.dw) a.dw[d] = x;
+    if (a.db) a.db[d] = y;
   }
 }
 
@@ -376,12 +385,27 @@ __global__ __launch_bounds__(kThreads) void norm_cols_sums_kernel(NormArgs a, in
   }
 }
 
+// f(slice, place of slice and channel, channel) for a thread's share of a group's
+// partial sums, slice after slice; the division is by 32 bits where it can be.
+template <typename F>
+__device__ __forceinline__ void each_partial(int64_t slices, int64_t W, int64_t D, F &&f) {
+  if (slices * W < int64_t{1} << 31) {
+    const uint32_t w = static_cast<uint32_t>(W), all = static_cast<uint32_t>(slices * W);
+#pragma unroll 4
+    for (uint32_t i = threadIdx.x; i < all; i += kThreads) {
+      const uint32_t slice = i / w, c = i - slice * w;
+      f(slice, slice * D + c, c);
+    }
+  } else {
+    for (int64_t i = threadIdx.x; i < slices * W; i += kThreads) f(i / W, i / W * D + i % W, i % W);
+  }
+}
+
 // one workgroup per (s, g): joins slices and channels
 __global__ __launch_bounds__(kThreads) void norm_cols_join_kernel(NormArgs a, int64_t rows, int64_t slices, float *stat) {
   __shared__ float s_red[4];
   const int64_t W = a.D / a.G, g = blockIdx.x % a.G, s = blockIdx.x / a.G;
   const float *pm = a.ws + s * slices * a.D + g * W, *p2 = pm + a.S * slices * a.D;
-  const int64_t all = slices * W;
   const float inv = 1.f / (static_cast<float>(a.T) * static_cast<float>(W));
   auto count = [&](int64_t slice) {
     return static_cast<float>(slice + 1 < slices ? rows : a.T - slice * rows);
@@ -389,15 +413,15 @@ __global__ __launch_bounds__(kThreads) void norm_cols_join_kernel(NormArgs a, in
   float mean = 0.f;
   if (a.center) {
     float m = 0.f;
-    for (int64_t i = threadIdx.x; i < all; i += kThreads) m = fmaf(count(i / W), pm[(i / W) * a.D + i % W], m);
+    each_partial(slices, W, a.D, [&](int64_t slice, int64_t at, int64_t) { m = fmaf(count(slice), pm[at], m); });
     mean = lanes_sum<256>(m, s_red) * inv;
   }
   float sq = 0.f, left = 0.f;
-  for (int64_t i = threadIdx.x; i < all; i += kThreads) {
-    const float d = pm[(i / W) * a.D + i % W] - mean, nd = count(i / W) * d;
+  each_partial(slices, W, a.D, [&](int64_t slice, int64_t at, int64_t) {
+    const float d = pm[at] - mean, nd = count(slice) * d;
     left += nd;
-    sq += fmaf(nd, d, p2[(i / W) * a.D + i % W]);
-  }
+    sq += fmaf(nd, d, p2[at]);
+  });
   const float delta = a.center ? lanes_sum<256>(left, s_red) * inv : 0.f;
   const float var = not_negative(fmaf(lanes_sum<256>(sq, s_red), inv, -delta * delta));
   const float rstd = 1.f / sqrtf(var + a.eps);
@@ -468,20 +492,27 @@ __global__ __launch_bounds__(kThreads) void norm_cols_bsums_kernel(NormArgs a, i
     bv[e] = a.b ? a.b[d + e] : 0.f;
     s1[e] = s2[e] = 0.f;
   }
-#pragma unroll 2
-  for (int64_t t = t0; t < t1; ++t) {
-    const int64_t at = (s * a.T + t) * a.D + d;
-    const Piece<T, VE> xr = load_piece<T, VE>(static_cast<const T *>(a.x) + at);
-    const Piece<T, VE> yr = load_piece<T, VE>(static_cast<const T *>(a.dy) + at);
-    Piece<T, VE> zr;
-    if (a.z) zr = load_piece<T, VE>(static_cast<const T *>(a.z) + at);
+  constexpr int kAhead = 4;  // tokens loaded together
+  for (int64_t t = t0; t < t1; t += kAhead) {
+    Piece<T, VE> xr[kAhead], yr[kAhead], zr[kAhead];
 #pragma unroll
-    for (int e = 0; e < VE; ++e) {
-      float xh, dn;
-      norm_elem(a, to_f32(xr.v[e]), a.z ? to_f32(zr.v[e]) : 0.f, to_f32(yr.v[e]), wv[e], bv[e], mean, rstd, xh, dn);
-      s1[e] += dn;
-      s2[e] = fmaf(dn, xh, s2[e]);
+    for (int i = 0; i < kAhead; ++i) {
+      const int64_t at = (s * a.T + (t + i < t1 ? t + i : t1 - 1)) * a.D + d;
+      xr[i] = load_piece<T, VE>(static_cast<const T *>(a.x) + at);
+      yr[i] = load_piece<T, VE>(static_cast<const T *>(a.dy) + at);
+      if (a.z) zr[i] = load_piece<T, VE>(static_cast<const T *>(a.z) + at);
     }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (t + i < t1)
+#pragma unroll
+        for (int e = 0; e < VE; ++e) {
+          float xh, dn;
+          norm_elem(a, to_f32(xr[i].v[e]), a.z ? to_f32(zr[i].v[e]) : 0.f, to_f32(yr[i].v[e]), wv[e], bv[e], mean, rstd,
+                    xh, dn);
+          s1[e] += dn;
+          s2[e] = fmaf(dn, xh, s2[e]);
+        }
   }
 #pragma unroll
   for (int e = 0; e < VE; ++e) {
@@ -496,15 +527,13 @@ __global__ __launch_bounds__(kThreads) void norm_cols_bjoin_kernel(NormArgs a, i
   __shared__ float s_red[4];
   const int64_t W = a.D / a.G, g = blockIdx.x % a.G, s = blockIdx.x / a.G;
   const float *p2 = a.ws + s * slices * a.D + g * W, *p1 = p2 + a.S * slices * a.D;
-  const int64_t all = slices * W;
   const float inv = 1.f / (static_cast<float>(a.T) * static_cast<float>(W));
   float x = 0.f, y = 0.f;
-  for (int64_t i = threadIdx.x; i < all; i += kThreads) {
-    const int64_t at = (i / W) * a.D + i % W;
-    const float w = a.w ? a.w[g * W + i % W] : 1.f;
+  each_partial(slices, W, a.D, [&](int64_t, int64_t at, int64_t c) {
+    const float w = a.w ? a.w[g * W + c] : 1.f;
     x = fmaf(w, p1[at], x);
     y = fmaf(w, p2[at], y);
-  }
+  });
   x = lanes_sum<256>(x, s_red);
   y = lanes_sum<256>(y, s_red);
   if (threadIdx.x == 0) {
@@ -612,10 +641,10 @@ RowBwd plan_rows_bwd(int64_t S, int64_t G, int lpg) {
   r.parts = r.blocks * r.rsub;
   return r;
 }
-// Tokens per slice: at least 32 where there are that many, at most 128 slices.
+// Tokens per slice: at least 8 where there are that many, at most 128 slices.
 int64_t slice_rows(int64_t T) {
   int64_t r = ceil_div(T, 128);
-  if (r < 32) r = 32;
+  if (r < 8) r = 8;
   return r;
 }
 int64_t cols_ws_floats(int64_t S, int64_t T, int64_t D, int64_t G) {
@@ -633,7 +662,7 @@ void rows_bwd(const NormArgs &a, hipStream_t s) {
   const RowBwd r = plan_rows_bwd(a.S, a.G, LPG);
   const dim3 grid(static_cast<unsigned>(ceil_div(a.G, r.gsub)), static_cast<unsigned>(r.blocks));
   norm_rows_bwd_kernel<T, VE, LPG, NV><<<grid, kThreads, 0, s>>>(a, r.gsub, r.rows, r.parts);
-  norm_params_kernel<<<static_cast<unsigned>(ceil_div(a.D, 64)), kThreads, 0, s>>>(a, r.parts, a.ws,
+  norm_params_kernel<<<static_cast<unsigned>(ceil_div(a.D, kParamChannels)), kThreads, 0, s>>>(a, r.parts, a.ws,
                                                                                    a.ws + r.parts * a.D);
 }
 template <typename T, int VE, bool BWD>
@@ -669,7 +698,7 @@ void cols(const NormArgs &a, hipStream_t s) {
     norm_cols_bsums_kernel<T, VE><<<gs, kThreads, 0, s>>>(a, rows, slices);
     norm_cols_bjoin_kernel<<<gj, kThreads, 0, s>>>(a, slices, stat);
     norm_cols_bapply_kernel<T, VE><<<ga, kThreads, 0, s>>>(a, stat);
-    norm_params_kernel<<<static_cast<unsigned>(ceil_div(a.D, 64)), kThreads, 0, s>>>(a, a.S * slices, a.ws,
+    norm_params_kernel<<<static_cast<unsigned>(ceil_div(a.D, kParamChannels)), kThreads, 0, s>>>(a, a.S * slices, a.ws,
                                                                                      a.ws + a.S * slices * a.D);
   } else {
     norm_cols_sums_kernel<T, VE><<<gs, kThreads, 0, s>>>(a, rows, slices);
@@ -724,7 +753,7 @@ int64_t group_norm_bwd_ws_floats(int64_t S, int64_t T, int64_t D, int64_t G) {
 hipError_t launch_group_norm_fwd(const NormArgs &a, hipStream_t s) { return launch<false>(a, s); }
 hipError_t launch_group_norm_bwd(const NormArgs &a, hipStream_t s) {
   if (a.S == 0 || a.T == 0) {
-    norm_params_kernel<<<static_cast<unsigned>(ceil_div(a.D, 64)), kThreads, 0, s>>>(a, 0, nullptr, nullptr);
+    norm_params_kernel<<<static_cast<unsigned>(ceil_div(a.D, kParamChannels)), kThreads, 0, s>>>(a, 0, nullptr, nullptr);
     return hipGetLastError();
   }
   return launch<true>(a, s);
