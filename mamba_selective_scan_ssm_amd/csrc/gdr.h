@@ -44,7 +44,11 @@ hipError_t launch_gdr_step(const GdrArgs &a, hipStream_t s);
 
 // By chunks of 64 tokens on the matrix cores (gdr_chunk.hip): bf16, N a
 // multiple of 8 up to 128, L >= kGdrChunkMinL, q, k and the states 16-byte
-// aligned; no workspace.
+// aligned; no workspace.  A chunk takes its time however few its tokens: 8
+// sequences, 32 heads of 128 x 128: 28 us for 32 to 64 tokens, by tokens 26 for 24,
+// 33 for 32, 56 for 64; gradients 112 to 118 us for 32 to 64 tokens, by tokens 137
+// for 24, 173 for 32, 327 for 64.  2 sequences, 80 heads of 64 x 128: gradients 68 to
+// 70, by tokens 73 for 16, 87 for 24, 149 for 64.
 constexpr int64_t kGdrChunkMinL = 32;
 bool gdr_chunk_applies(const GdrArgs &a);
 hipError_t launch_gdr_chunk(const GdrArgs &a, hipStream_t s);
@@ -91,7 +95,11 @@ hipError_t launch_gdr_bwd_seq(const GdrBwdArgs &a, hipStream_t s);
 // of the normalised q and k; sc_part: (2, tiles, B, L, H), the gradients of
 // beta and of the log decay; red: gdr_reduce_ws_floats floats.
 int64_t gdr_reduce_ws_floats(int64_t B, int64_t L, int64_t H);
-// the last of them alone: dA and dbias from nblk partial sums (2, H) each
+// Those of q and k alone, over `tiles` and each group's share of `parts` (H, or G
+// where the heads are summed already); and dA and dbias alone, from nblk partial
+// sums (2, H) each.
+hipError_t launch_gdr_reduce_qk(const GdrBwdArgs &a, int64_t tiles, int64_t parts, const float *dq_part,
+                                const float *dk_part, hipStream_t s);
 hipError_t launch_gdr_reduce_params(const GdrBwdArgs &a, int64_t nblk, const float *red, hipStream_t s);
 hipError_t launch_gdr_reduce(const GdrBwdArgs &a, int64_t tiles, const float *dq_part, const float *dk_part,
                              const float *sc_part, float *red, hipStream_t s);

@@ -243,11 +243,12 @@ __device__ __forceinline__ float wave_sum(float v) {
 }
 
 // dq (blockIdx.y 0) and dk (1): one wave per (token, group) sums the partial
-// gradients of the group's heads and tiles, in order, and takes them through
-// the norm: with u = r x, dx = r (g - u (g . u)).
+// gradients (tiles, B, L, parts, N) of the group's share of the parts (its heads, or
+// itself) and the tiles, in order, and takes them through the norm: with u = r x,
+// dx = r (g - u (g . u)).
 template <typename T>
-__global__ __launch_bounds__(kThreads) void gdr_reduce_qk_kernel(GdrBwdArgs ba, int64_t tiles, const float *dq_part,
-                                                                 const float *dk_part) {
+__global__ __launch_bounds__(kThreads) void gdr_reduce_qk_kernel(GdrBwdArgs ba, int64_t tiles, int64_t parts,
+                                                                 const float *dq_part, const float *dk_part) {
   const GdrArgs &a = ba.f;
   const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
   const int64_t item = static_cast<int64_t>(blockIdx.x) * kWaves + wave;
@@ -256,7 +257,7 @@ __global__ __launch_bounds__(kThreads) void gdr_reduce_qk_kernel(GdrBwdArgs ba, 
   const float *part = is_k ? dk_part : dq_part;
   const T *x = static_cast<const T *>(is_k ? a.k : a.q) + item * a.N;
   T *out = static_cast<T *>(is_k ? ba.dk : ba.dq) + item * a.N;
-  const int64_t tok = item / a.G, g = item % a.G, per = a.H / a.G;
+  const int64_t tok = item / a.G, g = item % a.G, per = parts / a.G;
   constexpr int kPer = 4;  // N <= 256
   float sum[kPer], xv[kPer];
 #pragma unroll
@@ -267,7 +268,7 @@ __global__ __launch_bounds__(kThreads) void gdr_reduce_qk_kernel(GdrBwdArgs ba, 
     if (n < a.N)
       for (int64_t t = 0; t < tiles; ++t)
         for (int64_t hh = 0; hh < per; ++hh)
-          sum[i] += part[((t * a.B * a.L + tok) * a.H + g * per + hh) * a.N + n];
+          sum[i] += part[((t * a.B * a.L + tok) * parts + g * per + hh) * a.N + n];
   }
   if (a.qk_norm) {
     float ss = 0.f, gx = 0.f;
@@ -363,17 +364,24 @@ hipError_t launch_gdr_reduce(const GdrBwdArgs &a, int64_t tiles, const float *dq
   const int64_t nblk = (BL + kTokBlock - 1) / kTokBlock;
   const bool bf = f.dt_type == DType::BF16;
   if (BL > 0) {
-    const dim3 gq(static_cast<unsigned>((BL * f.G + kWaves - 1) / kWaves), 2);
     const dim3 gg(static_cast<unsigned>(nblk), static_cast<unsigned>((f.H + 63) / 64));
+    const hipError_t e = launch_gdr_reduce_qk(a, tiles, f.H, dq_part, dk_part, s);
+    if (e != hipSuccess) return e;
     if (bf) {
-      gdr_reduce_qk_kernel<bf16_t><<<gq, kThreads, 0, s>>>(a, tiles, dq_part, dk_part);
       gdr_reduce_gates_kernel<bf16_t><<<gg, kThreads, 0, s>>>(a, tiles, sc_part, red);
     } else {
-      gdr_reduce_qk_kernel<float><<<gq, kThreads, 0, s>>>(a, tiles, dq_part, dk_part);
       gdr_reduce_gates_kernel<float><<<gg, kThreads, 0, s>>>(a, tiles, sc_part, red);
     }
   }
   return launch_gdr_reduce_params(a, nblk, red, s);
+}
+hipError_t launch_gdr_reduce_qk(const GdrBwdArgs &a, int64_t tiles, int64_t parts, const float *dq_part,
+                                const float *dk_part, hipStream_t s) {
+  const GdrArgs &f = a.f;
+  const dim3 grid(static_cast<unsigned>((f.B * f.L * f.G + kWaves - 1) / kWaves), 2);
+  if (f.dt_type == DType::BF16) gdr_reduce_qk_kernel<bf16_t><<<grid, kThreads, 0, s>>>(a, tiles, parts, dq_part, dk_part);
+  else gdr_reduce_qk_kernel<float><<<grid, kThreads, 0, s>>>(a, tiles, parts, dq_part, dk_part);
+  return hipGetLastError();
 }
 hipError_t launch_gdr_reduce_params(const GdrBwdArgs &a, int64_t nblk, const float *red, hipStream_t s) {
   gdr_reduce_params_kernel<<<static_cast<unsigned>(a.f.H), 64, 0, s>>>(a, nblk, red);

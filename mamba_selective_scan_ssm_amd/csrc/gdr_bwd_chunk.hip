@@ -451,13 +451,18 @@ struct GradLds {
 // sums over them in registers.  Wave 4 u + t: row tile t, half u of N.
 // FOUR: P is a multiple of 4 (as a choice made here, at each load, it would make
 // each wait for its value).
-template <int NT, bool FOUR>
-__global__ __launch_bounds__(kThreads) void gdr_bwd_grads_kernel(GdrBwdArgs ba, GdrSaved keep, float *red) {
+// SPLIT: the heads of a group are shared by `split` workgroups.
+template <int NT, bool FOUR, bool SPLIT>
+__global__ __launch_bounds__(kThreads) void gdr_bwd_grads_kernel(GdrBwdArgs ba, GdrSaved keep, int64_t split,
+                                                                                        float *qk_part, float *red) {
   constexpr int NH = NT / 2;  // tiles of N per wave
   __shared__ GradLds<NT> s;
   const GdrArgs &a = ba.f;
   const int64_t nc = (a.L + kC - 1) / kC, heads = a.H / a.G;
-  const int64_t grp = blockIdx.y, b = blockIdx.z, c = blockIdx.x;
+  const int64_t part = SPLIT ? blockIdx.z % split : 0;
+  const int64_t grp = blockIdx.y, b = SPLIT ? blockIdx.z / split : blockIdx.z, c = blockIdx.x;
+  const int64_t before = SPLIT ? part * heads / split : 0;
+  const int64_t first_head = grp * heads + before, count = SPLIT ? (part + 1) * heads / split - before : heads;
   const int tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64);
   const int r = lane % 16, g = lane / 16, own = wave % 4, half = wave / 4;
   const MinusOne minus;
@@ -624,17 +629,17 @@ __global__ __launch_bounds__(kThreads) void gdr_bwd_grads_kernel(GdrBwdArgs ba, 
     else if (lane == 0) s.head[wave - 6] = __uint_as_float(gw);
   };
 
-  load_gates(grp * heads);
-  load_rows(grp * heads, 0);
-  load_state(keep.S, grp * heads, 0);
-  for (int64_t hh = 0; hh < heads; ++hh) {
+  load_gates(first_head);
+  load_rows(first_head, 0);
+  load_state(keep.S, first_head, 0);
+  for (int64_t hh = 0; hh < count; ++hh) {
+    const int64_t h = first_head + hh;
     // What comes from the lane is made anew for each head and part, not kept in registers.
     int r = hold(lane % 16), g = hold(lane / 16);
 #pragma unroll
     for (int i = 0; i < NH; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) kq[i][e] = hold(kq[i][e]);
-    const int64_t h = grp * heads + hh;
     __syncthreads();  // the head before
     stage_gates();
     // what goes through the states
@@ -844,7 +849,7 @@ __global__ __launch_bounds__(kThreads) void gdr_bwd_grads_kernel(GdrBwdArgs ba, 
       GK[i] = GK[i] + KR[i] * sign;
     }
     __builtin_amdgcn_sched_barrier(0);
-    if (hh + 1 < heads && ptiles == 1) load_rows(h + 1, 0);
+    if (hh + 1 < count && ptiles == 1) load_rows(h + 1, 0);
     r = hold(r), g = hold(g);
     // Rows i and the own tile's j as columns.
     {
@@ -930,7 +935,7 @@ __global__ __launch_bounds__(kThreads) void gdr_bwd_grads_kernel(GdrBwdArgs ba, 
     dot = row_sum<64>(dot);
     if (lane == 0) s.dot[wave] = dot;
     __builtin_amdgcn_sched_barrier(0);
-    if (hh + 1 < heads) {
+    if (hh + 1 < count) {
       load_gates(h + 1);
       if (ptiles > 1) load_rows(h + 1, 0);
       load_state(keep.S, h + 1, 0);
@@ -979,6 +984,21 @@ __global__ __launch_bounds__(kThreads) void gdr_bwd_grads_kernel(GdrBwdArgs ba, 
     }
   }
 
+  if constexpr (SPLIT) {  // the heads' parts are summed, and taken through the norms, behind this
+    const int64_t all = a.B * a.L * a.G * N;
+#pragma unroll
+    for (int i = 0; i < NH; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int tok = 16 * own + 4 * g + e, n = 16 * (NH * half + i) + r;
+        if (tok < left && n < N) {
+          float *to = qk_part + part * all + ((b * a.L + t0 + tok) * a.G + grp) * N + n;
+          to[0] = GQ[i][e];
+          to[split * all] = GK[i][e];
+        }
+      }
+    return;
+  }
   // through the norms: with u = r x, dx = r (g - u (g . u))
   const f32x4 rko = *reinterpret_cast<const f32x4 *>(&s.rk[16 * own + 4 * g]);
   const f32x4 rqo = *reinterpret_cast<const f32x4 *>(&s.rq[16 * own + 4 * g]);
@@ -1034,9 +1054,32 @@ bool gdr_bwd_chunk_applies(const GdrBwdArgs &a) {
   return gdr_chunk_applies(a.f) && aligned16(a.dy) && aligned16(a.dh_final) && aligned16(a.dh0);
 }
 
+// Into how many workgroups the heads of a group are split: as many as make the
+// turns of 256 CUs, times the heads of a turn, fewest.  2 sequences of 64 tokens,
+// 80 heads of 64 x 128 in 8 groups: 170 us with a group's 10 heads one after the
+// other, 69 split.
+namespace {
+int64_t head_split(int64_t B, int64_t nc, int64_t G, int64_t heads) {
+  constexpr int64_t kCus = 256;
+  int64_t best = 1, least = (B * nc * G + kCus - 1) / kCus * heads;
+  for (int64_t split = 2; split <= heads && split <= 64 && B * split <= 65535; ++split) {
+    const int64_t turns = (B * nc * G * split + kCus - 1) / kCus * ((heads + split - 1) / split);
+    if (turns < least) {
+      least = turns;
+      best = split;
+    }
+  }
+  return best;
+}
+int64_t split_floats(int64_t split, int64_t B, int64_t L, int64_t G, int64_t N) {
+  return split > 1 ? pad4(2 * split * B * L * G * N) : 0;
+}
+}  // namespace
+
 int64_t gdr_bwd_chunk_ws_floats(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G, int64_t N) {
-  const int64_t items = B * H * ((L + kC - 1) / kC);
-  return items * (2 * pad4(P * N) + 2 * kC * P + 20 * 256 + kGdrVec) + pad4(2 * B * ((L + kC - 1) / kC) * H);
+  const int64_t nc = (L + kC - 1) / kC, items = B * H * nc;
+  return items * (2 * pad4(P * N) + 2 * kC * P + 20 * 256 + kGdrVec) + pad4(2 * B * nc * H) +
+         split_floats(head_split(B, nc, G, H / G), B, L, G, N);
 }
 
 hipError_t launch_gdr_bwd_chunk(const GdrBwdArgs &a, hipStream_t s) {
@@ -1057,18 +1100,29 @@ hipError_t launch_gdr_bwd_chunk(const GdrBwdArgs &a, hipStream_t s) {
   if (e != hipSuccess) return e;
   const int64_t ptiles = (f.P + kCols - 1) / kCols, per = f.H / f.G * ptiles;
   const unsigned grid = static_cast<unsigned>((f.B * f.G + 7) / 8 * 8 * per);
-  const dim3 gg(static_cast<unsigned>(nc), static_cast<unsigned>(f.G), static_cast<unsigned>(f.B));
-  if (f.N <= 64) {
-    gdr_bwd_chain_kernel<4><<<grid, kThreads, 0, s>>>(a, k, ptiles);
-    if (f.P % 4 == 0) gdr_bwd_grads_kernel<4, true><<<gg, kThreads, 0, s>>>(a, k, red);
-    else gdr_bwd_grads_kernel<4, false><<<gg, kThreads, 0, s>>>(a, k, red);
-  } else {
-    gdr_bwd_chain_kernel<8><<<grid, kThreads, 0, s>>>(a, k, ptiles);
-    if (f.P % 4 == 0) gdr_bwd_grads_kernel<8, true><<<gg, kThreads, 0, s>>>(a, k, red);
-    else gdr_bwd_grads_kernel<8, false><<<gg, kThreads, 0, s>>>(a, k, red);
-  }
+  const int64_t split = head_split(f.B, nc, f.G, f.H / f.G);
+  float *qk_part = red + pad4(2 * f.B * nc * f.H);
+  const dim3 gg(static_cast<unsigned>(nc), static_cast<unsigned>(f.G), static_cast<unsigned>(f.B * split));
+  if (f.N <= 64) gdr_bwd_chain_kernel<4><<<grid, kThreads, 0, s>>>(a, k, ptiles);
+  else gdr_bwd_chain_kernel<8><<<grid, kThreads, 0, s>>>(a, k, ptiles);
+  auto grads = [&](auto tiles, auto four) {
+    constexpr int NT = decltype(tiles)::value;
+    constexpr bool FOUR = decltype(four)::value;
+    if (split > 1) gdr_bwd_grads_kernel<NT, FOUR, true><<<gg, kThreads, 0, s>>>(a, k, split, qk_part, red);
+    else gdr_bwd_grads_kernel<NT, FOUR, false><<<gg, kThreads, 0, s>>>(a, k, split, qk_part, red);
+  };
+  auto of = [&](auto tiles) {
+    if (f.P % 4 == 0) grads(tiles, std::true_type());
+    else grads(tiles, std::false_type());
+  };
+  if (f.N <= 64) of(std::integral_constant<int, 4>());
+  else of(std::integral_constant<int, 8>());
   e = hipGetLastError();
   if (e != hipSuccess) return e;
+  if (split > 1) {
+    e = launch_gdr_reduce_qk(a, split, f.G, qk_part, qk_part + split * f.B * f.L * f.G * f.N, s);
+    if (e != hipSuccess) return e;
+  }
   return launch_gdr_reduce_params(a, f.B * nc, red, s);
 }
 

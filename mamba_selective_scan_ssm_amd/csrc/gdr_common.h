@@ -28,12 +28,12 @@ __device__ __forceinline__ float join_rows(float x, float y) {
 // getting it.
 template <int LPC>
 __device__ __forceinline__ float row_sum(float v) {
+  if constexpr (LPC == 32) v = join_rows(v, v);
   if constexpr (LPC >= 2) v += dpp_get<0xB1>(v);
   if constexpr (LPC >= 4) v += dpp_get<0x4E>(v);
   if constexpr (LPC >= 8) v += dpp_get<0x141>(v);
   if constexpr (LPC >= 16) v += dpp_get<0x140>(v);
-  if constexpr (LPC >= 32) v = join_rows(v, v);
-  if constexpr (LPC >= 64) v = join_halves(v, v);
+  if constexpr (LPC == 64) v = join_halves(join_rows(v, v), join_rows(v, v));
   return v;
 }
 
@@ -178,15 +178,20 @@ __device__ __forceinline__ void lds_row(const float *p, int lq, float *v) {
   for (int j = 0; j < NV; ++j) load4(p + 4 * (lq + LPC * j), v + 4 * j);
 }
 
+// The products of a row's states: of four at a time, fours 16 lanes apart added so
+// that 16 and 32 lanes a row give the same sum to the last bit.
 template <int LPC, int NV>
 __device__ __forceinline__ float row_dot(const float *x, const float *y) {
-  float s0 = 0.f, s1 = 0.f;
+  float s[NV];
 #pragma unroll
-  for (int i = 0; i < 4 * NV; i += 2) {
-    s0 = fmaf(x[i], y[i], s0);
-    s1 = fmaf(x[i + 1], y[i + 1], s1);
+  for (int j = 0; j < NV; ++j) {
+    const float *u = x + 4 * j, *v = y + 4 * j;
+    s[j] = fmaf(u[2], v[2], u[0] * v[0]) + fmaf(u[3], v[3], u[1] * v[1]);
   }
-  return row_sum<LPC>(s0 + s1);
+  if constexpr (NV == 4) return row_sum<LPC>((s[0] + s[2]) + (s[1] + s[3]));
+  if constexpr (NV == 3) return row_sum<LPC>((s[0] + s[2]) + s[1]);
+  if constexpr (NV == 2) return row_sum<LPC>(s[0] + s[1]);
+  return row_sum<LPC>(s[0]);
 }
 
 // One token of one row: S <- a S + (beta e rk) k with e = v - a rk (S . k);

@@ -435,3 +435,41 @@ def test_nan_stays_in_its_row():
     bad[0, 70:, 1, 5] = True
     assert torch.isnan(y[bad]).all() and torch.equal(y[~bad], clean[~bad])
     assert torch.isnan(h[0, 1, 5]).all() and not torch.isnan(h[0, 1, :5]).any()
+
+
+# what only larger calls take: several rows a lane group, 16 lanes a row of more
+# than 64 states, the heads of a group in one workgroup or shared unevenly by two
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("S,T,H,P,G,N", [(96, 2, 8, 72, 2, 20), (88, 1, 8, 40, 4, 64), (45, 2, 8, 90, 8, 100),
+                                         (64, 1, 8, 53, 2, 200)])
+def test_decode_of_many(S, T, H, P, G, N, dtype):
+    test_decode(S, T, H, P, G, N, True, dtype)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("B,L,H,P,G,N", [(4, 20, 8, 65, 2, 70), (4, 19, 8, 65, 4, 130), (5, 12, 7, 60, 7, 255)])
+def test_many_rows(B, L, H, P, G, N, dtype):
+    _say("gdr of many rows", B, L, H, P, G, N, dtype)
+    w = ref.make_gdr(B, L, H, P, G, N, dtype, 60 + N)
+    check_fwd(w, True, "prefill")
+    check_bwd(w, True, "gradients")
+
+
+@pytest.mark.parametrize("B,L,H,P,G,N", [(8, 65, 32, 16, 16, 16), (8, 66, 24, 13, 8, 72), (8, 65, 32, 12, 16, 72),
+                                         (4, 65, 24, 20, 8, 40)])
+def test_gradients_of_heads_sharing_keys(B, L, H, P, G, N):
+    _say("gdr_bwd of many workgroups", B, L, H, P, G, N)
+    w = ref.make_gdr(B, L, H, P, G, N, BF16, 61)
+    check_bwd(w, True, "gradients")
+
+
+@pytest.mark.parametrize("N", [68, 130, 192, 256])
+def test_a_batch_of_many_rows_is_its_sequences(N):
+    """Bitwise, though few rows take more lanes each than many do."""
+    _say("gdr_fwd of a batch and of its sequences", N)
+    w = ref.make_gdr(5, 21, 8, 65, 2, N, F32, 62)
+    y, h = fwd(w, True)
+    for b in (0, 4):
+        one = {n: t if t is None or n in ("A", "bias") else t[b:b + 1].contiguous() for n, t in w.items()}
+        y1, h1 = fwd(one, True)
+        assert torch.equal(y[b:b + 1], y1) and torch.equal(h[b:b + 1], h1)
