@@ -450,8 +450,9 @@ ssm_status ssm_conv1d_update(int64_t S, int64_t D, int64_t K, ssm_dtype dt, floa
  * workspace : ssm_gdr_fwd_workspace_size() bytes, 16-byte aligned (NULL where
  *             that is 0); contents ignored on entry; two calls that overlap
  *             in time must not share it.
- * Sizes: 1 <= N <= SSM_GDR_MAX_N, G divides H, B and H <= 65535 (else
- * SSM_ERR_UNSUPPORTED); any L >= 0 (L == 0 writes h_final = h0) and P >= 0.
+ * Sizes: 1 <= N <= SSM_GDR_MAX_N, G divides H, B and H <= 65535, H P <= 2^24
+ * (else SSM_ERR_UNSUPPORTED); any L >= 0 (L == 0 writes h_final = h0) and
+ * P >= 0.  A sequence's results do not depend on the batch (bitwise).
  */
 ssm_status ssm_gdr_fwd(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G, int64_t N,
                        ssm_dtype dt, const void *q, const void *k, const void *v,

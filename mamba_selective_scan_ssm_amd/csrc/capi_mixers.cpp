@@ -26,7 +26,9 @@ ssm_status gdr_sizes(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G, int6
   if (N < 1 || N > SSM_GDR_MAX_N) return SSM_ERR_UNSUPPORTED;
   if (G <= 0 || H % G != 0) return SSM_ERR_UNSUPPORTED;
   if (B > kMaxGridYZ || H > kMaxGridYZ) return SSM_ERR_UNSUPPORTED;
-  int64_t tok, ckpt;
+  int64_t tok, ckpt, chans;
+  // the rows of a chunk of 64 tokens within 32-bit offsets
+  if (!product({H, P}, &chans) || chans > int64_t{1} << 24) return SSM_ERR_UNSUPPORTED;
   if (!product({B, L, G, N}, &z->nQ) || !product({B, L, H, P}, &z->nV) || !product({B, L, H}, &z->nT) ||
       !product({B, H, P, N}, &z->nS) || !product({B, L, H, P, N}, &ckpt) || !product({B, L, G}, &tok) ||
       tok > kMaxGridX || P > kMaxGridX)

@@ -500,3 +500,10 @@ def test_mixer_binding_refusals():
         ssm.group_norm_fwd(x, 2, activation="gelu")
     with pytest.raises(ValueError, match="required"):
         ssm.group_norm_bwd(x, 2, x, None, None)
+
+
+def test_gdr_channels_of_a_token(lib):
+    """More than 2^24 channels a token are refused by all entry points."""
+    assert gdr(lib, H=4096, Pd=4097, N=1, L=0) == UNSUPPORTED
+    assert gdr(lib, H=2, Pd=1 << 40, N=1, L=0) == UNSUPPORTED
+    assert lib.ssm_gdr_bwd_workspace_size(1, 8, 4096, 4097, 2, 8, BF16, 1) == 0
