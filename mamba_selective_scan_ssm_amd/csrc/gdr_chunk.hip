@@ -29,6 +29,15 @@
 // two such operands leave out what is below 2^-24), what only y depends on in
 // two (at most 2^-16 of each term; y is rounded to bf16, by up to 2^-8).
 // Accumulation is fp32.
+//
+// Bound by the latency of both roles, not by a unit: 2 x 8192 tokens, 80 heads of
+// 64 x 128 take 0.56 ms (115 TFLOP/s of the 64 GFLOP that the rule needs, 0.75 TB/s
+// of its inputs and outputs), 10 thousand cycles a chunk, in which the preparation
+// and the chain each run from end to end; of those the matrix cores are busy 3.7
+// thousand a SIMD, the LDS 5.1 (1.9 of them conflicts, of transposing reads and
+// half-width writes).  160 workgroups on 256 CUs: a chunk's time is what counts.
+// Splitting P finer doubles the preparation for each CU that then holds two, and a
+// preparation of its own for all chunks writes and reads more than it takes away.
 #include "device_common.h"
 #include "gdr.h"
 #include "gdr_common.h"

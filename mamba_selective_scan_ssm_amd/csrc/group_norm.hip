@@ -20,6 +20,12 @@
 //    group sums are sums of its per-channel ones weighted by w); and a pass
 //    that applies them.
 // All sums are fp32 and in a fixed order.
+//
+// Bound by HBM where there is work: forward of 8 x 4096 tokens, 5120 channels in 8
+// groups, gate first: 0.200 ms, 5.0 TB/s, what a copy reaches; forward and backward
+// of 2 x 4096 tokens in 80 groups, gate last: 0.162 ms (54 + 106 + 5 us; the backward,
+// 12 waves a CU by its registers, 4.0 TB/s).  Small ones by their launches: 4 x 1003
+// tokens of 640 channels in 32 groups, fp32, over whole sequences 46 us in 7 kernels.
 #include "device_common.h"
 #include "group_norm.h"
 
