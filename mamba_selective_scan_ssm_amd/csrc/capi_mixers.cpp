@@ -123,20 +123,15 @@ ssm_status ssm_gdr_decode_steps(int64_t S, int64_t T, int64_t H, int64_t P, int6
   return hip_status(ssm::launch_gdr_step(a, static_cast<hipStream_t>(stream)));
 }
 
-// Whether sizes and type go by chunks, where the tensors are aligned too.
-static bool gdr_chunk_sizes(int64_t L, int64_t H, int64_t P, int64_t G, int64_t N, ssm_dtype dt) {
-  ssm::GdrArgs a{};
-  a.L = L; a.H = H; a.P = P; a.G = G; a.N = N;
-  a.dt_type = dt == SSM_BF16 ? DType::BF16 : DType::F32;
-  return ssm::gdr_chunk_applies(a);
-}
-
 size_t ssm_gdr_bwd_workspace_size(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G, int64_t N, ssm_dtype dt,
                                   int32_t aligned) {
   GdrSizes z;
   if (gdr_sizes(B, L, H, P, G, N, dt, 0, nullptr, &z) != SSM_OK || P < 1 || H < 1) return 0;
   if (aligned != 0 && aligned != 1) return 0;
-  const bool chunks = aligned == 1 && gdr_chunk_sizes(L, H, P, G, N, dt);
+  ssm::GdrBwdArgs a{};  // no pointers: all of them aligned
+  a.f.B = B; a.f.L = L; a.f.H = H; a.f.P = P; a.f.G = G; a.f.N = N;
+  a.f.dt_type = dt == SSM_BF16 ? DType::BF16 : DType::F32;
+  const bool chunks = aligned == 1 && ssm::gdr_bwd_chunk_applies(a);
   return static_cast<size_t>(chunks ? ssm::gdr_bwd_chunk_ws_floats(B, L, H, P, G, N)
                                     : ssm::gdr_bwd_seq_ws_floats(B, L, H, P, G, N)) * 4;
 }

@@ -507,3 +507,14 @@ def test_gdr_channels_of_a_token(lib):
     assert gdr(lib, H=4096, Pd=4097, N=1, L=0) == UNSUPPORTED
     assert gdr(lib, H=2, Pd=1 << 40, N=1, L=0) == UNSUPPORTED
     assert lib.ssm_gdr_bwd_workspace_size(1, 8, 4096, 4097, 2, 8, BF16, 1) == 0
+
+
+def test_gdr_bwd_workspace_follows_the_path(lib):
+    """What goes by tokens whatever the alignment says needs the tokens' workspace."""
+    size = lib.ssm_gdr_bwd_workspace_size
+    by_chunks, by_tokens = (2, 64, 4, 64, 2, 128, BF16), [
+        (2, 31, 4, 64, 2, 128, BF16), (2, 64, 4, 64, 2, 128, F32), (2, 64, 4, 64, 2, 130, BF16),
+        (1, 64, 1, (1 << 20) + 1, 1, 8, BF16), (65535, 32, 65535, 1, 1, 8, BF16)]
+    assert size(*by_chunks, 1) != size(*by_chunks, 0)
+    for c in by_tokens:
+        assert size(*c, 1) == size(*c, 0) > 0, c

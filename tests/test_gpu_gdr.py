@@ -473,3 +473,21 @@ def test_a_batch_of_many_rows_is_its_sequences(N):
         one = {n: t if t is None or n in ("A", "bias") else t[b:b + 1].contiguous() for n, t in w.items()}
         y1, h1 = fwd(one, True)
         assert torch.equal(y[b:b + 1], y1) and torch.equal(h[b:b + 1], h1)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_decode_of_many_is_its_sequences(dtype):
+    import mamba_selective_scan_ssm_amd as ssm
+    _say("gdr_decode_steps of a batch and of its sequences", dtype)
+    S, T, H, P, G, N = 90, 2, 8, 53, 4, 100
+    w = ref.make_gdr(S, T, H, P, G, N, dtype, 63)
+    q, k, v, dt, A, beta, h0, bias = up(w, "q", "k", "v", "dt", "A", "beta", "h0", "bias")
+    kw = {"qk_norm": True, "dt_bias": bias, "dt_softplus": bias is not None}
+    pool = h0.clone()
+    y = ssm.gdr_decode_steps(pool, q, k, v, dt, A, beta, **kw)
+    for s in (0, 57, S - 1):
+        one = h0[s:s + 1].clone()
+        part = [t[s:s + 1].contiguous() for t in (q, k, v, dt)]
+        ys = ssm.gdr_decode_steps(one, *part, A, beta[s:s + 1].contiguous(), **kw)
+        torch.cuda.synchronize()
+        assert torch.equal(y[s:s + 1], ys) and torch.equal(pool[s:s + 1], one)
