@@ -112,18 +112,11 @@ __device__ __forceinline__ void load4(const float *p, float *v) {
   v[2] = f.z;
   v[3] = f.w;
 }
-__device__ __forceinline__ void load4(const bf16_t *p, float *v) {
-  const uint2 u = *reinterpret_cast<const uint2 *>(p);
-  v[0] = __uint_as_float(u.x << 16);
-  v[1] = __uint_as_float(u.x & 0xffff0000u);
-  v[2] = __uint_as_float(u.y << 16);
-  v[3] = __uint_as_float(u.y & 0xffff0000u);
-}
 
 // A lane's part of a row of N values; states past N read as 0.  VEC: N is a
 // multiple of 4 and the row is aligned to four elements.
-template <bool VEC, int LPC, int NV, typename T>
-__device__ __forceinline__ void load_row(const T *p, int lq, int64_t N, float *v) {
+template <bool VEC, int LPC, int NV>
+__device__ __forceinline__ void load_row(const float *p, int lq, int64_t N, float *v) {
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int n = 4 * (lq + LPC * j);
@@ -132,7 +125,7 @@ __device__ __forceinline__ void load_row(const T *p, int lq, int64_t N, float *v
       else v[4 * j] = v[4 * j + 1] = v[4 * j + 2] = v[4 * j + 3] = 0.f;
     } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[4 * j + e] = n + e < N ? to_f32(p[n + e]) : 0.f;
+      for (int e = 0; e < 4; ++e) v[4 * j + e] = n + e < N ? p[n + e] : 0.f;
     }
   }
 }

@@ -70,9 +70,9 @@ struct Rows {
 // is.  Y false: the states alone, entering every kGdrSeg tokens (h_ckpt).
 template <typename T, int LPC, int NV, bool Y, bool VEC>
 __global__ __launch_bounds__(kThreads) void gdr_seq_kernel(GdrArgs a) {
-  constexpr int kRows = kThreads / LPC, NP = 4 * LPC * NV, kFours = (NP + 63) / 64;
+  constexpr int kRows = kThreads / LPC, NP = 4 * LPC * NV, kFours = NP / 64;
   constexpr uint32_t kSize = sizeof(T);
-  static_assert(kGdrSeg == 8 && kThreads == 16 * 16, "16 lanes for each of 8 rows of k and q");
+  static_assert(kGdrSeg == 8 && kThreads == 16 * 16 && NP % 64 == 0, "16 lanes for each of 8 rows of k and q");
   __shared__ __attribute__((aligned(16))) float s_x[2][2][8][NP];  // k, q
   __shared__ float s_norm[2][2][8];                                // and 1 / |k|, scale / |q|
   const int64_t L = a.L, H = a.H, P = a.P, G = a.G, N = a.N;
@@ -125,8 +125,7 @@ __global__ __launch_bounds__(kThreads) void gdr_seq_kernel(GdrArgs a) {
         f[e] = to_f32(x[w][j].v[e]);
         ss = fmaf(f[e], f[e], ss);
       }
-      const int n = 4 * (tid % 16 + 16 * j);
-      if (NP % 64 == 0 || n < NP) *reinterpret_cast<float4 *>(&s_x[w][wave / 2][tok][n]) = make_float4(f[0], f[1], f[2], f[3]);
+      *reinterpret_cast<float4 *>(&s_x[w][wave / 2][tok][4 * (tid % 16 + 16 * j)]) = make_float4(f[0], f[1], f[2], f[3]);
     }
     float r = 1.f;
     if (a.qk_norm) r = inverse_root(row_sum<16>(ss));
@@ -237,8 +236,8 @@ __global__ __launch_bounds__(kThreads) void gdr_step_kernel(GdrArgs a) {
         sk = fmaf(kv[i], kv[i], sk);
         sq = fmaf(qv[i], qv[i], sq);
       }
-      rk = 1.f / sqrtf(row_sum<LPC>(sk) + kQkNormEps);
-      rq = a.scale * (1.f / sqrtf(row_sum<LPC>(sq) + kQkNormEps));
+      rk = inverse_root(row_sum<LPC>(sk) + kQkNormEps);
+      rq = a.scale * inverse_root(row_sum<LPC>(sq) + kQkNormEps);
     }
 #pragma unroll
     for (int i = 0; i < R; ++i) {
