@@ -51,6 +51,18 @@ hipError_t launch_gdr_step(const GdrArgs &a, hipStream_t s);
 // 70, by tokens 73 for 16, 87 for 24, 149 for 64.
 constexpr int64_t kGdrChunkMinL = 32;
 bool gdr_chunk_applies(const GdrArgs &a);
+// Columns of a state that a workgroup of a chain takes, 16 a wave: as few as leave
+// each a CU of its own, where the waves that prepare the chunks are in the way of
+// fewer of the chain's.  64 / 32 / 16: 4001 tokens, 32 heads of 128 x 128 279 / 256 /
+// 245 us; 2048 tokens, 80 heads of 64 x 128 143 / 138 / (two on many CUs) 251;
+// gradients of 4096 tokens, 16 heads of 64 x 128 691 / 591 / 574, of 2048 tokens, 32
+// heads of 128 x 128 481 / 437 / 430.
+inline int gdr_chain_columns(int64_t B, int64_t H, int64_t P) {
+  constexpr int64_t kCus = 256;
+  for (int cols = 16; cols < 64; cols *= 2)
+    if (B * H * ((P + cols - 1) / cols) <= kCus) return cols;
+  return 64;
+}
 hipError_t launch_gdr_chunk(const GdrArgs &a, hipStream_t s);
 
 // What the chunked backward keeps of each (sequence, head, chunk), item

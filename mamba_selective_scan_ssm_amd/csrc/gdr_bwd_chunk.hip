@@ -358,7 +358,7 @@ struct RevPrepare {
 };
 
 template <int NT>
-__global__ __launch_bounds__(kThreads) void gdr_bwd_chain_kernel(GdrBwdArgs ba, GdrSaved keep, int64_t ptiles) {
+__global__ __launch_bounds__(kThreads) void gdr_bwd_chain_kernel(GdrBwdArgs ba, GdrSaved keep, int64_t ptiles, int cols) {
   __shared__ RevLds<NT> s;
   const GdrArgs &a = ba.f;
   const uint32_t heads = static_cast<uint32_t>(a.H / a.G), per = heads * static_cast<uint32_t>(ptiles);
@@ -367,7 +367,7 @@ __global__ __launch_bounds__(kThreads) void gdr_bwd_chain_kernel(GdrBwdArgs ba, 
   auto same = [](uint32_t v) { return static_cast<int64_t>(__builtin_amdgcn_readfirstlane(v)); };
   const uint32_t G = static_cast<uint32_t>(a.G);
   const int64_t b = same(bg / G), grp = same(bg % G), h = same(bg % G * heads + mem / static_cast<uint32_t>(ptiles));
-  const int64_t p0 = same(mem % static_cast<uint32_t>(ptiles) * kCols);
+  const int64_t p0 = same(mem % static_cast<uint32_t>(ptiles) * cols);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
   const int r = lane % 16, g = lane / 16;
   const int64_t nc = (a.L + kC - 1) / kC, item0 = (b * a.H + h) * nc;
@@ -397,7 +397,7 @@ __global__ __launch_bounds__(kThreads) void gdr_bwd_chain_kernel(GdrBwdArgs ba, 
 
   const int64_t p = p0 + 16 * wave + r;
   const uint32_t row = static_cast<uint32_t>(a.H * a.P);
-  const bool live = p0 + 16 * wave < a.P, col = p < a.P;
+  const bool live = 16 * wave < cols && p0 + 16 * wave < a.P, col = live && p < a.P;
   const int64_t head = (b * a.L * a.H + h) * a.P;
   RevChain<NT> w{ba, keep, item0, p, col, s, MinusOne(), r, g, static_cast<const uint16_t *>(ba.dy) + head,
                  static_cast<uint16_t *>(ba.dv) + head, row, static_cast<uint32_t>(a.P), 32 * row,
@@ -1105,13 +1105,14 @@ hipError_t launch_gdr_bwd_chunk(const GdrBwdArgs &a, hipStream_t s) {
   fw.h_final = nullptr;
   hipError_t e = launch_gdr_chunk_save(fw, k, s);
   if (e != hipSuccess) return e;
-  const int64_t ptiles = (f.P + kCols - 1) / kCols, per = f.H / f.G * ptiles;
+  const int cols = gdr_chain_columns(f.B, f.H, f.P);
+  const int64_t ptiles = (f.P + cols - 1) / cols, per = f.H / f.G * ptiles;
   const unsigned grid = static_cast<unsigned>((f.B * f.G + 7) / 8 * 8 * per);
   const int64_t split = head_split(f.B, nc, f.G, f.H / f.G);
   float *qk_part = red + pad4(2 * f.B * nc * f.H);
   const dim3 gg(static_cast<unsigned>(nc), static_cast<unsigned>(f.G), static_cast<unsigned>(f.B * split));
-  if (f.N <= 64) gdr_bwd_chain_kernel<4><<<grid, kThreads, 0, s>>>(a, k, ptiles);
-  else gdr_bwd_chain_kernel<8><<<grid, kThreads, 0, s>>>(a, k, ptiles);
+  if (f.N <= 64) gdr_bwd_chain_kernel<4><<<grid, kThreads, 0, s>>>(a, k, ptiles, cols);
+  else gdr_bwd_chain_kernel<8><<<grid, kThreads, 0, s>>>(a, k, ptiles, cols);
   auto grads = [&](auto tiles, auto four) {
     constexpr int NT = decltype(tiles)::value;
     constexpr bool FOUR = decltype(four)::value;

@@ -13,16 +13,17 @@
 // which is the token-by-token recurrence regrouped: only S, E and y depend on
 // the column p, so a column of the state is a chain of products of its own.
 //
-// One workgroup of 8 waves per (sequence, head, 64 columns).  Four waves, the
-// chain, hold 16 columns each: the state stays in their registers over the
-// whole sequence, and S0 -> R -> E -> S1 moves from product to product in
-// registers (gdr_mfma.h).  The other four prepare the next chunk meanwhile: K
-// and Q into LDS, K K^T and Q K^T, the decays (c in 64 bits: its differences
-// count, not its size), X by substitution in 16 x 16 blocks (the chunk's keys
-// may be all alike, where a series for the inverse loses everything) and block
-// rows joined by fp32 MFMA.  What they make is double-buffered, so one barrier
-// a chunk joins the two; the preparing waves meet among themselves at a count
-// in LDS.  Nothing but the inputs, y and the two states touches memory.
+// One workgroup of 8 waves per (sequence, head, 64 columns, or 32 or 16 where
+// that leaves each a CU).  Four waves (two, one), the chain, hold 16 columns
+// each: the state stays in their registers over the whole sequence, and S0 -> R
+// -> E -> S1 moves from product to product in registers (gdr_mfma.h).  The last
+// four prepare the next chunk meanwhile: K and Q into LDS, K K^T and Q K^T, the
+// decays (c in 64 bits: its differences count, not its size), X by substitution
+// in 16 x 16 blocks (the chunk's keys may be all alike, where a series for the
+// inverse loses everything) and block rows joined by fp32 MFMA.  What they make
+// is double-buffered, so one barrier a chunk joins the two; the preparing waves
+// meet among themselves at a count in LDS.  Nothing but the inputs, y and the
+// two states touches memory.
 //
 // Precision: k, q and v are exact in bf16.  What is computed -- S, R, E, X --
 // enters a product that makes S in three bf16 parts (all 24 bits; products of
@@ -36,7 +37,7 @@
 // and the chain each run from end to end; of those the matrix cores are busy 3.7
 // thousand a SIMD, the LDS 5.1 (1.9 of them conflicts, of transposing reads and
 // half-width writes).  160 workgroups on 256 CUs: a chunk's time is what counts.
-// Splitting P finer doubles the preparation for each CU that then holds two, and a
+// 4001 tokens, 32 heads of 128 x 128, 256 workgroups of 16 columns: 0.245 ms.  A
 // preparation of its own for all chunks writes and reads more than it takes away.
 #include "device_common.h"
 #include "gdr.h"
@@ -638,7 +639,7 @@ struct Prepare {
 };
 
 template <int NT, bool SAVE>
-__global__ __launch_bounds__(kThreads) void gdr_chunk_kernel(GdrArgs a, GdrSaved keep, int64_t ptiles) {
+__global__ __launch_bounds__(kThreads) void gdr_chunk_kernel(GdrArgs a, GdrSaved keep, int64_t ptiles, int cols) {
   __shared__ ChunkLds<NT> s;
   const uint32_t heads = static_cast<uint32_t>(a.H / a.G);  // of a group
   const uint32_t per = heads * static_cast<uint32_t>(ptiles);  // workgroups of a (sequence, group), which share K and Q
@@ -650,7 +651,7 @@ __global__ __launch_bounds__(kThreads) void gdr_chunk_kernel(GdrArgs a, GdrSaved
   auto same = [](uint32_t v) { return static_cast<int64_t>(__builtin_amdgcn_readfirstlane(v)); };
   const uint32_t G = static_cast<uint32_t>(a.G);
   const int64_t b = same(bg / G), grp = same(bg % G), h = same(bg % G * heads + mem / static_cast<uint32_t>(ptiles));
-  const int64_t p0 = same(mem % static_cast<uint32_t>(ptiles) * kCols);
+  const int64_t p0 = same(mem % static_cast<uint32_t>(ptiles) * cols);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
   const int r = lane % 16, g = lane / 16;
   const int64_t nc = (a.L + kC - 1) / kC;
@@ -682,7 +683,7 @@ __global__ __launch_bounds__(kThreads) void gdr_chunk_kernel(GdrArgs a, GdrSaved
 
   const int64_t p = p0 + 16 * wave + r;
   const uint32_t row = static_cast<uint32_t>(a.H * a.P);
-  const bool live = p0 + 16 * wave < a.P, col = p < a.P;  // some column, this lane's column
+  const bool live = 16 * wave < cols && p0 + 16 * wave < a.P, col = live && p < a.P;  // some column, this lane's column
   const int64_t head = (b * a.L * a.H + h) * a.P;
   Chain<NT, SAVE> w{a, keep, (b * a.H + h) * nc, p, col, s, MinusOne(), r, g, static_cast<const uint16_t *>(a.v) + head, static_cast<bf16_t *>(a.y) + head,
               row, static_cast<uint32_t>(a.P), 32 * row, {}, {}, {}, {}, {}, 0, {}, {}, {}};
@@ -729,10 +730,11 @@ bool gdr_chunk_applies(const GdrArgs &a) {
 namespace {
 template <bool SAVE>
 hipError_t launch(const GdrArgs &a, const GdrSaved &keep, hipStream_t s) {
-  const int64_t ptiles = (a.P + kCols - 1) / kCols, per = a.H / a.G * ptiles;
+  const int cols = gdr_chain_columns(a.B, a.H, a.P);
+  const int64_t ptiles = (a.P + cols - 1) / cols, per = a.H / a.G * ptiles;
   const unsigned grid = static_cast<unsigned>((a.B * a.G + 7) / 8 * 8 * per);
-  if (a.N <= 64) gdr_chunk_kernel<4, SAVE><<<grid, kThreads, 0, s>>>(a, keep, ptiles);
-  else gdr_chunk_kernel<8, SAVE><<<grid, kThreads, 0, s>>>(a, keep, ptiles);
+  if (a.N <= 64) gdr_chunk_kernel<4, SAVE><<<grid, kThreads, 0, s>>>(a, keep, ptiles, cols);
+  else gdr_chunk_kernel<8, SAVE><<<grid, kThreads, 0, s>>>(a, keep, ptiles, cols);
   return hipGetLastError();
 }
 }  // namespace

@@ -491,3 +491,24 @@ def test_decode_of_many_is_its_sequences(dtype):
         ys = ssm.gdr_decode_steps(one, *part, A, beta[s:s + 1].contiguous(), **kw)
         torch.cuda.synchronize()
         assert torch.equal(y[s:s + 1], ys) and torch.equal(pool[s:s + 1], one)
+
+
+# 32 and 64 columns of a state to a workgroup, where small calls take 16
+@pytest.mark.parametrize("qk_norm", [True, False])
+@pytest.mark.parametrize("B,L,H,P,G,N", [(8, 66, 24, 20, 8, 40), (8, 65, 24, 72, 4, 72), (5, 130, 27, 64, 3, 64)])
+def test_wide_columns(B, L, H, P, G, N, qk_norm):
+    _say("gdr of many workgroups", B, L, H, P, G, N, qk_norm)
+    w = ref.make_gdr(B, L, H, P, G, N, BF16, 64, qk_norm=qk_norm)
+    check_fwd(w, qk_norm, "prefill")
+    check_bwd(w, qk_norm, "gradients")
+
+
+def test_a_batch_by_chunks_is_its_sequences():
+    """Bitwise, though a batch's workgroups take more columns each."""
+    _say("gdr_fwd by chunks of a batch and of its sequences")
+    w = ref.make_gdr(7, 100, 24, 72, 4, 72, BF16, 65)
+    y, h = fwd(w, True)
+    for b in (0, 6):
+        one = {n: t if t is None or n in ("A", "bias") else t[b:b + 1].contiguous() for n, t in w.items()}
+        y1, h1 = fwd(one, True)
+        assert torch.equal(y[b:b + 1], y1) and torch.equal(h[b:b + 1], h1)
