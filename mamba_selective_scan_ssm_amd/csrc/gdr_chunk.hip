@@ -33,12 +33,13 @@
 //
 // Bound by the latency of both roles, not by a unit: 2 x 8192 tokens, 80 heads of
 // 64 x 128 take 0.56 ms (115 TFLOP/s of the 64 GFLOP that the rule needs, 0.75 TB/s
-// of its inputs and outputs), 10 thousand cycles a chunk, in which the preparation
-// and the chain each run from end to end; of those the matrix cores are busy 3.7
-// thousand a SIMD, the LDS 5.1 (1.9 of them conflicts, of transposing reads and
-// half-width writes).  160 workgroups on 256 CUs: a chunk's time is what counts.
-// 4001 tokens, 32 heads of 128 x 128, 256 workgroups of 16 columns: 0.245 ms.  A
-// preparation of its own for all chunks writes and reads more than it takes away.
+// of its inputs and outputs), 10.5 thousand cycles a chunk, of which the preparation
+// takes 8.3 and the chain 8.0 where the other is left out; the matrix cores are busy
+// for 3.7 thousand a SIMD, the LDS for 5.1 (1.9 of them conflicts, of transposing
+// reads and half-width writes).  160 workgroups on 256 CUs: a chunk's time is what
+// counts.  4001 tokens, 32 heads of 128 x 128, 256 workgroups of 16 columns: 0.245
+// ms.  A preparation of its own for all chunks would write and read 0.8 GB of tiles
+// at the first of these sizes, a third of the time that it has now.
 #include "device_common.h"
 #include "gdr.h"
 #include "gdr_common.h"
