@@ -121,12 +121,16 @@ def lib():
     return _lib
 
 
-def _dtype_code(t: torch.Tensor) -> int:
-    if t.dtype == torch.float32:
+def _code_of(dtype) -> int:
+    if dtype == torch.float32:
         return SSM_F32
-    if t.dtype == torch.bfloat16:
+    if dtype == torch.bfloat16:
         return SSM_BF16
-    raise TypeError(f"unsupported dtype {t.dtype}: expected float32 or bfloat16")
+    raise TypeError(f"unsupported dtype {dtype}: expected float32 or bfloat16")
+
+
+def _dtype_code(t: torch.Tensor) -> int:
+    return _code_of(t.dtype)
 
 
 def _check(name, t, shape, dtype, device):
@@ -536,10 +540,6 @@ def gdr_fwd(q, k, v, dt, A, beta, h0=None, *, scale=None, qk_norm=False, y=None,
               _scale(scale, N), int(bool(qk_norm)), _ptr(y), _ptr(h_final), _ptr(workspace), ws_len,
               _dopts(dt_bias, dt_softplus))
     return y, h_final
-
-
-def _code_of(dtype):
-    return _dtype_code(torch.empty(0, dtype=dtype))
 
 
 def gdr_fwd_workspace_size(B, L, H, P, G, N, dtype=torch.bfloat16) -> int:
