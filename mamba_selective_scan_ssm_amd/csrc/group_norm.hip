@@ -223,7 +223,7 @@ __device__ __forceinline__ void norm_elem_out(const NormArgs &a, float x, float 
 // The unit of the forward, its group fixed, walks the rows r0, r0 + step, ...
 // of a block: units of a workgroup are gsub groups by rsub rows.
 template <typename T, int VE, int LPG, int NV>
-__global__ __launch_bounds__(kThreads) void norm_rows_bwd_kernel(NormArgs a, int gsub, int64_t rows, int64_t parts) {
+__global__ __launch_bounds__(kThreads, NV == 1 ? 4 : 1) void norm_rows_bwd_kernel(NormArgs a, int gsub, int64_t rows, int64_t parts) {
   __shared__ float s_red[4];
   const int64_t W = a.D / a.G;
   const int l = threadIdx.x % LPG, ui = threadIdx.x / LPG;
@@ -630,19 +630,31 @@ RowPlan plan_rows(int64_t pieces, int ve, bool bwd) {
   return {0, 0};
 }
 
-constexpr int64_t kRowBlocks = 256;  // blocks of rows of the backward, at most
+// Blocks of rows of the backward: a workgroup's four waves find room four times a
+// CU where a lane holds one piece (128 registers), twice where it holds more, and
+// each writes its sums of dw and db, as much as 1.6 rows, so beyond one a CU there
+// are 8 rows and more for each.  With one a CU, 512, 768, 1024, 1536 in all (us):
+// 2 x 4096 tokens of 5120 channels in 80 groups (one piece) 124 (three a CU) and 151,
+// 122, 121, 130, 8 x 4096 of 2048 in 128 309, 188, 167, 162, 177; of 4096 in 1 (two
+// pieces) 149, 104, 136, 118, 135; of 1024 in 16 (one piece, 4 rows at 1024) 32, 29,
+// 32, 36, 42.
 struct RowBwd {
   int gsub, rsub;
   int64_t rows, blocks, parts;
 };
-RowBwd plan_rows_bwd(int64_t S, int64_t G, int lpg) {
+RowBwd plan_rows_bwd(int64_t S, int64_t G, RowPlan p) {
+  constexpr int64_t kCus = 256;
   RowBwd r;
-  const int units = kThreads / lpg;
+  const int units = kThreads / p.lpg;
   r.gsub = 1;
   while (r.gsub < units && r.gsub < G) r.gsub *= 2;
   r.rsub = units / r.gsub;
   const int64_t passes = ceil_div(S, r.rsub);  // rows in steps of rsub
-  r.rows = ceil_div(passes, kRowBlocks) * r.rsub;
+  const int64_t across = ceil_div(G, r.gsub), room = (p.nv == 1 ? 4 : 2) * kCus;
+  int64_t blocks = passes / 8;
+  if (blocks < ceil_div(kCus, across)) blocks = ceil_div(kCus, across);
+  if (blocks > room / across) blocks = room / across > 0 ? room / across : 1;
+  r.rows = ceil_div(passes, blocks) * r.rsub;
   r.blocks = ceil_div(S, r.rows > 0 ? r.rows : 1);
   r.parts = r.blocks * r.rsub;
   return r;
@@ -665,7 +677,7 @@ void rows_fwd(const NormArgs &a, hipStream_t s) {
 }
 template <typename T, int VE, int LPG, int NV>
 void rows_bwd(const NormArgs &a, hipStream_t s) {
-  const RowBwd r = plan_rows_bwd(a.S, a.G, LPG);
+  const RowBwd r = plan_rows_bwd(a.S, a.G, RowPlan{LPG, NV});
   const dim3 grid(static_cast<unsigned>(ceil_div(a.G, r.gsub)), static_cast<unsigned>(r.blocks));
   norm_rows_bwd_kernel<T, VE, LPG, NV><<<grid, kThreads, 0, s>>>(a, r.gsub, r.rows, r.parts);
   norm_params_kernel<<<static_cast<unsigned>(ceil_div(a.D, kParamChannels)), kThreads, 0, s>>>(a, r.parts, a.ws,
@@ -750,7 +762,7 @@ int64_t group_norm_bwd_ws_floats(int64_t S, int64_t T, int64_t D, int64_t G) {
   if (T != 1) return n;
   each_width(D / G, [&](int ve) {
     const RowPlan p = plan_rows(D / G / ve, ve, true);
-    const int64_t m = p.nv == 0 ? cols_ws_floats(S, T, D, G) : 2 * plan_rows_bwd(S, G, p.lpg).parts * D;
+    const int64_t m = p.nv == 0 ? cols_ws_floats(S, T, D, G) : 2 * plan_rows_bwd(S, G, p).parts * D;
     if (m > n) n = m;
   });
   return n;
