@@ -23,8 +23,8 @@
 //
 // Bound by HBM where there is work: forward of 8 x 4096 tokens, 5120 channels in 8
 // groups, gate first: 0.200 ms, 5.0 TB/s, what a copy reaches; forward and backward
-// of 2 x 4096 tokens in 80 groups, gate last: 0.162 ms (54 + 106 + 5 us; the backward,
-// 12 waves a CU by its registers, 4.0 TB/s).  Small ones by their launches: 4 x 1003
+// of 2 x 4096 tokens in 80 groups, gate last: 0.157 ms (54 + 103 + 7 us; the backward,
+// 16 waves a CU by its registers, 4.1 TB/s).  Small ones by their launches: 4 x 1003
 // tokens of 640 channels in 32 groups, fp32, over whole sequences 46 us in 7 kernels.
 #include "device_common.h"
 #include "group_norm.h"
@@ -615,6 +615,11 @@ RowPlan plan_rows(int64_t pieces, int ve, bool bwd) {
     if (pieces <= 32) return {16, 2};
     if (pieces <= 64) return {32, 2};
     if (pieces <= 128) return {64, 2};
+    // single elements leave registers for more of them, and a wave needs no barrier:
+    // 8 x 4096 tokens of 1001 channels in 7 groups 209 us, 541 by a workgroup a group,
+    // of 1197 in 3 groups 166 and 248
+    if (ve == 1 && pieces <= 256) return {64, 4};
+    if (ve == 1 && pieces <= 512) return {64, 8};
   } else {
     if (pieces <= 40) return {8, 5};
     if (pieces <= 48) return {16, 3};
@@ -695,11 +700,13 @@ bool rows(const NormArgs &a, hipStream_t s) {
   SSM_NORM_CASE(1, 1) SSM_NORM_CASE(2, 1) SSM_NORM_CASE(4, 1) SSM_NORM_CASE(8, 1) SSM_NORM_CASE(8, 2)
   if constexpr (BWD) {
     SSM_NORM_CASE(16, 2) SSM_NORM_CASE(32, 2) SSM_NORM_CASE(64, 2)
+    if constexpr (VE == 1) { SSM_NORM_CASE(64, 4) SSM_NORM_CASE(64, 8) }
   } else {
     SSM_NORM_CASE(8, 5) SSM_NORM_CASE(16, 3) SSM_NORM_CASE(16, 5) SSM_NORM_CASE(32, 3) SSM_NORM_CASE(32, 5)
     SSM_NORM_CASE(64, 5)
   }
-  SSM_NORM_CASE(256, 2) SSM_NORM_CASE(256, 3)
+  if constexpr (!(BWD && VE == 1)) { SSM_NORM_CASE(256, 2) }
+  SSM_NORM_CASE(256, 3)
   if constexpr (!(BWD && VE == 8)) { SSM_NORM_CASE(256, 5) }
   if constexpr (VE == 1) { SSM_NORM_CASE(256, 8) }
 #undef SSM_NORM_CASE

@@ -245,3 +245,10 @@ def test_after_the_mixer():
     ref.close(gg["dv"].view(B, L, H * P), vr.grad, "dv")
     for n, got in (("q", "dq"), ("k", "dk"), ("beta", "dbeta"), ("dt", "ddt"), ("A", "dA"), ("h0", "dh0")):
         ref.close(gg[got], r[n].grad, got)
+
+
+# single elements, from 3 to 8 of them a lane, and blocks of several rows each
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("B,L,D,G", [(1, 9, 429, 3), (2, 5, 1020, 4), (1, 7, 257, 1), (1, 6, 1022, 2), (3, 700, 66, 2)])
+def test_single_elements(B, L, D, G, dtype):
+    test_per_token(B, L, D, G, dtype)
