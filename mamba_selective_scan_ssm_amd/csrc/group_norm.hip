@@ -601,7 +601,7 @@ int vector_width(const NormArgs &a) {
 // Lanes and pieces per lane of a group of `pieces` pieces of ve elements: 8
 // lanes (128 bytes in a row) and more, with at most 5 pieces per lane; then the
 // workgroup.  The backward, which holds six values an element, takes at most 2
-// (3 where the workgroup shares the group).
+// (3 where the workgroup shares the group; 8 single elements).
 struct RowPlan {
   int lpg, nv;  // nv 0: the columns path
 };
