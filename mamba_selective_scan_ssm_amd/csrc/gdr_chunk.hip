@@ -25,11 +25,9 @@
 // meet among themselves at a count in LDS.  Nothing but the inputs, y and the
 // two states touches memory.
 //
-// Precision: k, q and v are exact in bf16.  What is computed -- S, R, E, X --
-// enters a product that makes S in three bf16 parts (all 24 bits; products of
-// two such operands leave out what is below 2^-24), what only y depends on in
-// two (at most 2^-16 of each term; y is rounded to bf16, by up to 2^-8).
-// Accumulation is fp32.
+// Precision: k, q and v are exact in bf16.  What is computed -- S, R, E, X, M --
+// enters a product in three bf16 parts (all 24 bits; products of two such operands
+// leave out what is below 2^-24).  Accumulation is fp32.
 //
 // Bound by the latency of both roles, not by a unit: 2 x 8192 tokens, 80 heads of
 // 64 x 128 take 0.56 ms (115 TFLOP/s of the 64 GFLOP that the rule needs, 0.75 TB/s
@@ -61,7 +59,7 @@ struct ChunkLds {
   __attribute__((aligned(16))) uint16_t k[2][kC * 16 * NT];
   __attribute__((aligned(16))) uint16_t q[2][kC * 16 * NT];
   __attribute__((aligned(16))) uint16_t x[2][3][kTriSize];
-  __attribute__((aligned(16))) uint16_t m[2][2][kTriSize];
+  __attribute__((aligned(128))) uint16_t m[2][3][kMixSize];  // a row's pieces by address bits
   // A'[i][j] at [j][i]; a diagonal block gives way to its inverse, transposed
   __attribute__((aligned(16))) float at[10 * 16 * kAtPitch];
   __attribute__((aligned(16))) float va[2][kC], vb[2][kC], vw[2][kC];
@@ -70,7 +68,7 @@ struct ChunkLds {
   float whole[2];
   uint32_t met;
   // byte offsets between the parts
-  static constexpr uint32_t kTile = 2 * kC * 16 * NT, kTri = 2 * kTriSize;
+  static constexpr uint32_t kTile = 2 * kC * 16 * NT, kTri = 2 * kTriSize, kMix = 2 * kMixSize;
 };
 
 // ---------------------------------------------------------------- the chain
@@ -91,8 +89,9 @@ struct Chain {
   const uint32_t rows16; // bytes of 16 rows
   uint32_t at[4];        // bytes to this lane's column in rows 4 g .. 4 g + 3
   // LDS addresses: rows r of K (Q behind it) by block of 32 states, the same
-  // for the transposing reads, rows r of X and M, element 4 g of the vectors
-  uint32_t lk[KB], lt[KB], lx[2], lm[2], lv;
+  // for the transposing reads, rows r of X and M (its last 32 by block of 32
+  // tokens), element 4 g of the vectors
+  uint32_t lk[KB], lt[KB], lx[2], lm[3], lv;
   f32x4 S[NT];
   uint16_t vr[16];  // v of the next chunk, on its way
   float vf[16];     // and of this one
@@ -104,10 +103,10 @@ struct Chain {
       lt[kb] = hold(lds_address(&s.k[0][tile_at<NT>(4 * g + r / 4, 4 * kb + r % 4)]));
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {  // rows r and 32 + r
+    for (int i = 0; i < 2; ++i)  // rows r and 32 + r
       lx[i] = hold(lds_address(&s.x[0][0][tri_at(32 * i + r) + 8 * g]));
-      lm[i] = hold(lds_address(&s.m[0][0][tri_at(32 * i + r) + 8 * g]));
-    }
+#pragma unroll
+    for (int i = 0; i < 3; ++i) lm[i] = hold(lds_address(&s.m[0][0][mix_at(i == 0 ? r : 32 + r, (i == 2 ? 4 : 0) + g)]));
     lv = hold(lds_address(&s.va[0][4 * g]));
   }
   // rows 16 rt + r, block kb of part `part` of X (M) in buffer buf
@@ -118,8 +117,8 @@ struct Chain {
   }
   template <int buf>
   __device__ __forceinline__ u32x4 row_m(int part, int rt, int kb) const {
-    return lds_get<u32x4>(lm[rt / 2] + (2 * buf + part) * ChunkLds<NT>::kTri +
-                          2 * (tri_at(16 * rt) - tri_at(32 * (rt / 2)) + 32 * kb));
+    return lds_get<u32x4>(lm[rt < 2 ? 0 : 1 + kb] + (3 * buf + part) * ChunkLds<NT>::kMix +
+                          2 * 16 * (rt % 2) * (rt < 2 ? 32 : 64));
   }
   // element 16 rt + 4 g .. + 3 of vector w (va, vb, vw) of the chunk
   template <int buf>
@@ -189,7 +188,7 @@ struct Chain {
         for (int rt = 0; rt < 4; ++rt) R[rt] = mma(ka[rt], sp[kb % 2][pl], R[rt]);
       if (!SAVE)
 #pragma unroll
-        for (int pl = 1; pl >= 0; --pl)
+        for (int pl = 2; pl >= 0; --pl)
 #pragma unroll
           for (int rt = 0; rt < 4; ++rt) Y[rt] = mma(qa[rt], sp[kb % 2][pl], Y[rt]);
     }
@@ -294,20 +293,20 @@ struct Chain {
       return;
     }
     // y = b (Q S0) + M E
-    u32x4 ep[2][2];
+    u32x4 ep[2][3];
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb) split_operand<2>(E[2 * kb], E[2 * kb + 1], ep[kb], minus);
+    for (int kb = 0; kb < 2; ++kb) split_operand<3>(E[2 * kb], E[2 * kb + 1], ep[kb], minus);
 #pragma unroll
     for (int rt = 0; rt < 4; ++rt) Y[rt] = Y[rt] * vec<buf>(1, rt);
 #pragma unroll
-    for (int mp = 1; mp >= 0; --mp) {
+    for (int mp = 2; mp >= 0; --mp) {
       u32x4 ma[4][2];
 #pragma unroll
       for (int rt = 0; rt < 4; ++rt)
 #pragma unroll
         for (int kb = 0; kb <= rt / 2; ++kb) ma[rt][kb] = row_m<buf>(mp, rt, kb);
 #pragma unroll
-      for (int pl = 1 - mp; pl >= 0; --pl)
+      for (int pl = 2 - mp; pl >= 0; --pl)
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
@@ -585,13 +584,14 @@ struct Prepare {
   __device__ __forceinline__ void publish(int buf) {
     constexpr int V = 3 - W;
     const uint32_t xw = hold(lds_address(&s.x[buf][0][tri_at(16 * W + r) + 8 * g]));
-    const uint32_t mv = hold(lds_address(&s.m[buf][0][tri_at(16 * V + r) + 8 * g]));
+    const uint32_t mv = hold(lds_address(&s.m[buf][0][mix_at(16 * V + r, g)]));
 #pragma unroll
     for (int j = 0; j <= V; ++j) {
-      u32x2 p[2];
-      split4<2>(M[j], p, minus);
+      u32x2 p[3];
+      split4<3>(M[j], p, minus);
+      // block 1 of 32 tokens lies four pieces on, or back
 #pragma unroll
-      for (int pl = 0; pl < 2; ++pl) lds_put(mv + pl * ChunkLds<NT>::kTri + 2 * kpos(16 * j), p[pl]);
+      for (int pl = 0; pl < 3; ++pl) lds_put((j < 2 ? mv : mv ^ 64) + pl * ChunkLds<NT>::kMix + 8 * (j % 2), p[pl]);
     }
 #pragma unroll
     for (int j = 0; j <= W; ++j) {
@@ -660,12 +660,12 @@ __global__ __launch_bounds__(kThreads) void gdr_chunk_kernel(GdrArgs a, GdrSaved
   // block pairs above the diagonal are read with their 32 tokens and stay 0
   for (int i = threadIdx.x; i < kTriSize / 2; i += kThreads)
 #pragma unroll
-    for (int bf = 0; bf < 2; ++bf) {
+    for (int bf = 0; bf < 2; ++bf)
 #pragma unroll
-      for (int pl = 0; pl < 3; ++pl) reinterpret_cast<uint32_t *>(s.x[bf][pl])[i] = 0;
-#pragma unroll
-      for (int pl = 0; pl < 2; ++pl) reinterpret_cast<uint32_t *>(s.m[bf][pl])[i] = 0;
-    }
+      for (int pl = 0; pl < 3; ++pl) {
+        reinterpret_cast<uint32_t *>(s.x[bf][pl])[i] = 0;
+        if (i < kMixSize / 2) reinterpret_cast<uint32_t *>(s.m[bf][pl])[i] = 0;
+      }
   if (threadIdx.x == 0) s.met = 0;
   __syncthreads();
 

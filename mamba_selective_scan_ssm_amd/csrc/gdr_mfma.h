@@ -50,8 +50,7 @@ __device__ __forceinline__ float less_half(float v, uint32_t pair, uint32_t minu
   return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, pair), __builtin_bit_cast(bf16x2, minus), v, false);
 }
 // fp32 as a sum of NP bf16 parts, each the rounded rest of those before it (the
-// differences are exact): three hold all 24 bits; two leave out at most 2^-16
-// of the value, and 3e-6 of it on the average.
+// differences are exact): three hold all 24 bits.
 template <int NP>
 __device__ __forceinline__ void split4(f32x4 v, u32x2 *out, const MinusOne &m) {
 #pragma unroll
@@ -77,10 +76,17 @@ __device__ __forceinline__ void split_operand(f32x4 top, f32x4 bottom, u32x4 *ou
 constexpr int kC = 64;          // tokens per chunk
 constexpr int kCols = 64;       // columns per workgroup
 
-// X and M, [i][j] by kpos(j): rows 0..31 meet 32 tokens, rows 32..63 all 64;
+// X, [i][j] by kpos(j): rows 0..31 meet 32 tokens, rows 32..63 all 64;
 // 16 bytes of padding put 16 rows on different banks.
 constexpr int kTriSize = 32 * 40 + 32 * 72;
 __device__ __forceinline__ constexpr int tri_at(int i) { return i < 32 ? i * 40 : 32 * 40 + (i - 32) * 72; }
+// M the same without the padding, for which the LDS has no room: the 16-byte pieces
+// `ch` (kpos / 8) of a row are exchanged by the row, so that one piece of eight rows
+// lies on 32 banks.
+constexpr int kMixSize = 32 * 32 + 32 * 64;
+__device__ __forceinline__ constexpr int mix_at(int i, int ch) {
+  return i < 32 ? i * 32 + 8 * (ch ^ (i / 2 % 4)) : 32 * 32 + (i - 32) * 64 + 8 * (ch ^ (i % 8));
+}
 // 16-byte piece `ch` (kpos / 8) of token `tok` in a K or Q tile.  Eight lanes
 // of an operand read (eight rows, one piece) and sixteen of a transposing one
 // (four rows by four pieces, half of each) share a cycle: the pieces of a row
