@@ -453,6 +453,10 @@ ssm_status ssm_conv1d_update(int64_t S, int64_t D, int64_t K, ssm_dtype dt, floa
  * Sizes: 1 <= N <= SSM_GDR_MAX_N, G divides H, B and H <= 65535, H P <= 2^24
  * (else SSM_ERR_UNSUPPORTED); any L >= 0 (L == 0 writes h_final = h0) and
  * P >= 0.  A sequence's results do not depend on the batch (bitwise).
+ * A value that is not finite reaches its own token and later ones alone, which
+ * are then not finite (NaN or an infinity, which of them is not specified): of v
+ * in its channel, of k in its group's heads, of beta and of dt in its head (a
+ * dt * A of -infinity is a decay of 0 and wipes the state); of q its token.
  */
 ssm_status ssm_gdr_fwd(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G, int64_t N,
                        ssm_dtype dt, const void *q, const void *k, const void *v,

@@ -66,6 +66,7 @@ struct ChunkLds {
   __attribute__((aligned(16))) double c[2][kC];                 // in units of log 2
   __attribute__((aligned(16))) float beta[2][kC], rk[kC], rq[kC];
   float whole[2];
+  int bad[2];  // the first token whose row of A' is not finite, kC where all are
   uint32_t met;
   // byte offsets between the parts
   static constexpr uint32_t kTile = 2 * kC * 16 * NT, kTri = 2 * kTriSize, kMix = 2 * kMixSize;
@@ -144,6 +145,17 @@ struct Chain {
     }
   }
 
+  // Zeros for what is not finite; its first token in this lane's column, or `bad`.
+  __device__ __forceinline__ int leave_out(f32x4 *rows, int bad) {
+#pragma unroll
+    for (int i = 15; i >= 0; --i)
+      if (!(fabsf(rows[i / 4][i % 4]) < __builtin_inff())) {
+        bad = min(bad, 16 * (i / 4) + 4 * g + i % 4);
+        rows[i / 4][i % 4] = 0.f;
+      }
+    bad = min(bad, __shfl_xor(bad, 16));
+    return min(bad, __shfl_xor(bad, 32));
+  }
   // A column whose token `bad` is not finite: its rows from there on, and the state.
   __device__ __forceinline__ void spoil(int bad, f32x4 *rows) {
 #pragma unroll
@@ -207,18 +219,9 @@ struct Chain {
       }
     }
     load_v(t0 + kC, more - kC);
-    int bad = kC;  // the first such token of this lane's column
-    const bool any_bad = __any(test != 0.f);
-    if (__builtin_expect(any_bad, 0)) {
-#pragma unroll
-      for (int i = 15; i >= 0; --i)
-        if (!(fabsf(R[i / 4][i % 4]) < __builtin_inff())) {
-          bad = 16 * (i / 4) + 4 * g + i % 4;
-          R[i / 4][i % 4] = 0.f;
-        }
-      bad = min(bad, __shfl_xor(bad, 16));
-      bad = min(bad, __shfl_xor(bad, 32));
-    }
+    int bad = SAVE ? kC : s.bad[buf];  // the first such token of this lane's column
+    bool any_bad = __any(test != 0.f) || bad < kC;
+    if (__builtin_expect(any_bad, 0)) bad = leave_out(R, bad);
 
     __builtin_amdgcn_sched_barrier(0);
     // E = X R: small terms first, the four row tiles side by side
@@ -245,6 +248,15 @@ struct Chain {
       }
     }
 
+    if (!SAVE) {  // sums that passed the largest number: left out of y's product likewise
+      float over = 0.f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) over = fmaf(E[i / 4][i % 4], 0.f, over);
+      if (__builtin_expect(__any(over != 0.f), 0)) {
+        any_bad = true;
+        bad = leave_out(E, bad);
+      }
+    }
     __builtin_amdgcn_sched_barrier(0);
     // S1 = whole S0 + K^T (w E)
     {
@@ -444,6 +456,7 @@ struct Prepare {
   }
   // K, Q and their norms of the loaded chunk
   __device__ __forceinline__ void stage(int buf) {
+    if (tid == 0) s.bad[buf] = kC;
     if (tid >= kLoaders) return;
     const int m = tid % kPieces, tq = 4 * (tid / kPieces);
 #pragma unroll
@@ -508,6 +521,7 @@ struct Prepare {
 #pragma unroll
     for (int e = 0; e < 4; ++e) ci[e] = c4(buf * kC + 16 * W + e);
     const f32x4 si = f4(kRk, 16 * W);
+    float test = 0.f;
 #pragma unroll
     for (int jt = 0; jt <= W; ++jt) {
       const double cj = c1(buf * kC + 16 * jt);
@@ -516,8 +530,24 @@ struct Prepare {
       for (int e = 0; e < 4; ++e) {
         const float f = ap[jt][e] * (si[e] * sj) * decay_of(ci[e] - cj);
         ap[jt][e] = jt < W || 4 * g + e > r ? f : 0.f;
+        test = fmaf(ap[jt][e], 0.f, test);
       }
       lds_put(la + block(jt, W), ap[jt]);
+    }
+    // A row that is not finite would reach X's rows before it, 0 times it, where
+    // blocks are joined.  It is left out, and the chain told from where on nothing
+    // is finite.  (What is kept for the gradients stays as it is.)
+    if (!SAVE && __builtin_expect(__any(test != 0.f), 0)) {
+#pragma unroll
+      for (int jt = 0; jt <= W; ++jt) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (!(fabsf(ap[jt][e]) < __builtin_inff())) {
+            atomicMin(&s.bad[buf], 16 * W + 4 * g + e);
+            ap[jt][e] = 0.f;
+          }
+        lds_put(la + block(jt, W), ap[jt]);
+      }
     }
     const double cv = c1(buf * kC + 16 * V);
     const float sv = f1(kRq, 16 * V) * a.scale;
