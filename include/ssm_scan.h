@@ -503,6 +503,10 @@ ssm_status ssm_gdr_decode_steps(int64_t S, int64_t T, int64_t H, int64_t P, int6
  * All sums are fp32 and in a fixed order: results are run-to-run
  * reproducible.  Outputs must not overlap inputs, the workspace or each other.
  * Sizes as ssm_gdr_fwd, and P, H >= 1.
+ * A dy that is not finite reaches its own token and earlier ones alone (dv and
+ * dh0 in its channel, dbeta and ddt in its head, dk in its group, dA, d_dt_bias),
+ * and of dq its token.  A q, k, v, dt or beta that is not finite reaches what it
+ * enters, and may reach the gradients of its heads at up to 63 tokens beside it.
  * workspace : ssm_gdr_bwd_workspace_size() bytes, 16-byte aligned.
  */
 ssm_status ssm_gdr_bwd(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G, int64_t N,

@@ -61,6 +61,8 @@ struct RevLds {
   static constexpr uint32_t kTile = 2 * kC * 16 * NT, kTri = 2 * kUpSize;
 };
 
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+
 // ------------------------------------------------------- 2. the chain backwards
 // The matrix cores' sums round downwards by a little, which shows in a gradient
 // that sums over all tokens.  All here is linear in dY and dS1, so every other
@@ -128,6 +130,21 @@ struct RevChain {
         dO[kb][e] = buf == 0 ? w : w ^ 0x80008000u;
       }
   }
+  // Zeros for dY's values that are not finite; the last such token of this lane's
+  // column, -1 where there is none.
+  __device__ __forceinline__ int leave_out() {
+    int bad = -1;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const uint32_t w = dO[i / 8][i % 8 / 2], half = i % 2 ? 0x7f800000u : 0x7f80u;
+      if ((w & half) == half) {
+        dO[i / 8][i % 8 / 2] = w & (i % 2 ? 0xffffu : 0xffff0000u);
+        bad = 16 * (i / 4) + 4 * g + i % 4;
+      }
+    }
+    bad = max(bad, __shfl_xor(bad, 16));
+    return max(bad, __shfl_xor(bad, 32));
+  }
   // dY of row tile rt in fp32
   __device__ __forceinline__ f32x4 dy_f32(int rt) const {
     const uint32_t lo = dO[rt / 2][rt % 2 * 2], hi = dO[rt / 2][rt % 2 * 2 + 1];
@@ -144,6 +161,15 @@ struct RevChain {
       for (int nt = 0; nt < NT; ++nt)
         if (16 * nt + 4 * g < ba.f.N)
           *reinterpret_cast<f32x4 *>(keep.dS + (item * ba.f.P + p) * ba.f.N + 16 * nt + 4 * g) = dS[nt];
+    // A dY that is not finite is left out of the products, where 0 times it would
+    // reach the tokens behind it; what it enters is set below.
+    u16x2 most = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2, dO[i / 4][i % 4] & 0x7fff7fffu));
+    const bool any_bad = __any(most[0] >= 0x7f80 || most[1] >= 0x7f80);
+    int bad = -1;
+    if (__builtin_expect(any_bad, 0)) bad = leave_out();
     // K dS1
     f32x4 G[4];
 #pragma unroll
@@ -237,6 +263,16 @@ struct RevChain {
               for (int i = 0; i < 4; ++i) dS[n0 + i] = mma(kt[i][kb], up[o][kb][pl], dS[n0 + i]);
         }
       }
+    }
+    if (__builtin_expect(any_bad, 0)) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (16 * (i / 4) + 4 * g + i % 4 <= bad) Wv[i / 4][i % 4] = __builtin_nanf("");
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (bad >= 0) dS[nt][e] = __builtin_nanf("");
     }
     __builtin_amdgcn_sched_barrier(0);
     take_dy<1 - buf>();   // before anything stored after them has to be waited for
