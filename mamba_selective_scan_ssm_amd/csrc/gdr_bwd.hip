@@ -245,47 +245,49 @@ __device__ __forceinline__ float wave_sum(float v) {
 // dq (blockIdx.y 0) and dk (1): one wave per (token, group) sums the partial
 // gradients (tiles, B, L, parts, N) of the group's share of the parts (its heads, or
 // itself) and the tiles, in order, and takes them through the norm: with u = r x,
-// dx = r (g - u (g . u)).
+// dx = r (g - u (g . u)).  More items than a grid of kMostBlocks holds take turns.
+constexpr int64_t kMostBlocks = int64_t(1) << 22;  // of 256 threads: a dimension holds fewer than 2^32
 template <typename T>
 __global__ __launch_bounds__(kThreads) void gdr_reduce_qk_kernel(GdrBwdArgs ba, int64_t tiles, int64_t parts,
                                                                  const float *dq_part, const float *dk_part) {
   const GdrArgs &a = ba.f;
   const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * kWaves + wave;
-  if (item >= a.B * a.L * a.G) return;
   const bool is_k = blockIdx.y != 0;
   const float *part = is_k ? dk_part : dq_part;
-  const T *x = static_cast<const T *>(is_k ? a.k : a.q) + item * a.N;
-  T *out = static_cast<T *>(is_k ? ba.dk : ba.dq) + item * a.N;
-  const int64_t tok = item / a.G, g = item % a.G, per = parts / a.G;
-  constexpr int kPer = 4;  // N <= 256
-  float sum[kPer], xv[kPer];
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int64_t n = lane + 64 * i;
-    sum[i] = 0.f;
-    xv[i] = n < a.N ? to_f32(x[n]) : 0.f;
-    if (n < a.N)
-      for (int64_t t = 0; t < tiles; ++t)
-        for (int64_t hh = 0; hh < per; ++hh)
-          sum[i] += part[((t * a.B * a.L + tok) * parts + g * per + hh) * a.N + n];
-  }
-  if (a.qk_norm) {
-    float ss = 0.f, gx = 0.f;
+  for (int64_t item = static_cast<int64_t>(blockIdx.x) * kWaves + wave; item < a.B * a.L * a.G;
+       item += static_cast<int64_t>(gridDim.x) * kWaves) {
+    const T *x = static_cast<const T *>(is_k ? a.k : a.q) + item * a.N;
+    T *out = static_cast<T *>(is_k ? ba.dk : ba.dq) + item * a.N;
+    const int64_t tok = item / a.G, g = item % a.G, per = parts / a.G;
+    constexpr int kPer = 4;  // N <= 256
+    float sum[kPer], xv[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      ss = fmaf(xv[i], xv[i], ss);
-      gx = fmaf(sum[i], xv[i], gx);
+      const int64_t n = lane + 64 * i;
+      sum[i] = 0.f;
+      xv[i] = n < a.N ? to_f32(x[n]) : 0.f;
+      if (n < a.N)
+        for (int64_t t = 0; t < tiles; ++t)
+          for (int64_t hh = 0; hh < per; ++hh)
+            sum[i] += part[((t * a.B * a.L + tok) * parts + g * per + hh) * a.N + n];
     }
-    const float r = 1.f / sqrtf(wave_sum(ss) + kQkNormEps);
-    const float gu = wave_sum(gx) * r;
+    if (a.qk_norm) {
+      float ss = 0.f, gx = 0.f;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) sum[i] = r * fmaf(-gu * r, xv[i], sum[i]);
-  }
+      for (int i = 0; i < kPer; ++i) {
+        ss = fmaf(xv[i], xv[i], ss);
+        gx = fmaf(sum[i], xv[i], gx);
+      }
+      const float r = 1.f / sqrtf(wave_sum(ss) + kQkNormEps);
+      const float gu = wave_sum(gx) * r;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int64_t n = lane + 64 * i;
-    if (n < a.N) out[n] = from_f32<T>(sum[i]);
+      for (int i = 0; i < kPer; ++i) sum[i] = r * fmaf(-gu * r, xv[i], sum[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int64_t n = lane + 64 * i;
+      if (n < a.N) out[n] = from_f32<T>(sum[i]);
+    }
   }
 }
 
@@ -299,38 +301,41 @@ __global__ __launch_bounds__(kThreads) void gdr_reduce_gates_kernel(GdrBwdArgs b
   __shared__ float s_a[kWaves][64], s_b[kWaves][64];
   const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
   const int64_t h = static_cast<int64_t>(blockIdx.y) * 64 + lane, H = a.H, BL = a.B * a.L;
-  const int64_t tok0 = static_cast<int64_t>(blockIdx.x) * kTokBlock;
-  float sa = 0.f, sb = 0.f;
-  if (h < H) {
-    const float Ah = a.A[h], bias = a.dt_bias ? a.dt_bias[h] : 0.f;
-    for (int64_t tok = tok0 + wave; tok < tok0 + kTokBlock && tok < BL; tok += kWaves) {
-      float db = 0.f, dl = 0.f;
-      for (int64_t t = 0; t < tiles; ++t) {
-        db += sc_part[(t * BL + tok) * H + h];
-        dl += sc_part[((tiles + t) * BL + tok) * H + h];
+  for (int64_t blk = blockIdx.x; blk * kTokBlock < BL; blk += gridDim.x) {
+    const int64_t tok0 = blk * kTokBlock;
+    float sa = 0.f, sb = 0.f;
+    if (h < H) {
+      const float Ah = a.A[h], bias = a.dt_bias ? a.dt_bias[h] : 0.f;
+      for (int64_t tok = tok0 + wave; tok < tok0 + kTokBlock && tok < BL; tok += kWaves) {
+        float db = 0.f, dl = 0.f;
+        for (int64_t t = 0; t < tiles; ++t) {
+          db += sc_part[(t * BL + tok) * H + h];
+          dl += sc_part[((tiles + t) * BL + tok) * H + h];
+        }
+        const float raw = to_f32(static_cast<const T *>(a.dt)[tok * H + h]);
+        const float d = step_size(raw, bias, a.dt_softplus);
+        const float slope = a.dt_softplus ? 1.f / (1.f + fast_exp2(-(raw + bias) * kLog2e)) : 1.f;
+        const float dd = dl * Ah * slope;
+        static_cast<T *>(ba.dbeta)[tok * H + h] = from_f32<T>(db);
+        static_cast<T *>(ba.ddt)[tok * H + h] = from_f32<T>(dd);
+        sa = fmaf(dl, d, sa);
+        sb += dd;
       }
-      const float raw = to_f32(static_cast<const T *>(a.dt)[tok * H + h]);
-      const float d = step_size(raw, bias, a.dt_softplus);
-      const float slope = a.dt_softplus ? 1.f / (1.f + fast_exp2(-(raw + bias) * kLog2e)) : 1.f;
-      const float dd = dl * Ah * slope;
-      static_cast<T *>(ba.dbeta)[tok * H + h] = from_f32<T>(db);
-      static_cast<T *>(ba.ddt)[tok * H + h] = from_f32<T>(dd);
-      sa = fmaf(dl, d, sa);
-      sb += dd;
     }
-  }
-  s_a[wave][lane] = sa;
-  s_b[wave][lane] = sb;
-  __syncthreads();
-  if (wave == 0 && h < H) {
-    float x = 0.f, y = 0.f;
+    s_a[wave][lane] = sa;
+    s_b[wave][lane] = sb;
+    __syncthreads();
+    if (wave == 0 && h < H) {
+      float x = 0.f, y = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-      x += s_a[w][lane];
-      y += s_b[w][lane];
+      for (int w = 0; w < kWaves; ++w) {
+        x += s_a[w][lane];
+        y += s_b[w][lane];
+      }
+      red[2 * blk * H + h] = x;
+      red[(2 * blk + 1) * H + h] = y;
     }
-    red[(2 * static_cast<int64_t>(blockIdx.x)) * H + h] = x;
-    red[(2 * static_cast<int64_t>(blockIdx.x) + 1) * H + h] = y;
+    __syncthreads();
   }
 }
 // one wave per head: the blocks' sums, in a fixed order
@@ -364,7 +369,7 @@ hipError_t launch_gdr_reduce(const GdrBwdArgs &a, int64_t tiles, const float *dq
   const int64_t nblk = (BL + kTokBlock - 1) / kTokBlock;
   const bool bf = f.dt_type == DType::BF16;
   if (BL > 0) {
-    const dim3 gg(static_cast<unsigned>(nblk), static_cast<unsigned>((f.H + 63) / 64));
+    const dim3 gg(static_cast<unsigned>(nblk < kMostBlocks ? nblk : kMostBlocks), static_cast<unsigned>((f.H + 63) / 64));
     const hipError_t e = launch_gdr_reduce_qk(a, tiles, f.H, dq_part, dk_part, s);
     if (e != hipSuccess) return e;
     if (bf) {
@@ -378,7 +383,8 @@ hipError_t launch_gdr_reduce(const GdrBwdArgs &a, int64_t tiles, const float *dq
 hipError_t launch_gdr_reduce_qk(const GdrBwdArgs &a, int64_t tiles, int64_t parts, const float *dq_part,
                                 const float *dk_part, hipStream_t s) {
   const GdrArgs &f = a.f;
-  const dim3 grid(static_cast<unsigned>((f.B * f.L * f.G + kWaves - 1) / kWaves), 2);
+  const int64_t blocks = (f.B * f.L * f.G + kWaves - 1) / kWaves;
+  const dim3 grid(static_cast<unsigned>(blocks < kMostBlocks ? blocks : kMostBlocks), 2);
   if (f.dt_type == DType::BF16) gdr_reduce_qk_kernel<bf16_t><<<grid, kThreads, 0, s>>>(a, tiles, parts, dq_part, dk_part);
   else gdr_reduce_qk_kernel<float><<<grid, kThreads, 0, s>>>(a, tiles, parts, dq_part, dk_part);
   return hipGetLastError();

@@ -1094,7 +1094,8 @@ int64_t pad4(int64_t n) { return (n + 3) / 4 * 4; }
 
 bool gdr_bwd_chunk_applies(const GdrBwdArgs &a) {
   return gdr_chunk_applies(a.f) && aligned16(a.dy) && aligned16(a.dh_final) && aligned16(a.dh0) &&
-         a.f.P <= (int64_t(1) << 20);  // what is kept of a chunk within 32-bit offsets
+         a.f.P <= (int64_t(1) << 20) &&  // what is kept of a chunk within 32-bit offsets
+         (a.f.L + kC - 1) / kC < (int64_t(1) << 32) / kThreads;  // a workgroup a chunk, in one dimension
 }
 
 // Into how many workgroups the heads of a group are split: as many as make the

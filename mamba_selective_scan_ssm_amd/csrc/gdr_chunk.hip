@@ -754,8 +754,9 @@ bool aligned16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0;
 bool gdr_chunk_applies(const GdrArgs &a) {
   return a.dt_type == DType::BF16 && a.N <= 128 && a.N % 8 == 0 && a.L >= kGdrChunkMinL && aligned16(a.q) &&
          aligned16(a.k) && aligned16(a.h0) && aligned16(a.h_final) &&
-         // the workgroups of the chains, eight groups side by side, in one dimension
-         (a.B * a.G + 7) / 8 * 8 * (a.H / a.G) * ((a.P + kCols - 1) / kCols) < (int64_t(1) << 31);
+         // the workgroups of the chains, eight groups side by side, in one dimension of
+         // fewer than 2^32 threads
+         (a.B * a.G + 7) / 8 * 8 * (a.H / a.G) * ((a.P + kCols - 1) / kCols) < (int64_t(1) << 32) / kThreads;
 }
 
 namespace {
