@@ -541,7 +541,7 @@ size_t ssm_gdr_bwd_workspace_size(int64_t B, int64_t L, int64_t H, int64_t P, in
  * weight, bias : (D) fp32; NULL = ones, zeros
  * mean, rstd   : (S, G) fp32 or NULL (not returned); mean only with center
  * Outputs must not overlap inputs or each other.  G divides D, T <= 2^20,
- * S * D < 2^31 (else SSM_ERR_UNSUPPORTED); eps finite and >= 0.  An empty x
+ * D and S * D < 2^31 (else SSM_ERR_UNSUPPORTED); eps finite and >= 0.  An empty x
  * is a no-op.
  * workspace : ssm_group_norm_fwd_workspace_size() bytes, 16-byte aligned
  *             (NULL where 0, as for T == 1 up to W = 1280 and more).

@@ -184,7 +184,7 @@ static ssm_status norm_sizes(int64_t S, int64_t T, int64_t D, int64_t G, ssm_dty
   if (!(eps >= 0.f) || !std::isfinite(eps)) return SSM_ERR_INVALID_ARG;
   if (G < 1 || D % G != 0) return SSM_ERR_UNSUPPORTED;
   int64_t sd;
-  if (!product({S, T, D}, n) || !product({S, D}, &sd) || sd > kMaxGridX || T > (int64_t(1) << 20))
+  if (!product({S, T, D}, n) || !product({S, D}, &sd) || sd > kMaxGridX || D > kMaxGridX || T > (int64_t(1) << 20))
     return SSM_ERR_UNSUPPORTED;
   return SSM_OK;
 }

@@ -44,6 +44,14 @@ __device__ __forceinline__ float silu_grad(float v, float &slope) {
   return v * s;
 }
 
+// A dimension of a grid holds fewer than 2^32 threads: more workgroups than kMostX
+// are laid out over z as well, and the last row's surplus ends at once.
+constexpr int64_t kMostX = int64_t(1) << 22;
+constexpr int64_t kMostTokens = 16 * 65535;  // at a time, 16 for a workgroup
+__device__ __forceinline__ int64_t flat_block() {
+  return blockIdx.x + static_cast<int64_t>(blockIdx.z) * gridDim.x;
+}
+
 // rounding may leave a variance below 0; a NaN stays one
 __device__ __forceinline__ float not_negative(float v) { return v < 0.f ? 0.f : v; }
 
@@ -326,7 +334,7 @@ __global__ __launch_bounds__(kThreads) void norm_params_kernel(NormArgs a, int64
   constexpr int kSplit = kThreads / kParamChannels;
   __shared__ float s_w[kSplit][kParamChannels], s_b[kSplit][kParamChannels];
   const int c = threadIdx.x % kParamChannels, k = threadIdx.x / kParamChannels;
-  const int64_t d = static_cast<int64_t>(blockIdx.x) * kParamChannels + c;
+  const int64_t d = flat_block() * kParamChannels + c;
   float x = 0.f, y = 0.f;
   if (d < a.D)
 #pragma unroll 8
@@ -356,10 +364,10 @@ __global__ __launch_bounds__(kThreads) void norm_params_kernel(NormArgs a, int64
 template <typename T, int VE>
 __global__ __launch_bounds__(kThreads) void norm_cols_sums_kernel(NormArgs a, int64_t rows, int64_t slices) {
   const int lane = threadIdx.x % 64;
-  const int64_t cb = (a.D + 64 * VE - 1) / (64 * VE), s = blockIdx.x / cb;
+  const int64_t cb = (a.D + 64 * VE - 1) / (64 * VE), block = flat_block(), s = block / cb;
   const int64_t slice = static_cast<int64_t>(blockIdx.y) * 4 + threadIdx.x / 64;
-  const int64_t d = (blockIdx.x % cb * 64 + lane) * VE;
-  if (slice >= slices || d >= a.D) return;
+  const int64_t d = (block % cb * 64 + lane) * VE;
+  if (s >= a.S || slice >= slices || d >= a.D) return;
   const int64_t t0 = slice * rows, t1 = t0 + rows < a.T ? t0 + rows : a.T;
   const bool gate = a.z && a.gate_first;
   float first[VE], s1[VE], s2[VE];
@@ -410,7 +418,8 @@ __device__ __forceinline__ void each_partial(int64_t slices, int64_t W, int64_t 
 // one workgroup per (s, g): joins slices and channels
 __global__ __launch_bounds__(kThreads) void norm_cols_join_kernel(NormArgs a, int64_t rows, int64_t slices, float *stat) {
   __shared__ float s_red[4];
-  const int64_t W = a.D / a.G, g = blockIdx.x % a.G, s = blockIdx.x / a.G;
+  const int64_t W = a.D / a.G, block = flat_block(), g = block % a.G, s = block / a.G;
+  if (s >= a.S) return;
   const float *pm = a.ws + s * slices * a.D + g * W, *p2 = pm + a.S * slices * a.D;
   const float inv = 1.f / (static_cast<float>(a.T) * static_cast<float>(W));
   auto count = [&](int64_t slice) {
@@ -444,9 +453,9 @@ __global__ __launch_bounds__(kThreads) void norm_cols_join_kernel(NormArgs a, in
 template <typename T, int VE>
 __global__ __launch_bounds__(kThreads) void norm_cols_apply_kernel(NormArgs a, const float *stat) {
   const int lane = threadIdx.x % 64;
-  const int64_t cb = (a.D + 64 * VE - 1) / (64 * VE), s = blockIdx.x / cb;
-  const int64_t W = a.D / a.G, d = (blockIdx.x % cb * 64 + lane) * VE;
-  if (d >= a.D) return;
+  const int64_t cb = (a.D + 64 * VE - 1) / (64 * VE), block = flat_block(), s = block / cb;
+  const int64_t W = a.D / a.G, d = (block % cb * 64 + lane) * VE;
+  if (s >= a.S || d >= a.D) return;
   const int64_t g = d / W;
   const float mean = stat[3 * (s * a.G + g)], rstd = stat[3 * (s * a.G + g) + 1];
   const float delta = stat[3 * (s * a.G + g) + 2];  // the mean's part below its fp32 step
@@ -456,27 +465,28 @@ __global__ __launch_bounds__(kThreads) void norm_cols_apply_kernel(NormArgs a, c
     wv[e] = a.w ? a.w[d + e] : 1.f;
     bv[e] = a.b ? a.b[d + e] : 0.f;
   }
-  const int64_t t0 = (static_cast<int64_t>(blockIdx.y) * 4 + threadIdx.x / 64) * 4;
+  for (int64_t t0 = (static_cast<int64_t>(blockIdx.y) * 4 + threadIdx.x / 64) * 4; t0 < a.T; t0 += 16 * gridDim.y) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t t = t0 + i;
-    if (t >= a.T) return;
-    const int64_t at = (s * a.T + t) * a.D + d;
-    const Piece<T, VE> xr = load_piece<T, VE>(static_cast<const T *>(a.x) + at);
-    Piece<T, VE> zr;
-    if (a.z) zr = load_piece<T, VE>(static_cast<const T *>(a.z) + at);
-    float out[VE];
+    for (int i = 0; i < 4; ++i) {
+      const int64_t t = t0 + i;
+      if (t >= a.T) return;
+      const int64_t at = (s * a.T + t) * a.D + d;
+      const Piece<T, VE> xr = load_piece<T, VE>(static_cast<const T *>(a.x) + at);
+      Piece<T, VE> zr;
+      if (a.z) zr = load_piece<T, VE>(static_cast<const T *>(a.z) + at);
+      float out[VE];
 #pragma unroll
-    for (int e = 0; e < VE; ++e) {
-      const float zs = a.z ? silu(to_f32(zr.v[e])) : 1.f;
-      float u = to_f32(xr.v[e]);
-      if (a.gate_first) u *= zs;
-      float n = fmaf((u - mean - delta) * rstd, wv[e], bv[e]);
-      if (a.act) n = silu(n);
-      if (!a.gate_first) n *= zs;
-      out[e] = n;
+      for (int e = 0; e < VE; ++e) {
+        const float zs = a.z ? silu(to_f32(zr.v[e])) : 1.f;
+        float u = to_f32(xr.v[e]);
+        if (a.gate_first) u *= zs;
+        float n = fmaf((u - mean - delta) * rstd, wv[e], bv[e]);
+        if (a.act) n = silu(n);
+        if (!a.gate_first) n *= zs;
+        out[e] = n;
+      }
+      store_piece<T, VE>(static_cast<T *>(a.y) + at, out);
     }
-    store_piece<T, VE>(static_cast<T *>(a.y) + at, out);
   }
 }
 
@@ -484,10 +494,10 @@ __global__ __launch_bounds__(kThreads) void norm_cols_apply_kernel(NormArgs a, c
 template <typename T, int VE>
 __global__ __launch_bounds__(kThreads) void norm_cols_bsums_kernel(NormArgs a, int64_t rows, int64_t slices) {
   const int lane = threadIdx.x % 64;
-  const int64_t cb = (a.D + 64 * VE - 1) / (64 * VE), s = blockIdx.x / cb;
+  const int64_t cb = (a.D + 64 * VE - 1) / (64 * VE), block = flat_block(), s = block / cb;
   const int64_t slice = static_cast<int64_t>(blockIdx.y) * 4 + threadIdx.x / 64;
-  const int64_t d = (blockIdx.x % cb * 64 + lane) * VE;
-  if (slice >= slices || d >= a.D) return;
+  const int64_t d = (block % cb * 64 + lane) * VE;
+  if (s >= a.S || slice >= slices || d >= a.D) return;
   const int64_t g = d / (a.D / a.G);
   const float mean = a.center ? a.mean[s * a.G + g] : 0.f, rstd = a.rstd[s * a.G + g];
   const int64_t t0 = slice * rows, t1 = t0 + rows < a.T ? t0 + rows : a.T;
@@ -531,7 +541,8 @@ __global__ __launch_bounds__(kThreads) void norm_cols_bsums_kernel(NormArgs a, i
 // one workgroup per (s, g): mean(g) and mean(g xh)
 __global__ __launch_bounds__(kThreads) void norm_cols_bjoin_kernel(NormArgs a, int64_t slices, float *stat) {
   __shared__ float s_red[4];
-  const int64_t W = a.D / a.G, g = blockIdx.x % a.G, s = blockIdx.x / a.G;
+  const int64_t W = a.D / a.G, block = flat_block(), g = block % a.G, s = block / a.G;
+  if (s >= a.S) return;
   const float *p2 = a.ws + s * slices * a.D + g * W, *p1 = p2 + a.S * slices * a.D;
   const float inv = 1.f / (static_cast<float>(a.T) * static_cast<float>(W));
   float x = 0.f, y = 0.f;
@@ -551,9 +562,9 @@ __global__ __launch_bounds__(kThreads) void norm_cols_bjoin_kernel(NormArgs a, i
 template <typename T, int VE>
 __global__ __launch_bounds__(kThreads) void norm_cols_bapply_kernel(NormArgs a, const float *stat) {
   const int lane = threadIdx.x % 64;
-  const int64_t cb = (a.D + 64 * VE - 1) / (64 * VE), s = blockIdx.x / cb;
-  const int64_t W = a.D / a.G, d = (blockIdx.x % cb * 64 + lane) * VE;
-  if (d >= a.D) return;
+  const int64_t cb = (a.D + 64 * VE - 1) / (64 * VE), block = flat_block(), s = block / cb;
+  const int64_t W = a.D / a.G, d = (block % cb * 64 + lane) * VE;
+  if (s >= a.S || d >= a.D) return;
   const int64_t g = d / W;
   const float mean = a.center ? a.mean[s * a.G + g] : 0.f, rstd = a.rstd[s * a.G + g];
   const float mg = stat[2 * (s * a.G + g)], mgx = stat[2 * (s * a.G + g) + 1];
@@ -563,32 +574,38 @@ __global__ __launch_bounds__(kThreads) void norm_cols_bapply_kernel(NormArgs a, 
     wv[e] = a.w ? a.w[d + e] : 1.f;
     bv[e] = a.b ? a.b[d + e] : 0.f;
   }
-  const int64_t t0 = (static_cast<int64_t>(blockIdx.y) * 4 + threadIdx.x / 64) * 4;
+  for (int64_t t0 = (static_cast<int64_t>(blockIdx.y) * 4 + threadIdx.x / 64) * 4; t0 < a.T; t0 += 16 * gridDim.y) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t t = t0 + i;
-    if (t >= a.T) return;
-    const int64_t at = (s * a.T + t) * a.D + d;
-    const Piece<T, VE> xr = load_piece<T, VE>(static_cast<const T *>(a.x) + at);
-    const Piece<T, VE> yr = load_piece<T, VE>(static_cast<const T *>(a.dy) + at);
-    Piece<T, VE> zr;
-    if (a.z) zr = load_piece<T, VE>(static_cast<const T *>(a.z) + at);
-    float ox[VE], oz[VE];
+    for (int i = 0; i < 4; ++i) {
+      const int64_t t = t0 + i;
+      if (t >= a.T) return;
+      const int64_t at = (s * a.T + t) * a.D + d;
+      const Piece<T, VE> xr = load_piece<T, VE>(static_cast<const T *>(a.x) + at);
+      const Piece<T, VE> yr = load_piece<T, VE>(static_cast<const T *>(a.dy) + at);
+      Piece<T, VE> zr;
+      if (a.z) zr = load_piece<T, VE>(static_cast<const T *>(a.z) + at);
+      float ox[VE], oz[VE];
 #pragma unroll
-    for (int e = 0; e < VE; ++e) {
-      const float x = to_f32(xr.v[e]), z = a.z ? to_f32(zr.v[e]) : 0.f, dy = to_f32(yr.v[e]);
-      float xh, dn;
-      norm_elem(a, x, z, dy, wv[e], bv[e], mean, rstd, xh, dn);
-      const float du = rstd * (dn * wv[e] - mg - xh * mgx);
-      norm_elem_out(a, x, z, dy, wv[e], bv[e], xh, du, ox[e], oz[e]);
+      for (int e = 0; e < VE; ++e) {
+        const float x = to_f32(xr.v[e]), z = a.z ? to_f32(zr.v[e]) : 0.f, dy = to_f32(yr.v[e]);
+        float xh, dn;
+        norm_elem(a, x, z, dy, wv[e], bv[e], mean, rstd, xh, dn);
+        const float du = rstd * (dn * wv[e] - mg - xh * mgx);
+        norm_elem_out(a, x, z, dy, wv[e], bv[e], xh, du, ox[e], oz[e]);
+      }
+      store_piece<T, VE>(static_cast<T *>(a.dx) + at, ox);
+      if (a.z) store_piece<T, VE>(static_cast<T *>(a.dz) + at, oz);
     }
-    store_piece<T, VE>(static_cast<T *>(a.dx) + at, ox);
-    if (a.z) store_piece<T, VE>(static_cast<T *>(a.dz) + at, oz);
   }
 }
 
 // ------------------------------------------------------------------ choice
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+// n workgroups for flat_block(), each y times
+dim3 flat_grid(int64_t n, int64_t y = 1) {
+  const int64_t x = n < kMostX ? n : kMostX;
+  return dim3(static_cast<unsigned>(x), static_cast<unsigned>(y), static_cast<unsigned>(ceil_div(n, x)));
+}
 bool aligned16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 int vector_width(const NormArgs &a) {
@@ -685,7 +702,7 @@ void rows_bwd(const NormArgs &a, hipStream_t s) {
   const RowBwd r = plan_rows_bwd(a.S, a.G, RowPlan{LPG, NV});
   const dim3 grid(static_cast<unsigned>(ceil_div(a.G, r.gsub)), static_cast<unsigned>(r.blocks));
   norm_rows_bwd_kernel<T, VE, LPG, NV><<<grid, kThreads, 0, s>>>(a, r.gsub, r.rows, r.parts);
-  norm_params_kernel<<<static_cast<unsigned>(ceil_div(a.D, kParamChannels)), kThreads, 0, s>>>(a, r.parts, a.ws,
+  norm_params_kernel<<<flat_grid(ceil_div(a.D, kParamChannels)), kThreads, 0, s>>>(a, r.parts, a.ws,
                                                                                    a.ws + r.parts * a.D);
 }
 template <typename T, int VE, bool BWD>
@@ -716,14 +733,15 @@ bool rows(const NormArgs &a, hipStream_t s) {
 template <typename T, int VE, bool BWD>
 void cols(const NormArgs &a, hipStream_t s) {
   const int64_t rows = slice_rows(a.T), slices = ceil_div(a.T, rows);
-  const unsigned cb = static_cast<unsigned>(ceil_div(a.D, 64 * VE) * a.S), gj = static_cast<unsigned>(a.G * a.S);
-  const dim3 gs(cb, static_cast<unsigned>(ceil_div(slices, 4))), ga(cb, static_cast<unsigned>(ceil_div(a.T, 16)));
+  const int64_t cb = ceil_div(a.D, 64 * VE) * a.S;
+  const dim3 gs = flat_grid(cb, ceil_div(slices, 4)), ga = flat_grid(cb, a.T <= kMostTokens ? ceil_div(a.T, 16) : kMostTokens / 16),
+             gj = flat_grid(a.G * a.S);
   float *stat = a.ws + 2 * a.S * slices * a.D;
   if constexpr (BWD) {
     norm_cols_bsums_kernel<T, VE><<<gs, kThreads, 0, s>>>(a, rows, slices);
     norm_cols_bjoin_kernel<<<gj, kThreads, 0, s>>>(a, slices, stat);
     norm_cols_bapply_kernel<T, VE><<<ga, kThreads, 0, s>>>(a, stat);
-    norm_params_kernel<<<static_cast<unsigned>(ceil_div(a.D, kParamChannels)), kThreads, 0, s>>>(a, a.S * slices, a.ws,
+    norm_params_kernel<<<flat_grid(ceil_div(a.D, kParamChannels)), kThreads, 0, s>>>(a, a.S * slices, a.ws,
                                                                                      a.ws + a.S * slices * a.D);
   } else {
     norm_cols_sums_kernel<T, VE><<<gs, kThreads, 0, s>>>(a, rows, slices);
@@ -778,7 +796,7 @@ int64_t group_norm_bwd_ws_floats(int64_t S, int64_t T, int64_t D, int64_t G) {
 hipError_t launch_group_norm_fwd(const NormArgs &a, hipStream_t s) { return launch<false>(a, s); }
 hipError_t launch_group_norm_bwd(const NormArgs &a, hipStream_t s) {
   if (a.S == 0 || a.T == 0) {
-    norm_params_kernel<<<static_cast<unsigned>(ceil_div(a.D, kParamChannels)), kThreads, 0, s>>>(a, 0, nullptr, nullptr);
+    norm_params_kernel<<<flat_grid(ceil_div(a.D, kParamChannels)), kThreads, 0, s>>>(a, 0, nullptr, nullptr);
     return hipGetLastError();
   }
   return launch<true>(a, s);
