@@ -543,8 +543,10 @@ size_t ssm_gdr_bwd_workspace_size(int64_t B, int64_t L, int64_t H, int64_t P, in
  * Outputs must not overlap inputs or each other.  G divides D, T <= 2^20,
  * D and S * D < 2^31 (else SSM_ERR_UNSUPPORTED); eps finite and >= 0.  An empty x
  * is a no-op.
- * workspace : ssm_group_norm_fwd_workspace_size() bytes, 16-byte aligned
- *             (NULL where 0, as for T == 1 up to W = 1280 and more).
+ * workspace : ssm_group_norm_fwd_workspace_size_ex() bytes, 16-byte aligned
+ *             (NULL where 0: for T == 1 up to W = 10240 in bf16, 5120 in fp32,
+ *             2048 where a tensor is not 16-byte aligned or a group's channels
+ *             are no whole 16 bytes).
  */
 ssm_status ssm_group_norm_fwd(int64_t S, int64_t T, int64_t D, int64_t G, ssm_dtype dt,
                               const void *x, const void *z, const float *weight,
@@ -553,6 +555,11 @@ ssm_status ssm_group_norm_fwd(int64_t S, int64_t T, int64_t D, int64_t G, ssm_dt
                               float *rstd, void *workspace, size_t workspace_bytes,
                               void *stream);
 
+/* Device workspace of ssm_group_norm_fwd (bytes); aligned == 1: x, z, y, weight
+ * and bias (those given) are 16-byte aligned; 0: some are not. */
+size_t ssm_group_norm_fwd_workspace_size_ex(int64_t S, int64_t T, int64_t D, int64_t G,
+                                            ssm_dtype dt, int32_t aligned);
+/* The most of these over both types and any alignment. */
 size_t ssm_group_norm_fwd_workspace_size(int64_t S, int64_t T, int64_t D, int64_t G);
 
 /*
@@ -562,6 +569,7 @@ size_t ssm_group_norm_fwd_workspace_size(int64_t S, int64_t T, int64_t D, int64_
  * (dz exactly when z is given), dweight, dbias (D) fp32 or NULL; each
  * overwritten, sums in fp32 and in a fixed order.  An empty x writes zeros to
  * dweight and dbias.
+ * workspace : ssm_group_norm_bwd_workspace_size_ex() bytes, 16-byte aligned.
  */
 ssm_status ssm_group_norm_bwd(int64_t S, int64_t T, int64_t D, int64_t G, ssm_dtype dt,
                               const void *x, const void *z, const float *weight,
@@ -571,6 +579,9 @@ ssm_status ssm_group_norm_bwd(int64_t S, int64_t T, int64_t D, int64_t G, ssm_dt
                               float *dweight, float *dbias, void *workspace,
                               size_t workspace_bytes, void *stream);
 
+/* As the forward's; aligned counts x, z, weight, bias, dy, dx and dz. */
+size_t ssm_group_norm_bwd_workspace_size_ex(int64_t S, int64_t T, int64_t D, int64_t G,
+                                            ssm_dtype dt, int32_t aligned);
 size_t ssm_group_norm_bwd_workspace_size(int64_t S, int64_t T, int64_t D, int64_t G);
 
 /* Static description of a status code. */

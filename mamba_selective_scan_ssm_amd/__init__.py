@@ -113,6 +113,9 @@ def lib():
         for f in (L.ssm_group_norm_fwd_workspace_size, L.ssm_group_norm_bwd_workspace_size):
             f.argtypes = [i64] * 4
             f.restype = sz
+        for f in (L.ssm_group_norm_fwd_workspace_size_ex, L.ssm_group_norm_bwd_workspace_size_ex):
+            f.argtypes = [i64] * 4 + [ctypes.c_int, i32]
+            f.restype = sz
         L.ssm_status_string.argtypes = [ctypes.c_int]
         L.ssm_status_string.restype = ctypes.c_char_p
         L.ssm_version.argtypes = []
@@ -592,13 +595,17 @@ def gdr_bwd(q, k, v, dt, A, beta, h0=None, dy=None, dh_final=None, *, scale=None
            "dA": torch.empty((H,), dtype=torch.float32, device=dev),
            "dh0": torch.empty((B, H, P, N), dtype=torch.float32, device=dev) if want_dh0 else None,
            "dbias": torch.empty((H,), dtype=torch.float32, device=dev) if want_dbias else None}
-    aligned = all(t is None or t.data_ptr() % 16 == 0 for t in (q, k, h0, dy, dh_final, out["dh0"]))
+    aligned = _aligned(q, k, h0, dy, dh_final, out["dh0"])
     workspace, ws_len = _workspace(workspace, gdr_bwd_workspace_size(*sizes, typ, aligned), dev)
     _gpu_call(dev, "ssm_gdr_bwd", *sizes, code, _ptr(q), _ptr(k), _ptr(v), _ptr(dt), _ptr(A), _ptr(beta), _ptr(h0),
               _ptr(dy), _ptr(dh_final), _scale(scale, N), int(bool(qk_norm)), _ptr(out["dq"]), _ptr(out["dk"]),
               _ptr(out["dv"]), _ptr(out["ddt"]), _ptr(out["dbeta"]), _ptr(out["dA"]), _ptr(out["dh0"]),
               _ptr(out["dbias"]), _ptr(workspace), ws_len, _dopts(dt_bias, dt_softplus))
     return out
+
+
+def _aligned(*tensors):
+    return int(all(t is None or t.data_ptr() % 16 == 0 for t in tensors))
 
 
 def _norm_args(x, groups, weight, bias, z, activation, gate, per_token):
@@ -641,7 +648,10 @@ def group_norm_fwd(x, groups, weight=None, bias=None, z=None, *, eps=1e-5, cente
     stat = (x.shape[0], x.shape[1], G) if per_token else (x.shape[0], G)
     mean = torch.empty(stat, dtype=torch.float32, device=dev) if return_stats and center else None
     rstd = torch.empty(stat, dtype=torch.float32, device=dev) if return_stats else None
-    workspace, ws_len = _workspace(workspace, int(lib().ssm_group_norm_fwd_workspace_size(*sizes)), dev)
+    need = int(lib().ssm_group_norm_fwd_workspace_size(*sizes))
+    if need > 0:  # for some type and alignment
+        need = int(lib().ssm_group_norm_fwd_workspace_size_ex(*sizes, code, _aligned(x, z, weight, bias, y)))
+    workspace, ws_len = _workspace(workspace, need, dev)
     _gpu_call(dev, "ssm_group_norm_fwd", *sizes, code, _ptr(x), _ptr(z), _ptr(weight), _ptr(bias), float(eps),
               int(bool(center)), act, first, _ptr(y), _ptr(mean), _ptr(rstd), _ptr(workspace), ws_len)
     return y, mean, rstd
@@ -664,7 +674,9 @@ def group_norm_bwd(x, groups, dy, mean, rstd, weight=None, bias=None, z=None, *,
     out = {"dx": torch.empty_like(x), "dz": None if z is None else torch.empty_like(z),
            "dweight": None if weight is None else torch.empty_like(weight),
            "dbias": None if bias is None else torch.empty_like(bias)}
-    workspace, ws_len = _workspace(workspace, int(lib().ssm_group_norm_bwd_workspace_size(*sizes)), dev)
+    need = int(lib().ssm_group_norm_bwd_workspace_size_ex(
+        *sizes, code, _aligned(x, z, weight, bias, dy, out["dx"], out["dz"])))
+    workspace, ws_len = _workspace(workspace, need, dev)
     _gpu_call(dev, "ssm_group_norm_bwd", *sizes, code, _ptr(x), _ptr(z), _ptr(weight), _ptr(bias), _ptr(dy),
               _ptr(mean) if center else None, _ptr(rstd), float(eps), int(bool(center)), act, first, _ptr(out["dx"]),
               _ptr(out["dz"]), _ptr(out["dweight"]), _ptr(out["dbias"]), _ptr(workspace), ws_len)

@@ -200,6 +200,27 @@ size_t ssm_group_norm_bwd_workspace_size(int64_t S, int64_t T, int64_t D, int64_
   return static_cast<size_t>(ssm::group_norm_bwd_ws_floats(S, T, D, G)) * 4;
 }
 
+// Sizes of a call whose tensors are all 16-byte aligned, or of one whose are not.
+static ssm::NormArgs norm_of(int64_t S, int64_t T, int64_t D, int64_t G, ssm_dtype dt, int32_t aligned) {
+  ssm::NormArgs a{};
+  a.S = S; a.T = T; a.D = D; a.G = G;
+  a.dt = dt == SSM_BF16 ? DType::BF16 : DType::F32;
+  a.x = aligned ? nullptr : reinterpret_cast<const void *>(uintptr_t{1});
+  return a;
+}
+size_t ssm_group_norm_fwd_workspace_size_ex(int64_t S, int64_t T, int64_t D, int64_t G, ssm_dtype dt,
+                                            int32_t aligned) {
+  int64_t n;
+  if (norm_sizes(S, T, D, G, dt, 0.f, 0, 0, 0, &n) != SSM_OK || n == 0 || (aligned != 0 && aligned != 1)) return 0;
+  return static_cast<size_t>(ssm::group_norm_fwd_ws_floats(norm_of(S, T, D, G, dt, aligned))) * 4;
+}
+size_t ssm_group_norm_bwd_workspace_size_ex(int64_t S, int64_t T, int64_t D, int64_t G, ssm_dtype dt,
+                                            int32_t aligned) {
+  int64_t n;
+  if (norm_sizes(S, T, D, G, dt, 0.f, 0, 0, 0, &n) != SSM_OK || n == 0 || (aligned != 0 && aligned != 1)) return 0;
+  return static_cast<size_t>(ssm::group_norm_bwd_ws_floats(norm_of(S, T, D, G, dt, aligned))) * 4;
+}
+
 ssm_status ssm_group_norm_fwd(int64_t S, int64_t T, int64_t D, int64_t G, ssm_dtype dt, const void *x, const void *z,
                               const float *weight, const float *bias, float eps, int32_t center, int32_t activation,
                               int32_t gate_first, void *y, float *mean, float *rstd, void *workspace,
@@ -212,13 +233,6 @@ ssm_status ssm_group_norm_fwd(int64_t S, int64_t T, int64_t D, int64_t G, ssm_dt
   if (mean && !center) return SSM_ERR_INVALID_ARG;
   const int64_t es = esize(dt);
   const Range ins[] = {{x, n * es}, {z, n * es}, {weight, D * 4}, {bias, D * 4}};
-  const int64_t need = static_cast<int64_t>(ssm_group_norm_fwd_workspace_size(S, T, D, G));
-  if (need > 0 && (!workspace || !aligned16(workspace) || static_cast<int64_t>(workspace_bytes) < need))
-    return SSM_ERR_WORKSPACE;
-  const Range outs[] = {{y, n * es}, {mean, S * G * 4}, {rstd, S * G * 4}, {workspace, need}};
-  for (const Range &r : outs)
-    if (overlaps_any(r, ins)) return SSM_ERR_INVALID_ARG;
-  if (any_pair(outs, sizeof(outs) / sizeof(outs[0]))) return SSM_ERR_INVALID_ARG;
   ssm::NormArgs a{};
   a.S = S; a.T = T; a.D = D; a.G = G;
   a.dt = dt == SSM_BF16 ? DType::BF16 : DType::F32;
@@ -226,6 +240,13 @@ ssm_status ssm_group_norm_fwd(int64_t S, int64_t T, int64_t D, int64_t G, ssm_dt
   a.center = center != 0; a.act = activation != 0; a.gate_first = gate_first != 0;
   a.y = y; a.mean = mean; a.rstd = rstd;
   a.ws = static_cast<float *>(workspace);
+  const int64_t need = ssm::group_norm_fwd_ws_floats(a) * 4;
+  if (need > 0 && (!workspace || !aligned16(workspace) || static_cast<int64_t>(workspace_bytes) < need))
+    return SSM_ERR_WORKSPACE;
+  const Range outs[] = {{y, n * es}, {mean, S * G * 4}, {rstd, S * G * 4}, {workspace, need}};
+  for (const Range &r : outs)
+    if (overlaps_any(r, ins)) return SSM_ERR_INVALID_ARG;
+  if (any_pair(outs, sizeof(outs) / sizeof(outs[0]))) return SSM_ERR_INVALID_ARG;
   return hip_status(ssm::launch_group_norm_fwd(a, static_cast<hipStream_t>(stream)));
 }
 
@@ -243,13 +264,6 @@ ssm_status ssm_group_norm_bwd(int64_t S, int64_t T, int64_t D, int64_t G, ssm_dt
   const int64_t es = esize(dt);
   const Range ins[] = {{x, n * es},    {z, n * es},         {weight, D * 4},     {bias, D * 4},
                        {dy, n * es}, {mean, S * G * 4}, {rstd, S * G * 4}};
-  const int64_t need = static_cast<int64_t>(ssm_group_norm_bwd_workspace_size(S, T, D, G));
-  if (need > 0 && (!workspace || !aligned16(workspace) || static_cast<int64_t>(workspace_bytes) < need))
-    return SSM_ERR_WORKSPACE;
-  const Range outs[] = {{dx, n * es}, {dz, n * es}, {dweight, D * 4}, {dbias, D * 4}, {workspace, need}};
-  for (const Range &r : outs)
-    if (overlaps_any(r, ins)) return SSM_ERR_INVALID_ARG;
-  if (any_pair(outs, sizeof(outs) / sizeof(outs[0]))) return SSM_ERR_INVALID_ARG;
   ssm::NormArgs a{};
   a.S = S; a.T = T; a.D = D; a.G = G;
   a.dt = dt == SSM_BF16 ? DType::BF16 : DType::F32;
@@ -258,6 +272,13 @@ ssm_status ssm_group_norm_bwd(int64_t S, int64_t T, int64_t D, int64_t G, ssm_dt
   a.mean = const_cast<float *>(mean); a.rstd = const_cast<float *>(rstd);
   a.dy = dy; a.dx = dx; a.dz = dz; a.dw = dweight; a.db = dbias;
   a.ws = static_cast<float *>(workspace);
+  const int64_t need = n > 0 ? ssm::group_norm_bwd_ws_floats(a) * 4 : 0;
+  if (need > 0 && (!workspace || !aligned16(workspace) || static_cast<int64_t>(workspace_bytes) < need))
+    return SSM_ERR_WORKSPACE;
+  const Range outs[] = {{dx, n * es}, {dz, n * es}, {dweight, D * 4}, {dbias, D * 4}, {workspace, need}};
+  for (const Range &r : outs)
+    if (overlaps_any(r, ins)) return SSM_ERR_INVALID_ARG;
+  if (any_pair(outs, sizeof(outs) / sizeof(outs[0]))) return SSM_ERR_INVALID_ARG;
   return hip_status(ssm::launch_group_norm_bwd(a, static_cast<hipStream_t>(stream)));
 }
 

@@ -26,6 +26,10 @@ struct NormArgs {
   float *ws;
 };
 
+// Floats of workspace: of this call (its type and alignment choose the path), and
+// the most that a call of these sizes takes.
+int64_t group_norm_fwd_ws_floats(const NormArgs &a);
+int64_t group_norm_bwd_ws_floats(const NormArgs &a);
 int64_t group_norm_fwd_ws_floats(int64_t S, int64_t T, int64_t D, int64_t G);
 int64_t group_norm_bwd_ws_floats(int64_t S, int64_t T, int64_t D, int64_t G);
 hipError_t launch_group_norm_fwd(const NormArgs &a, hipStream_t s);

@@ -768,29 +768,32 @@ hipError_t launch(const NormArgs &a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// The workspace covers either type and any alignment of these sizes.
+// Of these sizes in pieces of ve elements.
+int64_t fwd_floats(int64_t S, int64_t T, int64_t D, int64_t G, int ve) {
+  return T == 1 && plan_rows(D / G / ve, ve, false).nv != 0 ? 0 : cols_ws_floats(S, T, D, G);
+}
+int64_t bwd_floats(int64_t S, int64_t T, int64_t D, int64_t G, int ve) {
+  const RowPlan p = T == 1 ? plan_rows(D / G / ve, ve, true) : RowPlan{0, 0};
+  return p.nv != 0 ? 2 * plan_rows_bwd(S, G, p).parts * D : cols_ws_floats(S, T, D, G);
+}
+// The most over either type and any alignment.
 template <typename F>
-void each_width(int64_t W, F f) {
+int64_t of_any_width(int64_t W, F f) {
+  int64_t n = 0;
   for (int ve : {1, 4, 8})
-    if (W % ve == 0) f(ve);
+    if (W % ve == 0 && f(ve) > n) n = f(ve);
+  return n;
 }
 
 }  // namespace
 
+int64_t group_norm_fwd_ws_floats(const NormArgs &a) { return fwd_floats(a.S, a.T, a.D, a.G, vector_width(a)); }
+int64_t group_norm_bwd_ws_floats(const NormArgs &a) { return bwd_floats(a.S, a.T, a.D, a.G, vector_width(a)); }
 int64_t group_norm_fwd_ws_floats(int64_t S, int64_t T, int64_t D, int64_t G) {
-  bool cols = T != 1;
-  each_width(D / G, [&](int ve) { cols = cols || plan_rows(D / G / ve, ve, false).nv == 0; });
-  return cols ? cols_ws_floats(S, T, D, G) : 0;
+  return of_any_width(D / G, [&](int ve) { return fwd_floats(S, T, D, G, ve); });
 }
 int64_t group_norm_bwd_ws_floats(int64_t S, int64_t T, int64_t D, int64_t G) {
-  int64_t n = T != 1 ? cols_ws_floats(S, T, D, G) : 0;
-  if (T != 1) return n;
-  each_width(D / G, [&](int ve) {
-    const RowPlan p = plan_rows(D / G / ve, ve, true);
-    const int64_t m = p.nv == 0 ? cols_ws_floats(S, T, D, G) : 2 * plan_rows_bwd(S, G, p).parts * D;
-    if (m > n) n = m;
-  });
-  return n;
+  return of_any_width(D / G, [&](int ve) { return bwd_floats(S, T, D, G, ve); });
 }
 
 hipError_t launch_group_norm_fwd(const NormArgs &a, hipStream_t s) { return launch<false>(a, s); }
