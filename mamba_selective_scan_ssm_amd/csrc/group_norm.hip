@@ -16,7 +16,7 @@
 //    registers; the blocks' sums are added in order by a second kernel.
 //  - columns (everything else): per-channel sums over slices of the tokens,
 //    coalesced whatever W is; a kernel that joins the slices and the channels
-//    of a group (mean and squares about it by Chan's formula; the backward's
+//    of a group (mean and squares about it by Chan's formula, as within a slice; the backward's
 //    group sums are sums of its per-channel ones weighted by w); and a pass
 //    that applies them.
 // All sums are fp32 and in a fixed order.
@@ -359,8 +359,9 @@ __global__ __launch_bounds__(kThreads) void norm_params_kernel(NormArgs a, int64
 
 // ------------------------------------------------------------------ columns
 // Slices of `rows` tokens; a wave holds 64 VE channels of one slice, a
-// workgroup 4 slices.  fwd: per channel the mean and the squares about it,
-// from sums shifted by the slice's first value.
+// workgroup 4 slices.  fwd: per channel the mean (less the slice's first value) and
+// the squares about it, of four tokens after another joined with those before them:
+// differences of sums would lose what a token far from the others leaves of them.
 template <typename T, int VE>
 __global__ __launch_bounds__(kThreads) void norm_cols_sums_kernel(NormArgs a, int64_t rows, int64_t slices) {
   const int lane = threadIdx.x % 64;
@@ -370,32 +371,47 @@ __global__ __launch_bounds__(kThreads) void norm_cols_sums_kernel(NormArgs a, in
   if (s >= a.S || slice >= slices || d >= a.D) return;
   const int64_t t0 = slice * rows, t1 = t0 + rows < a.T ? t0 + rows : a.T;
   const bool gate = a.z && a.gate_first;
-  float first[VE], s1[VE], s2[VE];
+  constexpr int kAhead = 4;  // tokens loaded together
+  float first[VE], mean[VE], sq[VE];
 #pragma unroll
-  for (int e = 0; e < VE; ++e) s1[e] = s2[e] = first[e] = 0.f;
-#pragma unroll 4
-  for (int64_t t = t0; t < t1; ++t) {
-    const int64_t at = (s * a.T + t) * a.D + d;
-    const Piece<T, VE> xr = load_piece<T, VE>(static_cast<const T *>(a.x) + at);
-    Piece<T, VE> zr;
-    if (gate) zr = load_piece<T, VE>(static_cast<const T *>(a.z) + at);
+  for (int e = 0; e < VE; ++e) first[e] = mean[e] = sq[e] = 0.f;
+  for (int64_t t = t0; t < t1; t += kAhead) {
+    Piece<T, VE> xr[kAhead], zr[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int64_t at = (s * a.T + (t + i < t1 ? t + i : t1 - 1)) * a.D + d;
+      xr[i] = load_piece<T, VE>(static_cast<const T *>(a.x) + at);
+      if (gate) zr[i] = load_piece<T, VE>(static_cast<const T *>(a.z) + at);
+    }
+    // the four tokens' share of those so far
+    const float before = static_cast<float>(t - t0), n = t + kAhead < t1 ? kAhead : static_cast<float>(t1 - t);
+    const float inv = 1.f / n, share = n / (before + n);
 #pragma unroll
     for (int e = 0; e < VE; ++e) {
-      float u = to_f32(xr.v[e]);
-      if (gate) u *= silu(to_f32(zr.v[e]));
-      if (t == t0 && a.center) first[e] = u;
-      const float c = u - first[e];
-      s1[e] += c;
-      s2[e] = fmaf(c, c, s2[e]);
+      float u[kAhead], sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        u[i] = to_f32(xr[i].v[e]);
+        if (gate) u[i] *= silu(to_f32(zr[i].v[e]));
+        if (i == 0 && t == t0 && a.center) first[e] = u[0];
+        u[i] -= first[e];
+        if (t + i < t1) sum += u[i];
+      }
+      const float m = a.center ? sum * inv : 0.f, off = m - mean[e];
+      float about = 0.f;
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        if (t + i < t1) about = fmaf(u[i] - m, u[i] - m, about);
+      sq[e] += fmaf(off * off, before * share, about);
+      mean[e] = fmaf(off, share, mean[e]);
     }
   }
-  const float n = static_cast<float>(t1 - t0);
 #pragma unroll
   for (int e = 0; e < VE; ++e) {
     const int64_t at = (s * slices + slice) * a.D + d + e;
     // not centred: the squares about 0, and no mean
-    a.ws[at] = a.center ? first[e] + s1[e] / n : 0.f;
-    a.ws[a.S * slices * a.D + at] = a.center ? not_negative(s2[e] - s1[e] * (s1[e] / n)) : s2[e];
+    a.ws[at] = first[e] + mean[e];
+    a.ws[a.S * slices * a.D + at] = sq[e];
   }
 }
 
@@ -681,11 +697,11 @@ RowBwd plan_rows_bwd(int64_t S, int64_t G, RowPlan p) {
   r.parts = r.blocks * r.rsub;
   return r;
 }
-// Tokens per slice: at least 8 where there are that many, at most 128 slices.
+// Tokens per slice: at least 8 where there are that many, 128 slices where that is
+// more, at most 256 (sums one behind the other stay short).
 int64_t slice_rows(int64_t T) {
-  int64_t r = ceil_div(T, 128);
-  if (r < 8) r = 8;
-  return r;
+  const int64_t r = ceil_div(T, 128);
+  return r < 8 ? 8 : r < 256 ? r : 256;
 }
 int64_t cols_ws_floats(int64_t S, int64_t T, int64_t D, int64_t G) {
   const int64_t slices = ceil_div(T, slice_rows(T));
