@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from tests import mixer_reference as ref
-from tests.test_gpu_gdr import _say, fwd
+from tests.test_gpu_gdr import SHAPES, _say, fwd
 
 pytestmark = pytest.mark.gpu
 
@@ -46,3 +46,22 @@ def test_rows_behind_the_last_are_left():
                            dt_softplus=True, y=buf[:n].view(w["v"].shape))
         torch.cuda.synchronize()
         assert (buf[n:] == 7.0).all(), (L, P)
+
+
+@pytest.mark.parametrize("qk_norm", [True, False])
+@pytest.mark.parametrize("B,L,H,P,G,N", SHAPES)
+def test_prefill_without_slack(B, L, H, P, G, N, qk_norm):
+    """bf16 outputs within the common bar, by chunks, by tokens, and unaligned."""
+    import mamba_selective_scan_ssm_amd as ssm
+    _say("gdr_fwd bar", B, L, H, P, G, N, qk_norm)
+    w = ref.make_gdr(B, L, H, P, G, N, BF16, 73 + L, qk_norm=qk_norm)
+    r, _ = ref.gdr_of(w, qk_norm)
+    y, _ = fwd(w, qk_norm)
+    ref.close(y, r, "y")
+    d = {n: t.cuda() for n, t in w.items()}
+    q = torch.empty(w["q"].numel() + 1, dtype=BF16, device="cuda")[1:].view(w["q"].shape)
+    q.copy_(w["q"])
+    y, _ = ssm.gdr_fwd(q, d["k"], d["v"], d["dt"], d["A"], d["beta"], d["h0"], qk_norm=qk_norm, dt_bias=d["bias"],
+                       dt_softplus=True)
+    torch.cuda.synchronize()
+    ref.close(y, r, "y of unaligned q")

@@ -83,3 +83,28 @@ def test_not_finite_dy(value, dtype):
     bad["dh0"][1, 2, 5] = True
     for n in bad:
         same_where_clean(g[n], g0[n], bad[n], n)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("name,value", [("v", NAN), ("v", INF), ("beta", NAN), ("dt", NAN), ("k", NAN), ("k", INF), ("q", NAN)])
+def test_not_finite_inputs_backward(name, value, dtype):
+    """Gradients of inputs that are not finite: nothing finite where the definition
+    has nothing finite, its values where there is something, and what is lost beside
+    that is lost within 63 tokens, of the value's heads."""
+    _say("gdr_bwd not finite", name, value, dtype)
+    qk_norm = not (name == "k" and value == INF)
+    w, s = spoiled(dtype, name, value, qk_norm)
+    g, r = bwd(s, qk_norm), ref.gdr_grads_of(s, qk_norm)
+    slack = ref.gdr_grad_slack(w, qk_norm)
+    for n in r:
+        got, want = g["d" + n].cpu(), r[n]
+        lost = ~torch.isfinite(got)
+        assert lost[~torch.isfinite(want)].all(), f"d{n}: finite where the definition is not"
+        beside = lost & torch.isfinite(want)
+        if beside.any():
+            assert dtype == BF16 and n not in ("A", "h0"), n
+            b, t, h = (beside.nonzero()[:, i] for i in range(3))
+            assert (b == 1).all() and ((t - T_NAN).abs() <= 63).all(), n
+            assert (h == 1).all() if n in "qk" else (h >= 2).all(), n
+        clean = torch.where(lost, torch.zeros_like(want), want)
+        ref.close(torch.where(lost, torch.zeros_like(got), got), clean, "d" + n, slack.get(n))
