@@ -439,7 +439,10 @@ ssm_status ssm_conv1d_update(int64_t S, int64_t D, int64_t K, ssm_dtype dt, floa
  * qk_norm == 1: q and k are divided by sqrt(sum_n x[n]^2 + 1e-6) first.
  * beta enters as given (a model's sigmoid is applied by the caller); dt and A
  * as in ssm_ssd_fwd, the decay a_t = exp(dt * A) being at most 1 for the
- * positive dt and negative A that models have (neither sign is required).
+ * positive dt and negative A that models have.  A decay above 1 is taken as it
+ * is, but by chunks (bf16, N a multiple of 8 up to 128, L >= 32, aligned) the
+ * errors grow with the product of the decays over up to 64 tokens, and where
+ * that passes 2^127 the results are not finite, also of a state that is zero.
  *
  * q, k      : (B, L, G, N) dtype `dt`;  v, y : (B, L, H, P) dtype `dt`
  * dt_in, beta : (B, L, H) dtype `dt`;   A : (H) fp32
@@ -447,9 +450,8 @@ ssm_status ssm_conv1d_update(int64_t S, int64_t D, int64_t K, ssm_dtype dt, floa
  * y and h_final must not overlap any input or each other.  Arithmetic and
  * state are fp32 (on the matrix cores computed operands are split into three
  * bf16 parts, which hold all 24 bits).
- * workspace : ssm_gdr_fwd_workspace_size() bytes, 16-byte aligned (NULL where
- *             that is 0); contents ignored on entry; two calls that overlap
- *             in time must not share it.
+ * workspace : none is taken (ssm_gdr_fwd_workspace_size() is 0 for all sizes):
+ *             NULL and 0; what is passed is not touched.
  * Sizes: 1 <= N <= SSM_GDR_MAX_N, G divides H, B and H <= 65535, H P <= 2^24
  * (else SSM_ERR_UNSUPPORTED); any L >= 0 (L == 0 writes h_final = h0) and
  * P >= 0.  A sequence's results do not depend on the batch (bitwise).
@@ -465,7 +467,7 @@ ssm_status ssm_gdr_fwd(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G, in
                        void *workspace, size_t workspace_bytes,
                        const ssm_delta_opts *dopts, void *stream);
 
-/* Device workspace of ssm_gdr_fwd for these sizes (bytes). */
+/* Device workspace of ssm_gdr_fwd for these sizes (bytes): 0. */
 size_t ssm_gdr_fwd_workspace_size(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G,
                                   int64_t N, ssm_dtype dt);
 

@@ -528,7 +528,8 @@ def gdr_fwd(q, k, v, dt, A, beta, h0=None, *, scale=None, qk_norm=False, y=None,
     all bfloat16; A: (H,) float32; h0: (B, H, P, N) float32.  The decay is
     exp(dt * A), with dt_bias (H,) float32 added to dt and softplus applied if
     dt_softplus.  scale: of the output, N ** -0.5 by default.  qk_norm: q and k
-    are divided by their 2-norms.  Returns (y, h_final)."""
+    are divided by their 2-norms.  workspace: none is needed.  Returns (y,
+    h_final)."""
     sizes, code, typ, dev = _gdr_inputs(q, k, v, dt, A, beta, dt_bias)
     B, L, H, P, G, N = sizes
     _check("h0", h0, (B, H, P, N), torch.float32, dev)
@@ -538,7 +539,7 @@ def gdr_fwd(q, k, v, dt, A, beta, h0=None, *, scale=None, qk_norm=False, y=None,
     if h_final is None and return_final:
         h_final = torch.empty((B, H, P, N), dtype=torch.float32, device=dev)
     _check("h_final", h_final, (B, H, P, N), torch.float32, dev)
-    workspace, ws_len = _workspace(workspace, gdr_fwd_workspace_size(*sizes, typ), dev)
+    workspace, ws_len = _workspace(workspace, 0, dev)
     _gpu_call(dev, "ssm_gdr_fwd", *sizes, code, _ptr(q), _ptr(k), _ptr(v), _ptr(dt), _ptr(A), _ptr(beta), _ptr(h0),
               _scale(scale, N), int(bool(qk_norm)), _ptr(y), _ptr(h_final), _ptr(workspace), ws_len,
               _dopts(dt_bias, dt_softplus))

@@ -62,16 +62,13 @@ bool any_pair(const Range *r, size_t n) {
 
 extern "C" {
 
-size_t ssm_gdr_fwd_workspace_size(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G, int64_t N, ssm_dtype dt) {
-  GdrSizes z;
-  if (gdr_sizes(B, L, H, P, G, N, dt, 0, nullptr, &z) != SSM_OK) return 0;
-  return 0;
-}
+// The prefill's kernels keep everything in registers and LDS.
+size_t ssm_gdr_fwd_workspace_size(int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, ssm_dtype) { return 0; }
 
 ssm_status ssm_gdr_fwd(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G, int64_t N, ssm_dtype dt, const void *q,
                        const void *k, const void *v, const void *dt_in, const float *A, const void *beta,
-                       const float *h0, float scale, int32_t qk_norm, void *y, float *h_final, void *workspace,
-                       size_t workspace_bytes, const ssm_delta_opts *dopts, void *stream) {
+                       const float *h0, float scale, int32_t qk_norm, void *y, float *h_final, void * /*workspace*/,
+                       size_t /*workspace_bytes*/, const ssm_delta_opts *dopts, void *stream) {
   GdrSizes z;
   const ssm_status st = gdr_sizes(B, L, H, P, G, N, dt, qk_norm, dopts, &z);
   if (st != SSM_OK) return st;
@@ -82,12 +79,6 @@ ssm_status ssm_gdr_fwd(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G, in
                        {beta, z.nT * es}, {h0, z.nS * 4}, {dbias_of(dopts), H * 4}};
   const Range ry{y, z.nV * es}, rh{h_final, z.nS * 4};
   if (overlaps_any(ry, ins) || overlaps_any(rh, ins) || overlap(ry, rh)) return SSM_ERR_INVALID_ARG;
-  const int64_t need = static_cast<int64_t>(ssm_gdr_fwd_workspace_size(B, L, H, P, G, N, dt));
-  if (need > 0) {
-    if (!workspace || !aligned16(workspace) || static_cast<int64_t>(workspace_bytes) < need) return SSM_ERR_WORKSPACE;
-    const Range rw{workspace, need};
-    if (overlaps_any(rw, ins) || overlap(rw, ry) || overlap(rw, rh)) return SSM_ERR_INVALID_ARG;
-  }
   ssm::GdrArgs a = gdr_args(B, L, H, P, G, N, dt, q, k, v, dt_in, A, beta, h0, scale, qk_norm, dopts);
   a.y = y;
   a.h_final = h_final;
