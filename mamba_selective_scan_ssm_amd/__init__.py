@@ -158,12 +158,18 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+# not a public name of torch's: where it is missing, a Stream object is made
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(device):
     # the handle alone: a Stream object made for it costs 1.9 us more, of a 13 us call
     if device.type != "cuda":
         raise ValueError(f"tensors must be on a GPU, not on {device}")
+    if _raw_stream is None:
+        return torch.cuda.current_stream(device).cuda_stream
     index = torch.cuda.current_device() if device.index is None else device.index
-    return torch._C._cuda_getCurrentRawStream(index)
+    return _raw_stream(index)
 
 
 def _call(fn_name, *args):
