@@ -45,18 +45,18 @@ hipError_t launch_gdr_step(const GdrArgs &a, hipStream_t s);
 // By chunks of 64 tokens on the matrix cores (gdr_chunk.hip): bf16, N a
 // multiple of 8 up to 128, L >= kGdrChunkMinL, q, k and the states 16-byte
 // aligned; no workspace.  A chunk takes its time however few its tokens: 8
-// sequences, 32 heads of 128 x 128: 28 us for 32 to 64 tokens, by tokens 26 for 24,
-// 33 for 32, 56 for 64; gradients 112 to 118 us for 32 to 64 tokens, by tokens 137
-// for 24, 173 for 32, 327 for 64.  2 sequences, 80 heads of 64 x 128: gradients 68 to
-// 70, by tokens 73 for 16, 87 for 24, 149 for 64.
+// sequences, 32 heads of 128 x 128: 29 to 30 us for 32 to 64 tokens, by tokens 26 for
+// 24, 34 for 32, 57 for 64; gradients 109 to 115 us for 32 to 64 tokens, by tokens 137
+// for 24, 167 for 32, 323 for 64.  2 sequences, 80 heads of 64 x 128: gradients 69 to
+// 70, by tokens 75 for 16, 89 for 24, 151 for 64.
 constexpr int64_t kGdrChunkMinL = 32;
 bool gdr_chunk_applies(const GdrArgs &a);
 // Columns of a state that a workgroup of a chain takes, 16 a wave: as few as leave
 // each a CU of its own, where the waves that prepare the chunks are in the way of
-// fewer of the chain's.  64 / 32 / 16: 4001 tokens, 32 heads of 128 x 128 279 / 256 /
-// 245 us; 2048 tokens, 80 heads of 64 x 128 143 / 138 / (two on many CUs) 251;
-// gradients of 4096 tokens, 16 heads of 64 x 128 691 / 591 / 574, of 2048 tokens, 32
-// heads of 128 x 128 481 / 437 / 430.
+// fewer of the chain's.  64 / 32 / 16: 4001 tokens, 32 heads of 128 x 128 297 / 279 /
+// 260 us; 2048 tokens, 80 heads of 64 x 128 157 / 148 / (two on many CUs) 273;
+// gradients of 4096 tokens, 16 heads of 64 x 128 674 / 599 / 578, of 2048 tokens, 32
+// heads of 128 x 128 455 / 425 / 415.
 inline int gdr_chain_columns(int64_t B, int64_t H, int64_t P) {
   constexpr int64_t kCus = 256;
   for (int cols = 16; cols < 64; cols *= 2)

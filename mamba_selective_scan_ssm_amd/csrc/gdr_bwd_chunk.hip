@@ -30,7 +30,7 @@
 // throughout: dA and the bias' gradient are sums in fp32 of what goes through
 // all of it.
 //
-// 2 x 4096 tokens, 80 heads of 64 x 128: 1.43 ms; 0.35 for part 1, 0.39 for part 2
+// 2 x 4096 tokens, 80 heads of 64 x 128: 1.39 ms; 0.37 for part 1, 0.34 for part 2
 // (both bound by the latency of a chunk, as the forward), 0.68 for part 3, which
 // moves 2.0 GB (3 TB/s: two states of 32 KB, E and W a head and chunk, and spilled
 // registers) and computes 290 products a wave and head (matrix cores busy 22%):

@@ -27,17 +27,26 @@
 //
 // Precision: k, q and v are exact in bf16.  What is computed -- S, R, E, X, M --
 // enters a product in three bf16 parts (all 24 bits; products of two such operands
-// leave out what is below 2^-24).  Accumulation is fp32.
+// leave out what is below 2^-24).  Accumulation is fp32.  Two parts of what only y
+// depends on (S0, E and M there) took 0.56 instead of 0.60 ms at the first size
+// below, and were off by up to 2^-16 of each term: y differed from the rounded exact
+// value by 1.0e-4 of its norm, now by 1.4e-5, as by tokens.
+//
+// Values that are not finite stay behind their token: 0 times one of them, in the
+// zeros above a diagonal, would reach the tokens before it.  Rows of A', R and E that
+// are not finite are left out of the products, and y and the state set to NaN from
+// their token on.
 //
 // Bound by the latency of both roles, not by a unit: 2 x 8192 tokens, 80 heads of
-// 64 x 128 take 0.56 ms (115 TFLOP/s of the 64 GFLOP that the rule needs, 0.75 TB/s
-// of its inputs and outputs), 10.5 thousand cycles a chunk, of which the preparation
-// takes 8.3 and the chain 8.0 where the other is left out; the matrix cores are busy
-// for 3.7 thousand a SIMD, the LDS for 5.1 (1.9 of them conflicts, of transposing
+// 64 x 128 take 0.60 ms (107 TFLOP/s of the 64 GFLOP that the rule needs, 0.69 TB/s
+// of its inputs and outputs), 11.3 thousand cycles a chunk, of which the preparation
+// takes 8.3 and the chain 8.4 where the other is left out; the matrix cores are busy
+// for 4.3 thousand a SIMD, the LDS for 5.1 (1.8 of them conflicts, of transposing
 // reads and half-width writes).  160 workgroups on 256 CUs: a chunk's time is what
-// counts.  4001 tokens, 32 heads of 128 x 128, 256 workgroups of 16 columns: 0.245
+// counts.  4001 tokens, 32 heads of 128 x 128, 256 workgroups of 16 columns: 0.262
 // ms.  A preparation of its own for all chunks would write and read 0.8 GB of tiles
-// at the first of these sizes, a third of the time that it has now.
+// at the first of these sizes, a third of the time that it has now; at the second,
+// where eight workgroups prepare the same chunk, 40 MB (not tried).
 #include "device_common.h"
 #include "gdr.h"
 #include "gdr_common.h"

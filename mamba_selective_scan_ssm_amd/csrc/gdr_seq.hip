@@ -21,7 +21,8 @@
 // Bound: the prefill by the chain of one token (two sums over lanes, whose DPP
 // steps take 13 cycles each one behind the other, 7 beside others): fp32, 2048
 // tokens, 24 heads of 64 x 128 0.30 ms, 146 ns a token; with many rows by the
-// VALU: 16 x 32 heads of 128 x 128, 512 tokens 0.71 ms, 42 TFLOP/s.  The decode
+// VALU: 16 x 512 tokens, 32 heads of 128 x 128 in 16 groups, states in and out, 0.77
+// ms, 39 TFLOP/s.  The decode
 // step by the state's bytes, read and written once: 256 sequences of 80 heads of
 // 64 x 128 0.270 ms, 5.0 TB/s, what a copy reaches.
 #include "device_common.h"

@@ -23,9 +23,10 @@
 //
 // Bound by HBM where there is work: forward of 8 x 4096 tokens, 5120 channels in 8
 // groups, gate first: 0.200 ms, 5.0 TB/s, what a copy reaches; forward and backward
-// of 2 x 4096 tokens in 80 groups, gate last: 0.157 ms (54 + 103 + 7 us; the backward,
-// 16 waves a CU by its registers, 4.1 TB/s).  Small ones by their launches: 4 x 1003
-// tokens of 640 channels in 32 groups, fp32, over whole sequences 46 us in 7 kernels.
+// of 2 x 4096 tokens in 80 groups, gate last: 0.157 ms (53 + 98 + 7 us by themselves;
+// the backward, 16 waves a CU by its registers, 4.3 TB/s).  Small ones by their
+// launches: 4 x 1003 tokens of 640 channels in 32 groups, fp32, over whole sequences
+// 47 us in 7 kernels, two of which join what a workgroup of the next could join.
 #include "device_common.h"
 #include "group_norm.h"
 
