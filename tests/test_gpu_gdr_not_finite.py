@@ -108,3 +108,14 @@ def test_not_finite_inputs_backward(name, value, dtype):
             assert (h == 1).all() if n in "qk" else (h >= 2).all(), n
         clean = torch.where(lost, torch.zeros_like(want), want)
         ref.close(torch.where(lost, torch.zeros_like(got), got), clean, "d" + n, slack.get(n))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_infinite_step_wipes_the_state(dtype):
+    """A dt of infinity is a decay of 0: what came before is gone, and nothing else."""
+    _say("gdr_fwd infinite step", dtype)
+    _, s = spoiled(dtype, "dt", INF)
+    y, h = fwd(s, True)
+    ry, rh = ref.gdr_of(s, True)
+    ref.close(y, ry, "y")
+    ref.close(h, rh, "h")
