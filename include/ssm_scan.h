@@ -586,6 +586,166 @@ size_t ssm_group_norm_bwd_workspace_size_ex(int64_t S, int64_t T, int64_t D, int
                                             ssm_dtype dt, int32_t aligned);
 size_t ssm_group_norm_bwd_workspace_size(int64_t S, int64_t T, int64_t D, int64_t G);
 
+/* Largest N the linear attention kernels are built for, and the largest P of
+ * its gradients. */
+#define SSM_LINEAR_ATTN_MAX_N 256
+#define SSM_LINEAR_ATTN_BWD_MAX_P 4096
+
+/*
+ * ssm_linear_attn_fwd -- linear attention with a decay for each head, over a
+ * batch of L tokens each or over packed sequences of different lengths.
+ *
+ * Per sequence, head h and channel p, with group g = h / (H / G), the constant
+ * decay a = exp(log_decay[h]) and the state S (P, N), starting from h0 (zeros
+ * if NULL):
+ *   S_t[p,n] = a * S_{t-1}[p,n] + v[t,h,p] * k[t,g,n]
+ *   y[t,h,p] = scale * sum_n S_t[p,n] q[t,g,n]
+ *   h_final = S after the last token
+ * log_decay <= 0 as models have it; one above 0 is taken as it is, -infinity is
+ * a decay of 0 (no memory).
+ *
+ * q, k      : (B, L, G, N) dtype `dt`;  v, y : (B, L, H, P) dtype `dt`
+ * log_decay : (H) fp32
+ * h0, h_final : (S, H, P, N) fp32 or NULL, S sequences
+ * cu_seqlens NULL: S = B sequences of L tokens, n_seqs 0.  Else a DEVICE array
+ *   of n_seqs + 1 int32 that do not fall, from >= 0 to <= L, with B = 1: sequence
+ *   s has the tokens cu_seqlens[s] .. cu_seqlens[s+1] - 1 (none is allowed: its
+ *   h_final is its h0), S = n_seqs; y of tokens of no sequence is left as it was.
+ *   The host does not read it: values that break this give unspecified results,
+ *   inside the arrays.
+ * y and h_final must not overlap any input, the workspace or each other.
+ * Sums and states are fp32; bf16 inputs are exact in the matrix cores and what is
+ * computed enters a product in two or more bf16 parts, or in fp32.
+ * workspace : ssm_linear_attn_fwd_workspace_size() bytes, 16-byte aligned (0
+ *             where there are sequences and heads enough); contents on entry are
+ *             ignored.
+ * Sizes: 1 <= N <= SSM_LINEAR_ATTN_MAX_N, G divides H, H <= 65535, H P <= 2^24,
+ * B L < 2^31 - 256 (else SSM_ERR_UNSUPPORTED); any P >= 0 and L >= 0.
+ * Results are run-to-run reproducible; how sequences are cut for the GPU follows
+ * the sizes, so that the last bits may differ from one batch to another.
+ * A value that is not finite reaches its own token and later ones alone, which
+ * are then not finite (NaN or an infinity, which of them is not specified): of v
+ * in its channel, of k in its group's heads; of q its token.
+ */
+ssm_status ssm_linear_attn_fwd(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G, int64_t N,
+                               ssm_dtype dt, const void *q, const void *k, const void *v,
+                               const float *log_decay, const float *h0,
+                               const int32_t *cu_seqlens, int64_t n_seqs, float scale, void *y,
+                               float *h_final, void *workspace, size_t workspace_bytes,
+                               void *stream);
+
+/* Device workspace of ssm_linear_attn_fwd (bytes); packed == 1: with cu_seqlens. */
+size_t ssm_linear_attn_fwd_workspace_size(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G,
+                                          int64_t N, ssm_dtype dt, int32_t packed,
+                                          int64_t n_seqs);
+
+/*
+ * ssm_linear_attn_decode_steps -- T tokens of it for each of S sequences whose
+ * states are rows of a pool, in place (T = 1: one decode step).  Bitwise the
+ * results of T calls with one token each; a sequence's results do not depend on
+ * which others share the call.
+ *
+ * state_pool : (pool_rows, H, P, N) fp32, in/out
+ * slot_idx   : (S) int32 DEVICE array or NULL (slot s = s; pool_rows >= S);
+ *              slots outside [0, pool_rows) skip the sequence, whose y rows
+ *              are not written; the others must be distinct.
+ * q, k : (S, T, G, N);  v, y : (S, T, H, P)
+ * y and the pool must not overlap the inputs or each other.  Sizes as
+ * ssm_linear_attn_fwd.
+ */
+ssm_status ssm_linear_attn_decode_steps(int64_t S, int64_t T, int64_t H, int64_t P, int64_t G,
+                                        int64_t N, ssm_dtype dt, float *state_pool,
+                                        int64_t pool_rows, const int32_t *slot_idx,
+                                        const void *q, const void *k, const void *v,
+                                        const float *log_decay, float scale, void *y,
+                                        void *stream);
+
+/*
+ * ssm_linear_attn_bwd -- gradients of ssm_linear_attn_fwd for the loss gradients
+ * dy (B, L, H, P) and dh_final (S, H, P, N) fp32 (NULL = zero).  Outputs, each
+ * overwritten:
+ *   dq, dk     : (B, L, G, N) dtype `dt`, summed over the heads of a group
+ *   dv         : (B, L, H, P) dtype `dt`
+ *   dh0        : (S, H, P, N) fp32 or NULL
+ *   dlog_decay : (H) fp32 or NULL (a decay that is not learned: not formed)
+ * dq, dk and dv of tokens of no sequence are left as they were.  All sums are fp32
+ * (that of dlog_decay over tokens fp64) and in a fixed order: results are
+ * run-to-run reproducible.  Outputs must not overlap inputs, the workspace or
+ * each other.  Sizes as ssm_linear_attn_fwd, and 1 <= P <=
+ * SSM_LINEAR_ATTN_BWD_MAX_P, H >= 1.
+ * A dy that is not finite reaches its own token and earlier ones alone (dv in
+ * its channel, dk in its group, dh0, dlog_decay), and of dq its token.
+ * workspace : ssm_linear_attn_bwd_workspace_size() bytes, 16-byte aligned.
+ */
+ssm_status ssm_linear_attn_bwd(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G, int64_t N,
+                               ssm_dtype dt, const void *q, const void *k, const void *v,
+                               const float *log_decay, const float *h0,
+                               const int32_t *cu_seqlens, int64_t n_seqs, const void *dy,
+                               const float *dh_final, float scale, void *dq, void *dk, void *dv,
+                               float *dh0, float *dlog_decay, void *workspace,
+                               size_t workspace_bytes, void *stream);
+
+/* Device workspace of ssm_linear_attn_bwd (bytes); packed == 1: with cu_seqlens;
+ * decay == 1: with dlog_decay. */
+size_t ssm_linear_attn_bwd_workspace_size(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G,
+                                          int64_t N, ssm_dtype dt, int32_t packed,
+                                          int64_t n_seqs, int32_t decay);
+
+/* Most channels of a row of the norm below. */
+#define SSM_ADD_RMS_NORM_MAX_D 65536
+
+/*
+ * ssm_add_rms_norm_fwd -- the root-mean-square norm that opens a block, with the
+ * residual's addition before it and, where asked, an output in 8 bits behind it.
+ *
+ * Per row of D channels:
+ *   h = x + residual, rounded to stream_dt (residual NULL: h = x)
+ *   rstd = 1 / sqrt(average of h^2 + eps)
+ *   y[d] = h[d] * rstd * weight[d]
+ * quant == 0: y in dtype `dt`.  quant == 1 (e4m3, finite range +-448) or 2 (int8,
+ * +-127): for each group of quant_group consecutive channels (0: all D),
+ *   scale = max |y| / 448 (127), at least 2^-100;  q[d] = y[d] / scale, rounded to
+ *   nearest even;  y is q, (rows, D) bytes, which stand for q * scale.
+ * A group with a value that is not finite has a scale that is not; a row's
+ * NaN or infinity reaches its own row alone.
+ *
+ * x            : (rows, D) dtype `dt`
+ * residual, h  : (rows, D) dtype stream_dt, both or neither (then stream_dt ==
+ *                dt); h may be the residual itself, the sum taking its place.
+ *                stream_dt is fp32 where `dt` is.
+ * weight       : (D) fp32 or NULL (ones)
+ * scale        : (rows, D / quant_group) fp32, exactly with quant
+ * rstd         : (rows) fp32 or NULL (not returned)
+ * Outputs must not overlap inputs (but h the residual) or each other.  D <=
+ * SSM_ADD_RMS_NORM_MAX_D; quant_group divides D and is 8 or more, or D (else
+ * SSM_ERR_UNSUPPORTED); eps finite and >= 0.  An empty x is a no-op.  No
+ * workspace.  A row's results do not depend on the others (bitwise for one
+ * number of rows: few rows are spread over more threads).
+ */
+ssm_status ssm_add_rms_norm_fwd(int64_t rows, int64_t D, ssm_dtype dt, ssm_dtype stream_dt,
+                                const void *x, const void *residual, const float *weight,
+                                float eps, int32_t quant, int64_t quant_group, void *h, void *y,
+                                float *scale, float *rstd, void *stream);
+
+/*
+ * ssm_add_rms_norm_bwd -- gradients of ssm_add_rms_norm_fwd (quant == 0) from h
+ * (x where there was no residual) and rstd, for the output gradient dy (rows, D)
+ * dtype `dt` and the gradient dh of h itself (dtype stream_dt; NULL = zero: the
+ * stream went nowhere else).  The gradients of x and of the residual are the same
+ * numbers: dx in dtype `dt`, dresidual in dtype stream_dt, either may be NULL.
+ * dweight : (D) fp32 or NULL, sums over rows in fp32 and in a fixed order; zeros
+ * where there are no rows.  Each output is overwritten; outputs must not overlap
+ * inputs, the workspace or each other.
+ * workspace : ssm_add_rms_norm_bwd_workspace_size() bytes, 16-byte aligned (NULL
+ *             without dweight).
+ */
+ssm_status ssm_add_rms_norm_bwd(int64_t rows, int64_t D, ssm_dtype dt, ssm_dtype stream_dt,
+                                const void *h, const float *weight, const void *dy,
+                                const void *dh, const float *rstd, void *dx, void *dresidual,
+                                float *dweight, void *workspace, size_t workspace_bytes,
+                                void *stream);
+size_t ssm_add_rms_norm_bwd_workspace_size(int64_t rows, int64_t D);
+
 /* Static description of a status code. */
 const char *ssm_status_string(ssm_status s);
 

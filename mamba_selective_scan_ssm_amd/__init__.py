@@ -116,6 +116,23 @@ def lib():
         for f in (L.ssm_group_norm_fwd_workspace_size_ex, L.ssm_group_norm_bwd_workspace_size_ex):
             f.argtypes = [i64] * 4 + [ctypes.c_int, i32]
             f.restype = sz
+        L.ssm_linear_attn_fwd.argtypes = [i64] * 6 + [ctypes.c_int] + [vp] * 6 + [i64, f32, vp, vp, vp, sz, vp]
+        L.ssm_linear_attn_fwd.restype = ctypes.c_int
+        L.ssm_linear_attn_fwd_workspace_size.argtypes = [i64] * 6 + [ctypes.c_int, i32, i64]
+        L.ssm_linear_attn_fwd_workspace_size.restype = sz
+        L.ssm_linear_attn_decode_steps.argtypes = ([i64] * 6 + [ctypes.c_int, vp, i64] + [vp] * 5 + [f32, vp, vp])
+        L.ssm_linear_attn_decode_steps.restype = ctypes.c_int
+        L.ssm_linear_attn_bwd.argtypes = ([i64] * 6 + [ctypes.c_int] + [vp] * 6 + [i64, vp, vp, f32] + [vp] * 6 +
+                                          [sz, vp])
+        L.ssm_linear_attn_bwd.restype = ctypes.c_int
+        L.ssm_linear_attn_bwd_workspace_size.argtypes = [i64] * 6 + [ctypes.c_int, i32, i64, i32]
+        L.ssm_linear_attn_bwd_workspace_size.restype = sz
+        L.ssm_add_rms_norm_fwd.argtypes = [i64, i64, ctypes.c_int, ctypes.c_int] + [vp] * 3 + [f32, i32, i64] + [vp] * 5
+        L.ssm_add_rms_norm_fwd.restype = ctypes.c_int
+        L.ssm_add_rms_norm_bwd.argtypes = [i64, i64, ctypes.c_int, ctypes.c_int] + [vp] * 9 + [sz, vp]
+        L.ssm_add_rms_norm_bwd.restype = ctypes.c_int
+        L.ssm_add_rms_norm_bwd_workspace_size.argtypes = [i64, i64]
+        L.ssm_add_rms_norm_bwd_workspace_size.restype = sz
         L.ssm_status_string.argtypes = [ctypes.c_int]
         L.ssm_status_string.restype = ctypes.c_char_p
         L.ssm_version.argtypes = []
@@ -688,3 +705,198 @@ def group_norm_bwd(x, groups, dy, mean, rstd, weight=None, bias=None, z=None, *,
               _ptr(mean) if center else None, _ptr(rstd), float(eps), int(bool(center)), act, first, _ptr(out["dx"]),
               _ptr(out["dz"]), _ptr(out["dweight"]), _ptr(out["dbias"]), _ptr(workspace), ws_len)
     return out
+
+
+def _attn_inputs(q, k, v, log_decay, cu_seqlens):
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q must be (B, L, G, N) and v (B, L, H, P)")
+    B, L, G, N = q.shape
+    H, P = v.shape[2], v.shape[3]
+    dev, typ = q.device, q.dtype
+    code = _dtype_code(q)
+    _check("q", q, (B, L, G, N), typ, dev)
+    _check("k", k, (B, L, G, N), typ, dev)
+    _check("v", v, (B, L, H, P), typ, dev)
+    _check("log_decay", log_decay, (H,), torch.float32, dev)
+    n_seqs = 0
+    if cu_seqlens is not None:
+        if B != 1:
+            raise ValueError(f"packed sequences (cu_seqlens) lie one behind the other in one row: B is {B}, not 1")
+        if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+            raise ValueError("cu_seqlens must be (sequences + 1,)")
+        _check("cu_seqlens", cu_seqlens, cu_seqlens.shape, torch.int32, dev)
+        n_seqs = cu_seqlens.shape[0] - 1
+    return (B, L, H, P, G, N), code, typ, dev, n_seqs
+
+
+def linear_attn_fwd(q, k, v, log_decay, h0=None, *, scale=None, cu_seqlens=None, y=None, h_final=None,
+                    return_final=True, workspace=None):
+    """Linear attention with a decay for each head (ssm_linear_attn_fwd).
+
+    q, k: (B, L, G, N); v: (B, L, H, P), all float32 or all bfloat16;
+    log_decay: (H,) float32, the decay being exp(log_decay); h0: (S, H, P, N)
+    float32, S sequences.  S is B; or, with cu_seqlens, an int32 device tensor
+    (S + 1,) that does not fall and stays within 0 .. L (it is not read on the
+    host), B is 1 and sequence s has the tokens cu_seqlens[s] ..
+    cu_seqlens[s + 1] - 1; y of tokens of no sequence is left as it was (not
+    initialised where y is made here).  scale: of the output, N ** -0.5 by
+    default.  Returns (y, h_final)."""
+    sizes, code, typ, dev, n_seqs = _attn_inputs(q, k, v, log_decay, cu_seqlens)
+    B, L, H, P, G, N = sizes
+    packed = cu_seqlens is not None
+    states = (n_seqs if packed else B, H, P, N)
+    _check("h0", h0, states, torch.float32, dev)
+    if y is None:
+        y = torch.empty((B, L, H, P), dtype=typ, device=dev)
+    _check("y", y, (B, L, H, P), typ, dev)
+    if h_final is None and return_final:
+        h_final = torch.empty(states, dtype=torch.float32, device=dev)
+    _check("h_final", h_final, states, torch.float32, dev)
+    need = int(lib().ssm_linear_attn_fwd_workspace_size(*sizes, code, int(packed), n_seqs))
+    workspace, ws_len = _workspace(workspace, need, dev)
+    _gpu_call(dev, "ssm_linear_attn_fwd", *sizes, code, _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(h0),
+              _ptr(cu_seqlens), n_seqs, _scale(scale, N), _ptr(y), _ptr(h_final), _ptr(workspace), ws_len)
+    return y, h_final
+
+
+def linear_attn_fwd_workspace_size(B, L, H, P, G, N, dtype=torch.bfloat16, n_seqs=None) -> int:
+    """n_seqs: of packed sequences; None: a batch."""
+    return int(lib().ssm_linear_attn_fwd_workspace_size(B, L, H, P, G, N, _code_of(dtype), int(n_seqs is not None),
+                                                        n_seqs or 0))
+
+
+def linear_attn_bwd_workspace_size(B, L, H, P, G, N, dtype=torch.bfloat16, n_seqs=None, want_ddecay=False) -> int:
+    return int(lib().ssm_linear_attn_bwd_workspace_size(B, L, H, P, G, N, _code_of(dtype), int(n_seqs is not None),
+                                                        n_seqs or 0, int(bool(want_ddecay))))
+
+
+def linear_attn_decode_steps(state_pool, q, k, v, log_decay, *, slots=None, scale=None, y=None):
+    """T tokens of linear attention for S sequences whose states are rows of a
+    pool (ssm_linear_attn_decode_steps).  state_pool (rows, H, P, N) float32 is
+    updated in place; q, k: (S, T, G, N); v: (S, T, H, P); slots: (S,) int32
+    device tensor of pool rows (None: row s for sequence s; outside the pool:
+    skip, y's rows are left as they were).  Returns y."""
+    sizes, code, typ, dev, _ = _attn_inputs(q, k, v, log_decay, None)
+    S, T, H, P, G, N = sizes
+    if state_pool.dim() != 4:
+        raise ValueError("state_pool must be (rows, H, P, N)")
+    rows = state_pool.shape[0]
+    _check("state_pool", state_pool, (rows, H, P, N), torch.float32, dev)
+    _check("slots", slots, (S,), torch.int32, dev)
+    if y is None:
+        y = torch.empty((S, T, H, P), dtype=typ, device=dev)
+    _check("y", y, (S, T, H, P), typ, dev)
+    _gpu_call(dev, "ssm_linear_attn_decode_steps", *sizes, code, _ptr(state_pool), rows, _ptr(slots), _ptr(q), _ptr(k),
+              _ptr(v), _ptr(log_decay), _scale(scale, N), _ptr(y))
+    return y
+
+
+def linear_attn_bwd(q, k, v, log_decay, h0=None, dy=None, dh_final=None, *, scale=None, cu_seqlens=None, want_dh0=True,
+                    want_ddecay=False, workspace=None):
+    """Gradients of linear_attn_fwd (ssm_linear_attn_bwd) for the output gradient
+    dy and the final-state gradient dh_final (None = zero).  Returns a dict: dq,
+    dk, dv (input dtype; zero for tokens of no sequence), dh0 (float32; None
+    unless want_dh0), dlog_decay (float32; None unless want_ddecay)."""
+    sizes, code, typ, dev, n_seqs = _attn_inputs(q, k, v, log_decay, cu_seqlens)
+    B, L, H, P, G, N = sizes
+    if dy is None:
+        raise ValueError("dy is required")
+    packed = cu_seqlens is not None
+    states = (n_seqs if packed else B, H, P, N)
+    _check("dy", dy, (B, L, H, P), typ, dev)
+    _check("h0", h0, states, torch.float32, dev)
+    _check("dh_final", dh_final, states, torch.float32, dev)
+    new = torch.zeros_like if packed else torch.empty_like  # tokens of no sequence have no gradient
+    out = {"dq": new(q), "dk": new(k), "dv": new(v),
+           "dh0": torch.empty(states, dtype=torch.float32, device=dev) if want_dh0 else None,
+           "dlog_decay": torch.empty((H,), dtype=torch.float32, device=dev) if want_ddecay else None}
+    need = int(lib().ssm_linear_attn_bwd_workspace_size(*sizes, code, int(packed), n_seqs, int(bool(want_ddecay))))
+    workspace, ws_len = _workspace(workspace, need, dev)
+    _gpu_call(dev, "ssm_linear_attn_bwd", *sizes, code, _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(h0),
+              _ptr(cu_seqlens), n_seqs, _ptr(dy), _ptr(dh_final), _scale(scale, N), _ptr(out["dq"]), _ptr(out["dk"]),
+              _ptr(out["dv"]), _ptr(out["dh0"]), _ptr(out["dlog_decay"]), _ptr(workspace), ws_len)
+    return out
+
+
+_QUANT = {None: (0, None), "e4m3": (1, torch.float8_e4m3fn), "int8": (2, torch.int8)}
+
+
+def add_rms_norm_fwd(x, residual=None, weight=None, *, eps=1e-5, quant=None, quant_group=0, y=None, h=None, scale=None,
+                     return_rstd=True):
+    """Root-mean-square norm of x + residual over the last axis, with an output
+    in 8 bits where asked (ssm_add_rms_norm_fwd).
+
+    x: (..., D) float32 or bfloat16; residual: the same shape, of x's type or
+    float32: the stream, whose type the sum h is rounded to; weight: (D,)
+    float32.  quant: None (y in x's type), "e4m3" (torch.float8_e4m3fn) or "int8",
+    with a float32 scale for each quant_group channels (0: for each row), (...,
+    D // quant_group): y stands for y * scale.  h may be given as the residual
+    itself: the sum takes its place.  Returns (y, scale, h, rstd): scale None
+    without quant, h is x itself without a residual, rstd (...,) float32 None
+    unless return_rstd."""
+    if x.dim() < 1:
+        raise ValueError("x must be (..., D)")
+    if quant not in _QUANT:
+        raise ValueError(f"quant must be None, 'e4m3' or 'int8', got {quant!r}")
+    shape, dev, typ = x.shape, x.device, x.dtype
+    code = _dtype_code(x)
+    lead, D = shape[:-1], shape[-1]
+    rows = lead.numel()
+    _check("x", x, shape, typ, dev)
+    _check("weight", weight, (D,), torch.float32, dev)
+    stream = typ if residual is None else residual.dtype
+    stream_code = code if residual is None else _dtype_code(residual)
+    _check("residual", residual, shape, stream, dev)
+    if residual is None:
+        if h is not None:
+            raise ValueError("h is given without a residual: it would be x")
+    elif h is None:
+        h = torch.empty_like(residual)
+    _check("h", h, shape, stream, dev)
+    mode, kind = _QUANT[quant]
+    quant_group = int(quant_group)
+    if quant is None and (quant_group != 0 or scale is not None):
+        raise ValueError("quant_group and scale belong to an output in 8 bits (quant)")
+    if y is None:
+        y = torch.empty(shape, dtype=kind or typ, device=dev)
+    _check("y", y, shape, kind or typ, dev)
+    if mode:
+        if quant_group < 0 or (quant_group > 0 and D % quant_group != 0):
+            raise ValueError(f"quant_group {quant_group} does not divide the {D} channels")
+        groups = (*lead, D // quant_group if quant_group else 1)
+        if scale is None:
+            scale = torch.empty(groups, dtype=torch.float32, device=dev)
+        _check("scale", scale, groups, torch.float32, dev)
+    rstd = torch.empty(lead, dtype=torch.float32, device=dev) if return_rstd else None
+    _gpu_call(dev, "ssm_add_rms_norm_fwd", rows, D, code, stream_code, _ptr(x), _ptr(residual), _ptr(weight),
+              float(eps), mode, quant_group, _ptr(h), _ptr(y), _ptr(scale), _ptr(rstd))
+    return y, scale, x if residual is None else h, rstd
+
+
+def add_rms_norm_bwd(h, dy, rstd, weight=None, *, dh=None, workspace=None):
+    """Gradients of add_rms_norm_fwd (ssm_add_rms_norm_bwd) from the h and rstd
+    that it returned, for the output gradient dy (in x's type) and the gradient
+    dh of h itself (None = zero).  Returns a dict: dx (dy's type), dresidual
+    (h's type; dx itself where the types are the same), dweight (None without
+    weight)."""
+    if h.dim() < 1:
+        raise ValueError("h must be (..., D)")
+    shape, dev = h.shape, h.device
+    lead, D = shape[:-1], shape[-1]
+    rows = lead.numel()
+    code, stream_code = _dtype_code(dy), _dtype_code(h)
+    _check("h", h, shape, h.dtype, dev)
+    _check("dy", dy, shape, dy.dtype, dev)
+    _check("dh", dh, shape, h.dtype, dev)
+    _check("rstd", rstd, lead, torch.float32, dev)
+    _check("weight", weight, (D,), torch.float32, dev)
+    if rstd is None:
+        raise ValueError("rstd is required")
+    dx = torch.empty_like(dy)
+    dres = None if h.dtype == dy.dtype else torch.empty_like(h)
+    dw = None if weight is None else torch.empty_like(weight)
+    need = int(lib().ssm_add_rms_norm_bwd_workspace_size(rows, D)) if dw is not None else 0
+    workspace, ws_len = _workspace(workspace, need, dev)
+    _gpu_call(dev, "ssm_add_rms_norm_bwd", rows, D, code, stream_code, _ptr(h), _ptr(weight), _ptr(dy), _ptr(dh),
+              _ptr(rstd), _ptr(dx), _ptr(dres), _ptr(dw), _ptr(workspace), ws_len)
+    return {"dx": dx, "dresidual": dx if dres is None else dres, "dweight": dw}

@@ -35,6 +35,14 @@ inline bool overlaps_any(Range out, const Range (&ins)[K]) {
   return false;
 }
 
+// Whether two of the outputs share memory.
+inline bool any_pair(const Range *r, size_t n) {
+  for (size_t i = 0; i < n; ++i)
+    for (size_t j = i + 1; j < n; ++j)
+      if (overlap(r[i], r[j])) return true;
+  return false;
+}
+
 inline bool dopts_ok(const ssm_delta_opts *o) {
   if (!o) return true;
   for (int i = 0; i < 3; ++i)

@@ -50,14 +50,6 @@ ssm::GdrArgs gdr_args(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G, int
 
 bool aligned16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
-// Whether two of the outputs share memory.
-bool any_pair(const Range *r, size_t n) {
-  for (size_t i = 0; i < n; ++i)
-    for (size_t j = i + 1; j < n; ++j)
-      if (overlap(r[i], r[j])) return true;
-  return false;
-}
-
 }  // namespace
 
 extern "C" {

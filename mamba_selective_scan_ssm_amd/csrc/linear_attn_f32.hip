@@ -1,0 +1,356 @@
+// Linear attention by chunks of C tokens on the fp32 matrix instructions: any
+// type, size and alignment.
+//
+// Within a chunk of `left` tokens entered by the state S (n down, m across), with
+// the powers a^d of the head's decay, f = 1 and (where the pass runs backwards) 0:
+//   out_i = c_out (a^(i+f) S^T x_i + c_in sum_{j<=i} a^(i-j) (x_i . key_j) val_j)
+//   S    <- a^left S + c_in sum_j a^(left-1-j+(1-f)) key_j val_j^T
+// and the tangent T = dS / d log a, for the gradient of the decay (f = 1, c_in = 1):
+//   out'_i = c_out (a^(i+1) ((i+1) S + T)^T x_i + sum_{j<=i} (i-j) a^(i-j) (x_i . key_j) val_j)
+//   T     <- a^left (T + left S) + sum_j (left-1-j) a^(left-1-j) key_j val_j^T
+// All powers are of distances >= 0: nothing is divided by a decay, whatever it is.
+//
+// A workgroup of four waves runs 64 columns m of one head's chain over a segment;
+// 16 columns a wave, whose part of S stays in its registers.  A result tile of
+// v_mfma_f32_16x16x4_f32 is the B operand of the next product as it is (mma_f32),
+// so S goes into S^T x without leaving them.  The scores x . key are shared: each
+// wave forms tiles of 16 x 16 and leaves them in LDS.
+//
+// Values that are not finite stay behind their token: scores above the diagonal are
+// selected away, and a value's column is left out of the products and set to NaN
+// from its token on (0 times one of them would reach the tokens before it).
+#include "device_common.h"
+#include "linear_attn.h"
+#include "linear_attn_common.h"
+
+namespace ssm {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kColumns = 64;
+
+// f32x4 from a row of storage elements; elements from `left` on are 0
+template <typename T, bool VEC>
+__device__ __forceinline__ f32x4 load_four(const T *p, int left) {
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+  if constexpr (VEC) {
+    if (left >= 4) {
+      struct alignas(4 * sizeof(T)) Raw {
+        T v[4];
+      };
+      const Raw r = *reinterpret_cast<const Raw *>(p);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = to_f32(r.v[e]);
+      return v;
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (e < left) v[e] = to_f32(p[e]);
+  return v;
+}
+
+// KT: tiles of 16 that K is rounded up to.  Y: outputs (or the tangent's sum); else
+// the segment's own addition to the state.
+template <typename T, int KT, int C, bool Y, bool TAN, bool VEC>
+__global__ __launch_bounds__(kThreads) void la_f32_kernel(LaArgs a, LaPasses all, int64_t items, int64_t sub,
+                                                              int64_t base) {
+  constexpr int kPitch = 16 * KT + 4, kVal = kColumns + 4, kScore = C + 4;
+  constexpr int CT = C / 16, kPairs = CT * (CT + 1) / 2;
+  __shared__ __attribute__((aligned(16))) float s_x[Y ? C : 1][kPitch];
+  __shared__ __attribute__((aligned(16))) float s_k[C][kPitch];
+  __shared__ __attribute__((aligned(16))) float s_v[C][kVal];
+  __shared__ __attribute__((aligned(16))) float s_a[Y ? C : 1][kScore];
+  __shared__ float s_pw[C + 1];
+  __shared__ double s_sum[kThreads / 64];
+
+  const LaPass &p = all.p[blockIdx.y];
+  const int tid = threadIdx.x, wave = tid / 64, lane = tid % 64, r = lane % 16, g = lane / 16;
+  int64_t unit, in;
+  la_place(blockIdx.x, sub, unit, in);
+  const int64_t item = base + unit * sub + in;
+  if (item >= items) return;
+  const int64_t cols = (p.M + kColumns - 1) / kColumns;
+  const int64_t h = item / cols % a.H, slot = item / (cols * a.H);
+  const int m0 = static_cast<int>(item % cols) * kColumns, m = m0 + 16 * wave + r;
+  const bool col = m < p.M;
+  const LaSlot z = la_slot(a, slot, p.reverse);
+  if constexpr (TAN && Y) {  // every partial sum is written
+    if (z.len < 0 && tid == 0) p.dot_sum[item] = 0.0;
+  }
+  if (z.len < 0 || (!Y && z.last)) return;  // nothing follows the last segment
+  const double log_a = a.log_decay[h];
+  for (int d = tid; d <= C; d += kThreads) s_pw[d] = la_power(log_a, d);
+  const int f = p.reverse ? 0 : 1;
+  const float c_in = p.c_in, c_out = p.c_out;
+
+  // ---- the state that enters the segment
+  f32x4 S[KT], U[TAN ? KT : 1];
+  const int64_t at = (z.seq * a.H + h) * a.state + static_cast<int64_t>(m) * p.sm;
+#pragma unroll
+  for (int j = 0; j < KT; ++j) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int n = 16 * j + 4 * g + e;
+      S[j][e] = Y && p.s0 != nullptr && col && n < p.K ? p.s0[at + n * p.sn] : 0.f;
+      if constexpr (TAN) U[j][e] = 0.f;
+    }
+  }
+  const int64_t Kp = (p.K + 15) / 16 * 16;
+  if constexpr (Y) {
+    const LaCarry whole(log_a, a.seg_len);
+    const float n_whole = static_cast<float>(a.seg_len) * la_power(log_a, a.seg_len);
+    for (int64_t b = 0; b < z.before; ++b) {
+      const int64_t from = (((z.slot0 + b) * a.H + h) * p.M + m) * Kp;
+#pragma unroll
+      for (int j = 0; j < KT; ++j) {
+        const bool there = col && 16 * j < Kp;
+        const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+        const f32x4 own = there ? *reinterpret_cast<const f32x4 *>(p.local + from + 16 * j + 4 * g) : zero;
+        if constexpr (TAN) {
+          const f32x4 tan = there ? *reinterpret_cast<const f32x4 *>(p.local_tan + from + 16 * j + 4 * g) : zero;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) U[j][e] = whole(U[j][e]) + fmaf(n_whole, S[j][e], tan[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) S[j][e] = whole(S[j][e]) + own[e];
+      }
+    }
+  }
+
+  const T *x = static_cast<const T *>(p.x) + h / p.x_per * p.x_width;
+  const T *key = static_cast<const T *>(p.key) + h / p.key_per * p.key_width;
+  const T *val = static_cast<const T *>(p.val) + h / p.val_per * p.val_width;
+  const T *dot = TAN ? static_cast<const T *>(p.dot) + h / p.val_per * p.val_width : nullptr;
+  double sum = 0.0;
+
+  const LaCarry full(log_a, C);
+  for (int t0 = 0; t0 < z.len; t0 += C) {
+    const int left = z.len - t0 < C ? z.len - t0 : C;
+    __syncthreads();
+    // ---- x, keys and values into LDS; zeros behind the last token and width
+    auto row_of = [&](int i) { return z.first + static_cast<int64_t>(t0 + i) * z.step; };
+    for (int i = tid; i < C * 4 * KT; i += kThreads) {
+      const int t = i / (4 * KT), n = i % (4 * KT) * 4;
+      const int have = t < left ? p.K - n : 0;
+      const int64_t row = have > 0 ? row_of(t) : 0;
+      if constexpr (Y)
+        *reinterpret_cast<f32x4 *>(&s_x[t][n]) = load_four<T, VEC>(x + row * p.x_row + n, have);
+      *reinterpret_cast<f32x4 *>(&s_k[t][n]) = load_four<T, VEC>(key + row * p.key_row + n, have);
+    }
+    for (int i = tid; i < C * kColumns / 4; i += kThreads) {
+      const int t = i / (kColumns / 4), n = i % (kColumns / 4) * 4;
+      const int have = t < left ? p.M - m0 - n : 0;
+      const int64_t row = have > 0 ? row_of(t) : 0;
+      *reinterpret_cast<f32x4 *>(&s_v[t][n]) = load_four<T, VEC>(val + row * p.val_row + m0 + n, have);
+    }
+    __syncthreads();
+
+    // ---- scores, from the diagonal down, tile by tile
+    if constexpr (Y) {
+      for (int pair = wave; pair < kPairs; pair += kThreads / 64) {
+        int bt = 0;
+        while ((bt + 1) * (bt + 2) / 2 <= pair) ++bt;
+        const int bs = pair - bt * (bt + 1) / 2;
+        f32x4 w = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < KT; ++j)
+          w = mma_f32(*reinterpret_cast<const f32x4 *>(&s_k[16 * bs + r][16 * j + 4 * g]),
+                      *reinterpret_cast<const f32x4 *>(&s_x[16 * bt + r][16 * j + 4 * g]), w);
+        // token 16 bt + r, keys 16 bs + 4 g + e
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int d = 16 * (bt - bs) + r - 4 * g - e;
+          const float pw = c_in * s_pw[d < 0 ? 0 : d];
+          w[e] = d < 0 ? 0.f : w[e] * (TAN ? pw * static_cast<float>(d) : pw);
+        }
+        *reinterpret_cast<f32x4 *>(&s_a[16 * bt + r][16 * bs + 4 * g]) = w;
+      }
+    }
+    // ---- this lane's values, tokens 16 j + 4 g + e
+    f32x4 v[CT];
+    int bad = C;
+#pragma unroll
+    for (int j = 0; j < CT; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[j][e] = s_v[16 * j + 4 * g + e][16 * wave + r];
+#pragma unroll
+    for (int j = CT - 1; j >= 0; --j)
+#pragma unroll
+      for (int e = 3; e >= 0; --e)
+        if (!(fabsf(v[j][e]) < __builtin_huge_valf())) {
+          bad = 16 * j + 4 * g + e;
+          v[j][e] = 0.f;
+        }
+    if (__ballot(bad < C) != 0) {
+      bad = min(bad, __shfl_xor(bad, 16));
+      bad = min(bad, __shfl_xor(bad, 32));
+    }
+    f32x4 y[CT];
+    if constexpr (Y) {
+      // ---- what the state answers
+#pragma unroll
+      for (int i = 0; i < CT; ++i) {
+        f32x4 w = {0.f, 0.f, 0.f, 0.f}, u = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < KT; ++j) {
+          const f32x4 q = *reinterpret_cast<const f32x4 *>(&s_x[16 * i + r][16 * j + 4 * g]);
+          w = mma_f32(q, S[j], w);
+          if constexpr (TAN) u = mma_f32(q, U[j], u);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int t = 16 * i + 4 * g + e;
+          if constexpr (TAN) w[e] = fmaf(static_cast<float>(t + 1), w[e], u[e]);
+          w[e] *= s_pw[t + f];
+        }
+        y[i] = w;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < CT; ++i)
+#pragma unroll
+        for (int j = 0; j <= i; ++j)
+          y[i] = mma_f32(*reinterpret_cast<const f32x4 *>(&s_a[16 * i + r][16 * j + 4 * g]), v[j], y[i]);
+      // ---- out
+#pragma unroll
+      for (int i = 0; i < CT; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int t = 16 * i + 4 * g + e;
+          const float out = t >= bad ? __builtin_nanf("") : c_out * y[i][e];
+          if (t < left && col) {
+            if constexpr (TAN) {
+              sum += static_cast<double>(out) * to_f32(dot[row_of(t) * p.val_row + m]);
+            } else {
+              const int64_t o = row_of(t) * p.out_row + h * p.out_width + m;
+              if (p.out_f32) static_cast<float *>(p.out)[o] = out;
+              else static_cast<T *>(p.out)[o] = from_f32<T>(out);
+            }
+          }
+        }
+    }
+    // ---- the state that leaves the chunk
+    const LaCarry carry = left == C ? full : LaCarry(log_a, left);
+    const float n_left = static_cast<float>(left) * s_pw[left];
+    f32x4 u[TAN ? CT : 1];
+#pragma unroll
+    for (int j = 0; j < CT; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int d = left - 1 - (16 * j + 4 * g + e);
+        const float w = d < 0 ? 0.f : v[j][e] * (c_in * s_pw[d + 1 - f]);
+        if constexpr (TAN) u[j][e] = d < 0 ? 0.f : w * static_cast<float>(d);
+        v[j][e] = w;
+      }
+#pragma unroll
+    for (int i = 0; i < KT; ++i) {
+      if constexpr (TAN) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) U[i][e] = fmaf(n_left, S[i][e], carry(U[i][e]));
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) S[i][e] = carry(S[i][e]);
+#pragma unroll
+      for (int j = 0; j < CT; ++j) {
+        f32x4 k;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) k[e] = s_k[16 * j + 4 * g + e][16 * i + r];
+        S[i] = mma_f32(k, v[j], S[i]);
+        if constexpr (TAN) U[i] = mma_f32(k, u[j], U[i]);
+      }
+      if (bad < C) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          S[i][e] = __builtin_nanf("");
+          if constexpr (TAN) U[i][e] = __builtin_nanf("");
+        }
+      }
+    }
+  }
+
+  // ---- the state behind the segment
+  if constexpr (!Y) {
+    if (col) {
+      const int64_t to = ((slot * a.H + h) * p.M + m) * Kp;
+#pragma unroll
+      for (int j = 0; j < KT; ++j)
+        if (16 * j < Kp) {
+          *reinterpret_cast<f32x4 *>(p.local + to + 16 * j + 4 * g) = S[j];
+          if constexpr (TAN) *reinterpret_cast<f32x4 *>(p.local_tan + to + 16 * j + 4 * g) = U[j];
+        }
+    }
+  } else {
+    if (z.last && p.s_last != nullptr && col) {
+#pragma unroll
+      for (int j = 0; j < KT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int n = 16 * j + 4 * g + e;
+          if (n < p.K) p.s_last[at + n * p.sn] = S[j][e];
+        }
+    }
+    if constexpr (TAN) {
+      if (z.last && p.s_dot != nullptr && col) {
+#pragma unroll
+        for (int j = 0; j < KT; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int n = 16 * j + 4 * g + e;
+            if (n < p.K) sum += static_cast<double>(U[j][e]) * p.s_dot[at + n * p.sn];
+          }
+      }
+#pragma unroll
+      for (int d = 1; d < 64; d *= 2) sum += __shfl_xor(sum, d);
+      if (lane == 0) s_sum[wave] = sum;
+      __syncthreads();
+      if (tid == 0) p.dot_sum[item] = (s_sum[0] + s_sum[1]) + (s_sum[2] + s_sum[3]);
+    }
+  }
+}
+
+template <typename T, int KT, int C, bool TAN, bool VEC>
+hipError_t launch_kt(const LaArgs &a, const LaPasses &all, int n, int64_t cols, int64_t sub, hipStream_t s) {
+  return la_launches(a, cols, sub, n, [&](dim3 grid, bool y, int64_t items, int64_t base) {
+    if (y) la_f32_kernel<T, KT, C, true, TAN, VEC><<<grid, kThreads, 0, s>>>(a, all, items, sub, base);
+    else la_f32_kernel<T, KT, C, false, TAN, VEC><<<grid, kThreads, 0, s>>>(a, all, items, sub, base);
+  });
+}
+
+template <typename T>
+bool fours(const LaPass &p) {
+  for (const void *q : {p.x, p.key, p.val})
+    if (reinterpret_cast<uintptr_t>(q) % (4 * sizeof(T)) != 0) return false;
+  for (int64_t n : {p.x_row, p.key_row, p.val_row, p.x_width, p.key_width, p.val_width})
+    if (n % 4 != 0) return false;
+  return true;
+}
+
+template <typename T, bool TAN>
+hipError_t launch_type(const LaArgs &a, const LaPass *p, int n, hipStream_t s) {
+  LaPasses all{};
+  bool vec = true;
+  for (int i = 0; i < n; ++i) {
+    all.p[i] = p[i];
+    vec = vec && fours<T>(p[i]);
+  }
+  const int64_t cols = la_columns(p[0].M);
+  const int64_t sub = la_sub(a, p[0].x_per, cols);
+#define SSM_LA_KT(KT, C)                                                        \
+  return vec ? launch_kt<T, KT, C, TAN, true>(a, all, n, cols, sub, s)          \
+             : launch_kt<T, KT, C, TAN, false>(a, all, n, cols, sub, s)
+  if (p[0].K <= 64) SSM_LA_KT(4, 64);
+  if (p[0].K <= 128) SSM_LA_KT(8, 64);
+  SSM_LA_KT(16, 32);
+#undef SSM_LA_KT
+}
+
+}  // namespace
+
+hipError_t launch_la_f32(const LaArgs &a, const LaPass *p, int n, hipStream_t s) {
+  const bool tan = p[0].dot_sum != nullptr;  // dot may be empty
+  if (a.dt_type == DType::BF16) return tan ? launch_type<bf16_t, true>(a, p, n, s) : launch_type<bf16_t, false>(a, p, n, s);
+  return tan ? launch_type<float, true>(a, p, n, s) : launch_type<float, false>(a, p, n, s);
+}
+
+}  // namespace ssm
