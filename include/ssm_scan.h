@@ -672,7 +672,7 @@ ssm_status ssm_linear_attn_decode_steps(int64_t S, int64_t T, int64_t H, int64_t
  * (that of dlog_decay over tokens fp64) and in a fixed order: results are
  * run-to-run reproducible.  Outputs must not overlap inputs, the workspace or
  * each other.  Sizes as ssm_linear_attn_fwd, and 1 <= P <=
- * SSM_LINEAR_ATTN_BWD_MAX_P, H >= 1.
+ * SSM_LINEAR_ATTN_BWD_MAX_P, H >= 1, H N <= 2^22.
  * A dy that is not finite reaches its own token and earlier ones alone (dv in
  * its channel, dk in its group, dh0, dlog_decay), and of dq its token.
  * workspace : ssm_linear_attn_bwd_workspace_size() bytes, 16-byte aligned.

@@ -199,7 +199,8 @@ ssm_status ssm_linear_attn_bwd(int64_t B, int64_t L, int64_t H, int64_t P, int64
   const bool packed = cu_seqlens != nullptr;
   const ssm_status st = attn_sizes(B, L, H, P, G, N, dt, packed, n_seqs, &z);
   if (st != SSM_OK) return st;
-  if (P < 1 || H < 1 || P > SSM_LINEAR_ATTN_BWD_MAX_P) return SSM_ERR_UNSUPPORTED;
+  // the fp32 rows of a chunk of 64 tokens within 32-bit offsets
+  if (P < 1 || H < 1 || P > SSM_LINEAR_ATTN_BWD_MAX_P || H * N > int64_t{1} << 22) return SSM_ERR_UNSUPPORTED;
   if (!log_decay || (B * L > 0 && (!q || !k || !v || !dy || !dq || !dk || !dv))) return SSM_ERR_INVALID_ARG;
   const int64_t es = esize(dt);
   const AttnBwdSpace w =

@@ -63,6 +63,8 @@ inline bool la_cut(const LaArgs &a) { return a.slots > a.S; }
 // By chunks, in fp32 matrix instructions (linear_attn_f32.hip): any type, size
 // and alignment, K <= 256.  Passes of one number of columns run side by side.
 hipError_t launch_la_f32(const LaArgs &a, const LaPass *p, int n, hipStream_t s);
+// By chunks, bf16 inputs, on the bf16 matrix cores (linear_attn_bf16.hip).
+hipError_t launch_la_bf16(const LaArgs &a, const LaPass *p, int n, hipStream_t s);
 // The kernel that the type and the sizes choose.
 hipError_t launch_la(const LaArgs &a, const LaPass *p, int n, hipStream_t s);
 

@@ -163,7 +163,9 @@ void la_plan(LaArgs &a, int64_t columns) {
   a.slots = a.L < 0 ? a.T / len + a.S : a.S * ((a.L + len - 1) / len);
 }
 
-hipError_t launch_la(const LaArgs &a, const LaPass *p, int n, hipStream_t s) { return launch_la_f32(a, p, n, s); }
+hipError_t launch_la(const LaArgs &a, const LaPass *p, int n, hipStream_t s) {
+  return a.dt_type == DType::BF16 ? launch_la_bf16(a, p, n, s) : launch_la_f32(a, p, n, s);
+}
 
 hipError_t launch_la_step(const LaStepArgs &a, hipStream_t s) {
   return a.dt_type == DType::BF16 ? launch_step<bf16_t>(a, s) : launch_step<float>(a, s);

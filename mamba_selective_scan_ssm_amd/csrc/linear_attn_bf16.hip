@@ -1,0 +1,719 @@
+// Linear attention by chunks of 64 tokens on the bf16 matrix cores.
+//
+// The formulas are those of linear_attn_f32.hip.  A workgroup of four waves runs 64
+// (CB = 1) or 128 (CB = 2) columns m of one head's chain over a segment, 16 CB
+// columns a wave, whose part of the state S (n down, m across) stays in its
+// registers.  x, keys and values of a chunk lie in LDS, double-buffered behind one
+// barrier a chunk, and are loaded two chunks ahead.
+//
+// v_mfma_f32_16x16x32_bf16 on lane 16 g + r takes A[r][k], B[k][r] for the 8
+// contraction indices k of slot g and gives C[4 g + e][r]; which index a slot stands
+// for is free as long as both operands agree, so
+//  - n: slot (g, 4 u + e) of block kb is n = 32 kb + 8 g + 4 u + e, 16 bytes of a row
+//    as it lies in memory; rows 4 g + e of the state's tile 2 kb + u are these n (the
+//    transposing reads of the keys choose them so), and S is an operand as it is;
+//  - tokens: slot (g, 4 u + e) of block tb is token 32 tb + 16 u + 4 g + e, so two
+//    score tiles key . x, one above the other, are the operand of the values'
+//    product as they are: each wave forms all scores for itself, nothing is exchanged.
+// Outputs come out as C[m][token]: a lane's four channels are one store.
+//
+// Precision: inputs are exact in bf16.  What is computed enters a product in bf16
+// parts: the weighted values, from which the state is made, in three (all 24 bits),
+// the scores and S, from which the outputs are made, in two (off by 2^-17 of each
+// term; the output is rounded to 2^-9 or summed over heads in fp32).  Sums are fp32.
+#include "device_common.h"
+#include "linear_attn.h"
+#include "linear_attn_common.h"
+
+namespace ssm {
+namespace {
+
+// Element offset of 16-byte piece c of row t.  The LDS has 64 banks; which exchange of
+// a row's pieces meets fewest of them twice was measured for each kind of read, in
+// cycles a wave: x, sixteen rows' one piece, 5.8 (rows without an exchange 33); keys,
+// read transposing, four rows' four pieces and half of each, 5.6 (9.4 with x's); values,
+// four rows by two whole pieces, 4.0.  Rows of 128 bytes: by t % 8 for all of them.
+template <int PIECES>
+__device__ __forceinline__ constexpr int x_at(int t, int c) {
+  return t * PIECES * 8 + 8 * (c ^ t % (PIECES < 16 ? PIECES : 16));
+}
+template <int PIECES>
+__device__ __forceinline__ constexpr int key_at(int t, int c) {
+  return t * PIECES * 8 + 8 * (c ^ (PIECES < 16 ? t % PIECES : 4 * (t % 4) + t / 4 % 4));
+}
+template <int PIECES>
+__device__ __forceinline__ constexpr int value_at(int t, int c) {
+  return t * PIECES * 8 +
+         8 * (c ^ (PIECES < 16 ? t % PIECES : 4 * (t % 2) + 2 * (t / 2 % 2) + 8 * (t / 4 % 2) + t / 8 % 2));
+}
+
+__device__ __forceinline__ float low_half(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float high_half(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
+
+constexpr uint32_t kOutside = 0x80000000u;  // of every buffer, and so is what lies a little behind
+
+// 16 bytes of a row from element n on; those from `width` on are 0
+__device__ __forceinline__ u32x4 load_piece(__amdgpu_buffer_rsrc_t r, uint32_t at, int n, int width) {
+  u32x4 v;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int e = n + 2 * i;
+    const uint32_t lo = load_one<bf16_t>(r, e < width ? at + 2 * e : kOutside).bits;
+    const uint32_t hi = load_one<bf16_t>(r, e + 1 < width ? at + 2 * e + 2 : kOutside).bits;
+    v[i] = lo | hi << 16;
+  }
+  return v;
+}
+
+// 16 bytes of each lane's address into LDS at `to`, one lane's behind the other's.  In
+// assembly: of the builtin the compiler does not know which LDS it writes, and waits for
+// it before the next read of any; who reads it waits for it here (vmcnt).
+struct Rows {
+  u32x4 words;
+  __device__ __forceinline__ Rows(const void *base, uint32_t bytes) {
+    const uint64_t at = reinterpret_cast<uint64_t>(base);
+    words = u32x4{static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(at))),
+                  static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(at >> 32))) & 0xffffu,
+                  static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(bytes)), 0x00020000u};
+  }
+};
+__device__ __forceinline__ void fetch_lds(const Rows &r, uint32_t to, uint32_t at, uint32_t more) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(to), "v"(at), "s"(r.words),
+               "s"(__builtin_amdgcn_readfirstlane(more))
+               : "memory");
+}
+
+template <int N>
+using Number = std::integral_constant<int, N>;
+
+// Weights from the log decay in units of log 2: a^n, 1 for n = 0 whatever a.
+__device__ __forceinline__ float power_of(double log2_a, int n) {
+  return n == 0 ? 1.f : fast_exp2(static_cast<float>(log2_a * n));
+}
+
+// KB: blocks of 32 that K is rounded up to; W waves of 16 columns each.  SHARE: the
+// scores are formed once, by all waves, and shared through LDS; else by each wave.
+template <int KB, int W, bool SHARE, bool Y, bool TAN, bool VEC>
+__global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(KB == 8 || TAN ? 1 : 2)))
+void la_bf16_kernel(LaArgs a, LaPasses all, int64_t items, int64_t sub, int64_t base) {
+  constexpr int kThreads = 64 * W, C = 64, KP = 4 * KB, kColumns = 16 * W, VP = kColumns / 8;
+  constexpr int kRowsK = C * KP / kThreads, kRowsV = C * VP / kThreads;  // pieces a thread brings
+  constexpr uint32_t kTile = 2 * C * KP * 8, kTileV = 2 * C * VP * 8;    // bytes
+  // two buffers of keys, of values, of x, and (shared) two parts of the scores: one
+  // array, so that two workgroups find room where these are 80 KB
+  constexpr int kSizeK = C * KP * 8, kSizeV = C * VP * 8;
+  __shared__ __attribute__((aligned(128))) uint16_t lds[2 * kSizeK + 2 * kSizeV + (Y ? 2 * kSizeK : 0) +
+                                                        (Y && SHARE ? 2 * C * C : 0)];
+  uint16_t *const s_k = lds, *const s_v = lds + 2 * kSizeK, *const s_x = s_v + 2 * kSizeV,
+                  *const s_a = s_x + (Y ? 2 * kSizeK : 0);
+
+  const LaPass &p = all.p[blockIdx.y];
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / 64), lane = tid % 64, r = lane % 16,
+            g = lane / 16;
+  int64_t unit, in;
+  la_place(blockIdx.x, sub, unit, in);
+  const int64_t item = base + unit * sub + in;
+  if (item >= items) return;
+  const int64_t cols = (p.M + kColumns - 1) / kColumns;
+  const int64_t h = item / cols % a.H, slot = item / (cols * a.H);
+  const int m0 = static_cast<int>(item % cols) * kColumns, mw = 16 * wave;  // this wave's columns: m0 + mw ..
+  const LaSlot z = la_slot(a, slot, p.reverse);
+  if constexpr (TAN && Y) {  // every partial sum is written
+    if (z.len < 0 && tid == 0) p.dot_sum[item] = 0.0;
+  }
+  if (z.len < 0 || (!Y && z.last)) return;  // nothing follows the last segment
+  const double log_a = a.log_decay[h], log2_a = log_a * 1.4426950408889634;
+  const int f = p.reverse ? 0 : 1;
+
+  const uint16_t *x = static_cast<const uint16_t *>(p.x) + h / p.x_per * p.x_width;
+  const uint16_t *key = static_cast<const uint16_t *>(p.key) + h / p.key_per * p.key_width;
+  const uint16_t *val = static_cast<const uint16_t *>(p.val) + h / p.val_per * p.val_width + m0;
+  const int wide = p.M - m0 < kColumns ? p.M - m0 : kColumns;  // columns of this workgroup
+
+  // ---- the next chunk's rows.  VEC: from memory into LDS, 16 bytes a lane, a wave's
+  // 64 pieces one behind the other there (which piece of the row lands where is the
+  // lane's choice of address); else by registers.
+  u32x4 px[Y && !VEC ? kRowsK : 1], pk[VEC ? 1 : kRowsK], pv[VEC ? 1 : kRowsV];
+  // Row in memory of the chunk's first row there, and byte offset of its token t;
+  // behind the last token: outside every buffer.
+  auto low_row = [&](int t0, int left) {
+    return z.first + static_cast<int64_t>(p.reverse ? t0 + left - 1 : t0) * z.step;
+  };
+  auto at_row = [&](int t, int left, int64_t row, int size) {
+    const int i = p.reverse ? left - 1 - t : t;
+    return t < left ? static_cast<uint32_t>(i) * static_cast<uint32_t>(row) * size : kOutside;
+  };
+  // One tensor's rows of a chunk of `left` tokens to LDS address `to`.
+  auto fetch = [&](const Rows &rs, const uint16_t *to, int left, int64_t row, int width, auto pieces, auto place) {
+    constexpr int PIECES = decltype(pieces)::value, kAll = C * PIECES / kThreads;
+    constexpr int kStep = kThreads / PIECES;  // rows from one load of the thread to its next
+    const int c = tid % PIECES;
+#pragma unroll
+    for (int i = 0; i < kAll; ++i) {
+      const int t = tid / PIECES + kStep * i, n = place(t, c) - t * PIECES * 8;  // the element that belongs there
+      uint32_t at, more = 0;
+      if (left == C && kStep % 16 == 0) {  // the same address for each, and a step that all lanes share
+        const int first = tid / PIECES;
+        at = static_cast<uint32_t>(p.reverse ? kStep - 1 - first : first) * static_cast<uint32_t>(row) * 2;
+        more = static_cast<uint32_t>(kStep * (p.reverse ? kAll - 1 - i : i)) * static_cast<uint32_t>(row) * 2;
+      } else {
+        at = at_row(t, left, row, 2);
+      }
+      at = n < width ? at + 2 * n : kOutside;
+      fetch_lds(rs, __builtin_amdgcn_readfirstlane(lds_address(to)) + 2 * (kThreads * i + 64 * wave) * 8, at, more);
+    }
+  };
+  auto load = [&](int t0, int buf) {
+    const int left = z.len - t0 < C ? z.len - t0 : C;
+    if (left <= 0) return;
+    const int64_t low = low_row(t0, left);
+    auto rows = [&](const uint16_t *q, int64_t row, int width) {
+      return rows_of(q + low * row, left, static_cast<uint32_t>(row), static_cast<uint32_t>(width));
+    };
+    if constexpr (VEC) {
+      auto from = [&](const uint16_t *q, int64_t row, int width) {
+        return Rows(q + low * row, 2 * (static_cast<uint32_t>(left - 1) * static_cast<uint32_t>(row) + static_cast<uint32_t>(width)));
+      };
+      auto all = [&](int left) {
+        if constexpr (Y) fetch(from(x, p.x_row, p.K), s_x + buf * kSizeK, left, p.x_row, p.K, Number<KP>(), x_at<KP>);
+        fetch(from(key, p.key_row, p.K), s_k + buf * kSizeK, left, p.key_row, p.K, Number<KP>(), key_at<KP>);
+        fetch(from(val, p.val_row, wide), s_v + buf * kSizeV, left, p.val_row, wide, Number<VP>(), value_at<VP>);
+      };
+      if (left == C) all(C);
+      else all(left);
+    } else {
+      const __amdgpu_buffer_rsrc_t rk = rows(key, p.key_row, p.K), rv = rows(val, p.val_row, wide);
+      if constexpr (Y) {
+        const __amdgpu_buffer_rsrc_t rx = rows(x, p.x_row, p.K);
+#pragma unroll
+        for (int i = 0; i < kRowsK; ++i) {
+          const int q = tid + kThreads * i;
+          px[i] = load_piece(rx, at_row(q / KP, left, p.x_row, 2), 8 * (q % KP), p.K);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kRowsK; ++i) {
+        const int q = tid + kThreads * i;
+        pk[i] = load_piece(rk, at_row(q / KP, left, p.key_row, 2), 8 * (q % KP), p.K);
+      }
+#pragma unroll
+      for (int i = 0; i < kRowsV; ++i) {
+        const int q = tid + kThreads * i;
+        pv[i] = load_piece(rv, at_row(q / VP, left, p.val_row, 2), 8 * (q % VP), wide);
+      }
+    }
+  };
+  // What has been asked for is in LDS, as far as this wave is concerned.
+  auto stage = [&](int buf) {
+    if constexpr (VEC) {
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    } else {
+#pragma unroll
+      for (int i = 0; i < kRowsK; ++i) {
+        const int q = tid + kThreads * i;
+        if constexpr (Y) *reinterpret_cast<u32x4 *>(&s_x[buf * kSizeK + x_at<KP>(q / KP, q % KP)]) = px[i];
+        *reinterpret_cast<u32x4 *>(&s_k[buf * kSizeK + key_at<KP>(q / KP, q % KP)]) = pk[i];
+      }
+#pragma unroll
+      for (int i = 0; i < kRowsV; ++i) {
+        const int q = tid + kThreads * i;
+        *reinterpret_cast<u32x4 *>(&s_v[buf * kSizeV + value_at<VP>(q / VP, q % VP)]) = pv[i];
+      }
+    }
+  };
+  load(0, 0);
+
+  // ---- the state that enters the segment: tile 2 kb + u holds n = 32 kb + 8 g + 4 u + e
+  f32x4 S[2 * KB], U[TAN ? 2 * KB : 1];
+  const int64_t state0 = (z.seq * a.H + h) * a.state;
+  const int64_t Kp = (p.K + 15) / 16 * 16;
+  const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+  const int m = m0 + mw + r;
+  const bool col = m < p.M;
+  auto n_of = [&](int j) { return 32 * (j / 2) + 8 * g + 4 * (j % 2); };
+#pragma unroll
+  for (int j = 0; j < 2 * KB; ++j) {
+    S[j] = zero;
+    if constexpr (TAN) U[j] = zero;
+  }
+  if constexpr (Y) {
+    if (p.s0 != nullptr && col) {
+#pragma unroll
+      for (int j = 0; j < 2 * KB; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int n = n_of(j) + e;
+          if (n < p.K) S[j][e] = p.s0[state0 + static_cast<int64_t>(m) * p.sm + n * p.sn];
+        }
+    }
+    const LaCarry whole(log_a, a.seg_len);
+    const float n_whole = static_cast<float>(a.seg_len) * la_power(log_a, a.seg_len);
+    for (int64_t b = 0; b < z.before; ++b) {
+      const int64_t from = (((z.slot0 + b) * a.H + h) * p.M + m) * Kp;
+#pragma unroll
+      for (int j = 0; j < 2 * KB; ++j) {
+        const bool there = col && n_of(j) < Kp;
+        const f32x4 own = there ? *reinterpret_cast<const f32x4 *>(p.local + from + n_of(j)) : zero;
+        if constexpr (TAN) {
+          const f32x4 tan = there ? *reinterpret_cast<const f32x4 *>(p.local_tan + from + n_of(j)) : zero;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) U[j][e] = whole(U[j][e]) + fmaf(n_whole, S[j][e], tan[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) S[j][e] = whole(S[j][e]) + own[e];
+      }
+    }
+  }
+
+  // ---- LDS addresses: row r, block kb of x and keys; the transposing reads of the
+  // keys' block kb and of this wave's values, tokens 4 g + r / 4
+  uint32_t lx[Y ? KB : 1], lk[Y ? KB : 1], lt[KB];
+#pragma unroll
+  for (int kb = 0; kb < KB; ++kb) {
+    if constexpr (Y) {
+      lx[kb] = hold(lds_address(&s_x[x_at<KP>(r, 4 * kb + g)]));
+      lk[kb] = hold(lds_address(&s_k[key_at<KP>(r, 4 * kb + g)]));
+    }
+    lt[kb] = hold(lds_address(&s_k[key_at<KP>(4 * g + r / 4, 4 * kb + r % 4)]));
+  }
+  const uint32_t lv = hold(lds_address(&s_v[value_at<VP>(4 * g + r / 4, (mw + 4 * (r % 4)) / 8) + 4 * (r % 2)]));
+  // shared scores: row t, piece 4 tb + g holds the keys 32 tb + 16 u + 4 g + e
+  const uint32_t la[2] = {hold(lds_address(&s_a[SHARE ? C * r + 8 * (g ^ (r % 8)) : 0])),
+                          hold(lds_address(&s_a[SHARE ? C * r + 8 * ((4 + g) ^ (r % 8)) : 0]))};
+
+  // ---- weights: of scores (token less key 16 d + r - 4 g - e), of the state's
+  // answers (token 16 i + r), of values in the state (tokens 16 j + 4 g + e)
+  const float cc = p.c_in * p.c_out;
+  auto score_weight = [&](int d, int e) {
+    const int n = 16 * d + r - 4 * g - e;
+    const float w = cc * power_of(log2_a, n < 0 ? 0 : n);
+    return TAN ? w * static_cast<float>(n) : w;
+  };
+  f32x4 w_score[Y && !SHARE ? 4 : 1], w_val[4];
+  float w_out[Y ? 4 : 1];
+  if constexpr (Y) {
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+      if constexpr (!SHARE)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w_score[d][e] = score_weight(d, e);
+      w_out[d] = p.c_out * power_of(log2_a, 16 * d + r + f);
+    }
+  }
+  // Shared: this wave's tiles, key block bs of token block bt, two of the ten below
+  // the diagonal for the first two waves of eight and one for the others.
+  constexpr int kTiles = SHARE ? (10 + W - 1) / W : 1;
+  int bt_of[kTiles], bs_of[kTiles];
+  f32x4 w_tile[Y && SHARE ? kTiles : 1];
+  if constexpr (Y && SHARE) {
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i) {
+      const int n = wave + W * i;
+      bt_of[i] = n < 1 ? 0 : n < 3 ? 1 : n < 6 ? 2 : 3;
+      bs_of[i] = n - bt_of[i] * (bt_of[i] + 1) / 2;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w_tile[i][e] = n < 10 ? score_weight(bt_of[i] - bs_of[i], e) : 0.f;
+    }
+  }
+  auto weigh = [&](int left) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int d = left - 1 - (16 * j + 4 * g + e);
+        w_val[j][e] = d < 0 ? 0.f : p.c_in * power_of(log2_a, d + 1 - f);
+      }
+  };
+  weigh(C);
+  float carry = 0.f;
+  float n_left = static_cast<float>(C) * power_of(log2_a, C);
+  const MinusOne minus;
+  double sum = 0.0;
+
+  // One chunk from buffer buf.  CLEAN: all values are finite.
+  auto chunk = [&](int t0, int left, int buf, u32x4 (&v)[2], int bad, auto clean) {
+    constexpr bool CLEAN = decltype(clean)::value;
+    const uint32_t more = buf ? kTile : 0;
+    f32x4 y[Y ? 4 : 1], yu[TAN ? 4 : 1];
+    if constexpr (Y) {
+      if constexpr (SHARE) {
+        // ---- scores, keys 16 bs + 4 g + e of token 16 bt + r, for all waves
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i) {
+          if (wave + W * i >= 10) break;
+          f32x4 w = zero;
+          const uint32_t at_k = more + 2 * 8 * KP * 16 * bs_of[i], at_x = more + 2 * 8 * KP * 16 * bt_of[i];
+#pragma unroll
+          for (int kb = 0; kb < KB; ++kb) w = mma(lds_get<u32x4>(lk[kb] + at_k), lds_get<u32x4>(lx[kb] + at_x), w);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            w[e] *= w_tile[i][e];
+            w[e] = bt_of[i] == bs_of[i] && r < 4 * g + e ? 0.f : w[e];
+          }
+          u32x2 half[2];
+          split4<2>(w, half, minus);
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+            lds_put<u32x2>((bs_of[i] >= 2 ? la[1] : la[0]) + 2 * C * C * q + 2 * C * 16 * bt_of[i] + 8 * (bs_of[i] % 2), half[q]);
+        }
+      }
+      // ---- what the state answers
+      u32x4 xq[4][SHARE ? 1 : KB];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        y[i] = zero;
+        if constexpr (TAN) yu[i] = zero;
+      }
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb) {
+        const int k = SHARE ? 0 : kb;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) xq[i][k] = lds_get<u32x4>(lx[kb] + more + 2 * 8 * KP * 16 * i);
+        u32x4 part[2];
+        split_operand<2>(S[2 * kb], S[2 * kb + 1], part, minus);
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) y[i] = mma(part[q], xq[i][k], y[i]);
+        if constexpr (TAN) {
+          split_operand<2>(U[2 * kb], U[2 * kb + 1], part, minus);
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) yu[i] = mma(part[q], xq[i][k], yu[i]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if constexpr (TAN) y[i][e] = fmaf(static_cast<float>(16 * i + r + 1), y[i][e], yu[i][e]);
+          y[i][e] *= w_out[i];
+        }
+      // ---- the values under the scores
+      if constexpr (SHARE) {
+        meet_in_lds();
+#pragma unroll
+        for (int tb = 0; tb < 2; ++tb)
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int bt = 2 * tb; bt < 4; ++bt) {
+              u32x4 part = lds_get<u32x4>(la[tb] + 2 * C * C * q + 2 * C * 16 * bt);
+              if (bt == 2 * tb) part[2] = part[3] = 0;  // above the diagonal
+              y[bt] = mma(v[tb], part, y[bt]);
+            }
+      } else {
+#pragma unroll
+        for (int tb = 0; tb < 2; ++tb) {
+          u32x4 part[4][2];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const int bs = 2 * tb + u;
+            u32x4 kq[KB];
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) kq[kb] = lds_get<u32x4>(lk[kb] + more + 2 * 8 * KP * 16 * bs);
+#pragma unroll
+            for (int bt = 2 * tb; bt < 4; ++bt) {
+              u32x2 half[2] = {};
+              if (bt >= bs) {
+                f32x4 w = zero;
+#pragma unroll
+                for (int kb = 0; kb < KB; ++kb) w = mma(kq[kb], xq[bt][SHARE ? 0 : kb], w);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  w[e] *= w_score[SHARE ? 0 : bt - bs][e];
+                  if (bt == bs) w[e] = r < 4 * g + e ? 0.f : w[e];
+                }
+                split4<2>(w, half, minus);
+              }
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                part[bt][q][2 * u] = half[q][0];
+                part[bt][q][2 * u + 1] = half[q][1];
+              }
+            }
+          }
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int bt = 2 * tb; bt < 4; ++bt) y[bt] = mma(v[tb], part[bt][q], y[bt]);
+        }
+      }
+    }
+    // ---- the state that leaves the chunk
+    u32x4 wv[2][3], wu[TAN ? 2 : 1][3];
+#pragma unroll
+    for (int tb = 0; tb < 2; ++tb) {
+      f32x4 t[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t q = v[tb][2 * u + e / 2];
+          t[u][e] = (e % 2 ? high_half(q) : low_half(q)) * w_val[2 * tb + u][e];
+        }
+      split_operand<3>(t[0], t[1], wv[tb], minus);
+      if constexpr (TAN) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            t[u][e] *= static_cast<float>(max(left - 1 - (32 * tb + 16 * u + 4 * g + e), 0));
+        split_operand<3>(t[0], t[1], wu[tb], minus);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 2 * KB; ++j) {
+      u32x4 kt[2];
+#pragma unroll
+      for (int tb = 0; tb < 2; ++tb)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const u32x2 q = lds_transposed(lt[j / 2] + more + 2 * (8 * KP * (32 * tb + 16 * u) + 4 * (j % 2)));
+          kt[tb][2 * u] = q[0];
+          kt[tb][2 * u + 1] = q[1];
+        }
+      if constexpr (TAN) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) U[j][e] = fmaf(n_left, S[j][e], carry * U[j][e]);
+#pragma unroll
+        for (int tb = 0; tb < 2; ++tb)
+#pragma unroll
+          for (int q = 0; q < 3; ++q) U[j] = mma(kt[tb], wu[tb][q], U[j]);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) S[j][e] *= carry;
+#pragma unroll
+      for (int tb = 0; tb < 2; ++tb)
+#pragma unroll
+        for (int q = 0; q < 3; ++q) S[j] = mma(kt[tb], wv[tb][q], S[j]);
+    }
+    if constexpr (!CLEAN) {
+      if (bad < C) {
+#pragma unroll
+        for (int j = 0; j < 2 * KB; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            S[j][e] = __builtin_nanf("");
+            if constexpr (TAN) U[j][e] = __builtin_nanf("");
+          }
+      }
+    }
+    // the next chunk's loads, before anything that is stored after them has to be
+    // waited for too
+    if (t0 + C < z.len) stage(buf ^ 1);
+    if constexpr (Y) {
+      // ---- out: channels 4 g .. + 3 of token 16 i + r
+      if constexpr (!CLEAN) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int from = __shfl(bad, 4 * g + e);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (16 * i + r >= from) y[i][e] = __builtin_nanf("");
+        }
+      }
+      const int64_t low = low_row(t0, left);
+      const int mo = mw + 4 * g;
+      if constexpr (TAN) {
+        const uint16_t *dot = static_cast<const uint16_t *>(p.dot) + h / p.val_per * p.val_width + m0;
+        const __amdgpu_buffer_rsrc_t rd =
+            rows_of(dot + low * p.val_row, left, static_cast<uint32_t>(p.val_row), static_cast<uint32_t>(wide));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t at = at_row(16 * i + r, left, p.val_row, 2);
+          float d[4], s = 0.f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) d[e] = to_f32(load_one<bf16_t>(rd, mo + e < wide ? at + 2 * (mo + e) : kOutside));
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s = fmaf(mo + e < wide && 16 * i + r < left ? y[i][e] : 0.f, d[e], s);
+          sum += static_cast<double>(s);
+        }
+      } else {
+        auto store = [&](auto wide_type, bool full) {
+          constexpr int kSize = decltype(wide_type)::value;  // bytes of an element
+          char *out = static_cast<char *>(p.out) + kSize * (h * p.out_width + m0 + low * p.out_row);
+          const __amdgpu_buffer_rsrc_t ro = buffer_of(
+              out, kSize * (static_cast<uint32_t>(left - 1) * static_cast<uint32_t>(p.out_row) + static_cast<uint32_t>(wide)));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t at = at_row(16 * i + r, left, p.out_row, kSize), more = 0;
+            if (full) {  // one address a lane, and a step that all share
+              at = static_cast<uint32_t>(p.reverse ? 15 - r : r) * static_cast<uint32_t>(p.out_row) * kSize;
+              more = static_cast<uint32_t>(16 * (p.reverse ? 3 - i : i)) * static_cast<uint32_t>(p.out_row) * kSize;
+            }
+            if constexpr (VEC && kSize == 4) {
+              __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, y[i]), ro,
+                                                     static_cast<int>(mo < wide ? at + 4 * mo : kOutside),
+                                                     static_cast<int>(more), 0);
+            } else if constexpr (VEC) {
+              __builtin_amdgcn_raw_buffer_store_b64(
+                  u32x2{pack_bf16(y[i][0], y[i][1]), pack_bf16(y[i][2], y[i][3])}, ro,
+                  static_cast<int>(mo < wide ? at + 2 * mo : kOutside), static_cast<int>(more), 0);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t to = mo + e < wide ? at + more + kSize * (mo + e) : kOutside;
+                if constexpr (kSize == 4) store_one(y[i][e], ro, to);
+                else store_one(from_f32<bf16_t>(y[i][e]), ro, to);
+              }
+            }
+          }
+        };
+        auto sized = [&](bool full) {
+          if (p.out_f32) store(Number<4>(), full);
+          else store(Number<2>(), full);
+        };
+        if (left == C) sized(true);
+        else sized(false);
+      }
+    }
+  };
+
+  // The factor of a chunk's decay, so that their product over the chunks so far is the
+  // decay's to 2^-25 (one rounded factor again and again drifts off).
+  const double decay = exp(log_a * C), inverse = decay > 1e-30 ? 1.0 / decay : 0.0;
+  double drift = 1.0;
+  if (z.len > 0) stage(0);
+  __syncthreads();
+
+  for (int t0 = 0, buf = 0; t0 < z.len; t0 += C, buf ^= 1) {
+    const int left = z.len - t0 < C ? z.len - t0 : C;
+    load(t0 + C, buf ^ 1);
+    carry = static_cast<float>(decay * drift);
+    drift = fma(fma(decay, drift, -static_cast<double>(carry)), inverse, 1.0);
+    if (left < C) {
+      weigh(left);
+      carry = la_power(log_a, left);
+      n_left = static_cast<float>(left) * carry;
+    }
+    // ---- this wave's values, transposed: tokens 32 tb + 16 u + 4 g + e of column r
+    u32x4 v[2];
+#pragma unroll
+    for (int tb = 0; tb < 2; ++tb)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const u32x2 q = lds_transposed(lv + (buf ? kTileV : 0) + 2 * 8 * VP * (32 * tb + 16 * u));
+        v[tb][2 * u] = q[0];
+        v[tb][2 * u + 1] = q[1];
+      }
+    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+    u16x2 top = {0, 0};
+    if constexpr (Y)  // (the state's own column is not finite then, as it should be)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, v[i / 4][i % 4] & 0x7fff7fffu));
+    int bad = C;
+    if (!Y || __ballot(top[0] >= 0x7f80 || top[1] >= 0x7f80) == 0) {
+      chunk(t0, left, buf, v, bad, std::true_type());
+    } else {  // those that are not finite are left out of the products
+#pragma unroll
+      for (int i = 7; i >= 0; --i) {
+        uint32_t q = v[i / 4][i % 4];
+        const int t = 32 * (i / 4) + 16 * (i % 4 / 2) + 4 * g + 2 * (i % 2);
+        if ((q >> 16 & 0x7f80) == 0x7f80) {
+          bad = min(bad, t + 1);
+          q &= 0xffffu;
+        }
+        if ((q & 0x7f80) == 0x7f80) {
+          bad = min(bad, t);
+          q &= 0xffff0000u;
+        }
+        v[i / 4][i % 4] = q;
+      }
+      bad = min(bad, __shfl_xor(bad, 16));
+      bad = min(bad, __shfl_xor(bad, 32));
+      chunk(t0, left, buf, v, bad, std::false_type());
+    }
+    meet_in_lds();
+  }
+
+  // ---- the state behind the segment
+  if (col) {
+    if constexpr (!Y) {
+      const int64_t to = ((slot * a.H + h) * p.M + m) * Kp;
+#pragma unroll
+      for (int j = 0; j < 2 * KB; ++j)
+        if (n_of(j) < Kp) {
+          *reinterpret_cast<f32x4 *>(p.local + to + n_of(j)) = S[j];
+          if constexpr (TAN) *reinterpret_cast<f32x4 *>(p.local_tan + to + n_of(j)) = U[j];
+        }
+    } else if (z.last) {
+      const int64_t at = state0 + static_cast<int64_t>(m) * p.sm;
+#pragma unroll
+      for (int j = 0; j < 2 * KB; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int n = n_of(j) + e;
+          if (n >= p.K) continue;
+          if (p.s_last != nullptr) p.s_last[at + n * p.sn] = S[j][e];
+          if constexpr (TAN)
+            if (p.s_dot != nullptr) sum += static_cast<double>(U[j][e]) * p.s_dot[at + n * p.sn];
+        }
+    }
+  }
+  if constexpr (Y && TAN) {
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) sum += __shfl_xor(sum, d);
+    double *s_sum = reinterpret_cast<double *>(lds);  // the last chunk has been read
+    if (lane == 0) s_sum[wave] = sum;
+    __syncthreads();
+    if (tid == 0) {
+      for (int i = 1; i < W; ++i) sum += s_sum[i];
+      p.dot_sum[item] = sum;
+    }
+  }
+}
+
+template <int KB, int W, bool SHARE, bool TAN, bool VEC>
+hipError_t launch_kb(const LaArgs &a, const LaPasses &all, int n, hipStream_t s) {
+  constexpr int kThreads = 64 * W;
+  const int64_t cols = (all.p[0].M + 16 * W - 1) / (16 * W);
+  const int64_t sub = la_sub(a, all.p[0].x_per, cols);
+  return la_launches(a, cols, sub, n, [&](dim3 grid, bool y, int64_t items, int64_t base) {
+    if (y) la_bf16_kernel<KB, W, SHARE, true, TAN, VEC><<<grid, kThreads, 0, s>>>(a, all, items, sub, base);
+    else la_bf16_kernel<KB, W, SHARE, false, TAN, VEC><<<grid, kThreads, 0, s>>>(a, all, items, sub, base);
+  });
+}
+
+// 16-byte pieces of every row, head and output
+bool pieces(const LaPass &p) {
+  for (const void *q : {p.x, p.key, p.val, static_cast<const void *>(p.out)})
+    if (reinterpret_cast<uintptr_t>(q) % 16 != 0) return false;
+  for (int64_t n : {p.x_row, p.key_row, p.val_row, p.x_width, p.key_width, p.val_width, p.out_row, p.out_width,
+                    static_cast<int64_t>(p.K), static_cast<int64_t>(p.M)})
+    if (n % 8 != 0) return false;
+  return true;
+}
+
+template <bool TAN, bool VEC>
+hipError_t launch_vec(const LaArgs &a, const LaPasses &all, int n, hipStream_t s) {
+  const int64_t K = all.p[0].K, M = all.p[0].M;
+  if constexpr (TAN) {
+    if (K <= 64) return launch_kb<2, 4, false, TAN, VEC>(a, all, n, s);
+    if (K <= 128) return launch_kb<4, 4, false, TAN, VEC>(a, all, n, s);
+  } else if (M <= 64) {
+    if (K <= 64) return launch_kb<2, 4, false, TAN, VEC>(a, all, n, s);
+    if (K <= 128) return launch_kb<4, 4, false, TAN, VEC>(a, all, n, s);
+  } else {
+    if (K <= 64) return launch_kb<2, 8, true, TAN, VEC>(a, all, n, s);
+    if (K <= 128) return launch_kb<4, 8, true, TAN, VEC>(a, all, n, s);
+  }
+  return launch_kb<8, 4, false, TAN, VEC>(a, all, n, s);
+}
+
+}  // namespace
+
+hipError_t launch_la_bf16(const LaArgs &a, const LaPass *p, int n, hipStream_t s) {
+  LaPasses all{};
+  bool vec = true;
+  for (int i = 0; i < n; ++i) {
+    all.p[i] = p[i];
+    vec = vec && pieces(p[i]);
+  }
+  if (p[0].dot_sum != nullptr) return vec ? launch_vec<true, true>(a, all, n, s) : launch_vec<true, false>(a, all, n, s);
+  return vec ? launch_vec<false, true>(a, all, n, s) : launch_vec<false, false>(a, all, n, s);
+}
+
+}  // namespace ssm

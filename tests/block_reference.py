@@ -76,3 +76,18 @@ def scales(y, group, most):
     parts = y.reshape(*y.shape[:-1], y.shape[-1] // group, group)
     s = (parts.abs().amax(-1) / most).clamp(min=LEAST_SCALE)
     return s, (parts / s[..., None]).reshape(y.shape)
+
+
+def parts_slack(w, scale=None, cu=None):
+    """What y, dq, dk and dv of bf16 inputs may be off by beside the common bar.  On
+    the bf16 matrix cores the scores and the state enter the outputs' products in two
+    bf16 parts: the first is off by at most 2^-9 of the number, the second by 2^-9 of
+    that rest, so each term of a sum by 2^-18 of itself (1 + 2^-9 of it, for the first
+    part's own rounding up).  The sum of the terms' sizes is at most the same sum of
+    the inputs' sizes, which is formed here."""
+    if w["q"].dtype != torch.bfloat16:
+        return {n: None for n in ("y", "q", "k", "v")}
+    size = {n: None if t is None else t if n == "g" else t.abs() for n, t in w.items()}
+    y, _, grads = attention_grads(size, scale, cu)
+    factor = 2.0 ** -18 * (1 + 2.0 ** -8)
+    return {"y": factor * y, **{n: factor * grads[n] for n in ("q", "k", "v")}}

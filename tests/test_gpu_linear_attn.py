@@ -48,7 +48,7 @@ def test_prefill(B, L, H, G, P, N, dtype):
         y, h = ssm.linear_attn_fwd(*inputs(w))
         torch.cuda.synchronize()
         ry, rh = blk.attention(*(None if w[n] is None else w[n].double() for n in ("q", "k", "v", "g", "h0")))
-        close(y, ry, "y")
+        close(y, ry, "y", blk.parts_slack(w)["y"])
         close(h, rh, "h")
 
 
@@ -66,8 +66,9 @@ def test_gradients(B, L, H, G, P, N, dtype):
 
 
 def check_grads(d, r, w, cu=None):
+    slack = blk.parts_slack(w, cu=cu)
     for n in ("q", "k", "v"):
-        close(d["d" + n], r[n], "d" + n)
+        close(d["d" + n], r[n], "d" + n, slack[n])
     if w["h0"] is not None:
         close(d["dh0"], r["h0"], "dh0")
     if d["dlog_decay"] is not None:
@@ -126,7 +127,8 @@ def test_packed(lengths, before, after, dtype):
         assert (y.cpu()[0, out] == 7.0).all()
         for n in ("dq", "dk", "dv"):
             assert (d[n].cpu()[0, out] == 0).all()
-        close(y[:, cu[0]:cu[-1]], ry[:, cu[0]:cu[-1]], "y")
+        slack = blk.parts_slack(w, cu=cu)["y"]
+        close(y[:, cu[0]:cu[-1]], ry[:, cu[0]:cu[-1]], "y", None if slack is None else slack[:, cu[0]:cu[-1]])
         close(h, rh, "h")
         check_grads(d, r, w, cu)
 
@@ -145,14 +147,15 @@ def test_long_sequences_are_cut_and_whole(dtype):
     y, h = ssm.linear_attn_fwd(*args)
     again, h2 = ssm.linear_attn_fwd(*args)
     assert torch.equal(y, again) and torch.equal(h, h2)
-    close(y, ry, "y")
+    slack = blk.parts_slack(w)["y"]
+    close(y, ry, "y", slack)
     close(h, rh, "h")
     d = ssm.linear_attn_bwd(*args, up(w["dy"]), up(w["dh"]), want_ddecay=True)
     check_grads(d, r, w)
     many = 400
     assert ssm.linear_attn_fwd_workspace_size(many, L, 1, P, 1, N, dtype) == 0
     yb, hb = ssm.linear_attn_fwd(*(t if t.dim() == 1 else t.expand(many, *t.shape[1:]).contiguous() for t in args))
-    close(yb[many - 1:], ry, "y of a batch")
+    close(yb[many - 1:], ry, "y of a batch", slack)
     close(hb[:1], rh, "h of a batch")
 
 
@@ -205,7 +208,7 @@ def test_prefill_then_decode(dtype):
     head, tail = ([t[:, :cut].contiguous() for t in (q, k, v)], [t[:, cut:].contiguous() for t in (q, k, v)])
     y0, state = ssm.linear_attn_fwd(*head, g, h0)
     y1 = ssm.linear_attn_decode_steps(state, *tail, g)
-    close(torch.cat((y0, y1), 1), ry, "y")
+    close(torch.cat((y0, y1), 1), ry, "y", blk.parts_slack(w)["y"])
     close(state, rh, "h")
 
 
@@ -219,17 +222,21 @@ def test_extreme_decays(dtype):
     w["g"] = torch.tensor([float("-inf"), -60.0, -1e-6, 0.0, 0.01, -0.3])
     y, h = ssm.linear_attn_fwd(*inputs(w))
     ry, rh = blk.attention(*(w[n].double() for n in ("q", "k", "v", "g", "h0")))
+    w["g"][0] = -1e4  # exp is 0 too, and has a derivative
+    slack = blk.parts_slack(w)
+    at = (lambda n, i: None) if slack["y"] is None else (lambda n, i: slack[n][:, :, i])
+    w["g"][0] = float("-inf")
     for i in range(H):
-        close(y[:, :, i], ry[:, :, i], f"y of head {i}")
+        close(y[:, :, i], ry[:, :, i], f"y of head {i}", at("y", i))
         close(h[:, i], rh[:, i], f"h of head {i}")
     d = ssm.linear_attn_bwd(*inputs(w), up(w["dy"]), up(w["dh"]))
     keep = w["g"].clone()
-    w["g"][0] = -1e4  # exp is 0 too, and has a derivative
+    w["g"][0] = -1e4
     _, _, r = blk.attention_grads(w)
     w["g"] = keep
     for n in ("q", "k", "v"):
         for i in range(H):
-            close(d["d" + n][:, :, i], r[n][:, :, i], f"d{n} of head {i}")
+            close(d["d" + n][:, :, i], r[n][:, :, i], f"d{n} of head {i}", at(n, i))
     close(d["dh0"], r["h0"], "dh0")
 
 
@@ -313,7 +320,7 @@ def test_views_that_are_not_aligned():
         y, h = ssm.linear_attn_fwd(*args)
         d = ssm.linear_attn_bwd(*args, shifted(w["dy"]), shifted(w["dh"]), want_ddecay=True)
         ry, rh, r = blk.attention_grads(w)
-        close(y, ry, "y")
+        close(y, ry, "y", blk.parts_slack(w)["y"])
         close(h, rh, "h")
         check_grads(d, r, w)
 
