@@ -68,19 +68,65 @@ __device__ __forceinline__ u32x4 load_piece(__amdgpu_buffer_rsrc_t r, uint32_t a
 // 16 bytes of each lane's address into LDS at `to`, one lane's behind the other's.  In
 // assembly: of the builtin the compiler does not know which LDS it writes, and waits for
 // it before the next read of any; who reads it waits for it here (vmcnt).
+__device__ __forceinline__ float uniform(float v) {
+  return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(v)));
+}
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+  const uint64_t u = static_cast<uint64_t>(v);
+  return static_cast<int64_t>(
+      static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(u >> 32)))) << 32 |
+      static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(u))));
+}
+// Whether a state's rows are whole pieces of four consecutive n.
+__device__ __forceinline__ bool fours_of(const LaPass &p, const float *state) {
+  return p.sn == 1 && p.sm % 4 == 0 && p.K % 4 == 0 && reinterpret_cast<uintptr_t>(state) % 16 == 0;
+}
+// A slot's numbers in scalar registers (bounds that are loaded come in vector ones).
+__device__ __forceinline__ LaSlot la_uniform(const LaSlot &z) {
+  LaSlot r;
+  r.seq = uniform(z.seq);
+  r.first = uniform(z.first);
+  r.step = uniform(z.step);
+  r.before = uniform(z.before);
+  r.slot0 = uniform(z.slot0);
+  r.len = __builtin_amdgcn_readfirstlane(z.len);
+  r.last = __builtin_amdgcn_readfirstlane(static_cast<int>(z.last)) != 0;
+  return r;
+}
 struct Rows {
   u32x4 words;
   __device__ __forceinline__ Rows(const void *base, uint32_t bytes) {
     const uint64_t at = reinterpret_cast<uint64_t>(base);
-    words = u32x4{static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(at))),
-                  static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(at >> 32))) & 0xffffu,
-                  static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(bytes)), 0x00020000u};
+    words = u32x4{static_cast<uint32_t>(at), static_cast<uint32_t>(at >> 32) & 0xffffu, bytes, 0x00020000u};
   }
 };
 __device__ __forceinline__ void fetch_lds(const Rows &r, uint32_t to, uint32_t at, uint32_t more) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(to), "v"(at), "s"(r.words),
-               "s"(__builtin_amdgcn_readfirstlane(more))
+               "s"(more)
                : "memory");
+}
+
+// fp32 as a sum of NP bf16 parts, as split4 of gdr_mfma.h, the rest by a shift (or a
+// mask) and a subtraction: v_dot2c_f32_bf16 writes over its operand, which has to be
+// copied where it is wanted again, and is waited for.
+template <int NP>
+__device__ __forceinline__ void split_four(f32x4 v, u32x2 *out) {
+#pragma unroll
+  for (int p = 0; p < NP; ++p) {
+    out[p] = u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+    if (p + 1 < NP)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] -= e % 2 ? high_half(out[p][e / 2]) : low_half(out[p][e / 2]);
+  }
+}
+template <int NP>
+__device__ __forceinline__ void split_parts(f32x4 top, f32x4 bottom, u32x4 *out) {
+  u32x2 a[NP], b[NP];
+  split_four<NP>(top, a);
+  split_four<NP>(bottom, b);
+#pragma unroll
+  for (int p = 0; p < NP; ++p) out[p] = u32x4{a[p][0], a[p][1], b[p][0], b[p][1]};
 }
 
 template <int N>
@@ -117,18 +163,26 @@ void la_bf16_kernel(LaArgs a, LaPasses all, int64_t items, int64_t sub, int64_t 
   const int64_t cols = (p.M + kColumns - 1) / kColumns;
   const int64_t h = item / cols % a.H, slot = item / (cols * a.H);
   const int m0 = static_cast<int>(item % cols) * kColumns, mw = 16 * wave;  // this wave's columns: m0 + mw ..
-  const LaSlot z = la_slot(a, slot, p.reverse);
+  const LaSlot z = la_uniform(la_slot(a, slot, p.reverse));
   if constexpr (TAN && Y) {  // every partial sum is written
     if (z.len < 0 && tid == 0) p.dot_sum[item] = 0.0;
   }
   if (z.len < 0 || (!Y && z.last)) return;  // nothing follows the last segment
   const double log_a = a.log_decay[h], log2_a = log_a * 1.4426950408889634;
-  const int f = p.reverse ? 0 : 1;
+  const int f = z.step < 0 ? 0 : 1;
 
-  const uint16_t *x = static_cast<const uint16_t *>(p.x) + h / p.x_per * p.x_width;
-  const uint16_t *key = static_cast<const uint16_t *>(p.key) + h / p.key_per * p.key_width;
-  const uint16_t *val = static_cast<const uint16_t *>(p.val) + h / p.val_per * p.val_width + m0;
-  const int wide = p.M - m0 < kColumns ? p.M - m0 : kColumns;  // columns of this workgroup
+  // Elements from row to row; a row's byte offset within a chunk's rows stays below 2^31.
+  const uint32_t x_row = uniform(static_cast<uint32_t>(p.x_row)), key_row = uniform(static_cast<uint32_t>(p.key_row)),
+                 val_row = uniform(static_cast<uint32_t>(p.val_row)), out_row = uniform(static_cast<uint32_t>(p.out_row));
+  const bool reverse = z.step < 0;
+  auto start = [&](const void *q, int64_t from) {
+    return reinterpret_cast<const uint16_t *>(
+        uniform(static_cast<int64_t>(reinterpret_cast<uintptr_t>(static_cast<const uint16_t *>(q) + from))));
+  };
+  const uint16_t *const x = start(p.x, h / p.x_per * p.x_width), *const key = start(p.key, h / p.key_per * p.key_width),
+                 *const val = start(p.val, h / p.val_per * p.val_width + m0);
+  const int K = __builtin_amdgcn_readfirstlane(p.K);
+  const int wide = __builtin_amdgcn_readfirstlane(p.M - m0 < kColumns ? p.M - m0 : kColumns);  // columns of this workgroup
 
   // ---- the next chunk's rows.  VEC: from memory into LDS, 16 bytes a lane, a wave's
   // 64 pieces one behind the other there (which piece of the row lands where is the
@@ -137,69 +191,82 @@ void la_bf16_kernel(LaArgs a, LaPasses all, int64_t items, int64_t sub, int64_t 
   // Row in memory of the chunk's first row there, and byte offset of its token t;
   // behind the last token: outside every buffer.
   auto low_row = [&](int t0, int left) {
-    return z.first + static_cast<int64_t>(p.reverse ? t0 + left - 1 : t0) * z.step;
+    return z.first + (reverse ? -static_cast<int64_t>(t0 + left - 1) : static_cast<int64_t>(t0));
   };
-  auto at_row = [&](int t, int left, int64_t row, int size) {
-    const int i = p.reverse ? left - 1 - t : t;
-    return t < left ? static_cast<uint32_t>(i) * static_cast<uint32_t>(row) * size : kOutside;
+  auto at_row = [&](int t, int left, uint32_t row, uint32_t size) {
+    const int i = reverse ? left - 1 - t : t;
+    return t < left ? static_cast<uint32_t>(i) * row * size : kOutside;
+  };
+  // A thread's first piece of a whole chunk of a tensor of PIECES a row; the others are
+  // whole steps of rows behind it (where their places in the row are the same).
+  auto first_at = [&](uint32_t row, int width, auto pieces, auto place) {
+    constexpr int PIECES = decltype(pieces)::value, kStep = kThreads / PIECES;
+    const int t = tid / PIECES, n = place(t, tid % PIECES) - t * PIECES * 8;
+    const uint32_t at = static_cast<uint32_t>(reverse ? kStep - 1 - t : t) * row * 2;
+    return n < width ? at + 2 * n : kOutside;
   };
   // One tensor's rows of a chunk of `left` tokens to LDS address `to`.
-  auto fetch = [&](const Rows &rs, const uint16_t *to, int left, int64_t row, int width, auto pieces, auto place) {
+  auto fetch = [&](const uint16_t *from, const uint16_t *to, int left, uint32_t first, uint32_t row, int width,
+                   auto pieces, auto place) {
     constexpr int PIECES = decltype(pieces)::value, kAll = C * PIECES / kThreads;
     constexpr int kStep = kThreads / PIECES;  // rows from one load of the thread to its next
-    const int c = tid % PIECES;
+    const Rows rs(from, 2 * (static_cast<uint32_t>(left - 1) * row + static_cast<uint32_t>(width)));
+    const uint32_t at_lds = lds_address(to) + 2 * 64 * wave * 8;
+    if (left == C && kStep % 16 == 0) {
 #pragma unroll
-    for (int i = 0; i < kAll; ++i) {
-      const int t = tid / PIECES + kStep * i, n = place(t, c) - t * PIECES * 8;  // the element that belongs there
-      uint32_t at, more = 0;
-      if (left == C && kStep % 16 == 0) {  // the same address for each, and a step that all lanes share
-        const int first = tid / PIECES;
-        at = static_cast<uint32_t>(p.reverse ? kStep - 1 - first : first) * static_cast<uint32_t>(row) * 2;
-        more = static_cast<uint32_t>(kStep * (p.reverse ? kAll - 1 - i : i)) * static_cast<uint32_t>(row) * 2;
-      } else {
-        at = at_row(t, left, row, 2);
+      for (int i = 0; i < kAll; ++i)
+        fetch_lds(rs, at_lds + 2 * kThreads * i * 8, first, static_cast<uint32_t>(kStep * (reverse ? kAll - 1 - i : i)) * row * 2);
+    } else {
+      const int own = static_cast<int>(hold(static_cast<uint32_t>(tid)));
+#pragma unroll
+      for (int i = 0; i < kAll; ++i) {
+        const int t = own / PIECES + kStep * i, n = place(t, own % PIECES) - t * PIECES * 8;  // the element that belongs there
+        fetch_lds(rs, at_lds + 2 * kThreads * i * 8, n < width ? at_row(t, left, row, 2) + 2 * n : kOutside, 0);
       }
-      at = n < width ? at + 2 * n : kOutside;
-      fetch_lds(rs, __builtin_amdgcn_readfirstlane(lds_address(to)) + 2 * (kThreads * i + 64 * wave) * 8, at, more);
     }
   };
-  auto load = [&](int t0, int buf) {
+  const uint32_t x_first = VEC && Y ? first_at(x_row, K, Number<KP>(), x_at<KP>) : 0,
+                 key_first = VEC ? first_at(key_row, K, Number<KP>(), key_at<KP>) : 0,
+                 val_first = VEC ? first_at(val_row, wide, Number<VP>(), value_at<VP>) : 0;
+  const bool out_f32 = __builtin_amdgcn_readfirstlane(static_cast<int>(p.out_f32)) != 0;
+  char *const out = reinterpret_cast<char *>(uniform(static_cast<int64_t>(
+      reinterpret_cast<uintptr_t>(static_cast<char *>(p.out) + (out_f32 ? 4 : 2) * (h * p.out_width + m0)))));
+  // which: 0 x, 1 keys, 2 values, 3 all.  (They are asked for in three places: a wave's
+  // next instruction waits while more of them are issued than the memory pipeline takes.)
+  auto load = [&](int t0, int buf, int which) {
     const int left = z.len - t0 < C ? z.len - t0 : C;
     if (left <= 0) return;
     const int64_t low = low_row(t0, left);
-    auto rows = [&](const uint16_t *q, int64_t row, int width) {
-      return rows_of(q + low * row, left, static_cast<uint32_t>(row), static_cast<uint32_t>(width));
-    };
     if constexpr (VEC) {
-      auto from = [&](const uint16_t *q, int64_t row, int width) {
-        return Rows(q + low * row, 2 * (static_cast<uint32_t>(left - 1) * static_cast<uint32_t>(row) + static_cast<uint32_t>(width)));
-      };
       auto all = [&](int left) {
-        if constexpr (Y) fetch(from(x, p.x_row, p.K), s_x + buf * kSizeK, left, p.x_row, p.K, Number<KP>(), x_at<KP>);
-        fetch(from(key, p.key_row, p.K), s_k + buf * kSizeK, left, p.key_row, p.K, Number<KP>(), key_at<KP>);
-        fetch(from(val, p.val_row, wide), s_v + buf * kSizeV, left, p.val_row, wide, Number<VP>(), value_at<VP>);
+        if (Y && (which == 0 || which == 3)) fetch(x + low * x_row, s_x + buf * kSizeK, left, x_first, x_row, K, Number<KP>(), x_at<KP>);
+        if (which == 1 || which == 3) fetch(key + low * key_row, s_k + buf * kSizeK, left, key_first, key_row, K, Number<KP>(), key_at<KP>);
+        if (which == 2 || which == 3) fetch(val + low * val_row, s_v + buf * kSizeV, left, val_first, val_row, wide, Number<VP>(), value_at<VP>);
       };
       if (left == C) all(C);
       else all(left);
-    } else {
-      const __amdgpu_buffer_rsrc_t rk = rows(key, p.key_row, p.K), rv = rows(val, p.val_row, wide);
+    } else if (which == 0 || which == 3) {
+      auto rows = [&](const uint16_t *q, uint32_t row, int width) {
+        return rows_of(q + low * row, left, row, static_cast<uint32_t>(width));
+      };
+      const __amdgpu_buffer_rsrc_t rk = rows(key, key_row, K), rv = rows(val, val_row, wide);
       if constexpr (Y) {
-        const __amdgpu_buffer_rsrc_t rx = rows(x, p.x_row, p.K);
+        const __amdgpu_buffer_rsrc_t rx = rows(x, x_row, K);
 #pragma unroll
         for (int i = 0; i < kRowsK; ++i) {
           const int q = tid + kThreads * i;
-          px[i] = load_piece(rx, at_row(q / KP, left, p.x_row, 2), 8 * (q % KP), p.K);
+          px[i] = load_piece(rx, at_row(q / KP, left, x_row, 2), 8 * (q % KP), K);
         }
       }
 #pragma unroll
       for (int i = 0; i < kRowsK; ++i) {
         const int q = tid + kThreads * i;
-        pk[i] = load_piece(rk, at_row(q / KP, left, p.key_row, 2), 8 * (q % KP), p.K);
+        pk[i] = load_piece(rk, at_row(q / KP, left, key_row, 2), 8 * (q % KP), K);
       }
 #pragma unroll
       for (int i = 0; i < kRowsV; ++i) {
         const int q = tid + kThreads * i;
-        pv[i] = load_piece(rv, at_row(q / VP, left, p.val_row, 2), 8 * (q % VP), wide);
+        pv[i] = load_piece(rv, at_row(q / VP, left, val_row, 2), 8 * (q % VP), wide);
       }
     }
   };
@@ -221,16 +288,16 @@ void la_bf16_kernel(LaArgs a, LaPasses all, int64_t items, int64_t sub, int64_t 
       }
     }
   };
-  load(0, 0);
+  load(0, 0, 3);
 
-  // ---- the state that enters the segment: tile 2 kb + u holds n = 32 kb + 8 g + 4 u + e
+  // ---- the state that enters the segment: tile 2 kb + u holds n = 32 kb + 8 g + 4 u + e.
+  // Offsets within the workgroup's columns are small: 32 bits.
   f32x4 S[2 * KB], U[TAN ? 2 * KB : 1];
-  const int64_t state0 = (z.seq * a.H + h) * a.state;
-  const int64_t Kp = (p.K + 15) / 16 * 16;
+  const int64_t state0 = (z.seq * a.H + h) * a.state + static_cast<int64_t>(m0) * p.sm;
+  const int Kp = (p.K + 15) / 16 * 16;
   const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-  const int m = m0 + mw + r;
-  const bool col = m < p.M;
-  auto n_of = [&](int j) { return 32 * (j / 2) + 8 * g + 4 * (j % 2); };
+  const int mc = mw + r;  // this lane's column of the workgroup's
+  const bool col = mc < wide;
 #pragma unroll
   for (int j = 0; j < 2 * KB; ++j) {
     S[j] = zero;
@@ -238,24 +305,37 @@ void la_bf16_kernel(LaArgs a, LaPasses all, int64_t items, int64_t sub, int64_t 
   }
   if constexpr (Y) {
     if (p.s0 != nullptr && col) {
+      const float *from = p.s0 + state0;
+      const int sn = static_cast<int>(p.sn), at = mc * static_cast<int>(p.sm) + 8 * g * sn;
+      if (fours_of(p, from)) {
 #pragma unroll
-      for (int j = 0; j < 2 * KB; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int n = n_of(j) + e;
-          if (n < p.K) S[j][e] = p.s0[state0 + static_cast<int64_t>(m) * p.sm + n * p.sn];
+        for (int j = 0; j < 2 * KB; ++j) {
+          const int n = 32 * (j / 2) + 4 * (j % 2);
+          if (n + 8 * g < p.K) S[j] = *reinterpret_cast<const f32x4 *>(from + at + n);
         }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 2 * KB; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int n = 32 * (j / 2) + 4 * (j % 2) + e;
+            if (n + 8 * g < p.K) S[j][e] = from[at + n * sn];
+          }
+      }
     }
     const LaCarry whole(log_a, a.seg_len);
     const float n_whole = static_cast<float>(a.seg_len) * la_power(log_a, a.seg_len);
     for (int64_t b = 0; b < z.before; ++b) {
-      const int64_t from = (((z.slot0 + b) * a.H + h) * p.M + m) * Kp;
+      const int64_t from = (((z.slot0 + b) * a.H + h) * p.M + m0) * Kp;
+      const float *local = p.local + from, *local_tan = TAN ? p.local_tan + from : nullptr;
+      const int at = mc * Kp + 8 * g;
 #pragma unroll
       for (int j = 0; j < 2 * KB; ++j) {
-        const bool there = col && n_of(j) < Kp;
-        const f32x4 own = there ? *reinterpret_cast<const f32x4 *>(p.local + from + n_of(j)) : zero;
+        const int n = 32 * (j / 2) + 4 * (j % 2);
+        const bool there = col && n + 8 * g < Kp;
+        const f32x4 own = there ? *reinterpret_cast<const f32x4 *>(local + at + n) : zero;
         if constexpr (TAN) {
-          const f32x4 tan = there ? *reinterpret_cast<const f32x4 *>(p.local_tan + from + n_of(j)) : zero;
+          const f32x4 tan = there ? *reinterpret_cast<const f32x4 *>(local_tan + at + n) : zero;
 #pragma unroll
           for (int e = 0; e < 4; ++e) U[j][e] = whole(U[j][e]) + fmaf(n_whole, S[j][e], tan[e]);
         }
@@ -276,7 +356,7 @@ void la_bf16_kernel(LaArgs a, LaPasses all, int64_t items, int64_t sub, int64_t 
     }
     lt[kb] = hold(lds_address(&s_k[key_at<KP>(4 * g + r / 4, 4 * kb + r % 4)]));
   }
-  const uint32_t lv = hold(lds_address(&s_v[value_at<VP>(4 * g + r / 4, (mw + 4 * (r % 4)) / 8) + 4 * (r % 2)]));
+  uint32_t lv = hold(lds_address(&s_v[value_at<VP>(4 * g + r / 4, (mw + 4 * (r % 4)) / 8) + 4 * (r % 2)]));
   // shared scores: row t, piece 4 tb + g holds the keys 32 tb + 16 u + 4 g + e
   const uint32_t la[2] = {hold(lds_address(&s_a[SHARE ? C * r + 8 * (g ^ (r % 8)) : 0])),
                           hold(lds_address(&s_a[SHARE ? C * r + 8 * ((4 + g) ^ (r % 8)) : 0]))};
@@ -315,7 +395,10 @@ void la_bf16_kernel(LaArgs a, LaPasses all, int64_t items, int64_t sub, int64_t 
       for (int e = 0; e < 4; ++e) w_tile[i][e] = n < 10 ? score_weight(bt_of[i] - bs_of[i], e) : 0.f;
     }
   }
+  // (What the last chunk alone needs is formed from a copy that `hold` hides, or it
+  // would be formed before the loop and kept in registers over it.)
   auto weigh = [&](int left) {
+    const int g = static_cast<int>(hold(static_cast<uint32_t>(lane))) / 16;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -327,168 +410,194 @@ void la_bf16_kernel(LaArgs a, LaPasses all, int64_t items, int64_t sub, int64_t 
   weigh(C);
   float carry = 0.f;
   float n_left = static_cast<float>(C) * power_of(log2_a, C);
-  const MinusOne minus;
   double sum = 0.0;
+
+  // A product of a key and an x tile: weighted, masked, in two parts.
+  auto split_scores = [&](f32x4 w, const f32x4 &weight, bool diagonal, u32x2 *half) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      w[e] *= weight[e];
+      w[e] = diagonal && r < 4 * g + e ? 0.f : w[e];
+    }
+    split_four<2>(w, half);
+  };
+  // The weighted values of token block tb, in three parts.
+  auto weighted = [&](const u32x4 &v, int tb, int left, u32x4 *out, bool tan) {
+    f32x4 t[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t q = v[2 * u + e / 2];
+        t[u][e] = (e % 2 ? high_half(q) : low_half(q)) * w_val[2 * tb + u][e];
+        if (tan) t[u][e] *= static_cast<float>(max(left - 1 - (32 * tb + 16 * u + 4 * g + e), 0));
+      }
+    split_parts<3>(t[0], t[1], out);
+  };
 
   // One chunk from buffer buf.  CLEAN: all values are finite.
   auto chunk = [&](int t0, int left, int buf, u32x4 (&v)[2], int bad, auto clean) {
     constexpr bool CLEAN = decltype(clean)::value;
-    const uint32_t more = buf ? kTile : 0;
     f32x4 y[Y ? 4 : 1], yu[TAN ? 4 : 1];
     if constexpr (Y) {
       if constexpr (SHARE) {
         // ---- scores, keys 16 bs + 4 g + e of token 16 bt + r, for all waves
 #pragma unroll
-        for (int i = 0; i < kTiles; ++i) {
-          if (wave + W * i >= 10) break;
+        for (int i = kTiles - 1; i >= 0; --i) {
+          if (wave + W * i >= 10) continue;
           f32x4 w = zero;
-          const uint32_t at_k = more + 2 * 8 * KP * 16 * bs_of[i], at_x = more + 2 * 8 * KP * 16 * bt_of[i];
+          const uint32_t at_k = 2 * 8 * KP * 16 * bs_of[i], at_x = 2 * 8 * KP * 16 * bt_of[i];
 #pragma unroll
           for (int kb = 0; kb < KB; ++kb) w = mma(lds_get<u32x4>(lk[kb] + at_k), lds_get<u32x4>(lx[kb] + at_x), w);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            w[e] *= w_tile[i][e];
-            w[e] = bt_of[i] == bs_of[i] && r < 4 * g + e ? 0.f : w[e];
-          }
           u32x2 half[2];
-          split4<2>(w, half, minus);
+          split_scores(w, w_tile[i], bt_of[i] == bs_of[i], half);
 #pragma unroll
           for (int q = 0; q < 2; ++q)
             lds_put<u32x2>((bs_of[i] >= 2 ? la[1] : la[0]) + 2 * C * C * q + 2 * C * 16 * bt_of[i] + 8 * (bs_of[i] % 2), half[q]);
         }
-      }
-      // ---- what the state answers
-      u32x4 xq[4][SHARE ? 1 : KB];
+        load(t0 + C, buf ^ 1, 1);
+        // ---- what the state answers, the next block's x on its way
+        u32x4 xq[2][4], part[2][2];
+        auto read_x = [&](int kb) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        y[i] = zero;
-        if constexpr (TAN) yu[i] = zero;
-      }
+          for (int i = 0; i < 4; ++i) xq[kb % 2][i] = lds_get<u32x4>(lx[kb] + 2 * 8 * KP * 16 * i);
+        };
+        read_x(0);
+        split_parts<2>(S[0], S[1], part[0]);
 #pragma unroll
-      for (int kb = 0; kb < KB; ++kb) {
-        const int k = SHARE ? 0 : kb;
+        for (int i = 0; i < 4; ++i) y[i] = zero;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) xq[i][k] = lds_get<u32x4>(lx[kb] + more + 2 * 8 * KP * 16 * i);
-        u32x4 part[2];
-        split_operand<2>(S[2 * kb], S[2 * kb + 1], part, minus);
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) y[i] = mma(part[q], xq[i][k], y[i]);
-        if constexpr (TAN) {
-          split_operand<2>(U[2 * kb], U[2 * kb + 1], part, minus);
-#pragma unroll
-          for (int q = 0; q < 2; ++q)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) yu[i] = mma(part[q], xq[i][k], yu[i]);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if constexpr (TAN) y[i][e] = fmaf(static_cast<float>(16 * i + r + 1), y[i][e], yu[i][e]);
-          y[i][e] *= w_out[i];
-        }
-      // ---- the values under the scores
-      if constexpr (SHARE) {
-        meet_in_lds();
-#pragma unroll
-        for (int tb = 0; tb < 2; ++tb)
-#pragma unroll
-          for (int q = 0; q < 2; ++q)
-#pragma unroll
-            for (int bt = 2 * tb; bt < 4; ++bt) {
-              u32x4 part = lds_get<u32x4>(la[tb] + 2 * C * C * q + 2 * C * 16 * bt);
-              if (bt == 2 * tb) part[2] = part[3] = 0;  // above the diagonal
-              y[bt] = mma(v[tb], part, y[bt]);
-            }
-      } else {
-#pragma unroll
-        for (int tb = 0; tb < 2; ++tb) {
-          u32x4 part[4][2];
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const int bs = 2 * tb + u;
-            u32x4 kq[KB];
-#pragma unroll
-            for (int kb = 0; kb < KB; ++kb) kq[kb] = lds_get<u32x4>(lk[kb] + more + 2 * 8 * KP * 16 * bs);
-#pragma unroll
-            for (int bt = 2 * tb; bt < 4; ++bt) {
-              u32x2 half[2] = {};
-              if (bt >= bs) {
-                f32x4 w = zero;
-#pragma unroll
-                for (int kb = 0; kb < KB; ++kb) w = mma(kq[kb], xq[bt][SHARE ? 0 : kb], w);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  w[e] *= w_score[SHARE ? 0 : bt - bs][e];
-                  if (bt == bs) w[e] = r < 4 * g + e ? 0.f : w[e];
-                }
-                split4<2>(w, half, minus);
-              }
-#pragma unroll
-              for (int q = 0; q < 2; ++q) {
-                part[bt][q][2 * u] = half[q][0];
-                part[bt][q][2 * u + 1] = half[q][1];
-              }
-            }
+        for (int kb = 0; kb < KB; ++kb) {
+          __builtin_amdgcn_sched_barrier(0);
+          if (kb + 1 < KB) {
+            read_x(kb + 1);
+            split_parts<2>(S[2 * kb + 2], S[2 * kb + 3], part[(kb + 1) % 2]);
           }
 #pragma unroll
           for (int q = 0; q < 2; ++q)
 #pragma unroll
-            for (int bt = 2 * tb; bt < 4; ++bt) y[bt] = mma(v[tb], part[bt][q], y[bt]);
+            for (int i = 0; i < 4; ++i) y[i] = mma(part[kb % 2][q], xq[kb % 2][i], y[i]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[i][e] *= w_out[i];
+        load(t0 + C, buf ^ 1, 2);
+        meet_in_lds();
+        // ---- the values under the scores
+#pragma unroll
+        for (int tb = 0; tb < 2; ++tb) {
+          u32x4 sc[2][4];
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int bt = 2 * tb; bt < 4; ++bt) {
+              sc[q][bt] = lds_get<u32x4>(la[tb] + 2 * C * C * q + 2 * C * 16 * bt);
+              if (bt == 2 * tb) sc[q][bt][2] = sc[q][bt][3] = 0;  // above the diagonal
+            }
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int bt = 2 * tb; bt < 4; ++bt) y[bt] = mma(v[tb], sc[q][bt], y[bt]);
+        }
+      } else {
+        // ---- token block by token block: what the state answers, the scores and the
+        // values under them
+        load(t0 + C, buf ^ 1, 1);
+        u32x4 part[KB][2], pu[TAN ? KB : 1][2];
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) {
+          split_parts<2>(S[2 * kb], S[2 * kb + 1], part[kb]);
+          if constexpr (TAN) split_parts<2>(U[2 * kb], U[2 * kb + 1], pu[kb]);
+        }
+#pragma unroll
+        for (int bt = 0; bt < 4; ++bt) {
+          if (bt == 2) load(t0 + C, buf ^ 1, 2);
+          u32x4 xq[KB];
+#pragma unroll
+          for (int kb = 0; kb < KB; ++kb) xq[kb] = lds_get<u32x4>(lx[kb] + 2 * 8 * KP * 16 * bt);
+          f32x4 w[4];
+#pragma unroll
+          for (int bs = 0; bs <= bt; ++bs) {
+            w[bs] = zero;
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) w[bs] = mma(lds_get<u32x4>(lk[kb] + 2 * 8 * KP * 16 * bs), xq[kb], w[bs]);
+          }
+          y[bt] = zero;
+#pragma unroll
+          for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) y[bt] = mma(part[kb][q], xq[kb], y[bt]);
+          if constexpr (TAN) {
+            yu[bt] = zero;
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+              for (int q = 0; q < 2; ++q) yu[bt] = mma(pu[kb][q], xq[kb], yu[bt]);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if constexpr (TAN) y[bt][e] = fmaf(static_cast<float>(16 * bt + r + 1), y[bt][e], yu[bt][e]);
+            y[bt][e] *= w_out[bt];
+          }
+#pragma unroll
+          for (int tb = 0; tb <= bt / 2; ++tb) {
+            u32x2 half[2][2] = {};
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+              if (2 * tb + u <= bt) split_scores(w[2 * tb + u], w_score[SHARE ? 0 : bt - 2 * tb - u], 2 * tb + u == bt, half[u]);
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+              y[bt] = mma(v[tb], u32x4{half[0][q][0], half[0][q][1], half[1][q][0], half[1][q][1]}, y[bt]);
+          }
         }
       }
     }
-    // ---- the state that leaves the chunk
-    u32x4 wv[2][3], wu[TAN ? 2 : 1][3];
-#pragma unroll
-    for (int tb = 0; tb < 2; ++tb) {
-      f32x4 t[2];
+    // ---- the state that leaves the chunk, the next keys on their way
+    u32x4 kt[2][2];
+    auto read_keys = [&](int i) {  // block kb, transposed: rows n of its two tiles, tokens of block tb
+      const int tb = i / KB, kb = i % KB;
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t q = v[tb][2 * u + e / 2];
-          t[u][e] = (e % 2 ? high_half(q) : low_half(q)) * w_val[2 * tb + u][e];
+        for (int s = 0; s < 2; ++s) {
+          const u32x2 q = lds_transposed(lt[kb] + 2 * (8 * KP * (32 * tb + 16 * s) + 4 * u));
+          kt[i % 2][u][2 * s] = q[0];
+          kt[i % 2][u][2 * s + 1] = q[1];
         }
-      split_operand<3>(t[0], t[1], wv[tb], minus);
-      if constexpr (TAN) {
+    };
+    read_keys(0);
+    if constexpr (TAN) {
+#pragma unroll
+      for (int j = 0; j < 2 * KB; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) U[j][e] = fmaf(n_left, S[j][e], carry * U[j][e]);
+    }
+    u32x4 wv[3], wu[3];
+#pragma unroll
+    for (int i = 0; i < 2 * KB; ++i) {
+      const int tb = i / KB, kb = i % KB;
+      if (kb == 0) {
+        weighted(v[tb], tb, left, wv, false);
+        if constexpr (TAN) weighted(v[tb], tb, left, wu, true);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      if (i + 1 < 2 * KB) read_keys(i + 1);
+      if (tb == 0)
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            t[u][e] *= static_cast<float>(max(left - 1 - (32 * tb + 16 * u + 4 * g + e), 0));
-        split_operand<3>(t[0], t[1], wu[tb], minus);
-      }
-    }
+          for (int e = 0; e < 4; ++e) S[2 * kb + u][e] *= carry;
 #pragma unroll
-    for (int j = 0; j < 2 * KB; ++j) {
-      u32x4 kt[2];
-#pragma unroll
-      for (int tb = 0; tb < 2; ++tb)
+      for (int q = 0; q < 3; ++q)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const u32x2 q = lds_transposed(lt[j / 2] + more + 2 * (8 * KP * (32 * tb + 16 * u) + 4 * (j % 2)));
-          kt[tb][2 * u] = q[0];
-          kt[tb][2 * u + 1] = q[1];
+          S[2 * kb + u] = mma(kt[i % 2][u], wv[q], S[2 * kb + u]);
+          if constexpr (TAN) U[2 * kb + u] = mma(kt[i % 2][u], wu[q], U[2 * kb + u]);
         }
-      if constexpr (TAN) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) U[j][e] = fmaf(n_left, S[j][e], carry * U[j][e]);
-#pragma unroll
-        for (int tb = 0; tb < 2; ++tb)
-#pragma unroll
-          for (int q = 0; q < 3; ++q) U[j] = mma(kt[tb], wu[tb][q], U[j]);
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) S[j][e] *= carry;
-#pragma unroll
-      for (int tb = 0; tb < 2; ++tb)
-#pragma unroll
-        for (int q = 0; q < 3; ++q) S[j] = mma(kt[tb], wv[tb][q], S[j]);
     }
+    __builtin_amdgcn_sched_barrier(0);
     if constexpr (!CLEAN) {
       if (bad < C) {
 #pragma unroll
@@ -518,11 +627,10 @@ void la_bf16_kernel(LaArgs a, LaPasses all, int64_t items, int64_t sub, int64_t 
       const int mo = mw + 4 * g;
       if constexpr (TAN) {
         const uint16_t *dot = static_cast<const uint16_t *>(p.dot) + h / p.val_per * p.val_width + m0;
-        const __amdgpu_buffer_rsrc_t rd =
-            rows_of(dot + low * p.val_row, left, static_cast<uint32_t>(p.val_row), static_cast<uint32_t>(wide));
+        const __amdgpu_buffer_rsrc_t rd = rows_of(dot + low * val_row, left, val_row, static_cast<uint32_t>(wide));
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint32_t at = at_row(16 * i + r, left, p.val_row, 2);
+          const uint32_t at = at_row(16 * i + r, left, val_row, 2);
           float d[4], s = 0.f;
 #pragma unroll
           for (int e = 0; e < 4; ++e) d[e] = to_f32(load_one<bf16_t>(rd, mo + e < wide ? at + 2 * (mo + e) : kOutside));
@@ -531,17 +639,19 @@ void la_bf16_kernel(LaArgs a, LaPasses all, int64_t items, int64_t sub, int64_t 
           sum += static_cast<double>(s);
         }
       } else {
-        auto store = [&](auto wide_type, bool full) {
-          constexpr int kSize = decltype(wide_type)::value;  // bytes of an element
-          char *out = static_cast<char *>(p.out) + kSize * (h * p.out_width + m0 + low * p.out_row);
+        auto store = [&](auto element, bool full) {
+          constexpr int kSize = decltype(element)::value;  // bytes of it
           const __amdgpu_buffer_rsrc_t ro = buffer_of(
-              out, kSize * (static_cast<uint32_t>(left - 1) * static_cast<uint32_t>(p.out_row) + static_cast<uint32_t>(wide)));
+              out + kSize * (low * out_row), kSize * (static_cast<uint32_t>(left - 1) * out_row + static_cast<uint32_t>(wide)));
+          const int row0 = static_cast<int>(full ? static_cast<uint32_t>(r) : hold(static_cast<uint32_t>(r)));
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            uint32_t at = at_row(16 * i + r, left, p.out_row, kSize), more = 0;
-            if (full) {  // one address a lane, and a step that all share
-              at = static_cast<uint32_t>(p.reverse ? 15 - r : r) * static_cast<uint32_t>(p.out_row) * kSize;
-              more = static_cast<uint32_t>(16 * (p.reverse ? 3 - i : i)) * static_cast<uint32_t>(p.out_row) * kSize;
+            uint32_t at, more = 0;
+            if (!full) {
+              at = at_row(16 * i + row0, left, out_row, kSize);
+            } else {  // one address a lane, and a step that all share
+              at = static_cast<uint32_t>(reverse ? 15 - row0 : row0) * out_row * kSize;
+              more = static_cast<uint32_t>(16 * (reverse ? 3 - i : i)) * out_row * kSize;
             }
             if constexpr (VEC && kSize == 4) {
               __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, y[i]), ro,
@@ -562,7 +672,7 @@ void la_bf16_kernel(LaArgs a, LaPasses all, int64_t items, int64_t sub, int64_t 
           }
         };
         auto sized = [&](bool full) {
-          if (p.out_f32) store(Number<4>(), full);
+          if (out_f32) store(Number<4>(), full);
           else store(Number<2>(), full);
         };
         if (left == C) sized(true);
@@ -571,18 +681,23 @@ void la_bf16_kernel(LaArgs a, LaPasses all, int64_t items, int64_t sub, int64_t 
     }
   };
 
-  // The factor of a chunk's decay, so that their product over the chunks so far is the
-  // decay's to 2^-25 (one rounded factor again and again drifts off).
-  const double decay = exp(log_a * C), inverse = decay > 1e-30 ? 1.0 / decay : 0.0;
-  double drift = 1.0;
+  // The factor of a chunk's decay, a^C = high + low (low no more than half a step of
+  // high): high, and a step more or less now and then, so that their product over the
+  // chunks so far is the decay's to 2^-24 (one rounded factor again and again drifts
+  // off).  owed: what the product lacks, as a part of itself.
+  const double decay = exp(log_a * C);
+  const float high = uniform(static_cast<float>(decay)), low = uniform(static_cast<float>(decay - high)),
+              inverse = uniform(high > 1e-30f ? 1.f / high : 0.f);
+  float owed = 0.f;
   if (z.len > 0) stage(0);
   __syncthreads();
 
   for (int t0 = 0, buf = 0; t0 < z.len; t0 += C, buf ^= 1) {
     const int left = z.len - t0 < C ? z.len - t0 : C;
-    load(t0 + C, buf ^ 1);
-    carry = static_cast<float>(decay * drift);
-    drift = fma(fma(decay, drift, -static_cast<double>(carry)), inverse, 1.0);
+    load(t0 + C, buf ^ 1, Y ? 0 : 3);
+    const float lack = fmaf(high, owed, low);
+    carry = high + lack;
+    owed = (lack - (carry - high)) * inverse;
     if (left < C) {
       weigh(left);
       carry = la_power(log_a, left);
@@ -594,7 +709,7 @@ void la_bf16_kernel(LaArgs a, LaPasses all, int64_t items, int64_t sub, int64_t 
     for (int tb = 0; tb < 2; ++tb)
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const u32x2 q = lds_transposed(lv + (buf ? kTileV : 0) + 2 * 8 * VP * (32 * tb + 16 * u));
+        const u32x2 q = lds_transposed(lv + 2 * 8 * VP * (32 * tb + 16 * u));
         v[tb][2 * u] = q[0];
         v[tb][2 * u + 1] = q[1];
       }
@@ -627,29 +742,55 @@ void la_bf16_kernel(LaArgs a, LaPasses all, int64_t items, int64_t sub, int64_t 
       chunk(t0, left, buf, v, bad, std::false_type());
     }
     meet_in_lds();
+    const uint32_t step = buf ? -kTile : kTile;  // to the other buffer
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) {
+      if constexpr (Y) {
+        lx[kb] += step;
+        lk[kb] += step;
+      }
+      lt[kb] += step;
+    }
+    lv += buf ? -kTileV : kTileV;
   }
 
-  // ---- the state behind the segment
+  // ---- the state behind the segment (its offsets are formed anew: those of the one
+  // that entered it would be kept in registers over the loop)
+  const int g_end = static_cast<int>(hold(static_cast<uint32_t>(g)));
   if (col) {
     if constexpr (!Y) {
-      const int64_t to = ((slot * a.H + h) * p.M + m) * Kp;
+      const int64_t to = ((slot * a.H + h) * p.M + m0) * Kp;
+      float *local = p.local + to, *local_tan = TAN ? p.local_tan + to : nullptr;
+      const int at = mc * Kp + 8 * g_end;
 #pragma unroll
-      for (int j = 0; j < 2 * KB; ++j)
-        if (n_of(j) < Kp) {
-          *reinterpret_cast<f32x4 *>(p.local + to + n_of(j)) = S[j];
-          if constexpr (TAN) *reinterpret_cast<f32x4 *>(p.local_tan + to + n_of(j)) = U[j];
+      for (int j = 0; j < 2 * KB; ++j) {
+        const int n = 32 * (j / 2) + 4 * (j % 2);
+        if (n + 8 * g_end < Kp) {
+          *reinterpret_cast<f32x4 *>(local + at + n) = S[j];
+          if constexpr (TAN) *reinterpret_cast<f32x4 *>(local_tan + at + n) = U[j];
         }
+      }
     } else if (z.last) {
-      const int64_t at = state0 + static_cast<int64_t>(m) * p.sm;
+      float *to = p.s_last != nullptr ? p.s_last + state0 : nullptr;
+      const float *dot = TAN && p.s_dot != nullptr ? p.s_dot + state0 : nullptr;
+      const int sn = static_cast<int>(p.sn), at = mc * static_cast<int>(p.sm) + 8 * g_end * sn;
+      if (!TAN && to != nullptr && fours_of(p, to)) {
+#pragma unroll
+        for (int j = 0; j < 2 * KB; ++j) {
+          const int n = 32 * (j / 2) + 4 * (j % 2);
+          if (n + 8 * g_end < p.K) *reinterpret_cast<f32x4 *>(to + at + n) = S[j];
+        }
+        return;
+      }
 #pragma unroll
       for (int j = 0; j < 2 * KB; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int n = n_of(j) + e;
-          if (n >= p.K) continue;
-          if (p.s_last != nullptr) p.s_last[at + n * p.sn] = S[j][e];
+          const int n = 32 * (j / 2) + 4 * (j % 2) + e;
+          if (n + 8 * g_end >= p.K) continue;
+          if (to != nullptr) to[at + n * sn] = S[j][e];
           if constexpr (TAN)
-            if (p.s_dot != nullptr) sum += static_cast<double>(U[j][e]) * p.s_dot[at + n * p.sn];
+            if (dot != nullptr) sum += static_cast<double>(U[j][e]) * dot[at + n * sn];
         }
     }
   }
