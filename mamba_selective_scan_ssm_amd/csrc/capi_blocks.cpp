@@ -68,17 +68,19 @@ bool by_step(int64_t L, bool packed) { return !packed && L > 0 && L <= kTokenSte
 
 // The backward's workspace, in bytes from its start.
 struct AttnBwdSpace {
-  ssm::LaArgs plan;
+  ssm::LaArgs qk, v, tan;              // how each of its launches is cut
   int64_t parts;                       // of P, of up to kPart
   int64_t dq, dk, dv, tan_s, tan_u;    // local states
   int64_t part_q, part_k, dot, bytes;  // partial gradients (0 wide: written at once)
   bool direct;
 };
-AttnBwdSpace attn_bwd_space(ssm::LaArgs a, int64_t H, int64_t P, int64_t G, int64_t N, bool decay) {
+AttnBwdSpace attn_bwd_space(const ssm::LaArgs &a, int64_t H, int64_t P, int64_t G, int64_t N, bool decay) {
   AttnBwdSpace w{};
   const int64_t cN = ssm::la_columns(N), cP = ssm::la_columns(P);
-  ssm::la_plan(a, 2 * cN + (decay ? 2 : 1) * cP);
-  w.plan = a;
+  w.qk = w.v = w.tan = a;
+  ssm::la_plan(w.qk, 2 * cN);
+  ssm::la_plan(w.v, cP);
+  ssm::la_plan(w.tan, cP);
   w.parts = (P + kPart - 1) / kPart;
   w.direct = G == H && w.parts == 1;
   int64_t at = 0;
@@ -87,18 +89,19 @@ AttnBwdSpace attn_bwd_space(ssm::LaArgs a, int64_t H, int64_t P, int64_t G, int6
     at += up(bytes);
     return from;
   };
-  const bool cut = ssm::la_cut(a);
-  const int64_t wide = P < kPart ? P : kPart;
-  const int64_t qk = cut ? ssm::la_local_floats(a, wide, N) * 4 : 0, v = cut ? ssm::la_local_floats(a, N, P) * 4 : 0;
+  auto local = [&](const ssm::LaArgs &a, int64_t K, int64_t M) {
+    return ssm::la_cut(a) ? ssm::la_local_floats(a, K, M) * 4 : 0;
+  };
+  const int64_t qk = local(w.qk, P < kPart ? P : kPart, N), tan = decay ? local(w.tan, N, P) : 0;
   w.dq = take(qk);
   w.dk = take(qk);
-  w.dv = take(v);
-  w.tan_s = take(decay ? v : 0);
-  w.tan_u = take(decay ? v : 0);
+  w.dv = take(local(w.v, N, P));
+  w.tan_s = take(tan);
+  w.tan_u = take(tan);
   const int64_t part = w.direct ? 0 : w.parts * a.T * H * N * 4;
   w.part_q = take(part);
   w.part_k = take(part);
-  w.dot = take(decay ? a.slots * H * cP * 8 : 0);
+  w.dot = take(decay ? w.tan.slots * H * cP * 8 : 0);
   w.bytes = at;
   return w;
 }
@@ -218,7 +221,7 @@ ssm_status ssm_linear_attn_bwd(int64_t B, int64_t L, int64_t H, int64_t P, int64
   hipStream_t s = static_cast<hipStream_t>(stream);
   char *ws = static_cast<char *>(workspace);
   auto floats = [&](int64_t at) { return reinterpret_cast<float *>(ws + at); };
-  const ssm::LaArgs &a = w.plan;
+  const ssm::LaArgs &a = w.qk;
   if (z.S == 0) return hip_status(dlog_decay ? ssm::launch_la_reduce_dot(nullptr, 0, H, 1, dlog_decay, s) : hipSuccess);
 
   const int32_t per = static_cast<int32_t>(H / G);
@@ -259,7 +262,7 @@ ssm_status ssm_linear_attn_bwd(int64_t B, int64_t L, int64_t H, int64_t P, int64
   p.sm = N; p.sn = 1;
   p.local = floats(w.dv);
   p.out = dv; p.out_row = H * P; p.out_width = P;
-  e = ssm::launch_la(a, &p, 1, s);
+  e = ssm::launch_la(w.v, &p, 1, s);
   if (e != hipSuccess) return hip_status(e);
   if (dlog_decay != nullptr) {
     p = attn_pass(rq, rk, rv, N, P);
@@ -269,9 +272,9 @@ ssm_status ssm_linear_attn_bwd(int64_t B, int64_t L, int64_t H, int64_t P, int64
     p.local = floats(w.tan_s); p.local_tan = floats(w.tan_u);
     p.dot = dy; p.s_dot = dh_final;
     p.dot_sum = reinterpret_cast<double *>(ws + w.dot);
-    e = ssm::launch_la(a, &p, 1, s);
+    e = ssm::launch_la(w.tan, &p, 1, s);
     if (e == hipSuccess)
-      e = ssm::launch_la_reduce_dot(p.dot_sum, a.slots, H, ssm::la_columns(P), dlog_decay, s);
+      e = ssm::launch_la_reduce_dot(p.dot_sum, w.tan.slots, H, ssm::la_columns(P), dlog_decay, s);
     if (e != hipSuccess) return hip_status(e);
   }
   if (!w.direct) {

@@ -807,15 +807,20 @@ void la_bf16_kernel(LaArgs a, LaPasses all, int64_t items, int64_t sub, int64_t 
   }
 }
 
-template <int KB, int W, bool SHARE, bool TAN, bool VEC>
-hipError_t launch_kb(const LaArgs &a, const LaPasses &all, int n, hipStream_t s) {
-  constexpr int kThreads = 64 * W;
+template <int KB, int W, bool SHARE, bool Y, bool TAN, bool VEC>
+hipError_t launch_one(const LaArgs &a, const LaPasses &all, int n, hipStream_t s) {
   const int64_t cols = (all.p[0].M + 16 * W - 1) / (16 * W);
   const int64_t sub = la_sub(a, all.p[0].x_per, cols);
-  return la_launches(a, cols, sub, n, [&](dim3 grid, bool y, int64_t items, int64_t base) {
-    if (y) la_bf16_kernel<KB, W, SHARE, true, TAN, VEC><<<grid, kThreads, 0, s>>>(a, all, items, sub, base);
-    else la_bf16_kernel<KB, W, SHARE, false, TAN, VEC><<<grid, kThreads, 0, s>>>(a, all, items, sub, base);
+  return la_launches(a, cols, sub, n, [&](dim3 grid, int64_t items, int64_t base) {
+    la_bf16_kernel<KB, W, SHARE, Y, TAN, VEC><<<grid, 64 * W, 0, s>>>(a, all, items, sub, base);
   });
+}
+// The segments' own additions where the sequences are cut, by workgroups of four waves:
+// all but the last segment of a sequence have some, so they are few.
+template <int KB, int W, bool SHARE, bool TAN, bool VEC>
+hipError_t launch_kb(const LaArgs &a, const LaPasses &all, int n, hipStream_t s) {
+  const hipError_t e = la_cut(a) ? launch_one<KB, 4, false, false, TAN, VEC>(a, all, n, s) : hipSuccess;
+  return e != hipSuccess ? e : launch_one<KB, W, SHARE, true, TAN, VEC>(a, all, n, s);
 }
 
 // 16-byte pieces of every row, head and output

@@ -94,21 +94,20 @@ inline int64_t la_sub(const LaArgs &a, int64_t per, int64_t cols) {
   const int64_t heads = a.slots * a.H;
   return heads / per >= 64 ? per * cols : heads >= 64 ? cols : 1;
 }
-// The launches of n passes over all workgroups: the segments' own additions first
-// where the sequences are cut.  A grid stays below 2^32 threads.
+// n passes over all workgroups of `cols` columns each, in grids below 2^32 threads.
 struct LaPasses {
   LaPass p[3];
 };
 template <typename F>
 hipError_t la_launches(const LaArgs &a, int64_t cols, int64_t sub, int n, F &&launch) {
+  // at most 65535 heads, of 2^24 channels together: sub stays below 2^18 + 2^16
   const int64_t items = a.slots * a.H * cols, most = (int64_t{1} << 22) / (8 * sub) * (8 * sub);
-  for (int y = la_cut(a) ? 0 : 1; y < 2; ++y)
-    for (int64_t base = 0; base < items; base += most) {
-      const int64_t now = items - base < most ? items - base : most, units = (now + sub - 1) / sub;
-      launch(dim3(static_cast<unsigned>((units + 7) / 8 * 8 * sub), static_cast<unsigned>(n)), y == 1, items, base);
-      const hipError_t e = hipGetLastError();
-      if (e != hipSuccess) return e;
-    }
+  for (int64_t base = 0; base < items; base += most) {
+    const int64_t now = items - base < most ? items - base : most, units = (now + sub - 1) / sub;
+    launch(dim3(static_cast<unsigned>((units + 7) / 8 * 8 * sub), static_cast<unsigned>(n)), items, base);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
   return hipSuccess;
 }
 

@@ -311,10 +311,14 @@ __global__ __launch_bounds__(kThreads) void la_f32_kernel(LaArgs a, LaPasses all
 
 template <typename T, int KT, int C, bool TAN, bool VEC>
 hipError_t launch_kt(const LaArgs &a, const LaPasses &all, int n, int64_t cols, int64_t sub, hipStream_t s) {
-  return la_launches(a, cols, sub, n, [&](dim3 grid, bool y, int64_t items, int64_t base) {
-    if (y) la_f32_kernel<T, KT, C, true, TAN, VEC><<<grid, kThreads, 0, s>>>(a, all, items, sub, base);
-    else la_f32_kernel<T, KT, C, false, TAN, VEC><<<grid, kThreads, 0, s>>>(a, all, items, sub, base);
-  });
+  for (int y = la_cut(a) ? 0 : 1; y < 2; ++y) {
+    const hipError_t e = la_launches(a, cols, sub, n, [&](dim3 grid, int64_t items, int64_t base) {
+      if (y) la_f32_kernel<T, KT, C, true, TAN, VEC><<<grid, kThreads, 0, s>>>(a, all, items, sub, base);
+      else la_f32_kernel<T, KT, C, false, TAN, VEC><<<grid, kThreads, 0, s>>>(a, all, items, sub, base);
+    });
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 template <typename T>
