@@ -190,7 +190,7 @@ def _stream(device):
 
 
 def _call(fn_name, *args):
-    rc = getattr(lib(), fn_name)(*args)
+    rc = getattr(_lib or lib(), fn_name)(*args)
     if rc != 0:
         raise SSMError(fn_name, rc)
 
@@ -710,12 +710,14 @@ def group_norm_bwd(x, groups, dy, mean, rstd, weight=None, bias=None, z=None, *,
 def _attn_inputs(q, k, v, log_decay, cu_seqlens):
     if q.dim() != 4 or v.dim() != 4:
         raise ValueError("q must be (B, L, G, N) and v (B, L, H, P)")
-    B, L, G, N = q.shape
-    H, P = v.shape[2], v.shape[3]
+    shape = q.shape
+    B, L, G, N = shape
+    H, P = v.shape[2:]
     dev, typ = q.device, q.dtype
-    code = _dtype_code(q)
-    _check("q", q, (B, L, G, N), typ, dev)
-    _check("k", k, (B, L, G, N), typ, dev)
+    code = _code_of(typ)
+    if not q.is_contiguous():
+        raise ValueError("q must be contiguous")
+    _check("k", k, shape, typ, dev)
     _check("v", v, (B, L, H, P), typ, dev)
     _check("log_decay", log_decay, (H,), torch.float32, dev)
     n_seqs = 0
@@ -747,11 +749,13 @@ def linear_attn_fwd(q, k, v, log_decay, h0=None, *, scale=None, cu_seqlens=None,
     states = (n_seqs if packed else B, H, P, N)
     _check("h0", h0, states, torch.float32, dev)
     if y is None:
-        y = torch.empty((B, L, H, P), dtype=typ, device=dev)
-    _check("y", y, (B, L, H, P), typ, dev)
-    if h_final is None and return_final:
+        y = torch.empty_like(v)
+    else:
+        _check("y", y, (B, L, H, P), typ, dev)
+    if h_final is not None:
+        _check("h_final", h_final, states, torch.float32, dev)
+    elif return_final:
         h_final = torch.empty(states, dtype=torch.float32, device=dev)
-    _check("h_final", h_final, states, torch.float32, dev)
     need = int(lib().ssm_linear_attn_fwd_workspace_size(*sizes, code, int(packed), n_seqs))
     workspace, ws_len = _workspace(workspace, need, dev)
     _gpu_call(dev, "ssm_linear_attn_fwd", *sizes, code, _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(h0),
@@ -784,8 +788,9 @@ def linear_attn_decode_steps(state_pool, q, k, v, log_decay, *, slots=None, scal
     _check("state_pool", state_pool, (rows, H, P, N), torch.float32, dev)
     _check("slots", slots, (S,), torch.int32, dev)
     if y is None:
-        y = torch.empty((S, T, H, P), dtype=typ, device=dev)
-    _check("y", y, (S, T, H, P), typ, dev)
+        y = torch.empty_like(v)
+    else:
+        _check("y", y, (S, T, H, P), typ, dev)
     _gpu_call(dev, "ssm_linear_attn_decode_steps", *sizes, code, _ptr(state_pool), rows, _ptr(slots), _ptr(q), _ptr(k),
               _ptr(v), _ptr(log_decay), _scale(scale, N), _ptr(y))
     return y
@@ -839,34 +844,40 @@ def add_rms_norm_fwd(x, residual=None, weight=None, *, eps=1e-5, quant=None, qua
     if quant not in _QUANT:
         raise ValueError(f"quant must be None, 'e4m3' or 'int8', got {quant!r}")
     shape, dev, typ = x.shape, x.device, x.dtype
-    code = _dtype_code(x)
+    code = _code_of(typ)
     lead, D = shape[:-1], shape[-1]
     rows = lead.numel()
-    _check("x", x, shape, typ, dev)
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
     _check("weight", weight, (D,), torch.float32, dev)
-    stream = typ if residual is None else residual.dtype
-    stream_code = code if residual is None else _dtype_code(residual)
-    _check("residual", residual, shape, stream, dev)
     if residual is None:
         if h is not None:
             raise ValueError("h is given without a residual: it would be x")
-    elif h is None:
-        h = torch.empty_like(residual)
-    _check("h", h, shape, stream, dev)
+        stream_code = code
+    else:
+        stream = residual.dtype
+        stream_code = code if stream == typ else _code_of(stream)
+        _check("residual", residual, shape, stream, dev)
+        if h is None:
+            h = torch.empty_like(residual)
+        elif h is not residual:
+            _check("h", h, shape, stream, dev)
     mode, kind = _QUANT[quant]
-    quant_group = int(quant_group)
-    if quant is None and (quant_group != 0 or scale is not None):
-        raise ValueError("quant_group and scale belong to an output in 8 bits (quant)")
-    if y is None:
-        y = torch.empty(shape, dtype=kind or typ, device=dev)
-    _check("y", y, shape, kind or typ, dev)
     if mode:
+        quant_group = int(quant_group)
         if quant_group < 0 or (quant_group > 0 and D % quant_group != 0):
             raise ValueError(f"quant_group {quant_group} does not divide the {D} channels")
         groups = (*lead, D // quant_group if quant_group else 1)
         if scale is None:
             scale = torch.empty(groups, dtype=torch.float32, device=dev)
-        _check("scale", scale, groups, torch.float32, dev)
+        else:
+            _check("scale", scale, groups, torch.float32, dev)
+    elif quant_group != 0 or scale is not None:
+        raise ValueError("quant_group and scale belong to an output in 8 bits (quant)")
+    if y is not None:
+        _check("y", y, shape, kind or typ, dev)
+    else:
+        y = torch.empty(shape, dtype=kind, device=dev) if mode else torch.empty_like(x)
     rstd = torch.empty(lead, dtype=torch.float32, device=dev) if return_rstd else None
     _gpu_call(dev, "ssm_add_rms_norm_fwd", rows, D, code, stream_code, _ptr(x), _ptr(residual), _ptr(weight),
               float(eps), mode, quant_group, _ptr(h), _ptr(y), _ptr(scale), _ptr(rstd))

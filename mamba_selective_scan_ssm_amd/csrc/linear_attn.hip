@@ -150,14 +150,20 @@ __global__ __launch_bounds__(kThreads) void la_reduce_dot_kernel(const double *p
 }  // namespace
 
 void la_plan(LaArgs &a, int64_t columns) {
-  constexpr int64_t kWanted = 2 * kCus, kLeast = 256;
+  // As many segments as give each CU two workgroups of 64 columns (or one of 128), of
+  // 64 tokens and more in fp32 and of 256 in bf16, whose kernel takes longer to begin.
+  // At least 256 / 128 / 64 tokens: fp32, 2048 tokens of 24 heads of 64 x 64 86 / 69 / 69
+  // us, gradients of 1031 tokens of 6 heads of 40 x 48 251 / 158 / 120; bf16, gradients
+  // of 2048 tokens of 16 heads of 64 x 128 95 / 98 / 123.  Twice as many segments: bf16,
+  // 2 x 8192 tokens, 64 heads of 128 x 128 403 -> 437 us, 4096 tokens, 32 heads 78 -> 111.
+  constexpr int64_t kWanted = 2 * kCus;
+  const int64_t least = a.dt_type == DType::F32 ? 64 : 256;
   const int64_t longest = a.L < 0 ? a.T : a.L;
   a.seg_len = longest > 0 ? longest : 1;
   a.slots = a.S;
-  // As many segments as give each CU two workgroups, of 256 tokens and more.
   if (a.S <= 0 || (a.L >= 0 && a.S * a.H * columns * 4 >= kWanted * 3)) return;
   int64_t len = (a.T * a.H * columns + kWanted - 1) / kWanted;
-  len = len < kLeast ? kLeast : (len + 63) / 64 * 64;
+  len = len < least ? least : (len + 63) / 64 * 64;
   if (len >= longest) return;
   a.seg_len = len;
   a.slots = a.L < 0 ? a.T / len + a.S : a.S * ((a.L + len - 1) / len);
