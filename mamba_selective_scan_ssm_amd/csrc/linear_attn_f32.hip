@@ -124,27 +124,48 @@ __global__ __launch_bounds__(kThreads) void la_f32_kernel(LaArgs a, LaPasses all
   const T *dot = TAN ? static_cast<const T *>(p.dot) + h / p.val_per * p.val_width : nullptr;
   double sum = 0.0;
 
+  // ---- x, keys and values of the next chunk, on their way in registers; zeros behind
+  // the last token and width
+  constexpr int kFours = C * 4 * KT / kThreads, kFoursV = C * kColumns / 4 / kThreads;
+  f32x4 px[Y ? kFours : 1], pk[kFours], pv[kFoursV];
+  auto row_of = [&](int t) { return z.first + static_cast<int64_t>(t) * z.step; };
+  auto load = [&](int t0) {
+    const int left = z.len - t0 < C ? z.len - t0 : C;
+#pragma unroll
+    for (int i = 0; i < kFours; ++i) {
+      const int q = tid + kThreads * i, t = q / (4 * KT), n = q % (4 * KT) * 4;
+      const int have = t < left ? p.K - n : 0;
+      const int64_t row = have > 0 ? row_of(t0 + t) : 0;
+      if constexpr (Y) px[i] = load_four<T, VEC>(x + row * p.x_row + n, have);
+      pk[i] = load_four<T, VEC>(key + row * p.key_row + n, have);
+    }
+#pragma unroll
+    for (int i = 0; i < kFoursV; ++i) {
+      const int q = tid + kThreads * i, t = q / (kColumns / 4), n = q % (kColumns / 4) * 4;
+      const int have = t < left ? p.M - m0 - n : 0;
+      const int64_t row = have > 0 ? row_of(t0 + t) : 0;
+      pv[i] = load_four<T, VEC>(val + row * p.val_row + m0 + n, have);
+    }
+  };
+  if (z.len > 0) load(0);
+
   const LaCarry full(log_a, C);
   for (int t0 = 0; t0 < z.len; t0 += C) {
     const int left = z.len - t0 < C ? z.len - t0 : C;
     __syncthreads();
-    // ---- x, keys and values into LDS; zeros behind the last token and width
-    auto row_of = [&](int i) { return z.first + static_cast<int64_t>(t0 + i) * z.step; };
-    for (int i = tid; i < C * 4 * KT; i += kThreads) {
-      const int t = i / (4 * KT), n = i % (4 * KT) * 4;
-      const int have = t < left ? p.K - n : 0;
-      const int64_t row = have > 0 ? row_of(t) : 0;
-      if constexpr (Y)
-        *reinterpret_cast<f32x4 *>(&s_x[t][n]) = load_four<T, VEC>(x + row * p.x_row + n, have);
-      *reinterpret_cast<f32x4 *>(&s_k[t][n]) = load_four<T, VEC>(key + row * p.key_row + n, have);
+#pragma unroll
+    for (int i = 0; i < kFours; ++i) {
+      const int q = tid + kThreads * i, t = q / (4 * KT), n = q % (4 * KT) * 4;
+      if constexpr (Y) *reinterpret_cast<f32x4 *>(&s_x[t][n]) = px[i];
+      *reinterpret_cast<f32x4 *>(&s_k[t][n]) = pk[i];
     }
-    for (int i = tid; i < C * kColumns / 4; i += kThreads) {
-      const int t = i / (kColumns / 4), n = i % (kColumns / 4) * 4;
-      const int have = t < left ? p.M - m0 - n : 0;
-      const int64_t row = have > 0 ? row_of(t) : 0;
-      *reinterpret_cast<f32x4 *>(&s_v[t][n]) = load_four<T, VEC>(val + row * p.val_row + m0 + n, have);
+#pragma unroll
+    for (int i = 0; i < kFoursV; ++i) {
+      const int q = tid + kThreads * i, t = q / (kColumns / 4), n = q % (kColumns / 4) * 4;
+      *reinterpret_cast<f32x4 *>(&s_v[t][n]) = pv[i];
     }
     __syncthreads();
+    if (t0 + C < z.len) load(t0 + C);
 
     // ---- scores, from the diagonal down, tile by tile
     if constexpr (Y) {
@@ -221,9 +242,9 @@ __global__ __launch_bounds__(kThreads) void la_f32_kernel(LaArgs a, LaPasses all
           const float out = t >= bad ? __builtin_nanf("") : c_out * y[i][e];
           if (t < left && col) {
             if constexpr (TAN) {
-              sum += static_cast<double>(out) * to_f32(dot[row_of(t) * p.val_row + m]);
+              sum += static_cast<double>(out) * to_f32(dot[row_of(t0 + t) * p.val_row + m]);
             } else {
-              const int64_t o = row_of(t) * p.out_row + h * p.out_width + m;
+              const int64_t o = row_of(t0 + t) * p.out_row + h * p.out_width + m;
               if (p.out_f32) static_cast<float *>(p.out)[o] = out;
               else static_cast<T *>(p.out)[o] = from_f32<T>(out);
             }
@@ -343,8 +364,8 @@ hipError_t launch_type(const LaArgs &a, const LaPass *p, int n, hipStream_t s) {
 #define SSM_LA_KT(KT, C)                                                        \
   return vec ? launch_kt<T, KT, C, TAN, true>(a, all, n, cols, sub, s)          \
              : launch_kt<T, KT, C, TAN, false>(a, all, n, cols, sub, s)
-  if (p[0].K <= 64) SSM_LA_KT(4, 64);
-  if (p[0].K <= 128) SSM_LA_KT(8, 64);
+  if (p[0].K <= 64) SSM_LA_KT(4, 32);
+  if (p[0].K <= 128) SSM_LA_KT(8, 32);
   SSM_LA_KT(16, 32);
 #undef SSM_LA_KT
 }
