@@ -435,9 +435,48 @@ void la_bf16_kernel(LaArgs a, LaPasses all, int64_t items, int64_t sub, int64_t 
     split_parts<3>(t[0], t[1], out);
   };
 
-  // One chunk from buffer buf.  CLEAN: all values are finite.
-  auto chunk = [&](int t0, int left, int buf, u32x4 (&v)[2], int bad, auto clean) {
-    constexpr bool CLEAN = decltype(clean)::value;
+  // One chunk from buffer buf.
+  auto chunk = [&](int t0, int left, int buf) {
+    // ---- this wave's values, transposed: tokens 32 tb + 16 u + 4 g + e of column r
+    u32x4 v[2], wv[2][3];
+#pragma unroll
+    for (int tb = 0; tb < 2; ++tb)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const u32x2 q = lds_transposed(lv + 2 * 8 * VP * (32 * tb + 16 * u));
+        v[tb][2 * u] = q[0];
+        v[tb][2 * u + 1] = q[1];
+      }
+    // Those that are not finite are left out of the products; their column's outputs and
+    // state are set from their token `bad` on.
+    int bad = C;
+    bool dirty = false;
+    auto check = [&] {
+      typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+      u16x2 top = {0, 0};
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, v[i / 4][i % 4] & 0x7fff7fffu));
+      dirty = __ballot(top[0] >= 0x7f80 || top[1] >= 0x7f80) != 0;
+      if (!dirty) return;
+#pragma unroll
+      for (int i = 7; i >= 0; --i) {
+        uint32_t q = v[i / 4][i % 4];
+        const int t = 32 * (i / 4) + 16 * (i % 4 / 2) + 4 * g + 2 * (i % 2);
+        if ((q >> 16 & 0x7f80) == 0x7f80) {
+          bad = min(bad, t + 1);
+          q &= 0xffffu;
+        }
+        if ((q & 0x7f80) == 0x7f80) {
+          bad = min(bad, t);
+          q &= 0xffff0000u;
+        }
+        v[i / 4][i % 4] = q;
+      }
+      bad = min(bad, __shfl_xor(bad, 16));
+      bad = min(bad, __shfl_xor(bad, 32));
+    };
+    if constexpr (Y && !SHARE) check();
     f32x4 y[Y ? 4 : 1], yu[TAN ? 4 : 1];
     if constexpr (Y) {
       if constexpr (SHARE) {
@@ -484,6 +523,7 @@ void la_bf16_kernel(LaArgs a, LaPasses all, int64_t items, int64_t sub, int64_t 
 #pragma unroll
           for (int e = 0; e < 4; ++e) y[i][e] *= w_out[i];
         load(t0 + C, buf ^ 1, 2);
+        check();
         meet_in_lds();
         // ---- the values under the scores
 #pragma unroll
@@ -574,12 +614,12 @@ void la_bf16_kernel(LaArgs a, LaPasses all, int64_t items, int64_t sub, int64_t 
 #pragma unroll
         for (int e = 0; e < 4; ++e) U[j][e] = fmaf(n_left, S[j][e], carry * U[j][e]);
     }
-    u32x4 wv[3], wu[3];
+    u32x4 wu[3];
 #pragma unroll
     for (int i = 0; i < 2 * KB; ++i) {
       const int tb = i / KB, kb = i % KB;
       if (kb == 0) {
-        weighted(v[tb], tb, left, wv, false);
+        weighted(v[tb], tb, left, wv[tb], false);
         if constexpr (TAN) weighted(v[tb], tb, left, wu, true);
       }
       __builtin_amdgcn_sched_barrier(0);
@@ -593,12 +633,12 @@ void la_bf16_kernel(LaArgs a, LaPasses all, int64_t items, int64_t sub, int64_t 
       for (int q = 0; q < 3; ++q)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          S[2 * kb + u] = mma(kt[i % 2][u], wv[q], S[2 * kb + u]);
+          S[2 * kb + u] = mma(kt[i % 2][u], wv[tb][q], S[2 * kb + u]);
           if constexpr (TAN) U[2 * kb + u] = mma(kt[i % 2][u], wu[q], U[2 * kb + u]);
         }
     }
     __builtin_amdgcn_sched_barrier(0);
-    if constexpr (!CLEAN) {
+    if (dirty) {
       if (bad < C) {
 #pragma unroll
         for (int j = 0; j < 2 * KB; ++j)
@@ -614,7 +654,7 @@ void la_bf16_kernel(LaArgs a, LaPasses all, int64_t items, int64_t sub, int64_t 
     if (t0 + C < z.len) stage(buf ^ 1);
     if constexpr (Y) {
       // ---- out: channels 4 g .. + 3 of token 16 i + r
-      if constexpr (!CLEAN) {
+      if (dirty) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int from = __shfl(bad, 4 * g + e);
@@ -703,44 +743,7 @@ void la_bf16_kernel(LaArgs a, LaPasses all, int64_t items, int64_t sub, int64_t 
       carry = la_power(log_a, left);
       n_left = static_cast<float>(left) * carry;
     }
-    // ---- this wave's values, transposed: tokens 32 tb + 16 u + 4 g + e of column r
-    u32x4 v[2];
-#pragma unroll
-    for (int tb = 0; tb < 2; ++tb)
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const u32x2 q = lds_transposed(lv + 2 * 8 * VP * (32 * tb + 16 * u));
-        v[tb][2 * u] = q[0];
-        v[tb][2 * u + 1] = q[1];
-      }
-    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
-    u16x2 top = {0, 0};
-    if constexpr (Y)  // (the state's own column is not finite then, as it should be)
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, v[i / 4][i % 4] & 0x7fff7fffu));
-    int bad = C;
-    if (!Y || __ballot(top[0] >= 0x7f80 || top[1] >= 0x7f80) == 0) {
-      chunk(t0, left, buf, v, bad, std::true_type());
-    } else {  // those that are not finite are left out of the products
-#pragma unroll
-      for (int i = 7; i >= 0; --i) {
-        uint32_t q = v[i / 4][i % 4];
-        const int t = 32 * (i / 4) + 16 * (i % 4 / 2) + 4 * g + 2 * (i % 2);
-        if ((q >> 16 & 0x7f80) == 0x7f80) {
-          bad = min(bad, t + 1);
-          q &= 0xffffu;
-        }
-        if ((q & 0x7f80) == 0x7f80) {
-          bad = min(bad, t);
-          q &= 0xffff0000u;
-        }
-        v[i / 4][i % 4] = q;
-      }
-      bad = min(bad, __shfl_xor(bad, 16));
-      bad = min(bad, __shfl_xor(bad, 32));
-      chunk(t0, left, buf, v, bad, std::false_type());
-    }
+    chunk(t0, left, buf);
     meet_in_lds();
     const uint32_t step = buf ? -kTile : kTile;  // to the other buffer
 #pragma unroll
