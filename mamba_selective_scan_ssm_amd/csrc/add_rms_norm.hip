@@ -20,20 +20,28 @@ constexpr int64_t kCus = 256;
 constexpr int kLeastGroup = kAddNormLeastGroup;
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 
-// Eight channels from n on of a row; those behind D are 0.
-template <typename T, bool VEC>
-__device__ __forceinline__ void load8(const T *row, int n, int D, float *v) {
+// Channel e of a thread's piece i: pieces are eight consecutive channels where rows are
+// whole 16 bytes (VEC), else a channel of each thread after another's, so that a wave's
+// single elements lie side by side all the same.
+template <bool VEC, int THREADS>
+__device__ __forceinline__ int channel_of(int tid, int i, int e) {
+  return VEC ? 8 * (tid + THREADS * i) + e : tid + THREADS * (8 * i + e);
+}
+// A piece of a row; channels behind D are 0.
+template <typename T, bool VEC, int THREADS>
+__device__ __forceinline__ void load8(const T *row, int tid, int i, int D, float *v) {
   if constexpr (VEC) {  // D is a multiple of 8
     struct alignas(16) Raw {
       T v[16 / sizeof(T)];
     };
     constexpr int kEach = 16 / sizeof(T);
+    const int n = channel_of<VEC, THREADS>(tid, i, 0);
     if (n < D) {
 #pragma unroll
-      for (int i = 0; i < 8 / kEach; ++i) {
-        const Raw x = *reinterpret_cast<const Raw *>(row + n + i * kEach);
+      for (int q = 0; q < 8 / kEach; ++q) {
+        const Raw x = *reinterpret_cast<const Raw *>(row + n + q * kEach);
 #pragma unroll
-        for (int e = 0; e < kEach; ++e) v[i * kEach + e] = to_f32(x.v[e]);
+        for (int e = 0; e < kEach; ++e) v[q * kEach + e] = to_f32(x.v[e]);
       }
       return;
     }
@@ -41,28 +49,34 @@ __device__ __forceinline__ void load8(const T *row, int n, int D, float *v) {
     for (int e = 0; e < 8; ++e) v[e] = 0.f;
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = n + e < D ? to_f32(row[n + e]) : 0.f;
+    for (int e = 0; e < 8; ++e) {
+      const int n = channel_of<VEC, THREADS>(tid, i, e);
+      v[e] = n < D ? to_f32(row[n]) : 0.f;
+    }
   }
 }
-template <typename T, bool VEC>
-__device__ __forceinline__ void store8(T *row, int n, int D, const float *v) {
+template <typename T, bool VEC, int THREADS>
+__device__ __forceinline__ void store8(T *row, int tid, int i, int D, const float *v) {
   if constexpr (VEC) {
+    const int n = channel_of<VEC, THREADS>(tid, i, 0);
     if (n >= D) return;
     constexpr int kEach = 16 / sizeof(T);
     struct alignas(16) Raw {
       T v[kEach];
     };
 #pragma unroll
-    for (int i = 0; i < 8 / kEach; ++i) {
+    for (int q = 0; q < 8 / kEach; ++q) {
       Raw x;
 #pragma unroll
-      for (int e = 0; e < kEach; ++e) x.v[e] = from_f32<T>(v[i * kEach + e]);
-      *reinterpret_cast<Raw *>(row + n + i * kEach) = x;
+      for (int e = 0; e < kEach; ++e) x.v[e] = from_f32<T>(v[q * kEach + e]);
+      *reinterpret_cast<Raw *>(row + n + q * kEach) = x;
     }
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (n + e < D) row[n + e] = from_f32<T>(v[e]);
+    for (int e = 0; e < 8; ++e) {
+      const int n = channel_of<VEC, THREADS>(tid, i, e);
+      if (n < D) row[n] = from_f32<T>(v[e]);
+    }
   }
 }
 
@@ -96,8 +110,8 @@ __device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d
 }
 
 // Eight values times inv, in 8 bits: to nearest even, NaN to NaN (e4m3) or 0 (int8).
-template <bool VEC>
-__device__ __forceinline__ void store8_quant(uint8_t *row, int n, int D, const float *v, float inv, bool e4m3) {
+template <bool VEC, int THREADS>
+__device__ __forceinline__ void store8_quant(uint8_t *row, int tid, int piece, int D, const float *v, float inv, bool e4m3) {
   uint32_t q[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -117,11 +131,14 @@ __device__ __forceinline__ void store8_quant(uint8_t *row, int n, int D, const f
     }
   }
   if constexpr (VEC) {
+    const int n = channel_of<VEC, THREADS>(tid, piece, 0);
     if (n < D) *reinterpret_cast<u32x2_t *>(row + n) = u32x2_t{q[0], q[1]};
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (n + e < D) row[n + e] = static_cast<uint8_t>(q[e / 4] >> (8 * (e % 4)));
+    for (int e = 0; e < 8; ++e) {
+      const int n = channel_of<VEC, THREADS>(tid, piece, e);
+      if (n < D) row[n] = static_cast<uint8_t>(q[e / 4] >> (8 * (e % 4)));
+    }
   }
 }
 
@@ -151,9 +168,8 @@ __global__ __launch_bounds__(THREADS == 64 ? 256 : THREADS) void add_norm_kernel
   float w[NP][8];
 #pragma unroll
   for (int i = 0; i < NP; ++i) {
-    const int n = 8 * (tid + THREADS * i);
     if (a.w != nullptr) {
-      load8<float, VEC>(a.w, n, D, w[i]);
+      load8<float, VEC, THREADS>(a.w, tid, i, D, w[i]);
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) w[i][e] = 1.f;
@@ -165,17 +181,17 @@ __global__ __launch_bounds__(THREADS == 64 ? 256 : THREADS) void add_norm_kernel
     float v[NP][8];
     float ss = 0.f;
 #pragma unroll
-    for (int i = 0; i < NP; ++i) load8<X, VEC>(x + at, 8 * (tid + THREADS * i), D, v[i]);
+    for (int i = 0; i < NP; ++i) load8<X, VEC, THREADS>(x + at, tid, i, D, v[i]);
     if (res != nullptr) {
       float o[NP][8];
 #pragma unroll
-      for (int i = 0; i < NP; ++i) load8<H, VEC>(res + at, 8 * (tid + THREADS * i), D, o[i]);
+      for (int i = 0; i < NP; ++i) load8<H, VEC, THREADS>(res + at, tid, i, D, o[i]);
       // h may be the residual itself: it is written where it has been read
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[i][e] = to_f32(from_f32<H>(v[i][e] + o[i][e]));
-        store8<H, VEC>(static_cast<H *>(a.h) + at, 8 * (tid + THREADS * i), D, v[i]);
+        store8<H, VEC, THREADS>(static_cast<H *>(a.h) + at, tid, i, D, v[i]);
       }
     }
 #pragma unroll
@@ -190,7 +206,7 @@ __global__ __launch_bounds__(THREADS == 64 ? 256 : THREADS) void add_norm_kernel
       for (int e = 0; e < 8; ++e) v[i][e] = v[i][e] * r * w[i][e];
     if constexpr (QUANT == 0) {
 #pragma unroll
-      for (int i = 0; i < NP; ++i) store8<X, VEC>(static_cast<X *>(a.y) + at, 8 * (tid + THREADS * i), D, v[i]);
+      for (int i = 0; i < NP; ++i) store8<X, VEC, THREADS>(static_cast<X *>(a.y) + at, tid, i, D, v[i]);
     } else {
       uint8_t *q = static_cast<uint8_t *>(a.y) + at;
       float *scale = a.scale + row * groups;
@@ -212,18 +228,20 @@ __global__ __launch_bounds__(THREADS == 64 ? 256 : THREADS) void add_norm_kernel
         for (int i = 0; i < NP; ++i)
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const int n = 8 * (tid + THREADS * i) + e;
+            const int n = channel_of<VEC, THREADS>(tid, i, e);
             if (n < D) atomicMax(&s_max[n / group], __float_as_uint(v[i][e]) & 0x7fffffffu);
           }
         __syncthreads();
         for (int i = tid; i < groups; i += THREADS) scale[i] = scale_of(s_max[i], most);
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
-          const int n = 8 * (tid + THREADS * i);
           float u[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) u[e] = n + e < D ? v[i][e] / scale_of(s_max[(n + e) / group], most) : 0.f;
-          store8_quant<VEC>(q, n, D, u, 1.f, e4m3);
+          for (int e = 0; e < 8; ++e) {
+            const int n = channel_of<VEC, THREADS>(tid, i, e);
+            u[e] = n < D ? v[i][e] / scale_of(s_max[n / group], most) : 0.f;
+          }
+          store8_quant<VEC, THREADS>(q, tid, i, D, u, 1.f, e4m3);
         }
       } else if (groups == 1) {
         uint32_t all = top[0];
@@ -240,7 +258,7 @@ __global__ __launch_bounds__(THREADS == 64 ? 256 : THREADS) void add_norm_kernel
         const float sc = scale_of(all, most);
         if (tid == 0) scale[0] = sc;
 #pragma unroll
-        for (int i = 0; i < NP; ++i) store8_quant<VEC>(q, 8 * (tid + THREADS * i), D, v[i], 1.f / sc, e4m3);
+        for (int i = 0; i < NP; ++i) store8_quant<VEC, THREADS>(q, tid, i, D, v[i], 1.f / sc, e4m3);
       } else {
         const int span = group / 8;
 #pragma unroll
@@ -248,7 +266,7 @@ __global__ __launch_bounds__(THREADS == 64 ? 256 : THREADS) void add_norm_kernel
           const int piece = tid + THREADS * i;
           const float sc = scale_of(lanes_max(top[i], span), most);
           if (piece % span == 0 && 8 * piece < D) scale[piece / span] = sc;
-          store8_quant<VEC>(q, 8 * piece, D, v[i], 1.f / sc, e4m3);
+          store8_quant<VEC, THREADS>(q, tid, i, D, v[i], 1.f / sc, e4m3);
         }
       }
     }
@@ -266,9 +284,8 @@ __global__ __launch_bounds__(THREADS == 64 ? 256 : THREADS) void add_norm_bwd_ke
   float w[NP][8], dw[NP][8];
 #pragma unroll
   for (int i = 0; i < NP; ++i) {
-    const int n = 8 * (tid + THREADS * i);
     if (a.w != nullptr) {
-      load8<float, VEC>(a.w, n, D, w[i]);
+      load8<float, VEC, THREADS>(a.w, tid, i, D, w[i]);
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) w[i][e] = 1.f;
@@ -283,9 +300,8 @@ __global__ __launch_bounds__(THREADS == 64 ? 256 : THREADS) void add_norm_bwd_ke
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-      const int n = 8 * (tid + THREADS * i);
-      load8<H, VEC>(h + at, n, D, hv[i]);
-      load8<X, VEC>(dy + at, n, D, u[i]);
+      load8<H, VEC, THREADS>(h + at, tid, i, D, hv[i]);
+      load8<X, VEC, THREADS>(dy + at, tid, i, D, u[i]);
     }
 #pragma unroll
     for (int i = 0; i < NP; ++i)
@@ -299,23 +315,22 @@ __global__ __launch_bounds__(THREADS == 64 ? 256 : THREADS) void add_norm_bwd_ke
     s = threads_sum<THREADS>(s, s_sum) / static_cast<float>(D);
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-      const int n = 8 * (tid + THREADS * i);
       float o[8];
       if (dh != nullptr) {
-        load8<H, VEC>(dh + at, n, D, o);
+        load8<H, VEC, THREADS>(dh + at, tid, i, D, o);
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) o[e] = 0.f;
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) u[i][e] = fmaf(r, fmaf(-hv[i][e], s, u[i][e]), o[e]);
-      if (a.dx != nullptr) store8<X, VEC>(static_cast<X *>(a.dx) + at, n, D, u[i]);
-      if (a.dresidual != nullptr) store8<H, VEC>(static_cast<H *>(a.dresidual) + at, n, D, u[i]);
+      if (a.dx != nullptr) store8<X, VEC, THREADS>(static_cast<X *>(a.dx) + at, tid, i, D, u[i]);
+      if (a.dresidual != nullptr) store8<H, VEC, THREADS>(static_cast<H *>(a.dresidual) + at, tid, i, D, u[i]);
     }
   }
   if (a.dw != nullptr) {
 #pragma unroll
-    for (int i = 0; i < NP; ++i) store8<float, VEC>(a.ws + part * D, 8 * (tid + THREADS * i), D, dw[i]);
+    for (int i = 0; i < NP; ++i) store8<float, VEC, THREADS>(a.ws + part * D, tid, i, D, dw[i]);
   }
 }
 
@@ -406,7 +421,7 @@ template <typename X, typename H>
 hipError_t launch_fwd(const AddNormArgs &a, hipStream_t s) {
   const bool vec = a.D % 8 == 0 && aligned(a.x) && aligned(a.residual) && aligned(a.w) && aligned(a.h) && aligned(a.y);
   const int64_t span = a.quant ? a.group / 8 : 0;
-  const bool lanes = a.quant == 0 || a.group == a.D || (a.group % 8 == 0 && span <= 64 && (span & (span - 1)) == 0);
+  const bool lanes = a.quant == 0 || a.group == a.D || (vec && a.group % 8 == 0 && span <= 64 && (span & (span - 1)) == 0);
   const Shape z = shape_of(a.rows, a.D, !lanes);
   const unsigned grid = grid_of(a.rows, z);
   return by_shape(z, [&](auto threads, auto pieces) {
