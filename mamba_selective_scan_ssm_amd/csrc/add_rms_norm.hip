@@ -8,7 +8,15 @@
 //   u = dy w,  dx = dresidual = r (u - h r^2 mean(u h)) + dh,  dw = sum over rows of dy h r
 //
 // THREADS threads hold a row in registers, NP pieces of eight consecutive channels
-// each, so everything is read and written once.  Bound by bytes.
+// each, so everything is read and written once: a wave where rows are many and at most
+// 4096 wide (no barrier), 256 threads for few rows or up to 16384, else 1024.  NP is what
+// the row has, not a power of two: 2560 channels, 5 pieces of a wave's 8, 185 -> 154 us.
+// Bound by bytes: 32768 x 2560 bf16, stream in bf16, 143 us (4.7 TB/s); 16384 x 5120 with
+// the stream in fp32 and an output of e4m3 by 128 channels 181 us (5.1 TB/s, what a copy
+// reaches); forward and backward of 8192 x 2560, stream in fp32, 123 to 127 us (54 + 61 +
+// the sums of dw, 4.7 TB/s).  256 rows in 8 bits take 5.6 us of kernel, one row 3.4, in
+// calls of 9 to 12.  Rows that are no whole 16 bytes: 8000 x 2001 fp32 43 us (6.0 TB/s,
+// partly from the cache), bf16 77 (1.7: two bytes a lane and load).
 #include "add_rms_norm.h"
 #include "device_common.h"
 #include "gdr_common.h"
@@ -328,10 +336,25 @@ __global__ __launch_bounds__(THREADS == 64 ? 256 : THREADS) void add_norm_bwd_ke
       if (a.dresidual != nullptr) store8<H, VEC, THREADS>(static_cast<H *>(a.dresidual) + at, tid, i, D, u[i]);
     }
   }
-  if (a.dw != nullptr) {
+  if (a.dw == nullptr) return;
+  if constexpr (kRows > 1) {  // the four waves' sums, one after the other
+    __shared__ float s_dw[kRows > 1 ? 8 * 64 * NP : 1];
+    for (int q = 0; q < kRows; ++q) {
+      if (static_cast<int>(threadIdx.x) / THREADS == q)
 #pragma unroll
-    for (int i = 0; i < NP; ++i) store8<float, VEC, THREADS>(a.ws + part * D, tid, i, D, dw[i]);
+        for (int i = 0; i < NP; ++i)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int at = tid + THREADS * (8 * i + e);  // a place of its own, not its channel's
+            if (q > 0) dw[i][e] += s_dw[at];
+            s_dw[at] = dw[i][e];
+          }
+      __syncthreads();
+    }
+    if (static_cast<int>(threadIdx.x) / THREADS != kRows - 1) return;
   }
+#pragma unroll
+  for (int i = 0; i < NP; ++i) store8<float, VEC, THREADS>(a.ws + static_cast<int64_t>(blockIdx.x) * D, tid, i, D, dw[i]);
 }
 
 // dw: 64 channels a workgroup, 16 threads each over every 16th partial sum.
@@ -408,14 +431,15 @@ unsigned grid_of(int64_t rows, Shape z) {
   const int64_t most = kCus * (z.threads == 1024 ? 2 : z.threads == 64 ? 64 : 8);
   return static_cast<unsigned>(blocks < most ? blocks : most);
 }
-// The gradients': fewer, since each leaves a partial sum of dw.
+// The gradients': fewer, since each leaves a partial sum of dw: 8192 x 2560, forward and
+// backward, 123 us with 2 a CU, 129 with 4, 136 with 6.
 Shape bwd_shape(int64_t rows, int64_t D) { return shape_of(rows, D, false); }
 unsigned bwd_grid(int64_t rows, Shape z) {
   const int64_t blocks = z.threads == 64 ? (rows + 3) / 4 : rows;
   const int64_t most = kCus * (z.threads == 1024 ? 1 : 2);
   return static_cast<unsigned>(blocks < most ? blocks : most);
 }
-int64_t bwd_parts(int64_t rows, Shape z) { return static_cast<int64_t>(bwd_grid(rows, z)) * (z.threads == 64 ? 4 : 1); }
+int64_t bwd_parts(int64_t rows, Shape z) { return bwd_grid(rows, z); }
 
 template <typename X, typename H>
 hipError_t launch_fwd(const AddNormArgs &a, hipStream_t s) {

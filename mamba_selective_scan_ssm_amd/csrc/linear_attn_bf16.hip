@@ -1,10 +1,9 @@
 // Linear attention by chunks of 64 tokens on the bf16 matrix cores.
 //
-// The formulas are those of linear_attn_f32.hip.  A workgroup of four waves runs 64
-// (CB = 1) or 128 (CB = 2) columns m of one head's chain over a segment, 16 CB
-// columns a wave, whose part of the state S (n down, m across) stays in its
-// registers.  x, keys and values of a chunk lie in LDS, double-buffered behind one
-// barrier a chunk, and are loaded two chunks ahead.
+// The formulas are those of linear_attn_f32.hip.  A workgroup of W waves runs 16 W
+// columns m of one head's chain over a segment, 16 columns a wave, whose part of the
+// state S (n down, m across) stays in its registers.  x, keys and values of a chunk lie
+// in LDS, double-buffered, and come there straight from memory a chunk ahead.
 //
 // v_mfma_f32_16x16x32_bf16 on lane 16 g + r takes A[r][k], B[k][r] for the 8
 // contraction indices k of slot g and gives C[4 g + e][r]; which index a slot stands
@@ -14,13 +13,33 @@
 //    transposing reads of the keys choose them so), and S is an operand as it is;
 //  - tokens: slot (g, 4 u + e) of block tb is token 32 tb + 16 u + 4 g + e, so two
 //    score tiles key . x, one above the other, are the operand of the values'
-//    product as they are: each wave forms all scores for itself, nothing is exchanged.
+//    product as they are.
 // Outputs come out as C[m][token]: a lane's four channels are one store.
+//
+// Eight waves (128 columns, where M passes 64) form the ten score tiles below the
+// diagonal once and share them through LDS, behind the chunk's second barrier.  Four
+// waves (64 columns, two workgroups a CU) form them each for itself: 30 products of 132
+// more, but two workgroups are out of step with each other, and a buffer for the scores
+// would leave room for one.  K above 128 takes 144 KB and one workgroup a CU.
 //
 // Precision: inputs are exact in bf16.  What is computed enters a product in bf16
 // parts: the weighted values, from which the state is made, in three (all 24 bits),
-// the scores and S, from which the outputs are made, in two (off by 2^-17 of each
+// the scores and S, from which the outputs are made, in two (off by 2^-18 of each
 // term; the output is rounded to 2^-9 or summed over heads in fp32).  Sums are fp32.
+//
+// Bound by issue and the phases' latency, not by a unit: 2 x 8192 tokens, 64 heads of
+// 128 x 128 take 0.36 to 0.41 ms (by the box; 2.6 to 3.0 TB/s of inputs and outputs, 190
+// TFLOP/s of the recurrence's 4 P N), a chunk 7.8 thousand cycles on each CU, of which the
+// matrix cores are busy for 3.1, the vector units issue for 3.9, the LDS for 2.6.
+// Measured by a clock in each phase (cycles a chunk, the first and the last four of the
+// eight waves): asking for rows 0.4, scores 0.9 to 1.5, the state's answers 1.0 / 1.4,
+// scores' values 0.8, the state 1.7 / 2.7, stores 0.5, waiting for others 1.2.  What
+// counted: no spill in the loop (a reload waits for the rows on their way, which the
+// counter of loads returns first: 313 -> 380 us at 8 x 2048 tokens), the rows' loads in
+// assembly (see fetch_lds: 375 -> 306), pieces exchanged without conflicts, addresses in
+// scalars.  Measured and dropped: 32 columns a wave, four waves (395 us against 352 then:
+// one wave a SIMD), three buffers (no change: a chunk hides its loads), raised priority
+// of the later four waves (no change), the weighted values before the barrier (no change).
 #include "device_common.h"
 #include "linear_attn.h"
 #include "linear_attn_common.h"
@@ -819,7 +838,8 @@ hipError_t launch_one(const LaArgs &a, const LaPasses &all, int n, hipStream_t s
   });
 }
 // The segments' own additions where the sequences are cut, by workgroups of four waves:
-// all but the last segment of a sequence have some, so they are few.
+// there are half as many of them as of outputs' where sequences are cut in two (2 x 8192
+// tokens, 64 heads of 128 x 128: 416 -> 401 us).
 template <int KB, int W, bool SHARE, bool TAN, bool VEC>
 hipError_t launch_kb(const LaArgs &a, const LaPasses &all, int n, hipStream_t s) {
   const hipError_t e = la_cut(a) ? launch_one<KB, 4, false, false, TAN, VEC>(a, all, n, s) : hipSuccess;

@@ -16,6 +16,15 @@
 // so S goes into S^T x without leaving them.  The scores x . key are shared: each
 // wave forms tiles of 16 x 16 and leaves them in LDS.
 //
+// Chunks of 32 tokens, single-buffered, the next one's rows on their way in registers: 47
+// KB of LDS (K = 128), three workgroups a CU, one's loads and barriers under another's
+// products.  64 tokens (102 KB, one workgroup): 2048 tokens, 64 heads of 128 x 128 323
+// against 231 us; without the registers ahead 418 and 290.  Bound by the fp32 matrix
+// instructions: 66 KFLOP a token and head at 128 x 128, 10 GFLOP in these 231 us (44
+// TFLOP/s of 131), the rest the prologue, the segments' own states and the phases.  bf16
+// parts instead (six products of a sixteenth of the time each) would need three times the
+// LDS and the splitting of x and keys: not tried.
+//
 // Values that are not finite stay behind their token: scores above the diagonal are
 // selected away, and a value's column is left out of the products and set to NaN
 // from its token on (0 times one of them would reach the tokens before it).
