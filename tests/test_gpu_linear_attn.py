@@ -53,6 +53,21 @@ def test_prefill(B, L, H, G, P, N, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("L", [2, 4, 7, 8, 9, 16])
+def test_few_tokens(L, dtype):
+    """Both sides of the length up to which a prefill goes token by token."""
+    import mamba_selective_scan_ssm_amd as ssm
+    for B, H, G, P, N in ((1, 2, 1, 64, 64), (3, 4, 2, 40, 48), (2, 2, 2, 9, 130)):
+        _say("linear_attn_fwd few", B, L, H, G, P, N, dtype)
+        w = blk.make_attention(B, L, H, G, P, N, dtype, 5 + L, h0=True)
+        y, h = ssm.linear_attn_fwd(*inputs(w))
+        torch.cuda.synchronize()
+        ry, rh = blk.attention(*(w[n].double() for n in ("q", "k", "v", "g", "h0")))
+        close(y, ry, "y", blk.parts_slack(w)["y"])
+        close(h, rh, "h")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("B,L,H,G,P,N", SHAPES)
 def test_gradients(B, L, H, G, P, N, dtype):
     import mamba_selective_scan_ssm_amd as ssm
