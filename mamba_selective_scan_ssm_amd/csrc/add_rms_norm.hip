@@ -10,12 +10,12 @@
 // THREADS threads hold a row in registers, NP pieces of eight consecutive channels
 // each, so everything is read and written once: a wave where rows are many and at most
 // 4096 wide (no barrier), 256 threads for few rows or up to 16384, else 1024.  NP is what
-// the row has, not a power of two: 2560 channels, 5 pieces of a wave's 8, 185 -> 154 us.
+// the row has, not a power of two: 2560 channels are 5 pieces and not 8.
 // Bound by bytes: 32768 x 2560 bf16, stream in bf16, 143 us (4.7 TB/s); 16384 x 5120 with
 // the stream in fp32 and an output of e4m3 by 128 channels 181 us (5.1 TB/s, what a copy
-// reaches); forward and backward of 8192 x 2560, stream in fp32, 123 to 127 us (54 + 61 +
-// the sums of dw, 4.7 TB/s).  256 rows in 8 bits take 5.6 us of kernel, one row 3.4, in
-// calls of 9 to 12.  Rows that are no whole 16 bytes: 8000 x 2001 fp32 43 us (6.0 TB/s,
+// reaches); forward and backward of 8192 x 2560, stream in fp32, 123 us (kernels
+// of 53, 63 and, for the sums of dw, 5; 4.8 TB/s).  256 rows in 8 bits take 5 us of
+// kernel, one row 3, in calls of 9 to 12.  Rows that are no whole 16 bytes: 8000 x 2001 fp32 43 us (6.0 TB/s,
 // partly from the cache), bf16 77 (1.7: two bytes a lane and load).
 #include "add_rms_norm.h"
 #include "device_common.h"

@@ -18,28 +18,30 @@
 //
 // Eight waves (128 columns, where M passes 64) form the ten score tiles below the
 // diagonal once and share them through LDS, behind the chunk's second barrier.  Four
-// waves (64 columns, two workgroups a CU) form them each for itself: 30 products of 132
-// more, but two workgroups are out of step with each other, and a buffer for the scores
-// would leave room for one.  K above 128 takes 144 KB and one workgroup a CU.
+// waves (64 columns, two workgroups a CU) form them each for itself.  M = 128, 8 x 2048
+// tokens, 64 heads, K = 128: 285 us with eight, 344 with four; M = 64, 4 x 4096 tokens, 64
+// heads, K = 64: 214 with eight, half of them without a column, 171 with four.  K above 128
+// takes 144 KB and one workgroup a CU.
 //
 // Precision: inputs are exact in bf16.  What is computed enters a product in bf16
 // parts: the weighted values, from which the state is made, in three (all 24 bits),
 // the scores and S, from which the outputs are made, in two (off by 2^-18 of each
 // term; the output is rounded to 2^-9 or summed over heads in fp32).  Sums are fp32.
 //
-// Bound by issue and the phases' latency, not by a unit: 2 x 8192 tokens, 64 heads of
-// 128 x 128 take 0.36 to 0.41 ms (by the box; 2.6 to 3.0 TB/s of inputs and outputs, 190
-// TFLOP/s of the recurrence's 4 P N), a chunk 7.8 thousand cycles on each CU, of which the
-// matrix cores are busy for 3.1, the vector units issue for 3.9, the LDS for 2.6.
-// Measured by a clock in each phase (cycles a chunk, the first and the last four of the
-// eight waves): asking for rows 0.4, scores 0.9 to 1.5, the state's answers 1.0 / 1.4,
-// scores' values 0.8, the state 1.7 / 2.7, stores 0.5, waiting for others 1.2.  What
-// counted: no spill in the loop (a reload waits for the rows on their way, which the
-// counter of loads returns first: 313 -> 380 us at 8 x 2048 tokens), the rows' loads in
-// assembly (see fetch_lds: 375 -> 306), pieces exchanged without conflicts, addresses in
-// scalars.  Measured and dropped: 32 columns a wave, four waves (395 us against 352 then:
-// one wave a SIMD), three buffers (no change: a chunk hides its loads), raised priority
-// of the later four waves (no change), the weighted values before the barrier (no change).
+// Bound by the phases' latency and issue, not by a unit: 2 x 8192 tokens, 64 heads of
+// 128 x 128 take 0.36 to 0.41 ms (by the card; 2.6 to 3.0 TB/s of inputs and outputs, 170 to
+// 190 TFLOP/s of the recurrence's work).  A chunk takes 7.8 thousand cycles on its CU, of
+// which the matrix cores are busy for 3.1, the vector units issue for about as many, the
+// LDS for 2.6.  By a clock in each phase, thousand cycles of the first and the last four of
+// the eight waves: asking for rows 0.3 / 0.4, checks 0.3, scores 0.9 to 1.5, the state's
+// answers, the barrier and the scores' values 2.3 to 2.9 / 2.1 to 2.5, the state 1.7 / 2.6,
+// stores 0.5, the last barrier 1.2 / 0.2.  The loop holds no spill: its reload would wait
+// for the rows on their way, which the same counter counts.
+//
+// Measured and dropped: 32 columns a wave, four waves (14.3 thousand cycles for the same
+// chunk: one wave a SIMD), three buffers (2 x 8192 tokens: 424 -> 428 us, a chunk hides its
+// loads), a raised priority of the later four waves (no change), the weighted values
+// before the barrier (8 x 2048 tokens: 291 -> 300 us).
 #include "device_common.h"
 #include "linear_attn.h"
 #include "linear_attn_common.h"
@@ -837,9 +839,9 @@ hipError_t launch_one(const LaArgs &a, const LaPasses &all, int n, hipStream_t s
     la_bf16_kernel<KB, W, SHARE, Y, TAN, VEC><<<grid, 64 * W, 0, s>>>(a, all, items, sub, base);
   });
 }
-// The segments' own additions where the sequences are cut, by workgroups of four waves:
-// there are half as many of them as of outputs' where sequences are cut in two (2 x 8192
-// tokens, 64 heads of 128 x 128: 416 -> 401 us).
+// The segments' own additions where the sequences are cut, by workgroups of four waves
+// whatever W is: no scores are shared there, and eight take the same time (2 x 8192 tokens,
+// 64 heads of 128 x 128: 391 us against 390).
 template <int KB, int W, bool SHARE, bool TAN, bool VEC>
 hipError_t launch_kb(const LaArgs &a, const LaPasses &all, int n, hipStream_t s) {
   const hipError_t e = la_cut(a) ? launch_one<KB, 4, false, false, TAN, VEC>(a, all, n, s) : hipSuccess;

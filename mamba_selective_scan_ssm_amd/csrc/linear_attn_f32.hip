@@ -19,11 +19,10 @@
 // Chunks of 32 tokens, single-buffered, the next one's rows on their way in registers: 47
 // KB of LDS (K = 128), three workgroups a CU, one's loads and barriers under another's
 // products.  64 tokens (102 KB, one workgroup): 2048 tokens, 64 heads of 128 x 128 323
-// against 231 us; without the registers ahead 418 and 290.  Bound by the fp32 matrix
-// instructions: 66 KFLOP a token and head at 128 x 128, 10 GFLOP in these 231 us (44
-// TFLOP/s of 131), the rest the prologue, the segments' own states and the phases.  bf16
-// parts instead (six products of a sixteenth of the time each) would need three times the
-// LDS and the splitting of x and keys: not tried.
+// against 231 us; without the registers ahead 418 and 290.  Bound by the matrix products
+// and the phases about them: the recurrence's 66 KFLOP a token and head and 12 of a chunk's
+// scores, 10 GFLOP, in these 231 us are 44 TFLOP/s of the 131 of a large product in fp32.
+// The inputs in bf16 parts instead were not tried.
 //
 // Values that are not finite stay behind their token: scores above the diagonal are
 // selected away, and a value's column is left out of the products and set to NaN
