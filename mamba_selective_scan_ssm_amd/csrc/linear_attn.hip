@@ -160,6 +160,7 @@ void la_plan(LaArgs &a, int64_t columns) {
   // us, gradients of 1031 tokens of 6 heads of 40 x 48 251 / 158 / 120; bf16, gradients
   // of 2048 tokens of 16 heads of 64 x 128 95 / 98 / 123.  Twice as many segments: bf16,
   // 2 x 8192 tokens, 64 heads of 128 x 128 403 -> 437 us, 4096 tokens, 32 heads 78 -> 111.
+  // Left whole, the former: 413 -> 437 by eight waves, 128 workgroups, 413 -> 436 by four.
   constexpr int64_t kWanted = 2 * kCus;
   const int64_t least = a.dt_type == DType::F32 ? 64 : 256;
   const int64_t longest = a.L < 0 ? a.T : a.L;
