@@ -117,23 +117,20 @@ __device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d
   return static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(c, d, v, true));
 }
 
-// Eight values times inv, in 8 bits: to nearest even, NaN to NaN (e4m3) or 0 (int8).
+// Eight values in 8 bits: to nearest even, NaN to NaN (e4m3) or 0 (int8).
 template <bool VEC, int THREADS>
-__device__ __forceinline__ void store8_quant(uint8_t *row, int tid, int piece, int D, const float *v, float inv, bool e4m3) {
+__device__ __forceinline__ void store8_quant(uint8_t *row, int tid, int piece, int D, const float *u, bool e4m3) {
   uint32_t q[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    float u[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) u[e] = v[4 * i + e] * inv;
     if (e4m3) {
-      q[i] = pack_e4m3(u[0], u[1], u[2], u[3]);
+      q[i] = pack_e4m3(u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]);
     } else {
       q[i] = 0;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         // a NaN is neither below nor above: taken as 0
-        const float t = u[e] > -128.f && u[e] < 128.f ? u[e] : 0.f;
+        const float a = u[4 * i + e], t = a > -128.f && a < 128.f ? a : 0.f;
         q[i] |= (static_cast<uint32_t>(static_cast<int>(__builtin_rintf(t))) & 0xffu) << (8 * e);
       }
     }
@@ -150,11 +147,31 @@ __device__ __forceinline__ void store8_quant(uint8_t *row, int tid, int piece, i
   }
 }
 
-// The scale of values whose largest has these bits, and what they are multiplied by.
-// NaN has bits above infinity's, and stays.
+// The scale of values whose largest has these bits.  NaN has bits above infinity's, and
+// stays.
 __device__ __forceinline__ float scale_of(uint32_t bits, float most) {
   const float s = __uint_as_float(bits) / most;
   return s < kLeastScale ? kLeastScale : s;
+}
+
+// Eight values divided by the scale of their group, each rounded once: times the rounded
+// 1 / s, and what that lacks of the value (an fma has it exactly) times 1 / s once more,
+// which rounds as the division does (Markstein's theorem).  Outside of these scales what is
+// lacking can fall below the least number, or 1 / s is none.  16384 x 5120 by 128 channels
+// 185 us, by divisions 188, times 1 / s alone (one e4m3 in 2^19 a step off) 184; 32768 x
+// 2560 in bf16 by 64 channels 144, 150 and 142.
+__device__ __forceinline__ void divide8(float *v, float s) {
+  const float inverse = 1.f / s;
+  if (s > 0x1p-90f && s < __builtin_huge_valf()) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float q = v[e] * inverse;
+      v[e] = fmaf(fmaf(-q, s, v[e]), inverse, q);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] /= s;
+  }
 }
 
 // kRows rows a workgroup at a time, a wave each where THREADS is 64.  QUANT 0: none;
@@ -249,7 +266,7 @@ __global__ __launch_bounds__(THREADS == 64 ? 256 : THREADS) void add_norm_kernel
             const int n = channel_of<VEC, THREADS>(tid, i, e);
             u[e] = n < D ? v[i][e] / scale_of(s_max[n / group], most) : 0.f;
           }
-          store8_quant<VEC, THREADS>(q, tid, i, D, u, 1.f, e4m3);
+          store8_quant<VEC, THREADS>(q, tid, i, D, u, e4m3);
         }
       } else if (groups == 1) {
         uint32_t all = top[0];
@@ -266,7 +283,10 @@ __global__ __launch_bounds__(THREADS == 64 ? 256 : THREADS) void add_norm_kernel
         const float sc = scale_of(all, most);
         if (tid == 0) scale[0] = sc;
 #pragma unroll
-        for (int i = 0; i < NP; ++i) store8_quant<VEC, THREADS>(q, tid, i, D, v[i], 1.f / sc, e4m3);
+        for (int i = 0; i < NP; ++i) {
+          divide8(v[i], sc);
+          store8_quant<VEC, THREADS>(q, tid, i, D, v[i], e4m3);
+        }
       } else {
         const int span = group / 8;
 #pragma unroll
@@ -274,7 +294,8 @@ __global__ __launch_bounds__(THREADS == 64 ? 256 : THREADS) void add_norm_kernel
           const int piece = tid + THREADS * i;
           const float sc = scale_of(lanes_max(top[i], span), most);
           if (piece % span == 0 && 8 * piece < D) scale[piece / span] = sc;
-          store8_quant<VEC, THREADS>(q, tid, i, D, v[i], 1.f / sc, e4m3);
+          divide8(v[i], sc);
+          store8_quant<VEC, THREADS>(q, tid, i, D, v[i], e4m3);
         }
       }
     }
