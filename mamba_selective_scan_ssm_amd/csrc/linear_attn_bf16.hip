@@ -26,7 +26,8 @@
 // Precision: inputs are exact in bf16.  What is computed enters a product in bf16
 // parts: the weighted values, from which the state is made, in three (all 24 bits),
 // the scores and S, from which the outputs are made, in two (off by 2^-18 of each
-// term; the output is rounded to 2^-9 or summed over heads in fp32).  Sums are fp32.
+// term; the output is rounded to 2^-9, or summed over heads in fp32 and then rounded),
+// and in three where they make the decays' gradient, which stays in fp32.  Sums are fp32.
 //
 // Bound by the phases' latency and issue, not by a unit: 2 x 8192 tokens, 64 heads of
 // 128 x 128 take 0.36 to 0.41 ms (by the card; 2.6 to 3.0 TB/s of inputs and outputs, 170 to
@@ -166,6 +167,7 @@ void la_bf16_kernel(LaArgs a, LaPasses all, int64_t items, int64_t sub, int64_t 
   constexpr int kThreads = 64 * W, C = 64, KP = 4 * KB, kColumns = 16 * W, VP = kColumns / 8;
   constexpr int kRowsK = C * KP / kThreads, kRowsV = C * VP / kThreads;  // pieces a thread brings
   constexpr uint32_t kTile = 2 * C * KP * 8, kTileV = 2 * C * VP * 8;    // bytes
+  constexpr int kParts = TAN ? 3 : 2;  // of S and of the scores
   // two buffers of keys, of values, of x, and (shared) two parts of the scores: one
   // array, so that two workgroups find room where these are 80 KB
   constexpr int kSizeK = C * KP * 8, kSizeV = C * VP * 8;
@@ -433,14 +435,14 @@ void la_bf16_kernel(LaArgs a, LaPasses all, int64_t items, int64_t sub, int64_t 
   float n_left = static_cast<float>(C) * power_of(log2_a, C);
   double sum = 0.0;
 
-  // A product of a key and an x tile: weighted, masked, in two parts.
+  // A product of a key and an x tile: weighted, masked, in parts.
   auto split_scores = [&](f32x4 w, const f32x4 &weight, bool diagonal, u32x2 *half) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       w[e] *= weight[e];
       w[e] = diagonal && r < 4 * g + e ? 0.f : w[e];
     }
-    split_four<2>(w, half);
+    split_four<kParts>(w, half);
   };
   // The weighted values of token block tb, in three parts.
   auto weighted = [&](const u32x4 &v, int tb, int left, u32x4 *out, bool tan) {
@@ -566,11 +568,34 @@ void la_bf16_kernel(LaArgs a, LaPasses all, int64_t items, int64_t sub, int64_t 
         // ---- token block by token block: what the state answers, the scores and the
         // values under them
         load(t0 + C, buf ^ 1, 1);
-        u32x4 part[KB][2], pu[TAN ? KB : 1][2];
+        u32x4 part[TAN ? 1 : KB][2];
+        if constexpr (TAN) {
+          // what the state and the tangent answer goes first, a block of 32 of their rows
+          // at a time: all blocks' parts would not fit into the registers
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb) {
-          split_parts<2>(S[2 * kb], S[2 * kb + 1], part[kb]);
-          if constexpr (TAN) split_parts<2>(U[2 * kb], U[2 * kb + 1], pu[kb]);
+          for (int i = 0; i < 4; ++i) y[i] = yu[i] = zero;
+#pragma unroll
+          for (int kb = 0; kb < KB; ++kb) {
+            u32x4 xq[4], ps[kParts], pu[kParts];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) xq[i] = lds_get<u32x4>(lx[kb] + 2 * 8 * KP * 16 * i);
+            split_parts<kParts>(S[2 * kb], S[2 * kb + 1], ps);
+            split_parts<kParts>(U[2 * kb], U[2 * kb + 1], pu);
+#pragma unroll
+            for (int q = 0; q < kParts; ++q)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                y[i] = mma(ps[q], xq[i], y[i]);
+                yu[i] = mma(pu[q], xq[i], yu[i]);
+              }
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[i][e] = fmaf(static_cast<float>(16 * i + r + 1), y[i][e], yu[i][e]) * w_out[i];
+        } else {
+#pragma unroll
+          for (int kb = 0; kb < KB; ++kb) split_parts<2>(S[2 * kb], S[2 * kb + 1], part[kb]);
         }
 #pragma unroll
         for (int bt = 0; bt < 4; ++bt) {
@@ -585,31 +610,23 @@ void la_bf16_kernel(LaArgs a, LaPasses all, int64_t items, int64_t sub, int64_t 
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb) w[bs] = mma(lds_get<u32x4>(lk[kb] + 2 * 8 * KP * 16 * bs), xq[kb], w[bs]);
           }
-          y[bt] = zero;
-#pragma unroll
-          for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-            for (int q = 0; q < 2; ++q) y[bt] = mma(part[kb][q], xq[kb], y[bt]);
-          if constexpr (TAN) {
-            yu[bt] = zero;
+          if constexpr (!TAN) {
+            y[bt] = zero;
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-              for (int q = 0; q < 2; ++q) yu[bt] = mma(pu[kb][q], xq[kb], yu[bt]);
-          }
+              for (int q = 0; q < 2; ++q) y[bt] = mma(part[kb][q], xq[kb], y[bt]);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if constexpr (TAN) y[bt][e] = fmaf(static_cast<float>(16 * bt + r + 1), y[bt][e], yu[bt][e]);
-            y[bt][e] *= w_out[bt];
+            for (int e = 0; e < 4; ++e) y[bt][e] *= w_out[bt];
           }
 #pragma unroll
           for (int tb = 0; tb <= bt / 2; ++tb) {
-            u32x2 half[2][2] = {};
+            u32x2 half[2][kParts] = {};
 #pragma unroll
             for (int u = 0; u < 2; ++u)
               if (2 * tb + u <= bt) split_scores(w[2 * tb + u], w_score[SHARE ? 0 : bt - 2 * tb - u], 2 * tb + u == bt, half[u]);
 #pragma unroll
-            for (int q = 0; q < 2; ++q)
+            for (int q = 0; q < kParts; ++q)
               y[bt] = mma(v[tb], u32x4{half[0][q][0], half[0][q][1], half[1][q][0], half[1][q][1]}, y[bt]);
           }
         }
