@@ -601,8 +601,11 @@ size_t ssm_group_norm_bwd_workspace_size(int64_t S, int64_t T, int64_t D, int64_
  *   S_t[p,n] = a * S_{t-1}[p,n] + v[t,h,p] * k[t,g,n]
  *   y[t,h,p] = scale * sum_n S_t[p,n] q[t,g,n]
  *   h_final = S after the last token
- * log_decay <= 0 as models have it; one above 0 is taken as it is, -infinity is
- * a decay of 0 (no memory).
+ * log_decay <= 0 as models have it; -infinity is a decay of 0 (no memory).  One
+ * above 0 is taken as it is, but prefills and gradients form its powers over up to 64
+ * tokens and products with them: where 64 a^64, times scale q . k too, passes 2^127
+ * (log_decay from about 1.2 on), results may be NaN where the formulas' are finite, also
+ * of a state or of values that are zero.
  *
  * q, k      : (B, L, G, N) dtype `dt`;  v, y : (B, L, H, P) dtype `dt`
  * log_decay : (H) fp32

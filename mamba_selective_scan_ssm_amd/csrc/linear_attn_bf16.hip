@@ -346,8 +346,8 @@ void la_bf16_kernel(LaArgs a, LaPasses all, int64_t items, int64_t sub, int64_t 
           }
       }
     }
-    const LaCarry whole(log_a, a.seg_len);
-    const float n_whole = static_cast<float>(a.seg_len) * la_power(log_a, a.seg_len);
+    const LaWhole whole(log_a, a.seg_len);
+    const float n_whole = static_cast<float>(a.seg_len);
     for (int64_t b = 0; b < z.before; ++b) {
       const int64_t from = (((z.slot0 + b) * a.H + h) * p.M + m0) * Kp;
       const float *local = p.local + from, *local_tan = TAN ? p.local_tan + from : nullptr;
@@ -360,7 +360,7 @@ void la_bf16_kernel(LaArgs a, LaPasses all, int64_t items, int64_t sub, int64_t 
         if constexpr (TAN) {
           const f32x4 tan = there ? *reinterpret_cast<const f32x4 *>(local_tan + at + n) : zero;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) U[j][e] = whole(U[j][e]) + fmaf(n_whole, S[j][e], tan[e]);
+          for (int e = 0; e < 4; ++e) U[j][e] = whole(U[j][e]) + fmaf(n_whole, whole(S[j][e]), tan[e]);
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) S[j][e] = whole(S[j][e]) + own[e];

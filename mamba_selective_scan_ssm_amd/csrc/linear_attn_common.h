@@ -76,6 +76,21 @@ struct LaCarry {
   }
   __device__ __forceinline__ float operator()(float s) const { return fmaf(s, m, s * one); }
 };
+// The same over a whole segment, thousands of tokens it may be: there the power of a decay
+// above 1 passes fp32 where the state, zero or small, and the result do not, and is taken in
+// two halves.
+struct LaWhole {
+  LaCarry first;
+  float again;
+  __device__ __forceinline__ LaWhole(double log_a, int64_t n) : first(log_a, n), again(1.f) {
+    const double e = log_a * static_cast<double>(n);
+    if (e > 88.0) {
+      again = static_cast<float>(fmin(exp(0.5 * e), 3e38));
+      first.m = again;
+    }
+  }
+  __device__ __forceinline__ float operator()(float s) const { return first(s) * again; }
+};
 // a^n, 1 for n = 0 whatever a
 __device__ __forceinline__ float la_power(double log_a, int64_t n) {
   return n == 0 ? 1.f : static_cast<float>(exp(log_a * static_cast<double>(n)));

@@ -106,8 +106,8 @@ __global__ __launch_bounds__(kThreads) void la_f32_kernel(LaArgs a, LaPasses all
   }
   const int64_t Kp = (p.K + 15) / 16 * 16;
   if constexpr (Y) {
-    const LaCarry whole(log_a, a.seg_len);
-    const float n_whole = static_cast<float>(a.seg_len) * la_power(log_a, a.seg_len);
+    const LaWhole whole(log_a, a.seg_len);
+    const float n_whole = static_cast<float>(a.seg_len);
     for (int64_t b = 0; b < z.before; ++b) {
       const int64_t from = (((z.slot0 + b) * a.H + h) * p.M + m) * Kp;
 #pragma unroll
@@ -118,7 +118,7 @@ __global__ __launch_bounds__(kThreads) void la_f32_kernel(LaArgs a, LaPasses all
         if constexpr (TAN) {
           const f32x4 tan = there ? *reinterpret_cast<const f32x4 *>(p.local_tan + from + 16 * j + 4 * g) : zero;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) U[j][e] = whole(U[j][e]) + fmaf(n_whole, S[j][e], tan[e]);
+          for (int e = 0; e < 4; ++e) U[j][e] = whole(U[j][e]) + fmaf(n_whole, whole(S[j][e]), tan[e]);
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) S[j][e] = whole(S[j][e]) + own[e];
