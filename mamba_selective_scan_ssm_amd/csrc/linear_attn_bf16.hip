@@ -126,7 +126,7 @@ struct Rows {
 __device__ __forceinline__ void fetch_lds(const Rows &r, uint32_t to, uint32_t at, uint32_t more) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(to), "v"(at), "s"(r.words),
                "s"(more)
-               : "memory");
+               : "memory", "m0");
 }
 
 // fp32 as a sum of NP bf16 parts, as split4 of gdr_mfma.h, the rest by a shift (or a
