@@ -6,7 +6,6 @@
 
 namespace ssm {
 
-constexpr int64_t kAddNormMaxD = 65536;
 constexpr int kAddNormLeastGroup = 8;  // channels of a scale
 constexpr float kE4m3Max = 448.f, kInt8Max = 127.f;
 constexpr float kLeastScale = 7.888609052210118e-31f;  // 2^-100

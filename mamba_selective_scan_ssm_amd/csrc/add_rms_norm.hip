@@ -287,7 +287,7 @@ __global__ __launch_bounds__(THREADS == 64 ? 256 : THREADS) void add_norm_kernel
           divide8(v[i], sc);
           store8_quant<VEC, THREADS>(q, tid, i, D, v[i], e4m3);
         }
-      } else {
+      } else if constexpr (VEC) {
         const int span = group / 8;
 #pragma unroll
         for (int i = 0; i < NP; ++i) {

@@ -60,7 +60,7 @@ inline int64_t la_local_floats(const LaArgs &a, int64_t K, int64_t M) {
 inline int64_t la_columns(int64_t M) { return (M + 63) / 64; }
 inline bool la_cut(const LaArgs &a) { return a.slots > a.S; }
 
-// By chunks, in fp32 matrix instructions (linear_attn_f32.hip): any type, size
+// By chunks, fp32 inputs, in fp32 matrix instructions (linear_attn_f32.hip): any size
 // and alignment, K <= 256.  Passes of one number of columns run side by side.
 hipError_t launch_la_f32(const LaArgs &a, const LaPass *p, int n, hipStream_t s);
 // By chunks, bf16 inputs, on the bf16 matrix cores (linear_attn_bf16.hip).

@@ -67,7 +67,6 @@ __device__ __forceinline__ LaSlot la_slot(const LaArgs &a, int64_t slot, bool re
 // factor again and again (each time off by up to 2^-25 in the same direction).
 struct LaCarry {
   float m, one;
-  __device__ __forceinline__ LaCarry() {}
   __device__ __forceinline__ LaCarry(double log_a, int64_t n) {
     const double e = log_a * static_cast<double>(n);
     const bool near = e > -0.6931 && e < 0.6931;
@@ -109,9 +108,9 @@ inline int64_t la_sub(const LaArgs &a, int64_t per, int64_t cols) {
   const int64_t heads = a.slots * a.H;
   return heads / per >= 64 ? per * cols : heads >= 64 ? cols : 1;
 }
-// n passes over all workgroups of `cols` columns each, in grids below 2^32 threads.
+// One or two passes over all workgroups of `cols` columns each, in grids below 2^32 threads.
 struct LaPasses {
-  LaPass p[3];
+  LaPass p[2];
 };
 template <typename F>
 hipError_t la_launches(const LaArgs &a, int64_t cols, int64_t sub, int n, F &&launch) {

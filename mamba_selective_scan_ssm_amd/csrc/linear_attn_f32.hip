@@ -1,5 +1,5 @@
-// Linear attention by chunks of C tokens on the fp32 matrix instructions: any
-// type, size and alignment.
+// Linear attention by chunks of C tokens on the fp32 matrix instructions: fp32 inputs
+// of any size and alignment.
 //
 // Within a chunk of `left` tokens entered by the state S (n down, m across), with
 // the powers a^d of the head's decay, f = 1 and (where the pass runs backwards) 0:
@@ -36,33 +36,25 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kColumns = 64;
+constexpr int C = 32;  // tokens of a chunk
 
-// f32x4 from a row of storage elements; elements from `left` on are 0
-template <typename T, bool VEC>
-__device__ __forceinline__ f32x4 load_four(const T *p, int left) {
+// Four consecutive elements of a row; elements from `left` on are 0
+template <bool VEC>
+__device__ __forceinline__ f32x4 load_four(const float *p, int left) {
+  if constexpr (VEC)
+    if (left >= 4) return *reinterpret_cast<const f32x4 *>(p);
   f32x4 v = {0.f, 0.f, 0.f, 0.f};
-  if constexpr (VEC) {
-    if (left >= 4) {
-      struct alignas(4 * sizeof(T)) Raw {
-        T v[4];
-      };
-      const Raw r = *reinterpret_cast<const Raw *>(p);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = to_f32(r.v[e]);
-      return v;
-    }
-  }
 #pragma unroll
   for (int e = 0; e < 4; ++e)
-    if (e < left) v[e] = to_f32(p[e]);
+    if (e < left) v[e] = p[e];
   return v;
 }
 
 // KT: tiles of 16 that K is rounded up to.  Y: outputs (or the tangent's sum); else
 // the segment's own addition to the state.
-template <typename T, int KT, int C, bool Y, bool TAN, bool VEC>
+template <int KT, bool Y, bool TAN, bool VEC>
 __global__ __launch_bounds__(kThreads) void la_f32_kernel(LaArgs a, LaPasses all, int64_t items, int64_t sub,
-                                                              int64_t base) {
+                                                          int64_t base) {
   constexpr int kPitch = 16 * KT + 4, kVal = kColumns + 4, kScore = C + 4;
   constexpr int CT = C / 16, kPairs = CT * (CT + 1) / 2;
   __shared__ __attribute__((aligned(16))) float s_x[Y ? C : 1][kPitch];
@@ -126,10 +118,10 @@ __global__ __launch_bounds__(kThreads) void la_f32_kernel(LaArgs a, LaPasses all
     }
   }
 
-  const T *x = static_cast<const T *>(p.x) + h / p.x_per * p.x_width;
-  const T *key = static_cast<const T *>(p.key) + h / p.key_per * p.key_width;
-  const T *val = static_cast<const T *>(p.val) + h / p.val_per * p.val_width;
-  const T *dot = TAN ? static_cast<const T *>(p.dot) + h / p.val_per * p.val_width : nullptr;
+  const float *x = static_cast<const float *>(p.x) + h / p.x_per * p.x_width;
+  const float *key = static_cast<const float *>(p.key) + h / p.key_per * p.key_width;
+  const float *val = static_cast<const float *>(p.val) + h / p.val_per * p.val_width;
+  const float *dot = TAN ? static_cast<const float *>(p.dot) + h / p.val_per * p.val_width : nullptr;
   double sum = 0.0;
 
   // ---- x, keys and values of the next chunk, on their way in registers; zeros behind
@@ -144,15 +136,15 @@ __global__ __launch_bounds__(kThreads) void la_f32_kernel(LaArgs a, LaPasses all
       const int q = tid + kThreads * i, t = q / (4 * KT), n = q % (4 * KT) * 4;
       const int have = t < left ? p.K - n : 0;
       const int64_t row = have > 0 ? row_of(t0 + t) : 0;
-      if constexpr (Y) px[i] = load_four<T, VEC>(x + row * p.x_row + n, have);
-      pk[i] = load_four<T, VEC>(key + row * p.key_row + n, have);
+      if constexpr (Y) px[i] = load_four<VEC>(x + row * p.x_row + n, have);
+      pk[i] = load_four<VEC>(key + row * p.key_row + n, have);
     }
 #pragma unroll
     for (int i = 0; i < kFoursV; ++i) {
       const int q = tid + kThreads * i, t = q / (kColumns / 4), n = q % (kColumns / 4) * 4;
       const int have = t < left ? p.M - m0 - n : 0;
       const int64_t row = have > 0 ? row_of(t0 + t) : 0;
-      pv[i] = load_four<T, VEC>(val + row * p.val_row + m0 + n, have);
+      pv[i] = load_four<VEC>(val + row * p.val_row + m0 + n, have);
     }
   };
   if (z.len > 0) load(0);
@@ -250,11 +242,9 @@ __global__ __launch_bounds__(kThreads) void la_f32_kernel(LaArgs a, LaPasses all
           const float out = t >= bad ? __builtin_nanf("") : c_out * y[i][e];
           if (t < left && col) {
             if constexpr (TAN) {
-              sum += static_cast<double>(out) * to_f32(dot[row_of(t0 + t) * p.val_row + m]);
+              sum += static_cast<double>(out) * dot[row_of(t0 + t) * p.val_row + m];
             } else {
-              const int64_t o = row_of(t0 + t) * p.out_row + h * p.out_width + m;
-              if (p.out_f32) static_cast<float *>(p.out)[o] = out;
-              else static_cast<T *>(p.out)[o] = from_f32<T>(out);
+              static_cast<float *>(p.out)[row_of(t0 + t) * p.out_row + h * p.out_width + m] = out;
             }
           }
         }
@@ -338,52 +328,50 @@ __global__ __launch_bounds__(kThreads) void la_f32_kernel(LaArgs a, LaPasses all
   }
 }
 
-template <typename T, int KT, int C, bool TAN, bool VEC>
+template <int KT, bool TAN, bool VEC>
 hipError_t launch_kt(const LaArgs &a, const LaPasses &all, int n, int64_t cols, int64_t sub, hipStream_t s) {
   for (int y = la_cut(a) ? 0 : 1; y < 2; ++y) {
     const hipError_t e = la_launches(a, cols, sub, n, [&](dim3 grid, int64_t items, int64_t base) {
-      if (y) la_f32_kernel<T, KT, C, true, TAN, VEC><<<grid, kThreads, 0, s>>>(a, all, items, sub, base);
-      else la_f32_kernel<T, KT, C, false, TAN, VEC><<<grid, kThreads, 0, s>>>(a, all, items, sub, base);
+      if (y) la_f32_kernel<KT, true, TAN, VEC><<<grid, kThreads, 0, s>>>(a, all, items, sub, base);
+      else la_f32_kernel<KT, false, TAN, VEC><<<grid, kThreads, 0, s>>>(a, all, items, sub, base);
     });
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
 }
 
-template <typename T>
 bool fours(const LaPass &p) {
   for (const void *q : {p.x, p.key, p.val})
-    if (reinterpret_cast<uintptr_t>(q) % (4 * sizeof(T)) != 0) return false;
+    if (reinterpret_cast<uintptr_t>(q) % 16 != 0) return false;
   for (int64_t n : {p.x_row, p.key_row, p.val_row, p.x_width, p.key_width, p.val_width})
     if (n % 4 != 0) return false;
   return true;
 }
 
-template <typename T, bool TAN>
-hipError_t launch_type(const LaArgs &a, const LaPass *p, int n, hipStream_t s) {
+template <bool TAN>
+hipError_t launch_width(const LaArgs &a, const LaPass *p, int n, hipStream_t s) {
   LaPasses all{};
   bool vec = true;
   for (int i = 0; i < n; ++i) {
     all.p[i] = p[i];
-    vec = vec && fours<T>(p[i]);
+    vec = vec && fours(p[i]);
   }
   const int64_t cols = la_columns(p[0].M);
   const int64_t sub = la_sub(a, p[0].x_per, cols);
-#define SSM_LA_KT(KT, C)                                                        \
-  return vec ? launch_kt<T, KT, C, TAN, true>(a, all, n, cols, sub, s)          \
-             : launch_kt<T, KT, C, TAN, false>(a, all, n, cols, sub, s)
-  if (p[0].K <= 64) SSM_LA_KT(4, 32);
-  if (p[0].K <= 128) SSM_LA_KT(8, 32);
-  SSM_LA_KT(16, 32);
+#define SSM_LA_KT(KT)                                                    \
+  return vec ? launch_kt<KT, TAN, true>(a, all, n, cols, sub, s)         \
+             : launch_kt<KT, TAN, false>(a, all, n, cols, sub, s)
+  if (p[0].K <= 64) SSM_LA_KT(4);
+  if (p[0].K <= 128) SSM_LA_KT(8);
+  SSM_LA_KT(16);
 #undef SSM_LA_KT
 }
 
 }  // namespace
 
 hipError_t launch_la_f32(const LaArgs &a, const LaPass *p, int n, hipStream_t s) {
-  const bool tan = p[0].dot_sum != nullptr;  // dot may be empty
-  if (a.dt_type == DType::BF16) return tan ? launch_type<bf16_t, true>(a, p, n, s) : launch_type<bf16_t, false>(a, p, n, s);
-  return tan ? launch_type<float, true>(a, p, n, s) : launch_type<float, false>(a, p, n, s);
+  // dot may be empty
+  return p[0].dot_sum != nullptr ? launch_width<true>(a, p, n, s) : launch_width<false>(a, p, n, s);
 }
 
 }  // namespace ssm
