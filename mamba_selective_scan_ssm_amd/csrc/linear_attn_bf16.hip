@@ -632,10 +632,15 @@ void la_bf16_kernel(LaArgs a, LaPasses all, int64_t items, int64_t sub, int64_t 
         }
       }
     }
-    // ---- the state that leaves the chunk, the next keys on their way
+    // ---- the state that leaves the chunk, the next keys on their way.  What the chunk adds
+    // is summed from zero and joined with the state in one rounding: in products that
+    // begin with a large state the matrix cores cut off what lies below it, always
+    // towards zero (4096 chunks of positive terms, a memory of 800: states 3.6e-6 off on
+    // the average and up to 1.5e-5, now none and 2.2e-6; 2 x 8192 tokens, 64 heads of 128 x
+    // 128 407 -> 410 us).
     u32x4 kt[2][2];
     auto read_keys = [&](int i) {  // block kb, transposed: rows n of its two tiles, tokens of block tb
-      const int tb = i / KB, kb = i % KB;
+      const int kb = i / 2, tb = i % 2;
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -646,35 +651,41 @@ void la_bf16_kernel(LaArgs a, LaPasses all, int64_t items, int64_t sub, int64_t 
         }
     };
     read_keys(0);
-    if constexpr (TAN) {
+    u32x4 wu[TAN ? 2 : 1][3];
+    f32x4 add[2][2], add_u[2][TAN ? 2 : 1];
+    auto join = [&](int kb) {
 #pragma unroll
-      for (int j = 0; j < 2 * KB; ++j)
+      for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) U[j][e] = fmaf(n_left, S[j][e], carry * U[j][e]);
-    }
-    u32x4 wu[3];
+        for (int e = 0; e < 4; ++e) {
+          if constexpr (TAN)
+            U[2 * kb + u][e] = fmaf(n_left, S[2 * kb + u][e], fmaf(carry, U[2 * kb + u][e], add_u[kb % 2][u][e]));
+          S[2 * kb + u][e] = fmaf(carry, S[2 * kb + u][e], add[kb % 2][u][e]);
+        }
+    };
 #pragma unroll
     for (int i = 0; i < 2 * KB; ++i) {
-      const int tb = i / KB, kb = i % KB;
+      const int kb = i / 2, tb = i % 2;
       if (kb == 0) {
         weighted(v[tb], tb, left, wv[tb], false);
-        if constexpr (TAN) weighted(v[tb], tb, left, wu, true);
+        if constexpr (TAN) weighted(v[tb], tb, left, wu[tb], true);
       }
       __builtin_amdgcn_sched_barrier(0);
       if (i + 1 < 2 * KB) read_keys(i + 1);
-      if (tb == 0)
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) S[2 * kb + u][e] *= carry;
 #pragma unroll
       for (int q = 0; q < 3; ++q)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          S[2 * kb + u] = mma(kt[i % 2][u], wv[tb][q], S[2 * kb + u]);
-          if constexpr (TAN) U[2 * kb + u] = mma(kt[i % 2][u], wu[q], U[2 * kb + u]);
+          f32x4 &to = add[kb % 2][u];
+          to = mma(kt[i % 2][u], wv[tb][q], tb == 0 && q == 0 ? zero : to);
+          if constexpr (TAN) {
+            f32x4 &to = add_u[kb % 2][u];
+            to = mma(kt[i % 2][u], wu[tb][q], tb == 0 && q == 0 ? zero : to);
+          }
         }
+      if (tb == 0 && kb > 0) join(kb - 1);
     }
+    join(KB - 1);
     __builtin_amdgcn_sched_barrier(0);
     if (dirty) {
       if (bad < C) {

@@ -74,6 +74,8 @@ struct LaCarry {
     one = n == 0 || near ? 1.f : 0.f;
   }
   __device__ __forceinline__ float operator()(float s) const { return fmaf(s, m, s * one); }
+  // and what is added to it: the change first, then one sum
+  __device__ __forceinline__ float operator()(float s, float more) const { return fmaf(s, m, more) + s * one; }
 };
 // The same over a whole segment, thousands of tokens it may be: there the power of a decay
 // above 1 passes fp32 where the state, zero or small, and the result do not, and is taken in

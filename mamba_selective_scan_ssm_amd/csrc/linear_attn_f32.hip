@@ -262,21 +262,23 @@ __global__ __launch_bounds__(kThreads) void la_f32_kernel(LaArgs a, LaPasses all
         if constexpr (TAN) u[j][e] = d < 0 ? 0.f : w * static_cast<float>(d);
         v[j][e] = w;
       }
+    // What the chunk adds is summed from zero and joined with the state in one rounding: a
+    // large state in the products would round each of their sums to its own steps.
 #pragma unroll
     for (int i = 0; i < KT; ++i) {
-      if constexpr (TAN) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) U[i][e] = fmaf(n_left, S[i][e], carry(U[i][e]));
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) S[i][e] = carry(S[i][e]);
+      f32x4 add = {0.f, 0.f, 0.f, 0.f}, add_u = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int j = 0; j < CT; ++j) {
         f32x4 k;
 #pragma unroll
         for (int e = 0; e < 4; ++e) k[e] = s_k[16 * j + 4 * g + e][16 * i + r];
-        S[i] = mma_f32(k, v[j], S[i]);
-        if constexpr (TAN) U[i] = mma_f32(k, u[j], U[i]);
+        add = mma_f32(k, v[j], add);
+        if constexpr (TAN) add_u = mma_f32(k, u[j], add_u);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if constexpr (TAN) U[i][e] = fmaf(n_left, S[i][e], carry(U[i][e])) + add_u[e];
+        S[i][e] = carry(S[i][e], add[e]);
       }
       if (bad < C) {
 #pragma unroll
