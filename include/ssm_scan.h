@@ -710,7 +710,8 @@ size_t ssm_linear_attn_bwd_workspace_size(int64_t B, int64_t L, int64_t H, int64
  *   scale = max |y| / 448 (127), at least 2^-100;  q[d] = y[d] / scale, rounded to
  *   nearest even;  y is q, (rows, D) bytes, which stand for q * scale.
  * A group with a value that is not finite has a scale that is not; a row's
- * NaN or infinity reaches its own row alone.
+ * NaN or infinity reaches its own row alone.  Each operation is one of fp32, and so is the
+ * sum of h^2: values past 1e19, whose squares are not, have a rstd of 0.
  *
  * x            : (rows, D) dtype `dt`
  * residual, h  : (rows, D) dtype stream_dt, both or neither (then stream_dt ==

@@ -8,15 +8,19 @@
 //   u = dy w,  dx = dresidual = r (u - h r^2 mean(u h)) + dh,  dw = sum over rows of dy h r
 //
 // THREADS threads hold a row in registers, NP pieces of eight consecutive channels
-// each, so everything is read and written once: a wave where rows are many and at most
-// 4096 wide (no barrier), 256 threads for few rows or up to 16384, else 1024.  NP is what
-// the row has, not a power of two: 2560 channels are 5 pieces and not 8.
+// each, so up to 16384 channels everything is read and written once: a wave where rows are
+// many and at most 4096 wide (no barrier), 256 threads for few rows or up to 16384, else
+// 1024.  NP is what the row has, not a power of two: 2560 channels are 5 pieces and not 8.
+// Of 1024 threads each has 128 registers, which the row and the weights fill: wider rows
+// pass through scratch memory too (208 to 645 registers a thread, by types and pass): 2048 x
+// 32768 of bf16 222 us forward (2.4 TB/s), 339 in 8 bits, 1136 backward, where 4096 x 16384
+// take 144, 128 and 253.
 // Bound by bytes: 32768 x 2560 bf16, stream in bf16, 143 us (4.7 TB/s); 16384 x 5120 with
-// the stream in fp32 and an output of e4m3 by 128 channels 181 us (5.1 TB/s, what a copy
-// reaches); forward and backward of 8192 x 2560, stream in fp32, 123 us (kernels
-// of 53, 63 and, for the sums of dw, 5; 4.8 TB/s).  256 rows in 8 bits take 5 us of
-// kernel, one row 3, in calls of 9 to 12.  Rows that are no whole 16 bytes: 8000 x 2001 fp32 43 us (6.0 TB/s,
-// partly from the cache), bf16 77 (1.7: two bytes a lane and load).
+// the stream in fp32 and an output of e4m3 by 128 channels 182 us (5.1 TB/s, what a copy
+// of 1 GiB by copy_ reaches); forward and backward of 8192 x 2560, stream in fp32, 123 us
+// (kernels of 53, 64 and, for the sums of dw, 5; 4.8 TB/s).  256 rows in 8 bits take 5 us of
+// kernel, one row 3, in calls of 9 to 12.  Rows that are no whole 16 bytes: 8000 x 2001 fp32 41 us (6.3 TB/s,
+// partly from the cache), bf16 78 (1.7: two bytes a lane and load).
 #include "add_rms_norm.h"
 #include "device_common.h"
 #include "gdr_common.h"

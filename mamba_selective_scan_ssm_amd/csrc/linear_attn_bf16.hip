@@ -30,14 +30,17 @@
 // and in three where they make the decays' gradient, which stays in fp32.  Sums are fp32.
 //
 // Bound by the phases' latency and issue, not by a unit: 2 x 8192 tokens, 64 heads of
-// 128 x 128 take 0.36 to 0.41 ms (by the card; 2.6 to 3.0 TB/s of inputs and outputs, 170 to
+// 128 x 128 take 0.37 to 0.43 ms (by the card; 2.5 to 3.0 TB/s of inputs and outputs, 160 to
 // 190 TFLOP/s of the recurrence's work).  A chunk takes 7.8 thousand cycles on its CU, of
 // which the matrix cores are busy for 3.1, the vector units issue for about as many, the
-// LDS for 2.6.  By a clock in each phase, thousand cycles of the first and the last four of
-// the eight waves: asking for rows 0.3 / 0.4, checks 0.3, scores 0.9 to 1.5, the state's
-// answers, the barrier and the scores' values 2.3 to 2.9 / 2.1 to 2.5, the state 1.7 / 2.6,
-// stores 0.5, the last barrier 1.2 / 0.2.  The loop holds no spill: its reload would wait
-// for the rows on their way, which the same counter counts.
+// LDS for 2.6.  By a clock in each phase (8.2 with the clocks), thousand cycles of the first
+// and the last four of the eight waves: asking for rows 0.4, checks 0.3, scores 0.7 to 1.3 /
+// 0.7, the state's answers 1.5 / 2.2, the barrier and the scores' values 1.3 to 1.9 / 0.9 to
+// 1.1, the state 1.7 / 2.7, stores 0.7 / 0.6, the last barrier 1.1 / 0.1.  The loop of eight
+// waves with whole 16-byte rows holds no spill: its reload would wait for the rows on their
+// way, which the same counter counts.  Other kernels have some: of whole rows, four waves with
+// K from 65 to 128 7 registers; of rows that are no whole 16 bytes, whose next chunk is held in
+// registers too, four waves with K from 65 to 128 291, the others up to 46.
 //
 // Measured and dropped: 32 columns a wave, four waves (14.3 thousand cycles for the same
 // chunk: one wave a SIMD), three buffers (2 x 8192 tokens: 424 -> 428 us, a chunk hides its

@@ -16,9 +16,9 @@
 // so S goes into S^T x without leaving them.  The scores x . key are shared: each
 // wave forms tiles of 16 x 16 and leaves them in LDS.
 //
-// Chunks of 32 tokens, single-buffered, the next one's rows on their way in registers: 47
-// KB of LDS (K = 128), three workgroups a CU, one's loads and barriers under another's
-// products.  64 tokens (102 KB, one workgroup): 2048 tokens, 64 heads of 128 x 128 323
+// Chunks of 32 tokens, single-buffered, the next one's rows on their way in registers: two
+// workgroups a CU, one's loads and barriers under the other's products (232 registers a lane
+// at K = 128, 176 at 64; the 47 KB of LDS would hold three).  64 tokens (102 KB, one workgroup): 2048 tokens, 64 heads of 128 x 128 323
 // against 231 us; without the registers ahead 418 and 290.  Bound by the matrix products
 // and the phases about them: the recurrence's 66 KFLOP a token and head and 12 of a chunk's
 // scores, 10 GFLOP, in these 231 us are 44 TFLOP/s of the 131 of a large product in fp32.
